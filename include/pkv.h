@@ -76,9 +76,10 @@ enum {
   PKV_DEV_WAIT_TIMEOUT = 5,     /* a shared-memory copy did not complete in time */
   PKV_DEV_BAD_QUERY_RANGE = 6,  /* prefill: new tokens outside [0, context_len] or outside q, or
                                    more new tokens than max_query_len covers */
-  PKV_DEV_PREFIX_MISMATCH = 7   /* shared-prefix decode: a sequence's first prefix blocks differ
+  PKV_DEV_PREFIX_MISMATCH = 7,  /* shared-prefix decode: a sequence's first prefix blocks differ
                                    from its group's first sequence's, a bad group layout, or a
                                    group larger than max_group_size */
+  PKV_DEV_BAD_AXIS = 8          /* rotation: a pair's position axis outside [0, num_axes) */
 };
 
 /* Message for the last non-OK status returned on this thread ("" if none). */
@@ -382,6 +383,95 @@ int pkv_swap_blocks(const uint16_t* const* src_k_caches, const uint16_t* const* 
                     uint16_t* const* dst_k_caches, uint16_t* const* dst_v_caches, int num_layers,
                     const int64_t* block_mapping, int num_pairs, int num_heads, int head_dim,
                     int block_size, int src_num_blocks, int dst_num_blocks, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Queries and keys before attention: the RMS norm of each head and the rotation
+ * by position, in one pass (an addition of this library; the pages start at q, K
+ * and V as attention takes them).
+ *
+ * For every token t and head, with x the head's D values of q (or key):
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (y = x where the weight is NULL)
+ *   and pair i < R/2, R = rotary_dim, of y is turned by the angle
+ *   2 pi * positions[axis_i, t] * frequencies[i] / 2^64:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ *   (a, b) = (y[i], y[i + R/2]), or (y[2 i], y[2 i + 1]) if interleaved != 0.
+ * Values from R on are not turned.  Everything is computed in fp32 and rounded to
+ * fp16 once.  The angle is exact for every int32 position: position * frequency
+ * wraps modulo 2^64 = one turn.
+ *
+ *   q, key        device [num_tokens, num_heads or num_kv_heads, head_dim] fp16; a
+ *                 token's heads are contiguous, tokens are q_stride / k_stride
+ *                 elements apart (multiples of 8, at least a token's length)
+ *   q_weight,
+ *   k_weight      device [head_dim] fp16 or NULL, 16-byte aligned
+ *   positions     device [num_axes, num_tokens] int32, 1 <= num_axes <= 8
+ *   frequencies   device [rotary_dim / 2] int64: parts of a turn per position in
+ *                 units of 2^-64 turns (pkv_rope_frequencies makes them)
+ *   pair_axis     device [rotary_dim / 2] int32: the position axis of each pair
+ *                 (time, height, width, ...), or NULL: all on axis 0.  A value
+ *                 outside [0, num_axes) records PKV_DEV_BAD_AXIS and its pair is
+ *                 not turned.
+ *   q_out, k_out  device fp16, laid out like q and key with strides of their own,
+ *                 16-byte aligned.  Each may be its input (same pointer and
+ *                 stride); otherwise no output may overlap an input.
+ * head_dim in {64, 128}; rotary_dim a multiple of 16 in [16, head_dim].
+ * ------------------------------------------------------------------------- */
+int pkv_qk_norm_rope(const uint16_t* q, const uint16_t* key, const uint16_t* q_weight, const uint16_t* k_weight,
+                     float eps, const int32_t* positions, int num_axes, const int64_t* frequencies,
+                     const int32_t* pair_axis, int rotary_dim, int interleaved, int num_tokens, int num_heads,
+                     int num_kv_heads, int head_dim, int64_t q_stride, int64_t k_stride, uint16_t* q_out,
+                     uint16_t* k_out, int64_t q_out_stride, int64_t k_out_stride, void* stream);
+
+/* frequencies_out[i] = inv_freq[i] / (2 pi) turns per position, in units of 2^-64
+ * turns (whole turns dropped).  Host only; inv_freq host [n], in radians per
+ * position (base^(-2i/R), or any scaled variant), finite. */
+int pkv_rope_frequencies(const double* inv_freq, int n, int64_t* frequencies_out);
+
+/* ---------------------------------------------------------------------------
+ * K/V cache held in four bits (an addition of this library): 3.8 times the tokens
+ * of the fp16 pools in the same memory, and as much less to read per token.
+ *
+ * A row (one token's D values of one head) is held as D/2 bytes, value 2j in the
+ * low half of byte j and value 2j + 1 in its high half, and two fp16 numbers, a
+ * scale and a zero point.  It stands for zero + scale * n, with
+ *   zero = least value, scale = (greatest - least) / 15 (fp32, rounded to fp16),
+ *   n = (x - zero) / scale to the nearest whole number in 0..15, halves to even
+ *   (n = 0 where the scale is 0).
+ * A row holding a NaN or an infinity stands for NaNs.
+ *
+ * Pool: [num_blocks, num_kv_heads, B * (D/2 + 4)] bytes; a (block, head) tile is
+ * its B rows of D/2 bytes, then their B (scale, zero) pairs, contiguous.  Slots,
+ * block tables and the block manager are those of the fp16 pools.
+ * ------------------------------------------------------------------------- */
+
+/* pkv_reshape_and_cache into four-bit pools.  key and value: device
+ * [num_tokens, num_kv_heads, head_dim] fp16, 16-byte aligned, a token's heads
+ * contiguous, tokens key_stride / value_stride elements apart (multiples of 8, at
+ * least a token's length).  Negative slots are skipped; a slot outside the pool
+ * records PKV_DEV_BAD_SLOT and is not written. */
+int pkv_reshape_and_cache_int4(const uint16_t* key, const uint16_t* value, uint8_t* k_cache, uint8_t* v_cache,
+                               const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
+                               int block_size, int num_blocks, int64_t key_stride, int64_t value_stride,
+                               void* stream);
+
+/* The inverse: rows key[t] and value[t] (device [num_tokens, num_kv_heads,
+ * head_dim] fp16, contiguous, 16-byte aligned) receive what slot slot_mapping[t]
+ * stands for, zero + scale * n rounded to fp16 once.  For the next chunk of a
+ * prompt, whose tokens attend over the cached context (pkv_prompt_attention).
+ * Rows with a negative slot are left as they were; a slot outside the pool records
+ * PKV_DEV_BAD_SLOT and leaves its row. */
+int pkv_gather_cache_int4(const uint8_t* k_cache, const uint8_t* v_cache, const int64_t* slot_mapping,
+                          uint16_t* key, uint16_t* value, int num_tokens, int num_kv_heads, int head_dim,
+                          int block_size, int num_blocks, void* stream);
+
+/* pkv_copy_blocks and pkv_swap_blocks on four-bit pools (num_heads: K/V heads). */
+int pkv_copy_blocks_int4(uint8_t* const* k_caches, uint8_t* const* v_caches, int num_layers,
+                         const int64_t* block_mapping, int num_pairs, int num_heads, int head_dim,
+                         int block_size, int num_blocks, void* stream);
+int pkv_swap_blocks_int4(const uint8_t* const* src_k_caches, const uint8_t* const* src_v_caches,
+                         uint8_t* const* dst_k_caches, uint8_t* const* dst_v_caches, int num_layers,
+                         const int64_t* block_mapping, int num_pairs, int num_heads, int head_dim,
+                         int block_size, int src_num_blocks, int dst_num_blocks, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Host block manager ([note] 关键设计 2 and 3; [lecture] PagedAttention 原理 and

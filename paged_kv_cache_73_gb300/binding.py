@@ -27,7 +27,7 @@ PKV_ERR_DEVICE_CHECK = -6
 PKV_ERR_NOT_FOUND = -7
 
 DEV_CODES = {0: "ok", 1: "bad block id", 2: "bad context length", 3: "bad slot", 4: "bad copy pair",
-             5: "wait timeout", 6: "bad query range", 7: "shared prefix mismatch"}
+             5: "wait timeout", 6: "bad query range", 7: "shared prefix mismatch", 8: "bad position axis"}
 
 
 class PkvError(RuntimeError):
@@ -68,6 +68,13 @@ _SIGNATURES = {
     "pkv_reshape_and_cache_layers": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P]),
     "pkv_copy_blocks": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _I, _P]),
     "pkv_swap_blocks": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "pkv_qk_norm_rope": (_I, [_P, _P, _P, _P, _c.c_float, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I64, _I64, _P, _P,
+                              _I64, _I64, _P]),
+    "pkv_rope_frequencies": (_I, [_P, _I, _P]),
+    "pkv_reshape_and_cache_int4": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I64, _I64, _P]),
+    "pkv_gather_cache_int4": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "pkv_copy_blocks_int4": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _I, _P]),
+    "pkv_swap_blocks_int4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P]),
     "pkv_bm_create": (_P, [_I, _I, _P]),
     "pkv_bm_destroy": (None, [_P]),
     "pkv_bm_add_seq": (_I, [_P, _I64, _I, _P]),
@@ -460,6 +467,173 @@ def swap_blocks(src_k: Sequence[torch.Tensor], src_v: Sequence[torch.Tensor], ds
     arr = lambda ts: ctypes.cast((ctypes.c_void_p * L)(*[t.data_ptr() for t in ts]), ctypes.c_void_p)
     _check(load().pkv_swap_blocks(arr(src_k), arr(src_v), arr(dst_k), arr(dst_v), L, block_mapping.data_ptr(),
                                   block_mapping.shape[0], H, D, B, Ns, Nd, _stream(stream)))
+
+
+# ---- queries and keys before attention ---------------------------------------------------------
+
+def _need_rows(t: torch.Tensor, name: str) -> int:
+    """A CUDA fp16 [tokens, heads, D] tensor whose tokens may be strided; returns their stride."""
+    if (t.dtype != torch.float16 or t.dim() != 3 or not t.is_cuda
+            or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise PkvError(PKV_ERR_INVALID_ARG,
+                       f"{name}: want a CUDA torch.float16 tensor of rank 3 with each token's heads contiguous, "
+                       f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} device={t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise PkvError(PKV_ERR_INVALID_ARG,
+                       f"{name}: on {t.device}, but the current CUDA device is cuda:{torch.cuda.current_device()} "
+                       f"(make it current, e.g. with torch.cuda.device({t.device}))")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def rope_frequencies(inv_freq: Sequence[float], device="cuda") -> torch.Tensor:
+    """The int64 ``frequencies`` of qk_norm_rope from angular frequencies in radians per position
+    (``base ** (-2 i / rotary_dim)``, or any scaled variant), one per rotated pair."""
+    inv = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+    if inv.ndim != 1:
+        raise PkvError(PKV_ERR_INVALID_ARG, "rope_frequencies: want one frequency per pair")
+    out = np.empty(inv.shape[0], dtype=np.int64)
+    _check(load().pkv_rope_frequencies(inv.ctypes.data, inv.shape[0], out.ctypes.data))
+    return torch.from_numpy(out).to(device)
+
+
+def qk_norm_rope(q: torch.Tensor, key: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 pair_axis: Optional[torch.Tensor] = None, interleaved: bool = False,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of every head of q and key (where a weight is given), then the rotation of its first
+    2 * len(frequencies) values by position, in one pass.
+
+    positions is [T] or [num_axes, T] int32; with several axes (time, height, width) pair_axis gives
+    each pair's.  q and key may be views into a packed projection (tokens strided); q_out and k_out
+    may be q and key themselves (in place)."""
+    qs, ks = _need_rows(q, "q"), _need_rows(key, "key")
+    T, H, D = q.shape
+    if key.shape[0] != T or key.shape[2] != D:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"qk_norm_rope: key {tuple(key.shape)} does not match q {tuple(q.shape)}")
+    _need(positions, "positions", torch.int32, 2 if positions.dim() == 2 else 1)
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if positions.shape[-1] != T:
+        raise PkvError(PKV_ERR_INVALID_ARG, "qk_norm_rope: positions must be [T] or [num_axes, T]")
+    _need(frequencies, "frequencies", torch.int64, 1)
+    pairs = frequencies.shape[0]
+    if pair_axis is not None:
+        _need(pair_axis, "pair_axis", torch.int32, 1)
+        if pair_axis.shape[0] != pairs:
+            raise PkvError(PKV_ERR_INVALID_ARG, "qk_norm_rope: pair_axis must have one entry per frequency")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, torch.float16, 1)
+            if w.shape[0] != D:
+                raise PkvError(PKV_ERR_INVALID_ARG, f"qk_norm_rope: {name} must have head_dim entries")
+    if q_out is None:
+        q_out = torch.empty((T, H, D), dtype=torch.float16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(tuple(key.shape), dtype=torch.float16, device=q.device)
+    if q_out.shape != q.shape or k_out.shape != key.shape:
+        raise PkvError(PKV_ERR_INVALID_ARG, "qk_norm_rope: outputs must be shaped like q and key")
+    qos, kos = _need_rows(q_out, "q_out"), _need_rows(k_out, "k_out")
+    _check(load().pkv_qk_norm_rope(
+        q.data_ptr(), key.data_ptr(), _ptr(q_weight), _ptr(k_weight), float(eps), positions.data_ptr(), axes,
+        frequencies.data_ptr(), _ptr(pair_axis), 2 * pairs, int(interleaved), T, H, key.shape[1], D, qs, ks,
+        q_out.data_ptr(), k_out.data_ptr(), qos, kos, _stream(stream)))
+    return q_out, k_out
+
+
+# ---- the cache held in four bits -----------------------------------------------------------------
+
+def int4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int) -> Tuple[int, int, int]:
+    """Shape of a four-bit pool (uint8): per (block, head) the rows' packed values, then their scales
+    and zero points."""
+    return num_blocks, num_kv_heads, block_size * (head_dim // 2 + 4)
+
+
+def _need_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, block_size: int) -> Tuple[int, int, int]:
+    """(num_blocks, num_kv_heads, head_dim) of two four-bit pools."""
+    _need(k_cache, "k_cache", torch.uint8, 3)
+    _need(v_cache, "v_cache", torch.uint8, 3)
+    N, H, tile = k_cache.shape
+    if block_size <= 0 or tile % block_size or v_cache.shape != k_cache.shape:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"four-bit pools {tuple(k_cache.shape)} and {tuple(v_cache.shape)} are not "
+                                            f"[N, H, {block_size} * (head_dim / 2 + 4)]")
+    return N, H, (tile // block_size - 4) * 2
+
+
+def reshape_and_cache_int4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           slot_mapping: torch.Tensor, block_size: int, stream=None) -> None:
+    """Hold key[t], value[t] in four bits at slot_mapping[t] (negative = skip) of the pools.  key and
+    value may be views into a packed projection (tokens strided)."""
+    ks, vs = _need_rows(key, "key"), _need_rows(value, "value")
+    N, H, D = _need_int4(k_cache, v_cache, block_size)
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    T = key.shape[0]
+    if tuple(key.shape[1:]) != (H, D) or value.shape != key.shape or slot_mapping.shape[0] != T:
+        raise PkvError(PKV_ERR_INVALID_ARG, "reshape_and_cache_int4: inconsistent shapes")
+    _check(load().pkv_reshape_and_cache_int4(key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                             slot_mapping.data_ptr(), T, H, D, block_size, N, ks, vs,
+                                             _stream(stream)))
+
+
+def gather_cache_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor, block_size: int,
+                      key: Optional[torch.Tensor] = None, value: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """fp16 rows [T, H, D] of what slots slot_mapping[t] of the pools stand for (rows with a negative
+    slot are left as they were)."""
+    N, H, D = _need_int4(k_cache, v_cache, block_size)
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    T = slot_mapping.shape[0]
+    if key is None:
+        key = torch.empty((T, H, D), dtype=torch.float16, device=k_cache.device)
+    if value is None:
+        value = torch.empty((T, H, D), dtype=torch.float16, device=k_cache.device)
+    _need(key, "key", torch.float16, 3)
+    _need(value, "value", torch.float16, 3)
+    if tuple(key.shape) != (T, H, D) or value.shape != key.shape:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"gather_cache_int4: key and value must be [{T}, {H}, {D}]")
+    _check(load().pkv_gather_cache_int4(k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
+                                        key.data_ptr(), value.data_ptr(), T, H, D, block_size, N, _stream(stream)))
+    return key, value
+
+
+def copy_blocks_int4(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor], block_mapping: torch.Tensor,
+                     block_size: int, stream=None) -> None:
+    """copy_blocks on four-bit pools."""
+    L = len(k_caches)
+    if len(v_caches) != L or L == 0:
+        raise PkvError(PKV_ERR_INVALID_ARG, "copy_blocks_int4: need as many K as V pools, at least one")
+    for k, v in zip(k_caches, v_caches):
+        N, H, D = _need_int4(k, v, block_size)
+        if k.shape != k_caches[0].shape:
+            raise PkvError(PKV_ERR_INVALID_ARG, "copy_blocks_int4: pools differ in shape")
+    _need(block_mapping, "block_mapping", torch.int64, 2, host_ok=True)
+    if block_mapping.shape[1] != 2:
+        raise PkvError(PKV_ERR_INVALID_ARG, "copy_blocks_int4: block_mapping must be [P, 2]")
+    arr = lambda ts: ctypes.cast((ctypes.c_void_p * L)(*[t.data_ptr() for t in ts]), ctypes.c_void_p)
+    _check(load().pkv_copy_blocks_int4(arr(k_caches), arr(v_caches), L, block_mapping.data_ptr(),
+                                       block_mapping.shape[0], H, D, block_size, N, _stream(stream)))
+
+
+def swap_blocks_int4(src_k: Sequence[torch.Tensor], src_v: Sequence[torch.Tensor], dst_k: Sequence[torch.Tensor],
+                     dst_v: Sequence[torch.Tensor], block_mapping: torch.Tensor, block_size: int, stream=None) -> None:
+    """swap_blocks between four-bit pools (CUDA tensors or pinned CPU tensors)."""
+    L = len(src_k)
+    if not (len(src_v) == len(dst_k) == len(dst_v) == L) or L == 0:
+        raise PkvError(PKV_ERR_INVALID_ARG, "swap_blocks_int4: need the same number (>= 1) of pools on each side")
+    for side in ((src_k, src_v), (dst_k, dst_v)):
+        for t in list(side[0]) + list(side[1]):
+            _need(t, "pool", torch.uint8, 3, host_ok=True)
+            if t.shape != side[0][0].shape or t.shape[1:] != src_k[0].shape[1:]:
+                raise PkvError(PKV_ERR_INVALID_ARG, "swap_blocks_int4: pools differ in shape")
+    Ns, H, tile = src_k[0].shape
+    if block_size <= 0 or tile % block_size:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"swap_blocks_int4: pools are not [N, H, {block_size} * (head_dim / 2 + 4)]")
+    _need(block_mapping, "block_mapping", torch.int64, 2, host_ok=True)
+    if block_mapping.shape[1] != 2:
+        raise PkvError(PKV_ERR_INVALID_ARG, "swap_blocks_int4: block_mapping must be [P, 2]")
+    arr = lambda ts: ctypes.cast((ctypes.c_void_p * L)(*[t.data_ptr() for t in ts]), ctypes.c_void_p)
+    _check(load().pkv_swap_blocks_int4(arr(src_k), arr(src_v), arr(dst_k), arr(dst_v), L, block_mapping.data_ptr(),
+                                       block_mapping.shape[0], H, (tile // block_size - 4) * 2, block_size, Ns,
+                                       dst_k[0].shape[0], _stream(stream)))
 
 
 # ---- host block manager -----------------------------------------------------------------------

@@ -35,14 +35,17 @@ int pkv_device_error(void* stream, int reset, int* code) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess)
     return pkv::fail(PKV_ERR_CUDA, "pkv_device_error: cudaStreamSynchronize: %s", cudaGetErrorString(e));
-  int a = 0, c = 0, f = 0;
-  int st = pkv::read_device_error_attention(reset, &a);
-  if (st != PKV_OK) return st;
-  st = pkv::read_device_error_cache_ops(reset, &c);
-  if (st != PKV_OK) return st;
-  st = pkv::read_device_error_prefill(reset, &f);
-  if (st != PKV_OK) return st;
-  int first = a ? a : (c ? c : f);
+  // one check word per translation unit that launches kernels
+  int (*const readers[])(int, int*) = {pkv::read_device_error_attention, pkv::read_device_error_cache_ops,
+                                       pkv::read_device_error_prefill, pkv::read_device_error_rope,
+                                       pkv::read_device_error_cache_int4};
+  int first = 0;
+  for (auto read : readers) {
+    int word = 0;
+    const int st = read(reset, &word);
+    if (st != PKV_OK) return st;
+    if (!first) first = word;
+  }
   if (code) *code = first;
   if (first) return pkv::fail(PKV_ERR_DEVICE_CHECK, "a kernel recorded device check code %d", first);
   return PKV_OK;

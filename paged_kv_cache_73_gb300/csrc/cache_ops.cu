@@ -215,6 +215,98 @@ int check_shape(const char* fn, int num_heads, int head_dim, int block_size, int
   return PKV_OK;
 }
 
+// The body of pkv_copy_blocks and pkv_copy_blocks_int4 (fn): row_bytes is what one row of a head takes
+// in the pool.
+int copy_blocks(const char* fn, void* const* k_caches, void* const* v_caches, int num_layers,
+                const int64_t* block_mapping, int num_pairs, int num_heads, int head_dim, int row_bytes,
+                int block_size, int num_blocks, void* stream) {
+  int rc = check_shape(fn, num_heads, head_dim, block_size, num_blocks);
+  if (rc != PKV_OK) return rc;
+  if (num_pairs < 0 || num_layers < 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "%s: num_pairs=%d num_layers=%d", fn, num_pairs, num_layers);
+  if (num_pairs == 0 || num_layers == 0) {
+    pkv::clear_error();
+    return PKV_OK;
+  }
+  if (!k_caches || !v_caches || !block_mapping)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "%s: null pointer", fn);
+  for (int l = 0; l < num_layers; ++l) {
+    if (!k_caches[l] || !v_caches[l] || !aligned16(k_caches[l]) || !aligned16(v_caches[l]))
+      return pkv::fail(PKV_ERR_INVALID_ARG, "%s: layer %d cache pointer null or not 16-byte aligned", fn, l);
+  }
+  const int64_t vec_per_block = static_cast<int64_t>(num_heads) * block_size * row_bytes / 16;
+  // enough CTAs per pair to keep every SM streaming even when there are few pairs
+  int splits = static_cast<int>((vec_per_block + 256 * 8 - 1) / (256 * 8));
+  if (splits < 1) splits = 1;
+  if (splits > 64) splits = 64;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  for (int l0 = 0; l0 < num_layers; l0 += kMaxLayersPerLaunch) {
+    const int nl = num_layers - l0 < kMaxLayersPerLaunch ? num_layers - l0 : kMaxLayersPerLaunch;
+    LayerPtrs ptrs{};
+    for (int l = 0; l < nl; ++l) {
+      ptrs.k[l] = reinterpret_cast<uint4*>(k_caches[l0 + l]);
+      ptrs.v[l] = reinterpret_cast<uint4*>(v_caches[l0 + l]);
+    }
+    cudaError_t e = pkv::launch_pdl(copy_blocks_kernel, dim3(num_pairs, nl, splits), dim3(256), 0, st, ptrs,
+                                    block_mapping, vec_per_block, num_blocks);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+  }
+  pkv::clear_error();
+  return PKV_OK;
+}
+
+// The body of pkv_swap_blocks and pkv_swap_blocks_int4 (fn).
+int swap_blocks(const char* fn, const void* const* src_k_caches, const void* const* src_v_caches,
+                void* const* dst_k_caches, void* const* dst_v_caches, int num_layers, const int64_t* block_mapping,
+                int num_pairs, int num_heads, int head_dim, int row_bytes, int block_size, int src_num_blocks,
+                int dst_num_blocks, void* stream) {
+  int rc = check_shape(fn, num_heads, head_dim, block_size, src_num_blocks);
+  if (rc != PKV_OK) return rc;
+  if (dst_num_blocks <= 0 || num_pairs < 0 || num_layers < 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "%s: dst_num_blocks=%d num_pairs=%d num_layers=%d", fn,
+                     dst_num_blocks, num_pairs, num_layers);
+  if (num_pairs == 0 || num_layers == 0) {
+    pkv::clear_error();
+    return PKV_OK;
+  }
+  if (!src_k_caches || !src_v_caches || !dst_k_caches || !dst_v_caches || !block_mapping)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!device_accessible(block_mapping))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "%s: block_mapping is not device-accessible memory", fn);
+  for (int l = 0; l < num_layers; ++l) {
+    const void* p4[4] = {src_k_caches[l], src_v_caches[l], dst_k_caches[l], dst_v_caches[l]};
+    for (const void* ptr : p4) {
+      if (!ptr || !aligned16(ptr))
+        return pkv::fail(PKV_ERR_INVALID_ARG, "%s: layer %d pool pointer null or not 16-byte aligned", fn, l);
+      if (!device_accessible(ptr))
+        return pkv::fail(PKV_ERR_INVALID_ARG,
+                         "%s: layer %d pool is neither device memory nor page-locked host memory", fn, l);
+    }
+  }
+  const int64_t vec_per_block = static_cast<int64_t>(num_heads) * block_size * row_bytes / 16;
+  int splits = static_cast<int>((vec_per_block + 256 * 8 - 1) / (256 * 8));
+  if (splits < 1) splits = 1;
+  if (splits > 64) splits = 64;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  for (int l0 = 0; l0 < num_layers; l0 += kMaxLayersPerLaunch) {
+    const int nl = num_layers - l0 < kMaxLayersPerLaunch ? num_layers - l0 : kMaxLayersPerLaunch;
+    PoolPairPtrs ptrs{};
+    for (int l = 0; l < nl; ++l) {
+      ptrs.src_k[l] = reinterpret_cast<const uint4*>(src_k_caches[l0 + l]);
+      ptrs.src_v[l] = reinterpret_cast<const uint4*>(src_v_caches[l0 + l]);
+      ptrs.dst_k[l] = reinterpret_cast<uint4*>(dst_k_caches[l0 + l]);
+      ptrs.dst_v[l] = reinterpret_cast<uint4*>(dst_v_caches[l0 + l]);
+    }
+    cudaError_t e = pkv::launch_pdl(swap_blocks_kernel, dim3(num_pairs, nl, splits), dim3(256), 0, st, ptrs,
+                                    block_mapping, vec_per_block, src_num_blocks, dst_num_blocks);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+  }
+  pkv::clear_error();
+  return PKV_OK;
+}
+
 }  // namespace
 
 namespace pkv {
@@ -263,90 +355,37 @@ int pkv_reshape_and_cache(const uint16_t* key, const uint16_t* value, uint16_t* 
 int pkv_copy_blocks(uint16_t* const* k_caches, uint16_t* const* v_caches, int num_layers,
                     const int64_t* block_mapping, int num_pairs, int num_heads, int head_dim, int block_size,
                     int num_blocks, void* stream) {
-  int rc = check_shape("pkv_copy_blocks", num_heads, head_dim, block_size, num_blocks);
-  if (rc != PKV_OK) return rc;
-  if (num_pairs < 0 || num_layers < 0)
-    return pkv::fail(PKV_ERR_INVALID_ARG, "pkv_copy_blocks: num_pairs=%d num_layers=%d", num_pairs, num_layers);
-  if (num_pairs == 0 || num_layers == 0) {
-    pkv::clear_error();
-    return PKV_OK;
-  }
-  if (!k_caches || !v_caches || !block_mapping)
-    return pkv::fail(PKV_ERR_INVALID_ARG, "pkv_copy_blocks: null pointer");
-  for (int l = 0; l < num_layers; ++l) {
-    if (!k_caches[l] || !v_caches[l] || !aligned16(k_caches[l]) || !aligned16(v_caches[l]))
-      return pkv::fail(PKV_ERR_INVALID_ARG, "pkv_copy_blocks: layer %d cache pointer null or not 16-byte aligned", l);
-  }
-  const int64_t vec_per_block = static_cast<int64_t>(num_heads) * block_size * head_dim / 8;
-  // enough CTAs per pair to keep every SM streaming even when there are few pairs
-  int splits = static_cast<int>((vec_per_block + 256 * 8 - 1) / (256 * 8));
-  if (splits < 1) splits = 1;
-  if (splits > 64) splits = 64;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  for (int l0 = 0; l0 < num_layers; l0 += kMaxLayersPerLaunch) {
-    const int nl = num_layers - l0 < kMaxLayersPerLaunch ? num_layers - l0 : kMaxLayersPerLaunch;
-    LayerPtrs ptrs{};
-    for (int l = 0; l < nl; ++l) {
-      ptrs.k[l] = reinterpret_cast<uint4*>(k_caches[l0 + l]);
-      ptrs.v[l] = reinterpret_cast<uint4*>(v_caches[l0 + l]);
-    }
-    cudaError_t e = pkv::launch_pdl(copy_blocks_kernel, dim3(num_pairs, nl, splits), dim3(256), 0, st, ptrs,
-                                    block_mapping, vec_per_block, num_blocks);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_copy_blocks launch: %s", cudaGetErrorString(e));
-  }
-  pkv::clear_error();
-  return PKV_OK;
+  return copy_blocks("pkv_copy_blocks", reinterpret_cast<void* const*>(k_caches),
+                     reinterpret_cast<void* const*>(v_caches), num_layers, block_mapping, num_pairs, num_heads,
+                     head_dim, 2 * head_dim, block_size, num_blocks, stream);
+}
+
+int pkv_copy_blocks_int4(uint8_t* const* k_caches, uint8_t* const* v_caches, int num_layers,
+                         const int64_t* block_mapping, int num_pairs, int num_heads, int head_dim, int block_size,
+                         int num_blocks, void* stream) {
+  return copy_blocks("pkv_copy_blocks_int4", reinterpret_cast<void* const*>(k_caches),
+                     reinterpret_cast<void* const*>(v_caches), num_layers, block_mapping, num_pairs, num_heads,
+                     head_dim, head_dim / 2 + 4, block_size, num_blocks, stream);
 }
 
 int pkv_swap_blocks(const uint16_t* const* src_k_caches, const uint16_t* const* src_v_caches,
                     uint16_t* const* dst_k_caches, uint16_t* const* dst_v_caches, int num_layers,
                     const int64_t* block_mapping, int num_pairs, int num_heads, int head_dim, int block_size,
                     int src_num_blocks, int dst_num_blocks, void* stream) {
-  int rc = check_shape("pkv_swap_blocks", num_heads, head_dim, block_size, src_num_blocks);
-  if (rc != PKV_OK) return rc;
-  if (dst_num_blocks <= 0 || num_pairs < 0 || num_layers < 0)
-    return pkv::fail(PKV_ERR_INVALID_ARG, "pkv_swap_blocks: dst_num_blocks=%d num_pairs=%d num_layers=%d",
-                     dst_num_blocks, num_pairs, num_layers);
-  if (num_pairs == 0 || num_layers == 0) {
-    pkv::clear_error();
-    return PKV_OK;
-  }
-  if (!src_k_caches || !src_v_caches || !dst_k_caches || !dst_v_caches || !block_mapping)
-    return pkv::fail(PKV_ERR_INVALID_ARG, "pkv_swap_blocks: null pointer");
-  if (!device_accessible(block_mapping))
-    return pkv::fail(PKV_ERR_INVALID_ARG, "pkv_swap_blocks: block_mapping is not device-accessible memory");
-  for (int l = 0; l < num_layers; ++l) {
-    const void* p4[4] = {src_k_caches[l], src_v_caches[l], dst_k_caches[l], dst_v_caches[l]};
-    for (const void* ptr : p4) {
-      if (!ptr || !aligned16(ptr))
-        return pkv::fail(PKV_ERR_INVALID_ARG, "pkv_swap_blocks: layer %d pool pointer null or not 16-byte aligned", l);
-      if (!device_accessible(ptr))
-        return pkv::fail(PKV_ERR_INVALID_ARG,
-                         "pkv_swap_blocks: layer %d pool is neither device memory nor page-locked host memory", l);
-    }
-  }
-  const int64_t vec_per_block = static_cast<int64_t>(num_heads) * block_size * head_dim / 8;
-  int splits = static_cast<int>((vec_per_block + 256 * 8 - 1) / (256 * 8));
-  if (splits < 1) splits = 1;
-  if (splits > 64) splits = 64;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  for (int l0 = 0; l0 < num_layers; l0 += kMaxLayersPerLaunch) {
-    const int nl = num_layers - l0 < kMaxLayersPerLaunch ? num_layers - l0 : kMaxLayersPerLaunch;
-    PoolPairPtrs ptrs{};
-    for (int l = 0; l < nl; ++l) {
-      ptrs.src_k[l] = reinterpret_cast<const uint4*>(src_k_caches[l0 + l]);
-      ptrs.src_v[l] = reinterpret_cast<const uint4*>(src_v_caches[l0 + l]);
-      ptrs.dst_k[l] = reinterpret_cast<uint4*>(dst_k_caches[l0 + l]);
-      ptrs.dst_v[l] = reinterpret_cast<uint4*>(dst_v_caches[l0 + l]);
-    }
-    cudaError_t e = pkv::launch_pdl(swap_blocks_kernel, dim3(num_pairs, nl, splits), dim3(256), 0, st, ptrs,
-                                    block_mapping, vec_per_block, src_num_blocks, dst_num_blocks);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_swap_blocks launch: %s", cudaGetErrorString(e));
-  }
-  pkv::clear_error();
-  return PKV_OK;
+  return swap_blocks("pkv_swap_blocks", reinterpret_cast<const void* const*>(src_k_caches),
+                     reinterpret_cast<const void* const*>(src_v_caches), reinterpret_cast<void* const*>(dst_k_caches),
+                     reinterpret_cast<void* const*>(dst_v_caches), num_layers, block_mapping, num_pairs, num_heads,
+                     head_dim, 2 * head_dim, block_size, src_num_blocks, dst_num_blocks, stream);
+}
+
+int pkv_swap_blocks_int4(const uint8_t* const* src_k_caches, const uint8_t* const* src_v_caches,
+                         uint8_t* const* dst_k_caches, uint8_t* const* dst_v_caches, int num_layers,
+                         const int64_t* block_mapping, int num_pairs, int num_heads, int head_dim, int block_size,
+                         int src_num_blocks, int dst_num_blocks, void* stream) {
+  return swap_blocks("pkv_swap_blocks_int4", reinterpret_cast<const void* const*>(src_k_caches),
+                     reinterpret_cast<const void* const*>(src_v_caches), reinterpret_cast<void* const*>(dst_k_caches),
+                     reinterpret_cast<void* const*>(dst_v_caches), num_layers, block_mapping, num_pairs, num_heads,
+                     head_dim, head_dim / 2 + 4, block_size, src_num_blocks, dst_num_blocks, stream);
 }
 
 int pkv_reshape_and_cache_layers(const uint16_t* const* keys, const uint16_t* const* values, uint16_t* const* k_caches,
