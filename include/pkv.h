@@ -43,7 +43,8 @@
  * (block, head) tile of a pool is block_size*head_dim*2 contiguous bytes.
  *
  * Supported shapes: head_dim in {64, 128}, block_size in {4, 8, 16, 32}, one K/V
- * head per query head.  Other values return PKV_ERR_UNSUPPORTED.
+ * head per query head (the four-bit cache also takes grouped heads).  Other values
+ * return PKV_ERR_UNSUPPORTED.
  */
 #ifndef PKV_H_
 #define PKV_H_
@@ -472,6 +473,26 @@ int pkv_swap_blocks_int4(const uint8_t* const* src_k_caches, const uint8_t* cons
                          uint8_t* const* dst_k_caches, uint8_t* const* dst_v_caches, int num_layers,
                          const int64_t* block_mapping, int num_pairs, int num_heads, int head_dim,
                          int block_size, int src_num_blocks, int dst_num_blocks, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged decode attention over four-bit pools, with grouped heads:
+ *   out[s,h,:] = sum_{t < ctx_s} softmax_t(scale * q[s,h,:] . k_t) v_t
+ * with k_t, v_t what the pools' rows of head h / (num_heads / num_kv_heads) stand
+ * for.  num_heads is a multiple of num_kv_heads.  q (device [num_seqs, num_heads,
+ * head_dim] fp16), tables, lengths, out, workspace, errors and the meaning of a
+ * zero length are as for pkv_paged_attention_decode, except that q, tables,
+ * lengths and out must be device memory.  Products of q and the cached whole
+ * numbers are exact, sums are fp32; the softmax weights, times the rows' V scales,
+ * are rounded to fp16 before they multiply V.
+ * ------------------------------------------------------------------------- */
+size_t pkv_paged_attention_int4_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                               int max_blocks_per_seq, int block_size);
+
+int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                    const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                                    int num_heads, int num_kv_heads, int head_dim, int num_blocks,
+                                    int max_blocks_per_seq, float scale, int block_size, uint16_t* out,
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Host block manager ([note] 关键设计 2 and 3; [lecture] PagedAttention 原理 and

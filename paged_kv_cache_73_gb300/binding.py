@@ -73,6 +73,9 @@ _SIGNATURES = {
     "pkv_rope_frequencies": (_I, [_P, _I, _P]),
     "pkv_reshape_and_cache_int4": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I64, _I64, _P]),
     "pkv_gather_cache_int4": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "pkv_paged_attention_int4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "pkv_paged_attention_decode_int4": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _c.c_float, _I, _P, _P, _SZ,
+                                             _P]),
     "pkv_copy_blocks_int4": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _I, _P]),
     "pkv_swap_blocks_int4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P]),
     "pkv_bm_create": (_P, [_I, _I, _P]),
@@ -634,6 +637,45 @@ def swap_blocks_int4(src_k: Sequence[torch.Tensor], src_v: Sequence[torch.Tensor
     _check(load().pkv_swap_blocks_int4(arr(src_k), arr(src_v), arr(dst_k), arr(dst_v), L, block_mapping.data_ptr(),
                                        block_mapping.shape[0], H, (tile // block_size - 4) * 2, block_size, Ns,
                                        dst_k[0].shape[0], _stream(stream)))
+
+
+def paged_attention_int4_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                        max_blocks_per_seq: int, block_size: int) -> int:
+    return int(load().pkv_paged_attention_int4_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                              max_blocks_per_seq, block_size))
+
+
+def paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                                block_size: int, out: Optional[torch.Tensor] = None,
+                                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[s, h] = softmax attention of q[s, h] over the sequence's rows of four-bit pools; num_heads
+    may be a multiple of the pools' heads (grouped heads)."""
+    _need(q, "q", torch.float16, 3)
+    N, Hk, D = _need_int4(k_cache, v_cache, block_size)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    S, H, _ = q.shape
+    if q.shape[2] != D:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"paged_attention_decode_int4: q has head_dim {q.shape[2]}, the pools {D}")
+    if block_tables.shape[0] != S or context_lens.shape[0] != S:
+        raise PkvError(PKV_ERR_INVALID_ARG, "block_tables / context_lens rows != num_seqs")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", torch.float16, 3)
+        if out.shape != q.shape:
+            raise PkvError(PKV_ERR_INVALID_ARG, "paged_attention_decode_int4: out must be shaped like q")
+    max_blocks = block_tables.shape[1]
+    if workspace is None:
+        n = paged_attention_int4_workspace_size(S, H, Hk, D, max_blocks, block_size)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().pkv_paged_attention_decode_int4(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+        S, H, Hk, D, N, max_blocks, float(scale), block_size, out.data_ptr(), _ptr(workspace), ws_bytes,
+        _stream(stream)))
+    return out
 
 
 # ---- host block manager -----------------------------------------------------------------------

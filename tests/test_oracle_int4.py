@@ -161,3 +161,48 @@ def test_int4_copy_and_swap_refuse(lib):
     assert lib.pkv_copy_blocks_int4(None, None, 0, None, 0, 2, 64, 16, 4, None) == pkv.PKV_OK
     assert lib.pkv_swap_blocks_int4(None, None, None, None, 1, 16, 1, 2, 64, 16, 4, 4, None) == pkv.PKV_ERR_INVALID_ARG
     assert lib.pkv_swap_blocks_int4(None, None, None, None, 1, 16, 0, 2, 64, 16, 4, 4, None) == pkv.PKV_OK
+
+
+def _decode(lib, **kw):
+    a = dict(q=16, k=16, v=16, tables=16, lens=16, S=2, H=4, Hk=2, D=64, N=8, maxb=4, scale=0.125, B=16, out=16,
+             ws=None, ws_bytes=0)
+    a.update(kw)
+    return lib.pkv_paged_attention_decode_int4(a["q"], a["k"], a["v"], a["tables"], a["lens"], a["S"], a["H"], a["Hk"],
+                                               a["D"], a["N"], a["maxb"], a["scale"], a["B"], a["out"], a["ws"],
+                                               a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(D=96), pkv.PKV_ERR_UNSUPPORTED),
+    (dict(B=12), pkv.PKV_ERR_UNSUPPORTED),
+    (dict(Hk=0), pkv.PKV_ERR_INVALID_ARG),
+    (dict(Hk=3), pkv.PKV_ERR_INVALID_ARG),                 # 4 heads over 3
+    (dict(S=-1), pkv.PKV_ERR_INVALID_ARG),
+    (dict(S=70000), pkv.PKV_ERR_UNSUPPORTED),
+    (dict(maxb=1 << 27), pkv.PKV_ERR_UNSUPPORTED),
+    (dict(q=None), pkv.PKV_ERR_INVALID_ARG),
+    (dict(v=8), pkv.PKV_ERR_INVALID_ARG),
+    (dict(scale=float("nan")), pkv.PKV_ERR_INVALID_ARG),
+    (dict(maxb=4096), pkv.PKV_ERR_WORKSPACE),              # split, and no workspace
+    (dict(S=0, q=None), pkv.PKV_OK),
+])
+def test_decode_int4_refuses(lib, kw, status):
+    assert _decode(lib, **kw) == status
+    if status != pkv.PKV_OK:
+        assert lib.pkv_last_error()
+
+
+def test_decode_int4_oracle_groups_heads():
+    rng = np.random.default_rng(4)
+    kp, vp = o4.empty_pool(4, 2, 4, 64), o4.empty_pool(4, 2, 4, 64)
+    rows = rng.standard_normal((2, 7, 2, 64)).astype(np.float16)
+    slots = [9, 10, 11, 8, 2, 3, 1]
+    for pool, x in ((kp, rows[0]), (vp, rows[1])):
+        o4.store(pool, x, slots, 4)
+    tables, lens = np.array([[2, 0]], np.int32), np.array([8], np.int32)
+    q = rng.standard_normal((1, 6, 64)).astype(np.float16)
+    out = o4.paged_decode_attention(q, kp, vp, tables, lens, 0.2, 4)
+    k, v = (np.concatenate([o4.pool_values(p, 4)[2], o4.pool_values(p, 4)[0]], 1) for p in (kp, vp))
+    for h in range(6):
+        w = np.exp(0.2 * k[h // 3] @ q[0, h].astype(np.float64))
+        assert np.allclose(out[0, h], w @ v[h // 3] / w.sum(), rtol=1e-12)
