@@ -43,8 +43,8 @@
  * (block, head) tile of a pool is block_size*head_dim*2 contiguous bytes.
  *
  * Supported shapes: head_dim in {64, 128}, block_size in {4, 8, 16, 32}, one K/V
- * head per query head (the four-bit cache also takes grouped heads).  Other values
- * return PKV_ERR_UNSUPPORTED.
+ * head per query head (the four-bit cache and prompt attention also take grouped
+ * heads).  Other values return PKV_ERR_UNSUPPORTED.
  */
 #ifndef PKV_H_
 #define PKV_H_
@@ -493,6 +493,43 @@ int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, c
                                     int num_heads, int num_kv_heads, int head_dim, int num_blocks,
                                     int max_blocks_per_seq, float scale, int block_size, uint16_t* out,
                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Prompt attention over contiguous keys and values: causal, grouped heads, packed
+ * sequences ([note] 关键设计 1, first equation).  It is the prompt phase of a
+ * request whose K/V go to a four-bit cache: its own fresh rows in fp16, or gathered
+ * cached rows (pkv_gather_cache_int4) followed by fresh ones.
+ *
+ * Sequence s has queries query_start[s] .. query_start[s+1]-1 (n_s of them) and
+ * keys key_start[s] .. key_start[s+1]-1 (m_s >= n_s).  Query i sits at position
+ * p = m_s - n_s + i:
+ *   out[query_start[s] + i, h, :] = sum_{t <= p} softmax_t(scale * q . k_t) v_t
+ * with head h / (num_heads / num_kv_heads) of key and value.
+ *
+ *   q             device [total_q, num_heads, head_dim] fp16
+ *   key, value    device [total_k, num_kv_heads, head_dim] fp16
+ *                 (all three: 16-byte aligned, a token's heads contiguous, tokens
+ *                 q_stride / key_stride / value_stride elements apart, multiples of
+ *                 8 and at least a token's length)
+ *   query_start   device [num_seqs + 1] int32, non-decreasing
+ *   key_start     device [num_seqs + 1] int32, non-decreasing, or NULL: query_start
+ *   max_query_len host: the largest n_s (sizes the grid).  A larger n_s records
+ *                 PKV_DEV_BAD_QUERY_RANGE, and its rows past the grid are not
+ *                 written.
+ *   out           device [total_q, num_heads, head_dim] fp16, contiguous, 16-byte
+ *                 aligned; must not overlap the inputs
+ * scale must be positive.  A sequence without queries is skipped; n_s > m_s or
+ * rows outside q or key record PKV_DEV_BAD_QUERY_RANGE and the sequence's rows are
+ * not written.  Rows of out in no sequence are left as they were.  Keys and values
+ * that a query does not see (after it, or after its sequence's end) do not reach its
+ * row, whatever they hold.
+ * Tensor cores: fp16 products, fp32 sums; the softmax weights are rounded to fp16
+ * before they multiply V.  No workspace.
+ * ------------------------------------------------------------------------- */
+int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t* value, const int32_t* query_start,
+                         const int32_t* key_start, int num_seqs, int total_q, int total_k, int max_query_len,
+                         int num_heads, int num_kv_heads, int head_dim, int64_t q_stride, int64_t key_stride,
+                         int64_t value_stride, float scale, uint16_t* out, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Host block manager ([note] 关键设计 2 and 3; [lecture] PagedAttention 原理 and

@@ -76,6 +76,7 @@ _SIGNATURES = {
     "pkv_paged_attention_int4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "pkv_paged_attention_decode_int4": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _c.c_float, _I, _P, _P, _SZ,
                                              _P]),
+    "pkv_prompt_attention": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I64, _I64, _I64, _c.c_float, _P, _P]),
     "pkv_copy_blocks_int4": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _I, _P]),
     "pkv_swap_blocks_int4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P]),
     "pkv_bm_create": (_P, [_I, _I, _P]),
@@ -675,6 +676,40 @@ def paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
         S, H, Hk, D, N, max_blocks, float(scale), block_size, out.data_ptr(), _ptr(workspace), ws_bytes,
         _stream(stream)))
+    return out
+
+
+# ---- prompt attention ----------------------------------------------------------------------------
+
+def prompt_attention(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, query_start: torch.Tensor, scale: float,
+                     max_query_len: int, key_start: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Causal attention of packed sequences over contiguous keys and values, grouped heads.
+
+    Sequence s has queries query_start[s]..query_start[s+1] and keys key_start[s]..key_start[s+1]
+    (key_start None: the same), the last of which are its queries' own.  q, key and value may be views
+    into a packed projection (tokens strided)."""
+    qs, ks, vs = _need_rows(q, "q"), _need_rows(key, "key"), _need_rows(value, "value")
+    T, H, D = q.shape
+    Tk, Hk, Dk = key.shape
+    if Dk != D or value.shape != key.shape:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"prompt_attention: key {tuple(key.shape)} and value {tuple(value.shape)} do "
+                                            f"not match q {tuple(q.shape)}")
+    _need(query_start, "query_start", torch.int32, 1)
+    S = query_start.shape[0] - 1
+    if key_start is not None:
+        _need(key_start, "key_start", torch.int32, 1)
+        if key_start.shape[0] != S + 1:
+            raise PkvError(PKV_ERR_INVALID_ARG, "prompt_attention: query_start and key_start differ in length")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.float16, device=q.device)
+    else:
+        _need(out, "out", torch.float16, 3)
+        if out.shape != q.shape:
+            raise PkvError(PKV_ERR_INVALID_ARG, "prompt_attention: out must be shaped like q")
+    _check(load().pkv_prompt_attention(
+        q.data_ptr(), key.data_ptr(), value.data_ptr(), query_start.data_ptr(), _ptr(key_start), S, T, Tk,
+        int(max_query_len), H, Hk, D, qs, ks, vs, float(scale), out.data_ptr(), _stream(stream)))
     return out
 
 

@@ -38,7 +38,8 @@ int pkv_device_error(void* stream, int reset, int* code) {
   // one check word per translation unit that launches kernels
   int (*const readers[])(int, int*) = {pkv::read_device_error_attention, pkv::read_device_error_cache_ops,
                                        pkv::read_device_error_prefill, pkv::read_device_error_rope,
-                                       pkv::read_device_error_cache_int4, pkv::read_device_error_attention_int4};
+                                       pkv::read_device_error_cache_int4, pkv::read_device_error_attention_int4,
+                                       pkv::read_device_error_prompt};
   int first = 0;
   for (auto read : readers) {
     int word = 0;

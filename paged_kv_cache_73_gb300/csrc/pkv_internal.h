@@ -26,6 +26,7 @@ int read_device_error_prefill(int reset, int* code);
 int read_device_error_rope(int reset, int* code);
 int read_device_error_cache_int4(int reset, int* code);
 int read_device_error_attention_int4(int reset, int* code);
+int read_device_error_prompt(int reset, int* code);
 
 // Shared-prefix decode reads a group's prefix once only for groups of at least this many members;
 // smaller groups (where the prefix mostly comes from L2 anyway and a 128-row tensor-core tile would

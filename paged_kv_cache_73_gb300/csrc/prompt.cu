@@ -1,0 +1,588 @@
+// Prompt attention for sm_103a: packed sequences of queries over contiguous keys and
+// values, causal, groups of query heads sharing a key head.
+//
+//   o_i = sum_{t <= p} softmax_t(scale q_i . k_t) v_t,   p = m - n + i
+//
+// for query i of a sequence with n queries and m >= n keys ([note] "vLLM /
+// PagedAttention -- 把 LLM 服务的瓶颈从显存碎片里救出来", 关键设计 1, first equation).  It serves
+// requests whose K/V go to a four-bit cache: the prompt attends over its own fp16 rows
+// (and over gathered rows of its cached context) before or while they are quantised.
+//
+// 4 D flops per (query, key) pair that the mask leaves, against two rows read per
+// 128-query tile: bound by the tensor cores.  Scores and outputs live in tensor memory
+// (tcgen05.mma, fp16 in, fp32 accumulation); a softmax thread owns a query row, which is
+// a tensor-memory lane.  One CTA has two query tiles of 128 rows that share every K/V tile
+// it loads:
+//  * in a group with an even number of heads, two heads of the same 128 queries: both
+//    see the same keys, so a short prompt fills both tiles and none computes keys that
+//    only the other needs;
+//  * otherwise 256 queries of one head; the first tile stops at its own last key.
+// Key tiles of 64 positions come by TMA through a four-slot ring.  The tiles that some
+// row of the CTA does not see whole (the diagonal, and the one that holds the sequence's
+// end) are read through registers instead where V is concerned: rows past the end become
+// zeros, and values that are not finite become zeros too and are put back in the end for
+// the rows that see them, since a masked weight of 0 would make a NaN of them.
+//
+// Per 64-key tile and CTA the products take 2 x (768 + 512) / 2 = 1280 clocks: S is bound
+// by shared memory (an SS product of 128 x 64 x 16 reads 6 KB), PV by math.  Two S buffers
+// per query tile keep S(j + 1) running under the softmax of tile j.
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "launch.cuh"
+#include "pkv_internal.h"
+#include "tcgen05.cuh"
+
+namespace {
+
+using namespace pkv::tc;
+
+__device__ int g_dev_error_prompt = 0;
+__device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_prompt, 0, code); }
+
+constexpr int BM = 128;            // queries per query tile (MMA M)
+constexpr int BN = 64;             // keys per tile (S MMA N, PV MMA K)
+constexpr int NS = 4;              // ring slots each for K and for V
+constexpr int THREADS = 384;
+constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
+constexpr uint32_t TMEM_COLS = 512, O_COL = 0, S_COL = 256;
+
+struct PromptParams {
+  CUtensorMap tmap_q, tmap_k, tmap_v;   // (D, heads, tokens), boxes of 64 x 1 x 128 (q) or 64, 128-byte swizzle
+  const __half* k;
+  const __half* v;
+  const int32_t* qstart;
+  const int32_t* kstart;
+  __half* out;
+  int64_t k_stride, v_stride;
+  int num_heads, group, pair;           // pair: the two query tiles are two heads
+  int total_q, total_k;
+  float scale_log2;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int Q_BYTES = BM * D * 2;
+  static constexpr int KV_BYTES = BN * D * 2;
+  // sized as for D = 128 whatever D is, so that one CTA (with all 512 tensor-memory columns) runs per SM
+  static constexpr int SMEM = 1024 + 2 * BM * 128 * 2 + 2 * NS * BN * 128 * 2 + 256;
+};
+
+__device__ __forceinline__ bool finite16(unsigned h) { return (h & 0x7c00u) != 0x7c00u; }
+
+// Warp roles (12 warps):
+//   0-3 / 4-7  softmax of query tile 0 / 1: waits S(j), releases K slot j % 4, masks, takes the row
+//              maximum (moving the running one, and O, only past 2^8), writes P = 2^(S - m) as fp16
+//              over the scores and arrives on p_full
+//   8          one lane issues S_g(j) = Q_g K(j)^T once K(j) landed and PV_g(j - 2), the last reader
+//              of its buffer, is done
+//   11         one lane issues O_g += P_g(j) V(j) once V(j) and P_g(j) are there, then releases V
+//   9, 10      load K, V tiles into slot j % 4 once tile j - 4 is done with it
+// Every wait is bounded; a role that gives up records PKV_DEV_WAIT_TIMEOUT and leaves its loop, the
+// others give up in turn, and the CTA still reaches its final barrier.
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __grid_constant__ PromptParams p) {
+  using C = Cfg<D>;
+  constexpr int CPR = D / 8;                                  // 16-byte chunks per row
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* smem = smem_raw + (base - raw);
+  const uint32_t sq = base, sk = sq + 2 * C::Q_BYTES, sv = sk + NS * C::KV_BYTES, bars = sv + NS * C::KV_BYTES;
+  auto s_full = [&](int g, int u) { return bars + 8u * (2 * g + u); };
+  auto p_full = [&](int g, int u) { return bars + 32u + 8u * (2 * g + u); };
+  auto pv_done = [&](int g, int u) { return bars + 64u + 8u * (2 * g + u); };
+  auto k_full = [&](int b) { return bars + 96u + 8u * b; };
+  auto v_full = [&](int b) { return bars + 96u + 8u * (NS + b); };
+  auto k_free = [&](int b) { return bars + 96u + 8u * (2 * NS + b); };
+  auto v_free = [&](int b) { return bars + 96u + 8u * (3 * NS + b); };
+  const uint32_t q_full = bars + 96 + 32 * NS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + 104 + 32 * NS - base));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + 108 + 32 * NS - base));
+  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + 112 + 32 * NS - base));
+  static_assert(116 + 32 * NS <= 256, "barrier area");
+
+  pkv::pdl_trigger();
+  pkv::pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int s = blockIdx.z, H = p.num_heads;
+  const int qt = gridDim.x - 1 - blockIdx.x;                  // the tiles that see the most keys first
+  const int h0 = p.pair ? 2 * blockIdx.y : blockIdx.y;        // the first query tile's head
+  const int kvh = h0 / p.group;
+  const int q0 = p.qstart[s], n = p.qstart[s + 1] - q0;
+  const int k0 = p.kstart[s], m = p.kstart[s + 1] - k0;
+  const int rows = p.pair ? BM : 2 * BM;                      // queries per CTA
+  const int i0 = qt * rows;
+  if (n < 0 || n > m || q0 < 0 || q0 > p.total_q - n || k0 < 0 || k0 > p.total_k - m) {
+    if (tid == 0 && qt == 0) record_error(PKV_DEV_BAD_QUERY_RANGE);
+    return;
+  }
+  // more queries than the grid covers (the caller's max_query_len understated them)
+  if (tid == 0 && qt == 0 && blockIdx.y == 0 && n > static_cast<int>(gridDim.x) * rows)
+    record_error(PKV_DEV_BAD_QUERY_RANGE);
+  if (i0 >= n) return;
+  const int ntile = p.pair || i0 + BM < n ? 2 : 1;            // query tiles with real queries
+  auto tile_row = [&](int g) { return i0 + (p.pair ? 0 : g * BM); };
+  auto tile_head = [&](int g) { return h0 + (p.pair ? g : 0); };
+  // key tiles that query tile g sees, and the CTA's (those of its last query tile)
+  auto tiles_of = [&](int g) { return (m - n + min(tile_row(g) + BM, n) - 1) / BN + 1; };
+  const int n_tiles = tiles_of(ntile - 1);
+  const int tiles0 = tiles_of(0);
+  const int first_pos = m - n + i0;                           // the CTA's first query's position
+  // tiles from here on hold keys that some row does not see, or the sequence's end
+  const int edge = min((first_pos + 1) / BN, m / BN);
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  if (tid == 0) {
+    for (int g = 0; g < 2; ++g)
+      for (int u = 0; u < 2; ++u) {
+        mbar_init_count(s_full(g, u), 1);
+        mbar_init_count(p_full(g, u), 128);
+        mbar_init_count(pv_done(g, u), 1);
+      }
+    for (int b = 0; b < NS; ++b) {
+      mbar_init_count(k_full(b), 32);
+      mbar_init_count(v_full(b), 32);
+      mbar_init_count(k_free(b), 4 * ntile);
+      mbar_init_count(v_free(b), 1);
+    }
+    *abort_flag = 0;
+    *not_finite = 0;
+    mbar_init_count(q_full, 1);
+    mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(ntile) * C::Q_BYTES);
+    // rows past the sequence's queries read the next one's (or zeros past the tensor): never stored
+    for (int g = 0; g < ntile; ++g)
+#pragma unroll
+      for (int half = 0; half < D / 64; ++half)
+        tma_load_3d(sq + g * C::Q_BYTES + half * (BM * 128), &p.tmap_q, half * 64, tile_head(g), q0 + tile_row(g), q_full);
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto t_s = [&](int g, int u) { return tmem + S_COL + 128u * g + 64u * u; };
+  auto t_o = [&](int g) { return tmem + O_COL + 128u * g; };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_or_abort(bar, parity, abort_flag); };
+  auto give_up = [&]() {
+    if (!*abort_flag) record_error(PKV_DEV_WAIT_TIMEOUT);
+    *abort_flag = 1;
+  };
+  bool failed = false;
+  float l = 0.f, m_ref = -INFINITY;
+
+  if (warp == 9 || warp == 10) {
+    // ---------------- loads: warp 9 K tiles, warp 10 V tiles ----------------
+    const bool is_k = warp == 9;
+    const CUtensorMap* map = is_k ? &p.tmap_k : &p.tmap_v;
+    if (lane == 0) prefetch_tensormap(map);
+    const __half* src = (is_k ? p.k : p.v) + static_cast<int64_t>(kvh) * D;
+    const int64_t stride = is_k ? p.k_stride : p.v_stride;
+    // K's diagonal tiles need no care (their scores are masked); V's and the one with the end do
+    const int plain = is_k ? m / BN : edge;
+    int issued = 0;
+    for (int j = 0; j < n_tiles; ++j) {
+      const int b = j % NS;
+      if (j >= NS && !wait(is_k ? k_free(b) : v_free(b), (j / NS - 1) & 1)) {
+        failed = true;
+        break;
+      }
+      const uint32_t full = is_k ? k_full(b) : v_full(b);
+      const uint32_t dst = (is_k ? sk : sv) + b * C::KV_BYTES;
+      if (j < plain) {
+        if (lane == 0) {
+          mbar_expect_tx(full, C::KV_BYTES);
+#pragma unroll
+          for (int half = 0; half < D / 64; ++half)
+            tma_load_3d(dst + half * (BN * 128), map, half * 64, kvh, k0 + j * BN, full);
+        }
+        __syncwarp();
+      } else {
+        constexpr int RPW = 32 / CPR;                         // rows per warp-wide load
+        constexpr int U = 16;                                 // loads in flight per lane
+        const int c = lane % CPR;
+        unsigned char* tile = smem + (dst - base);
+        for (int r0 = 0; r0 < BN; r0 += U * RPW) {
+          uint4 x[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int t = j * BN + r0 + u * RPW + lane / CPR;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (r0 + u * RPW < BN && t < m) x[u] = *reinterpret_cast<const uint4*>(src + (k0 + t) * stride + c * 8);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (r0 + u * RPW >= BN) break;
+            if (!is_k) {
+              unsigned w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (!finite16(w[e]) || !finite16(w[e] >> 16)) {
+                  *not_finite = 1;
+                  w[e] = (finite16(w[e]) ? w[e] & 0xffffu : 0u) | (finite16(w[e] >> 16) ? w[e] & 0xffff0000u : 0u);
+                }
+              }
+              x[u] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            *reinterpret_cast<uint4*>(tile + sw128(r0 + u * RPW + lane / CPR, c, BN)) = x[u];
+          }
+        }
+        fence_proxy_async_smem();                             // these stores -> tensor-core reads
+      }
+      mbar_arrive(full);
+      ++issued;
+    }
+    if (failed) give_up();
+    if (*abort_flag) {
+      // let the copies this warp issued land (bounded) before the CTA's shared memory is released
+      for (int t = max(0, issued - NS); t < issued; ++t) mbar_wait(is_k ? k_full(t % NS) : v_full(t % NS), (t / NS) & 1);
+    }
+  } else if (warp == 8) {
+    // ---------------- S = Q K^T issue (one lane) ----------------
+    if (lane == 0) {
+      constexpr uint32_t IDESC_QK = umma_idesc_f16(BM, BN, false);
+      const uint64_t a_desc0 = umma_smem_desc(sq, 16, 1024), a_desc1 = umma_smem_desc(sq + C::Q_BYTES, 16, 1024);
+      int issued[2] = {0, 0};
+      failed = !wait(q_full, 0);
+      for (int j = 0; j < n_tiles && !failed; ++j) {
+        if (!wait(k_full(j % NS), (j / NS) & 1)) {
+          failed = true;
+          break;
+        }
+        const int u = j & 1;
+        const uint64_t b0 = umma_smem_desc(sk + (j % NS) * C::KV_BYTES, 16, 1024);
+        for (int g = 0; g < ntile; ++g) {
+          if (j >= 2 && !wait(pv_done(g, u), ((j - 2) >> 1) & 1)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          if (g != 0 || j < tiles0) {                         // past its last key, tile 0 only keeps step
+            const uint64_t a0 = g == 0 ? a_desc0 : a_desc1;
+            const uint32_t d = t_s(g, u);
+            umma_ss(d, a0, b0, IDESC_QK, 0u);
+#pragma unroll
+            for (int kk = 1; kk < D / 16; ++kk)
+              umma_ss(d, a0 + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4),
+                      b0 + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), IDESC_QK, 1u);
+          }
+          umma_commit(s_full(g, u));
+          ++issued[g];
+        }
+      }
+      if (failed) {
+        give_up();
+        for (int g = 0; g < ntile; ++g)
+          if (issued[g] > 0) mbar_wait(s_full(g, (issued[g] - 1) & 1), ((issued[g] - 1) >> 1) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    // ---------------- O += P V issue (one lane) ----------------
+    if (lane == 0) {
+      constexpr uint32_t IDESC_PV = umma_idesc_f16(BM, D, true);
+      int issued[2] = {0, 0};
+      for (int j = 0; j < n_tiles && !failed; ++j) {
+        if (!wait(v_full(j % NS), (j / NS) & 1)) {
+          failed = true;
+          break;
+        }
+        const int u = j & 1;
+        const uint64_t v0 = umma_smem_desc(sv + (j % NS) * C::KV_BYTES, BN * 128, 1024);
+        for (int g = 0; g < ntile; ++g) {
+          if (!wait(p_full(g, u), (j >> 1) & 1)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          if (g != 0 || j < tiles0) {
+            const uint32_t o = t_o(g), pa = t_s(g, u);
+            umma_ts(o, pa, v0, IDESC_PV, j > 0 ? 1u : 0u);
+#pragma unroll
+            for (int kk = 1; kk < BN / 16; ++kk) umma_ts(o, pa + kk * 8, v0 + ((kk * 16 * 128) >> 4), IDESC_PV, 1u);
+          }
+          umma_commit(pv_done(g, u));
+          ++issued[g];
+        }
+        if (failed) break;
+        umma_commit(v_free(j % NS));
+      }
+      if (failed) {
+        give_up();
+        for (int g = 0; g < ntile; ++g)
+          if (issued[g] > 0) mbar_wait(pv_done(g, (issued[g] - 1) & 1), ((issued[g] - 1) >> 1) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 4 * ntile) {
+    // ---------------- softmax ----------------
+    const int g = warp >> 2;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t to = t_o(g);
+    const int tile_first = m - n + tile_row(g);               // the query tile's first position
+    const int pos = tile_first + (tid & (BM - 1));
+    const int my_tiles = g == 0 ? tiles0 : n_tiles;
+    for (int j = 0; j < n_tiles; ++j) {
+      // decisions stay warp-uniform: the tcgen05.ld/st below are warp-collective
+      const int u = j & 1;
+      const uint32_t ts = t_s(g, u);
+      if (!__all_sync(0xffffffffu, wait(s_full(g, u), (j >> 1) & 1))) {
+        failed = true;
+        break;
+      }
+      tc_fence_after();
+      if (lane == 0) mbar_arrive(k_free(j % NS));
+      if (j >= my_tiles) {                                    // no product was issued
+        mbar_arrive(p_full(g, u));
+        continue;
+      }
+      float sv_[BN];
+      tmem_ld32_nowait(ts + lane_off, *reinterpret_cast<float(*)[32]>(sv_));
+      tmem_ld32_nowait(ts + lane_off + 32, *reinterpret_cast<float(*)[32]>(sv_ + 32));
+      tmem_ld_wait();
+      const int key0 = j * BN;
+      if (key0 + BN - 1 > tile_first) {                       // keys after the query (and past the end)
+#pragma unroll
+        for (int c = 0; c < BN; ++c)
+          if (key0 + c > pos) sv_[c] = -INFINITY;
+      }
+      float m8[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m8[i] = fmaxf(sv_[i], sv_[8 + i]);
+#pragma unroll
+      for (int c = 16; c < BN; c += 16)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m8[i] = max3(m8[i], sv_[c + i], sv_[c + 8 + i]);
+      float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+      mx *= p.scale_log2;
+      const bool rescale = mx > m_ref + kRescale;             // also the first finite maximum
+      float alpha = 1.f;
+      if (rescale) {
+        alpha = exp2f(m_ref - mx);
+        m_ref = mx;
+      }
+      const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
+      if (__any_sync(0xffffffffu, rescale && j > 0)) {
+        if (!__all_sync(0xffffffffu, wait(pv_done(g, (j - 1) & 1), ((j - 1) >> 1) & 1))) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld32(to + lane_off + c * 32, o);
+          uint32_t ob[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e] * alpha);
+          tmem_st32(to + lane_off + c * 32, ob);
+        }
+      }
+      // P as fp16; the row sum adds the rounded weights, the ones that multiply V
+      float sum8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      uint32_t pk[BN / 2];
+#pragma unroll
+      for (int e = 0; e < BN / 2; ++e) {
+        float x0, x1;
+        fma2(x0, x1, sv_[2 * e], sv_[2 * e + 1], p.scale_log2, nref);
+        pk[e] = pack_half2(fast_exp2(x0), fast_exp2(x1));
+        add_half2(sum8[2 * (e & 3)], sum8[2 * (e & 3) + 1], pk[e]);
+      }
+      float sum4[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum4[i] = sum8[2 * i] + sum8[2 * i + 1];
+      tmem_st32(ts + lane_off, pk);
+      l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(p_full(g, u));
+    }
+    if (!failed) {
+      failed = !__all_sync(0xffffffffu, wait(pv_done(g, (n_tiles - 1) & 1), ((n_tiles - 1) >> 1) & 1));
+      tc_fence_after();
+    }
+    if (failed) give_up();
+  }
+
+  // ---------------- epilogue ----------------
+  __syncthreads();
+  const bool aborted = *abort_flag != 0;
+  if (warp < 4 * ntile && !aborted) {
+    // each thread normalises its O row and stages it in the K/V ring (every MMA is done), chunks XOR-ed
+    // with the row's low bits; the warp then stores whole rows
+    const int g = warp >> 2;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float inv = 1.f / l;                                // a query sees its own key at least
+    unsigned char* stage = smem + (sk - base);                // [256 rows][D * 2 bytes]
+    constexpr int RB = D * 2;
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      float o[32];
+      tmem_ld32(t_o(g) + lane_off + c * 32, o);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] *= inv;
+      if (*not_finite) {
+        // values that are not finite in the edge tiles were left out: add them where they are seen
+        const int pos = min(m - n + tile_row(g) + (tid & (BM - 1)), m - 1);
+        for (int t = edge * BN; t <= pos; ++t) {
+          const __half* row = p.v + (k0 + t) * p.v_stride + static_cast<int64_t>(kvh) * D + c * 32;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const __half x = row[e];
+            if (!finite16(__half_as_ushort(x))) o[e] += __half2float(x);
+          }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint4 w;
+        w.x = pack_half2(o[8 * k], o[8 * k + 1]);
+        w.y = pack_half2(o[8 * k + 2], o[8 * k + 3]);
+        w.z = pack_half2(o[8 * k + 4], o[8 * k + 5]);
+        w.w = pack_half2(o[8 * k + 6], o[8 * k + 7]);
+        *reinterpret_cast<uint4*>(stage + tid * RB + (((c * 4 + k) ^ (tid & (CPR - 1))) << 4)) = w;
+      }
+    }
+    __syncwarp();
+    constexpr int RPI = 32 / CPR;
+    const int c = lane % CPR;
+#pragma unroll 4
+    for (int r0 = 0; r0 < 32; r0 += RPI) {
+      const int row = warp * 32 + r0 + lane / CPR;            // CTA row
+      const int i = tile_row(g) + (row & (BM - 1));
+      if (i < n) {
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + row * RB + ((c ^ (row & (CPR - 1))) << 4));
+        *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(q0 + i) * H + tile_head(g)) * D + c * 8) = w;
+      }
+    }
+  }
+  if (tid == 0) mbar_wait(q_full, 0);                         // landed, unless the CTA gave up early: bounded
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+  }
+}
+
+bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
+
+// x [T][H][D] fp16, tokens `stride` elements apart, as the 3-D tensor (D, H, T); a box is `box_tokens`
+// tokens of one head and one 64-element half of the head dimension, written with the 128-byte swizzle.
+int encode_rows_map(CUtensorMap* map, const void* x, int D, int H, int T, int64_t stride, int box_tokens) {
+  const EncodeTiledFn fn = tensor_map_encoder();
+  if (!fn) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention: cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(x), dims, strides, box, elem,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention: tensor map encoding failed (%d)", static_cast<int>(r));
+  return PKV_OK;
+}
+
+template <int D>
+int launch(const PromptParams& p, int num_seqs, int max_query_len, cudaStream_t st) {
+  static std::mutex mu;
+  static bool done[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) {
+    std::lock_guard<std::mutex> g(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+      e = cudaFuncSetAttribute(prompt_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+      if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    }
+  }
+  if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention setup: %s", cudaGetErrorString(e));
+  const int rows = p.pair ? BM : 2 * BM;
+  const dim3 grid((max_query_len - 1) / rows + 1, p.pair ? p.num_heads / 2 : p.num_heads, num_seqs);
+  e = pkv::launch_pdl(prompt_attention_kernel<D>, grid, dim3(THREADS), Cfg<D>::SMEM, st, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention launch: %s", cudaGetErrorString(e));
+  return PKV_OK;
+}
+
+}  // namespace
+
+namespace pkv {
+int read_device_error_prompt(int reset, int* code) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_dev_error_prompt, sizeof(int));
+  if (e == cudaSuccess && reset && v) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbol(g_dev_error_prompt, &zero, sizeof(int));
+  }
+  if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "reading the prompt attention's check word: %s", cudaGetErrorString(e));
+  *code = v;
+  return PKV_OK;
+}
+}  // namespace pkv
+
+extern "C" {
+
+int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t* value, const int32_t* query_start,
+                         const int32_t* key_start, int num_seqs, int total_q, int total_k, int max_query_len,
+                         int num_heads, int num_kv_heads, int head_dim, int64_t q_stride, int64_t key_stride,
+                         int64_t value_stride, float scale, uint16_t* out, void* stream) {
+  const char* fn = "pkv_prompt_attention";
+  if (num_seqs < 0 || total_q < 0 || total_k < 0 || max_query_len < 0 || num_heads <= 0 || num_kv_heads <= 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG,
+                     "%s: num_seqs=%d total_q=%d total_k=%d max_query_len=%d num_heads=%d num_kv_heads=%d", fn, num_seqs,
+                     total_q, total_k, max_query_len, num_heads, num_kv_heads);
+  if (num_heads % num_kv_heads)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "%s: num_heads=%d is not a multiple of num_kv_heads=%d", fn, num_heads,
+                     num_kv_heads);
+  if (head_dim != 64 && head_dim != 128)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: head_dim %d not in {64, 128}", fn, head_dim);
+  if (num_seqs == 0 || total_q == 0 || max_query_len == 0) {
+    pkv::clear_error();
+    return PKV_OK;
+  }
+  if (num_seqs > 65535 || num_heads > 65535)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: num_seqs/num_heads above 65535", fn);
+  if (total_q > (1 << 30) || total_k > (1 << 30) || max_query_len > (1 << 30))
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: more than 2^30 tokens", fn);
+  if (total_k == 0) return pkv::fail(PKV_ERR_INVALID_ARG, "%s: queries but no keys", fn);
+  if (!q || !key || !value || !query_start || !out) return pkv::fail(PKV_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!aligned16(q) || !aligned16(key) || !aligned16(value) || !aligned16(out))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "%s: q, key, value and out must be 16-byte aligned", fn);
+  const int64_t q_row = static_cast<int64_t>(num_heads) * head_dim, k_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (q_stride < q_row || key_stride < k_row || value_stride < k_row || q_stride % 8 || key_stride % 8 || value_stride % 8)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "%s: strides must be multiples of 8 and at least a token's length", fn);
+  if (!std::isfinite(scale) || !(scale > 0.f))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "%s: scale must be finite and positive", fn);
+  PromptParams p{};
+  int rc = encode_rows_map(&p.tmap_q, q, head_dim, num_heads, total_q, q_stride, BM);
+  if (rc == PKV_OK) rc = encode_rows_map(&p.tmap_k, key, head_dim, num_kv_heads, total_k, key_stride, BN);
+  if (rc == PKV_OK) rc = encode_rows_map(&p.tmap_v, value, head_dim, num_kv_heads, total_k, value_stride, BN);
+  if (rc != PKV_OK) return rc;
+  p.k = reinterpret_cast<const __half*>(key);
+  p.v = reinterpret_cast<const __half*>(value);
+  p.qstart = query_start;
+  p.kstart = key_start ? key_start : query_start;
+  p.out = reinterpret_cast<__half*>(out);
+  p.k_stride = key_stride;
+  p.v_stride = value_stride;
+  p.num_heads = num_heads;
+  p.group = num_heads / num_kv_heads;
+  p.pair = p.group % 2 == 0 ? 1 : 0;
+  p.total_q = total_q;
+  p.total_k = total_k;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = head_dim == 128 ? launch<128>(p, num_seqs, max_query_len, st) : launch<64>(p, num_seqs, max_query_len, st);
+  if (rc == PKV_OK) pkv::clear_error();
+  return rc;
+}
+
+}  // extern "C"

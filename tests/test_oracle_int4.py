@@ -206,3 +206,32 @@ def test_decode_int4_oracle_groups_heads():
     for h in range(6):
         w = np.exp(0.2 * k[h // 3] @ q[0, h].astype(np.float64))
         assert np.allclose(out[0, h], w @ v[h // 3] / w.sum(), rtol=1e-12)
+
+
+def _prompt(lib, **kw):
+    a = dict(q=16, k=16, v=16, qs=16, ks=None, S=2, T=8, Tk=8, maxq=4, H=4, Hk=2, D=64, sq=256, sk=128, sv=128, scale=0.1,
+             out=16)
+    a.update(kw)
+    return lib.pkv_prompt_attention(a["q"], a["k"], a["v"], a["qs"], a["ks"], a["S"], a["T"], a["Tk"], a["maxq"], a["H"],
+                                    a["Hk"], a["D"], a["sq"], a["sk"], a["sv"], a["scale"], a["out"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(D=96), pkv.PKV_ERR_UNSUPPORTED),
+    (dict(Hk=0), pkv.PKV_ERR_INVALID_ARG),
+    (dict(Hk=3), pkv.PKV_ERR_INVALID_ARG),
+    (dict(T=-1), pkv.PKV_ERR_INVALID_ARG),
+    (dict(Tk=0), pkv.PKV_ERR_INVALID_ARG),                 # queries without keys
+    (dict(S=70000), pkv.PKV_ERR_UNSUPPORTED),
+    (dict(qs=None), pkv.PKV_ERR_INVALID_ARG),
+    (dict(k=40), pkv.PKV_ERR_INVALID_ARG),
+    (dict(sk=64), pkv.PKV_ERR_INVALID_ARG),
+    (dict(sq=260), pkv.PKV_ERR_INVALID_ARG),
+    (dict(scale=0.0), pkv.PKV_ERR_INVALID_ARG),
+    (dict(T=0, q=None), pkv.PKV_OK),
+    (dict(S=0, q=None), pkv.PKV_OK),
+])
+def test_prompt_attention_refuses(lib, kw, status):
+    assert _prompt(lib, **kw) == status
+    if status != pkv.PKV_OK:
+        assert lib.pkv_last_error()
