@@ -141,7 +141,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle: building torch's Stream object takes as long as a small launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -475,18 +476,24 @@ def swap_blocks(src_k: Sequence[torch.Tensor], src_v: Sequence[torch.Tensor], ds
 
 # ---- queries and keys before attention ---------------------------------------------------------
 
-def _need_rows(t: torch.Tensor, name: str) -> int:
-    """A CUDA fp16 [tokens, heads, D] tensor whose tokens may be strided; returns their stride."""
-    if (t.dtype != torch.float16 or t.dim() != 3 or not t.is_cuda
-            or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
-        raise PkvError(PKV_ERR_INVALID_ARG,
-                       f"{name}: want a CUDA torch.float16 tensor of rank 3 with each token's heads contiguous, "
-                       f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} device={t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise PkvError(PKV_ERR_INVALID_ARG,
-                       f"{name}: on {t.device}, but the current CUDA device is cuda:{torch.cuda.current_device()} "
-                       f"(make it current, e.g. with torch.cuda.device({t.device}))")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _is(t: torch.Tensor, dtype: torch.dtype, dim: int, device: int) -> bool:
+    """What _need asks of a CUDA tensor, at a fraction of its time (where this fails, _need says why)."""
+    return t.dtype is dtype and t.dim() == dim and t.get_device() == device and t.is_contiguous()
+
+
+def _rows(t: torch.Tensor, name: str, device: int) -> Tuple[int, int, int, int]:
+    """(tokens, heads, D, token stride) of a CUDA fp16 [tokens, heads, D] tensor whose tokens may be strided."""
+    if t.dtype is torch.float16 and t.dim() == 3 and t.get_device() == device:
+        T, H, D = t.shape
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and (s1 == D or H == 1):
+            return T, H, D, (s0 if T > 1 else H * D)
+    if t.is_cuda and t.get_device() != device:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"{name}: on {t.device}, but the current CUDA device is cuda:{device} "
+                                            f"(make it current, e.g. with torch.cuda.device({t.device}))")
+    raise PkvError(PKV_ERR_INVALID_ARG,
+                   f"{name}: want a CUDA torch.float16 tensor of rank 3 with each token's heads contiguous, "
+                   f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} device={t.device}")
 
 
 def rope_frequencies(inv_freq: Sequence[float], device="cuda") -> torch.Tensor:
@@ -511,35 +518,47 @@ def qk_norm_rope(q: torch.Tensor, key: torch.Tensor, positions: torch.Tensor, fr
     positions is [T] or [num_axes, T] int32; with several axes (time, height, width) pair_axis gives
     each pair's.  q and key may be views into a packed projection (tokens strided); q_out and k_out
     may be q and key themselves (in place)."""
-    qs, ks = _need_rows(q, "q"), _need_rows(key, "key")
-    T, H, D = q.shape
-    if key.shape[0] != T or key.shape[2] != D:
+    dev = torch.cuda.current_device()
+    T, H, D, qs = _rows(q, "q", dev)
+    Tk, Hk, Dk, ks = _rows(key, "key", dev)
+    if Tk != T or Dk != D:
         raise PkvError(PKV_ERR_INVALID_ARG, f"qk_norm_rope: key {tuple(key.shape)} does not match q {tuple(q.shape)}")
-    _need(positions, "positions", torch.int32, 2 if positions.dim() == 2 else 1)
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    if positions.shape[-1] != T:
-        raise PkvError(PKV_ERR_INVALID_ARG, "qk_norm_rope: positions must be [T] or [num_axes, T]")
-    _need(frequencies, "frequencies", torch.int64, 1)
+    dim = positions.dim()
+    if not _is(positions, torch.int32, 2 if dim == 2 else 1, dev):
+        _need(positions, "positions", torch.int32, 2 if dim == 2 else 1)
+    if not _is(frequencies, torch.int64, 1, dev):
+        _need(frequencies, "frequencies", torch.int64, 1)
+    axes = positions.shape[0] if dim == 2 else 1
     pairs = frequencies.shape[0]
+    if positions.shape[dim - 1] != T:
+        raise PkvError(PKV_ERR_INVALID_ARG, "qk_norm_rope: positions must be [T] or [num_axes, T]")
     if pair_axis is not None:
-        _need(pair_axis, "pair_axis", torch.int32, 1)
+        if not _is(pair_axis, torch.int32, 1, dev):
+            _need(pair_axis, "pair_axis", torch.int32, 1)
         if pair_axis.shape[0] != pairs:
             raise PkvError(PKV_ERR_INVALID_ARG, "qk_norm_rope: pair_axis must have one entry per frequency")
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
-            _need(w, name, torch.float16, 1)
+            if not _is(w, torch.float16, 1, dev):
+                _need(w, name, torch.float16, 1)
             if w.shape[0] != D:
                 raise PkvError(PKV_ERR_INVALID_ARG, f"qk_norm_rope: {name} must have head_dim entries")
+    qos, kos = H * D, Hk * D
     if q_out is None:
         q_out = torch.empty((T, H, D), dtype=torch.float16, device=q.device)
+    else:
+        *shape, qos = _rows(q_out, "q_out", dev)
+        if shape != [T, H, D]:
+            raise PkvError(PKV_ERR_INVALID_ARG, "qk_norm_rope: q_out must be shaped like q")
     if k_out is None:
-        k_out = torch.empty(tuple(key.shape), dtype=torch.float16, device=q.device)
-    if q_out.shape != q.shape or k_out.shape != key.shape:
-        raise PkvError(PKV_ERR_INVALID_ARG, "qk_norm_rope: outputs must be shaped like q and key")
-    qos, kos = _need_rows(q_out, "q_out"), _need_rows(k_out, "k_out")
+        k_out = torch.empty((T, Hk, D), dtype=torch.float16, device=q.device)
+    else:
+        *shape, kos = _rows(k_out, "k_out", dev)
+        if shape != [T, Hk, D]:
+            raise PkvError(PKV_ERR_INVALID_ARG, "qk_norm_rope: k_out must be shaped like key")
     _check(load().pkv_qk_norm_rope(
-        q.data_ptr(), key.data_ptr(), _ptr(q_weight), _ptr(k_weight), float(eps), positions.data_ptr(), axes,
-        frequencies.data_ptr(), _ptr(pair_axis), 2 * pairs, int(interleaved), T, H, key.shape[1], D, qs, ks,
+        q.data_ptr(), key.data_ptr(), _ptr(q_weight), _ptr(k_weight), eps, positions.data_ptr(), axes,
+        frequencies.data_ptr(), _ptr(pair_axis), 2 * pairs, int(interleaved), T, H, Hk, D, qs, ks,
         q_out.data_ptr(), k_out.data_ptr(), qos, kos, _stream(stream)))
     return q_out, k_out
 
@@ -554,8 +573,10 @@ def int4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_d
 
 def _need_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, block_size: int) -> Tuple[int, int, int]:
     """(num_blocks, num_kv_heads, head_dim) of two four-bit pools."""
-    _need(k_cache, "k_cache", torch.uint8, 3)
-    _need(v_cache, "v_cache", torch.uint8, 3)
+    dev = torch.cuda.current_device()
+    if not (_is(k_cache, torch.uint8, 3, dev) and _is(v_cache, torch.uint8, 3, dev)):
+        _need(k_cache, "k_cache", torch.uint8, 3)
+        _need(v_cache, "v_cache", torch.uint8, 3)
     N, H, tile = k_cache.shape
     if block_size <= 0 or tile % block_size or v_cache.shape != k_cache.shape:
         raise PkvError(PKV_ERR_INVALID_ARG, f"four-bit pools {tuple(k_cache.shape)} and {tuple(v_cache.shape)} are not "
@@ -567,11 +588,14 @@ def reshape_and_cache_int4(key: torch.Tensor, value: torch.Tensor, k_cache: torc
                            slot_mapping: torch.Tensor, block_size: int, stream=None) -> None:
     """Hold key[t], value[t] in four bits at slot_mapping[t] (negative = skip) of the pools.  key and
     value may be views into a packed projection (tokens strided)."""
-    ks, vs = _need_rows(key, "key"), _need_rows(value, "value")
+    dev = torch.cuda.current_device()
+    *rows, ks = _rows(key, "key", dev)
+    *vrows, vs = _rows(value, "value", dev)
     N, H, D = _need_int4(k_cache, v_cache, block_size)
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
-    T = key.shape[0]
-    if tuple(key.shape[1:]) != (H, D) or value.shape != key.shape or slot_mapping.shape[0] != T:
+    if not _is(slot_mapping, torch.int64, 1, dev):
+        _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    T = slot_mapping.shape[0]
+    if rows != [T, H, D] or vrows != rows:
         raise PkvError(PKV_ERR_INVALID_ARG, "reshape_and_cache_int4: inconsistent shapes")
     _check(load().pkv_reshape_and_cache_int4(key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                              slot_mapping.data_ptr(), T, H, D, block_size, N, ks, vs,
@@ -584,16 +608,20 @@ def gather_cache_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping
     """fp16 rows [T, H, D] of what slots slot_mapping[t] of the pools stand for (rows with a negative
     slot are left as they were)."""
     N, H, D = _need_int4(k_cache, v_cache, block_size)
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
-    T = slot_mapping.shape[0]
-    if key is None:
-        key = torch.empty((T, H, D), dtype=torch.float16, device=k_cache.device)
-    if value is None:
-        value = torch.empty((T, H, D), dtype=torch.float16, device=k_cache.device)
-    _need(key, "key", torch.float16, 3)
-    _need(value, "value", torch.float16, 3)
-    if tuple(key.shape) != (T, H, D) or value.shape != key.shape:
-        raise PkvError(PKV_ERR_INVALID_ARG, f"gather_cache_int4: key and value must be [{T}, {H}, {D}]")
+    if not _is(slot_mapping, torch.int64, 1, torch.cuda.current_device()):
+        _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    shape = (slot_mapping.shape[0], H, D)
+    T = shape[0]
+    outs = []
+    for t, name in ((key, "key"), (value, "value")):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.float16, device=k_cache.device)
+        else:
+            _need(t, name, torch.float16, 3)
+            if tuple(t.shape) != shape:
+                raise PkvError(PKV_ERR_INVALID_ARG, f"gather_cache_int4: {name} must be [{T}, {H}, {D}]")
+        outs.append(t)
+    key, value = outs
     _check(load().pkv_gather_cache_int4(k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
                                         key.data_ptr(), value.data_ptr(), T, H, D, block_size, N, _stream(stream)))
     return key, value
@@ -652,14 +680,18 @@ def paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
                                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out[s, h] = softmax attention of q[s, h] over the sequence's rows of four-bit pools; num_heads
     may be a multiple of the pools' heads (grouped heads)."""
-    _need(q, "q", torch.float16, 3)
+    dev = torch.cuda.current_device()
     N, Hk, D = _need_int4(k_cache, v_cache, block_size)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(context_lens, "context_lens", torch.int32, 1)
-    S, H, _ = q.shape
-    if q.shape[2] != D:
-        raise PkvError(PKV_ERR_INVALID_ARG, f"paged_attention_decode_int4: q has head_dim {q.shape[2]}, the pools {D}")
-    if block_tables.shape[0] != S or context_lens.shape[0] != S:
+    if not (_is(q, torch.float16, 3, dev) and _is(block_tables, torch.int32, 2, dev)
+            and _is(context_lens, torch.int32, 1, dev)):
+        _need(q, "q", torch.float16, 3)
+        _need(block_tables, "block_tables", torch.int32, 2)
+        _need(context_lens, "context_lens", torch.int32, 1)
+    S, H, Dq = q.shape
+    if Dq != D:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"paged_attention_decode_int4: q has head_dim {Dq}, the pools {D}")
+    rows, max_blocks = block_tables.shape
+    if rows != S or context_lens.shape[0] != S:
         raise PkvError(PKV_ERR_INVALID_ARG, "block_tables / context_lens rows != num_seqs")
     if out is None:
         out = torch.empty_like(q)
@@ -667,7 +699,6 @@ def paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
         _need(out, "out", torch.float16, 3)
         if out.shape != q.shape:
             raise PkvError(PKV_ERR_INVALID_ARG, "paged_attention_decode_int4: out must be shaped like q")
-    max_blocks = block_tables.shape[1]
     if workspace is None:
         n = paged_attention_int4_workspace_size(S, H, Hk, D, max_blocks, block_size)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
@@ -689,16 +720,19 @@ def prompt_attention(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, qu
     Sequence s has queries query_start[s]..query_start[s+1] and keys key_start[s]..key_start[s+1]
     (key_start None: the same), the last of which are its queries' own.  q, key and value may be views
     into a packed projection (tokens strided)."""
-    qs, ks, vs = _need_rows(q, "q"), _need_rows(key, "key"), _need_rows(value, "value")
-    T, H, D = q.shape
-    Tk, Hk, Dk = key.shape
-    if Dk != D or value.shape != key.shape:
+    dev = torch.cuda.current_device()
+    T, H, D, qs = _rows(q, "q", dev)
+    Tk, Hk, Dk, ks = _rows(key, "key", dev)
+    *vrows, vs = _rows(value, "value", dev)
+    if Dk != D or vrows != [Tk, Hk, D]:
         raise PkvError(PKV_ERR_INVALID_ARG, f"prompt_attention: key {tuple(key.shape)} and value {tuple(value.shape)} do "
                                             f"not match q {tuple(q.shape)}")
-    _need(query_start, "query_start", torch.int32, 1)
+    if not _is(query_start, torch.int32, 1, dev):
+        _need(query_start, "query_start", torch.int32, 1)
     S = query_start.shape[0] - 1
     if key_start is not None:
-        _need(key_start, "key_start", torch.int32, 1)
+        if not _is(key_start, torch.int32, 1, dev):
+            _need(key_start, "key_start", torch.int32, 1)
         if key_start.shape[0] != S + 1:
             raise PkvError(PKV_ERR_INVALID_ARG, "prompt_attention: query_start and key_start differ in length")
     if out is None:
