@@ -4,9 +4,15 @@
 // s = (max x - lo) / 15: half a byte a value and four bytes a row (s and lo in fp16),
 // 68 bytes for D = 128 where fp16 takes 256.  It stands for lo + s * n.
 //
-// Both kernels are HBM-bound: 16 bytes of fp16 against 4 bytes of packed values per
-// lane, D/8 lanes a row, one CTA a token.  A row's minimum and maximum are taken on
-// packed fp16 pairs and reduced over its lanes by shuffles.
+// Both kernels are HBM-bound.  A warp takes a token's rows (or a part of them, where there
+// are few tokens), D/16 lanes a row, 16 values a lane in two 16-byte chunks half a row
+// apart, so that every access of a row is contiguous over its lanes.
+//
+// The write has about 4.5 values to handle per clock and SM at HBM rate, so it counts
+// instructions: minimum and maximum on packed fp16 pairs, and the quotients two to an
+// instruction.  u = x / s - lo / s is rounded by adding and taking off 1.5 * 2^23; only
+// where u comes nearer to a half than its error bound (some 2^-16 of all values) is n
+// decided by the exact remainder.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -20,7 +26,7 @@ namespace {
 __device__ int g_dev_error_cache_int4 = 0;
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_cache_int4, 0, code); }
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8;            // per CTA
 
 struct Int4RowParams {
   const __half* key;
@@ -35,7 +41,8 @@ struct Int4RowParams {
   int num_heads;
   int log2_block;
   int tile_bytes;
-  int rows_per_cta;
+  int num_tokens;
+  int rows_per_warp;
 };
 
 // n of one value by the definition, from the estimate n0 (off by at most one): n s against d = x - lo,
@@ -49,128 +56,193 @@ __device__ __forceinline__ unsigned nearest_exact(float d, float s, float n0) {
   return static_cast<unsigned>(fminf(fmaxf(n, 0.f), 15.f));
 }
 
-// grid (tokens, parts of a token's K and V rows)
+// two fp32 sums or fused products in one instruction
+__device__ __forceinline__ float2 add2(float2 a, float b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %6};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Eight values' n, four bits each.  d / s = u + e with u = x inv + b, b = -lo inv: inv is off by 2^-23
+// relative and the sum by 2^-24 of it, so e is below 2^-18 + 2^-23 |b|; `sure` is one half less more
+// than that.
+__device__ __forceinline__ unsigned pack8(const uint4& raw, float inv, float b, float lo, float s, float sure, bool past) {
+  constexpr float kMagic = 12582912.f;              // 1.5 * 2^23: the sum's low bits are the whole number
+  const __half2* h2 = reinterpret_cast<const __half2*>(&raw);
+  unsigned word = 0;
+  float most = 0.f, least = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 u = fma2(__half22float2(h2[e]), inv, make_float2(b, b));
+    const float2 m = add2(u, kMagic);
+    const float2 r = fma2(add2(m, -kMagic), -1.f, u);
+    most = fmaxf(most, fmaxf(r.x, r.y));
+    least = fminf(least, fminf(r.x, r.y));
+    word += __float_as_uint(m.x) << (8 * e);
+    word += __float_as_uint(m.y) << (8 * e + 4);
+  }
+  word -= 0x4B400000u * 0x11111111u;                // the magic number's own bits, eight times
+  if (past || most >= sure || least <= -sure) {
+    word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = (i & 1) ? __high2float(h2[i / 2]) : __low2float(h2[i / 2]);
+      const float d = x - lo;
+      word |= s > 0.f ? nearest_exact(d, s, rintf(d * inv)) << (4 * i) : 0u;
+    }
+  }
+  return word;
+}
+
+// grid (tokens / kWarps, parts of a token's K and V rows)
 template <int D>
-__global__ void __launch_bounds__(kThreads) reshape_and_cache_int4_kernel(const Int4RowParams p) {
-  constexpr int LPR = D / 8;
-  constexpr int RPP = kThreads / LPR;
-  constexpr int U = 3;                              // passes whose loads are in flight together
+__global__ void __launch_bounds__(kWarps * 32) reshape_and_cache_int4_kernel(const Int4RowParams p) {
+  constexpr int LPR = D / 16;                       // lanes per row
+  constexpr int RPP = 32 / LPR;                     // rows a warp takes at a time
+  constexpr int PF = 2;                             // of which so many are in flight
   pkv::pdl_trigger();
   pkv::pdl_wait();
-  const int t = blockIdx.x;
-  const int tid = threadIdx.x, c = tid % LPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR;
+  const int t = blockIdx.x * kWarps + warp;
+  if (t >= p.num_tokens) return;
   const int H = p.num_heads;
-  const int begin = blockIdx.y * p.rows_per_cta, end = min(2 * H, begin + p.rows_per_cta);
-  const int first = begin + tid / LPR;
-  auto load = [&](int r) {
-    return r >= end ? make_uint4(0, 0, 0, 0)
-           : r < H  ? *reinterpret_cast<const uint4*>(p.key + t * p.key_stride + r * D + c * 8)
-                    : *reinterpret_cast<const uint4*>(p.value + t * p.value_stride + (r - H) * D + c * 8);
+  const int begin = blockIdx.y * p.rows_per_warp, end = min(2 * H, begin + p.rows_per_warp);
+  const __half* key = p.key + t * p.key_stride + c * 8;
+  const __half* value = p.value + t * p.value_stride + c * 8 - static_cast<int64_t>(H) * D;
+  uint4 raw[PF][2];
+  auto load = [&](int r, uint4 (&x)[2]) {
+    if (r < end) {
+      const __half* src = (r < H ? key : value) + r * D;
+      x[0] = *reinterpret_cast<const uint4*>(src);
+      x[1] = *reinterpret_cast<const uint4*>(src + D / 2);
+    } else {
+      x[0] = x[1] = make_uint4(0, 0, 0, 0);
+    }
   };
-  uint4 raw[U];
+  const int first = begin + lane / LPR;
 #pragma unroll
-  for (int u = 0; u < U; ++u) raw[u] = load(first + u * RPP);
+  for (int u = 0; u < PF; ++u) load(first + u * RPP, raw[u]);
   const int64_t slot = p.slots[t];
   if (slot < 0) return;                             // padding token
   if (slot >= p.num_slots) {
-    if (tid == 0 && blockIdx.y == 0) record_error(PKV_DEV_BAD_SLOT);
+    if (lane == 0 && blockIdx.y == 0) record_error(PKV_DEV_BAD_SLOT);
     return;
   }
-  const int64_t blk = slot >> p.log2_block;
   const int in_block = static_cast<int>(slot & ((1 << p.log2_block) - 1));
-  const int64_t block_base = blk * H * p.tile_bytes;
+  const int64_t block_base = (slot >> p.log2_block) * H * p.tile_bytes;
+  uint8_t* k_block = p.k_cache + block_base;
+  uint8_t* v_block = p.v_cache + block_base - static_cast<int64_t>(H) * p.tile_bytes;
   const int data_off = in_block * (D / 2) + c * 4;
   const int meta_off = ((D / 2) << p.log2_block) + in_block * 4;
-  for (int row = first; row - tid / LPR < end; row += U * RPP) {
+  for (int row = first; row - lane / LPR < end; row += PF * RPP) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < PF; ++u) {
       const int r = row + u * RPP;
-      const uint4 x4 = raw[u];
-      raw[u] = load(r + U * RPP);
-      const __half2* h2 = reinterpret_cast<const __half2*>(&x4);
+      const uint4 x0 = raw[u][0], x1 = raw[u][1];
+      load(r + PF * RPP, raw[u]);
       // NaN-keeping minimum and maximum: a row that holds a NaN gets a NaN scale
-      __half2 lo2 = __hmin2_nan(__hmin2_nan(h2[0], h2[1]), __hmin2_nan(h2[2], h2[3]));
-      __half2 hi2 = __hmax2_nan(__hmax2_nan(h2[0], h2[1]), __hmax2_nan(h2[2], h2[3]));
-      // lowest and (negated) highest side by side: one shuffle a step
-      __half2 both = __halves2half2(__hmin_nan(__low2half(lo2), __high2half(lo2)),
-                                    __hneg(__hmax_nan(__low2half(hi2), __high2half(hi2))));
+      const __half2* h0 = reinterpret_cast<const __half2*>(&x0);
+      const __half2* h1 = reinterpret_cast<const __half2*>(&x1);
+      __half2 lo2 = h0[0], hi2 = h0[0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) {
+        lo2 = __hmin2_nan(lo2, e < 4 ? h0[e] : h1[e - 4]);
+        hi2 = __hmax2_nan(hi2, e < 4 ? h0[e] : h1[e - 4]);
+      }
+      // lowest and negated highest side by side: one shuffle a step
+      __half2 both = __hmin2_nan(__lows2half2(lo2, __hneg2(hi2)), __highs2half2(lo2, __hneg2(hi2)));
 #pragma unroll
       for (int o = LPR / 2; o > 0; o /= 2) both = __hmin2_nan(both, __shfl_xor_sync(0xffffffffu, both, o));
-      const __half lo_h = __low2half(both);
-      const float lo = __half2float(lo_h), hi = -__half2float(__high2half(both));
-      __half s_h = __float2half_rn(__fdiv_rn(hi - lo, 15.f));
+      const float lo = __low2float(both), span = -__high2float(both) - lo;
+      // span / 15 correctly rounded: one step of Markstein's division by a constant
+      constexpr float kFifteenth = 1.f / 15.f;
+      const float s0 = span * kFifteenth;
+      __half s_h = __float2half_rn(fmaf(fmaf(-s0, 15.f, span), kFifteenth, s0));
       const float s = __half2float(s_h);
       if (!(s <= 65504.f)) s_h = __ushort_as_half(0x7fff);   // a row that is not finite stands for NaNs
-      const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-      // d / s to the nearest whole number: adding 1.5 * 2^23 rounds u = d * inv there.  u is within
-      // 2^-18 of the quotient, so only a fraction that close to one half (or a quotient past 15,
-      // where a scale below 2^-14 was rounded) needs the exact rule.
-      constexpr float kMagic = 12582912.f;
-      float d[8];
-      unsigned word = 0;
-      float far = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(h2[e]);
-        d[2 * e] = f.x - lo;
-        d[2 * e + 1] = f.y - lo;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = d[i] * inv;
-        const float m = v + kMagic;
-        far = fmaxf(far, fabsf(v - (m - kMagic)));
-        word += __float_as_uint(m) << (4 * i);
-      }
-      // the whole numbers sit in the low bits of 0x4B400000 + n: take the constants' sum off
-      constexpr unsigned kOnes = 0x11111111u;
-      word -= 0x4B400000u * kOnes;
-      if (far >= 0.5f - 0x1p-18f || (hi - lo) * inv > 15.25f) {
-        word = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) word |= s > 0.f ? nearest_exact(d[i], s, rintf(d[i] * inv)) << (4 * i) : 0u;
-      }
+      const float inv = s > 0.f ? rcp_approx(s) : 0.f;
+      const float b = -lo * inv;
+      const float sure = 0.5f - 0x1p-17f - fabsf(b) * 0x1p-22f;
+      const bool past = span * inv > 15.25f;        // only where a scale below 2^-14 was rounded down
+      const unsigned w0 = pack8(x0, inv, b, lo, s, sure, past), w1 = pack8(x1, inv, b, lo, s, sure, past);
       if (r < end) {
-        uint8_t* tile = (r < H ? p.k_cache : p.v_cache) + block_base + static_cast<int64_t>(r < H ? r : r - H) * p.tile_bytes;
-        *reinterpret_cast<unsigned*>(tile + data_off) = word;
-        if (c == 0) *reinterpret_cast<__half2*>(tile + meta_off) = __halves2half2(s_h, lo_h);
+        uint8_t* tile = (r < H ? k_block : v_block) + static_cast<int64_t>(r) * p.tile_bytes;
+        *reinterpret_cast<unsigned*>(tile + data_off) = w0;
+        *reinterpret_cast<unsigned*>(tile + data_off + D / 4) = w1;
+        if (c == 0) *reinterpret_cast<__half2*>(tile + meta_off) = __halves2half2(s_h, __low2half(both));
       }
     }
   }
 }
 
-// grid (tokens, parts of a token's K and V rows)
+// Eight values of a row: 1024 + n has n in its low bits in fp16, and the fused product rounds
+// zero + scale * n once.
+__device__ __forceinline__ uint4 unpack8(unsigned word, __half2 s2, __half2 z2) {
+  unsigned pair[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned bits = ((word >> (4 * i)) & 0x000f000fu) | 0x64006400u;      // values i and i + 4
+    const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&bits), __float2half2_rn(1024.f));
+    const __half2 y = __hfma2(n, s2, z2);
+    pair[i] = *reinterpret_cast<const unsigned*>(&y);
+  }
+  return make_uint4(__byte_perm(pair[0], pair[1], 0x5410), __byte_perm(pair[2], pair[3], 0x5410),
+                    __byte_perm(pair[0], pair[1], 0x7632), __byte_perm(pair[2], pair[3], 0x7632));
+}
+
+// grid (tokens / kWarps, parts of a token's K and V rows)
 template <int D>
-__global__ void __launch_bounds__(kThreads) gather_cache_int4_kernel(const Int4RowParams p) {
-  constexpr int LPR = D / 8;
-  constexpr int RPP = kThreads / LPR;
-  constexpr int U = 5;                              // rows a lane has in flight together
+__global__ void __launch_bounds__(kWarps * 32) gather_cache_int4_kernel(const Int4RowParams p) {
+  constexpr int LPR = D / 16;
+  constexpr int RPP = 32 / LPR;
+  constexpr int U = 4;                              // rows a lane has in flight together
   pkv::pdl_trigger();
   pkv::pdl_wait();
-  const int t = blockIdx.x;
-  const int tid = threadIdx.x, c = tid % LPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR;
+  const int t = blockIdx.x * kWarps + warp;
+  if (t >= p.num_tokens) return;
   const int H = p.num_heads;
-  const int begin = blockIdx.y * p.rows_per_cta, end = min(2 * H, begin + p.rows_per_cta);
+  const int begin = blockIdx.y * p.rows_per_warp, end = min(2 * H, begin + p.rows_per_warp);
   const int64_t slot = p.slots[t];
   if (slot < 0) return;
   if (slot >= p.num_slots) {
-    if (tid == 0 && blockIdx.y == 0) record_error(PKV_DEV_BAD_SLOT);
+    if (lane == 0 && blockIdx.y == 0) record_error(PKV_DEV_BAD_SLOT);
     return;
   }
-  const int64_t blk = slot >> p.log2_block;
   const int in_block = static_cast<int>(slot & ((1 << p.log2_block) - 1));
-  const int64_t block_base = blk * H * p.tile_bytes;
+  const int64_t block_base = (slot >> p.log2_block) * H * p.tile_bytes;
+  const uint8_t* k_block = p.k_cache + block_base;
+  const uint8_t* v_block = p.v_cache + block_base - static_cast<int64_t>(H) * p.tile_bytes;
   const int data_off = in_block * (D / 2) + c * 4;
   const int meta_off = ((D / 2) << p.log2_block) + in_block * 4;
-  for (int row = begin + tid / LPR; row < end; row += U * RPP) {
-    unsigned word[U];
+  __half* key = p.key_out + static_cast<int64_t>(t) * H * D + c * 8;
+  __half* value = p.value_out + static_cast<int64_t>(t) * H * D + c * 8 - static_cast<int64_t>(H) * D;
+  for (int row = begin + lane / LPR; row < end; row += U * RPP) {
+    unsigned word[U][2];
     __half2 meta[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = row + u * RPP;
       if (r < end) {
-        const uint8_t* tile = (r < H ? p.k_cache : p.v_cache) + block_base + static_cast<int64_t>(r < H ? r : r - H) * p.tile_bytes;
-        word[u] = *reinterpret_cast<const unsigned*>(tile + data_off);
+        const uint8_t* tile = (r < H ? k_block : v_block) + static_cast<int64_t>(r) * p.tile_bytes;
+        word[u][0] = *reinterpret_cast<const unsigned*>(tile + data_off);
+        word[u][1] = *reinterpret_cast<const unsigned*>(tile + data_off + D / 4);
         meta[u] = *reinterpret_cast<const __half2*>(tile + meta_off);
       }
     }
@@ -179,23 +251,9 @@ __global__ void __launch_bounds__(kThreads) gather_cache_int4_kernel(const Int4R
       const int r = row + u * RPP;
       if (r < end) {
         const __half2 s2 = __low2half2(meta[u]), z2 = __high2half2(meta[u]);
-        uint4 out;
-        unsigned* o = reinterpret_cast<unsigned*>(&out);
-        unsigned pair[4];
-        // 1024 + n has n in its low bits in fp16; the fused product rounds zero + scale * n once
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const unsigned bits = ((word[u] >> (4 * i)) & 0x000f000fu) | 0x64006400u;      // values i and i + 4
-          const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&bits), __float2half2_rn(1024.f));
-          const __half2 y = __hfma2(n, s2, z2);
-          pair[i] = *reinterpret_cast<const unsigned*>(&y);
-        }
-        o[0] = __byte_perm(pair[0], pair[1], 0x5410);
-        o[1] = __byte_perm(pair[2], pair[3], 0x5410);
-        o[2] = __byte_perm(pair[0], pair[1], 0x7632);
-        o[3] = __byte_perm(pair[2], pair[3], 0x7632);
-        __half* dst = (r < H ? p.key_out : p.value_out) + (static_cast<int64_t>(t) * H + (r < H ? r : r - H)) * D + c * 8;
-        *reinterpret_cast<uint4*>(dst) = out;
+        __half* dst = (r < H ? key : value) + r * D;
+        *reinterpret_cast<uint4*>(dst) = unpack8(word[u][0], s2, z2);
+        *reinterpret_cast<uint4*>(dst + D / 2) = unpack8(word[u][1], s2, z2);
       }
     }
   }
@@ -215,7 +273,7 @@ int check_shape(const char* fn, int num_tokens, int num_heads, int head_dim, int
   return PKV_OK;
 }
 
-// One CTA per token; with few tokens a token's 2 H rows are split over CTAs.
+// A warp per token; where that leaves SMs short of warps, a token's 2 H rows are split.
 template <typename Kernel>
 int launch_rows(const char* fn, Kernel k64, Kernel k128, Int4RowParams p, int num_tokens, int head_dim, int block_size,
                 int num_blocks, void* stream) {
@@ -224,13 +282,14 @@ int launch_rows(const char* fn, Kernel k64, Kernel k128, Int4RowParams p, int nu
   p.log2_block = lb;
   p.tile_bytes = block_size * (head_dim / 2 + 4);
   p.num_slots = static_cast<int64_t>(num_blocks) * block_size;
-  const int rpp = kThreads / (head_dim / 8), passes = (2 * p.num_heads + rpp - 1) / rpp;
-  int splits = num_tokens >= 1024 ? 1 : (1024 + num_tokens - 1) / num_tokens;
+  p.num_tokens = num_tokens;
+  const int rpp = 512 / head_dim, passes = (2 * p.num_heads + rpp - 1) / rpp;
+  int splits = num_tokens >= pkv::kFullWarps ? 1 : (pkv::kFullWarps + num_tokens - 1) / num_tokens;
   if (splits > passes) splits = passes;
   const int per = (passes + splits - 1) / splits;
-  p.rows_per_cta = per * rpp;
-  const dim3 grid(num_tokens, (passes + per - 1) / per);
-  cudaError_t e = pkv::launch_pdl(head_dim == 128 ? k128 : k64, grid, dim3(kThreads), 0,
+  p.rows_per_warp = per * rpp;
+  const dim3 grid((num_tokens - 1) / kWarps + 1, (passes + per - 1) / per);
+  cudaError_t e = pkv::launch_pdl(head_dim == 128 ? k128 : k64, grid, dim3(kWarps * 32), 0,
                                   static_cast<cudaStream_t>(stream), p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));

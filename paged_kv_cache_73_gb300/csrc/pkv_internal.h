@@ -34,6 +34,10 @@ int read_device_error_prompt(int reset, int* code);
 // 1024-token prefix: 4 members break even, 8 are 1.4x faster, 64 are 1.9x.
 constexpr int kMinSharedGroup = 8;
 
+// Warps that fill the GPU (152 SMs x 16): the kernels that give a warp a token's rows split the rows
+// of a token over warps until there are this many.
+constexpr int kFullWarps = 2432;
+
 // Shared-prefix partials (prefill.cu, tensor cores): for every member s of every group g and every
 // head h, the partial (max m and sum l in the base-2 log domain of scale * q.k, unnormalised
 // output o) of q[s, h] over the keys [0, prefix_lens[g]) read through block_tables row

@@ -10,15 +10,17 @@
 // HBM-bound: each value is read once and written once, 8 flops between, so the
 // kernel is 16-byte loads, a reduction over the lanes that hold a head, and
 // 16-byte stores.
-//  * One CTA takes one token (or a part of its heads, where there are few tokens):
-//    the R/2 sines and cosines are computed once in shared memory and used by all
-//    of its heads.
+//  * One warp takes one token (or a part of its heads, where there are few tokens): it
+//    computes the token's R/2 sines and cosines once, two a lane, and uses them for all
+//    of its heads.  No CTA barrier: warps run free of one another.
 //  * The angle is computed in whole numbers: f is given in units of 2^-64 turns, so
 //    position * f wraps modulo one turn by itself, exactly, however far the
 //    position; its top 32 bits then go to sincospif.  A product in fp32 would be off
 //    by whole radians at position 10^6 and beyond.
-//  * D/8 lanes hold a row, 8 values each, so a pair's two halves (R/2 apart) are in
-//    two lanes: one shuffle exchanges them.
+//  * D/16 lanes hold a row, each eight pairs: eight first values and their eight second
+//    values, R/2 further on (or interleaved with them).  No shuffle is needed to turn
+//    them, and weights times sines are formed once per token, so a pair takes four fused
+//    operations (two to an instruction) and the product with the norm.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -33,7 +35,7 @@ namespace {
 __device__ int g_dev_error_rope = 0;
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_rope, 0, code); }
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8;            // per CTA
 constexpr int kMaxAxes = 8;
 
 struct RopeParams {
@@ -48,120 +50,179 @@ struct RopeParams {
   __half* k_out;
   int64_t q_stride, k_stride, q_out_stride, k_out_stride;
   int num_axes, rotary_dim, num_tokens, num_heads, num_kv_heads;
-  int rows_per_cta;
+  int rows_per_warp;
   float eps;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& raw, float (&x)[8]) {
-  const __half2* h2 = reinterpret_cast<const __half2*>(&raw);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = __half22float2(h2[e]);
-    x[2 * e] = f.x;
-    x[2 * e + 1] = f.y;
-  }
+// two fp32 products, sums or fused products in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
 
-// grid (tokens, parts of a token's query and key heads)
+// grid (tokens / kWarps, parts of a token's query and key heads)
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeParams p) {
-  constexpr int LPR = D / 8;                        // lanes per row
-  constexpr int RPP = kThreads / LPR;               // rows per pass
-  constexpr int U = 3;                              // passes whose loads are in flight together
-  __shared__ float2 turn[D / 2];                    // (cos, sin) of each pair
+__global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const RopeParams p) {
+  constexpr int LPR = D / 16;                       // lanes per row
+  constexpr int RPP = 32 / LPR;                     // rows a warp takes at a time
+  constexpr int PF = 2;                             // of which so many are in flight
+  __shared__ __align__(16) float cos_of[kWarps][D / 2], sin_of[kWarps][D / 2];
   pkv::pdl_trigger();
   pkv::pdl_wait();
-  const int t = blockIdx.x;
-  const int tid = threadIdx.x, c = tid % LPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR;
+  const int t = blockIdx.x * kWarps + warp;
+  if (t >= p.num_tokens) return;
   const int total = p.num_heads + p.num_kv_heads;
-  const int begin = blockIdx.y * p.rows_per_cta, end = min(total, begin + p.rows_per_cta);
-  auto load = [&](int row) {
-    return row >= end ? make_uint4(0, 0, 0, 0)
-           : row < p.num_heads
-               ? *reinterpret_cast<const uint4*>(p.q + t * p.q_stride + row * D + c * 8)
-               : *reinterpret_cast<const uint4*>(p.k + t * p.k_stride + (row - p.num_heads) * D + c * 8);
+  const int begin = blockIdx.y * p.rows_per_warp, end = min(total, begin + p.rows_per_warp);
+  // this lane's values of a row: eight from first_off and eight from second_off.  The lanes past the
+  // turned ones hold 16 values in a row as they are.
+  const int turned_lanes = p.rotary_dim / 16;
+  const bool turned = c < turned_lanes;
+  const int first_off = INTERLEAVED || !turned ? c * 16 : c * 8;
+  const int second_off = INTERLEAVED || !turned ? c * 16 + 8 : c * 8 + p.rotary_dim / 2;
+  const __half* q = p.q + t * p.q_stride;
+  const __half* k = p.k + t * p.k_stride - static_cast<int64_t>(p.num_heads) * D;
+  __half* q_out = p.q_out + t * p.q_out_stride;
+  __half* k_out = p.k_out + t * p.k_out_stride - static_cast<int64_t>(p.num_heads) * D;
+  uint4 raw[PF][2];
+  auto load = [&](int r, uint4 (&x)[2]) {
+    if (r < end) {
+      const __half* src = (r < p.num_heads ? q : k) + r * D;
+      x[0] = *reinterpret_cast<const uint4*>(src + first_off);
+      x[1] = *reinterpret_cast<const uint4*>(src + second_off);
+    } else {
+      x[0] = x[1] = make_uint4(0, 0, 0, 0);
+    }
   };
-  const int first = begin + tid / LPR;
-  uint4 raw[U];
+  const int sub = lane / LPR;
 #pragma unroll
-  for (int u = 0; u < U; ++u) raw[u] = load(first + u * RPP);
-  if (tid < p.rotary_dim / 2) {
-    const int axis = p.pair_axis == nullptr ? 0 : p.pair_axis[tid];
+  for (int u = 0; u < PF; ++u) load(begin + u * RPP + sub, raw[u]);
+
+  for (int pair = lane; pair < p.rotary_dim / 2; pair += 32) {
+    const int axis = p.pair_axis == nullptr ? 0 : p.pair_axis[pair];
     float cs = 1.f, sn = 0.f;
     if (axis >= 0 && axis < p.num_axes) {
       const int64_t pos = p.positions[static_cast<int64_t>(axis) * p.num_tokens + t];
-      // turns modulo one in [-1/2, 1/2), as a signed 64-bit fraction; its top 32 bits are 2^-32 turns
-      const uint64_t turns = static_cast<uint64_t>(pos) * static_cast<uint64_t>(p.frequencies[tid]);
-      const float half_turns = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f;
-      sincospif(half_turns, &sn, &cs);
+      // turns modulo one as a signed 64-bit fraction: the top 32 bits are 2^-32 turns in [-1/2, 1/2)
+      const uint64_t turns = static_cast<uint64_t>(pos) * static_cast<uint64_t>(p.frequencies[pair]);
+      sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f, &sn, &cs);
     } else if (blockIdx.y == 0) {
       record_error(PKV_DEV_BAD_AXIS);
     }
-    turn[tid] = make_float2(cs, sn);
+    cos_of[warp][pair] = cs;
+    sin_of[warp][pair] = sn;
   }
-  float wq[8], wk[8];
-  const bool norm_q = p.q_weight != nullptr, norm_k = p.k_weight != nullptr;
-  unpack8(norm_q ? *reinterpret_cast<const uint4*>(p.q_weight + c * 8) : make_uint4(0, 0, 0, 0), wq);
-  unpack8(norm_k ? *reinterpret_cast<const uint4*>(p.k_weight + c * 8) : make_uint4(0, 0, 0, 0), wk);
-  __syncthreads();
-  // this lane's turns: of its 8 values' pairs (half layout), or of its 4 pairs (interleaved)
-  constexpr int NT = INTERLEAVED ? 4 : 8;
-  const int lanes = p.rotary_dim / 8;               // lanes that hold turned values
-  const bool turned = c < lanes;
-  const bool upper = c >= lanes / 2;                // half layout: this lane holds the pairs' second values
-  float2 cs[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int pair = INTERLEAVED ? c * 4 + i : (upper ? c - lanes / 2 : c) * 8 + i;
-    cs[i] = turned ? turn[pair] : make_float2(1.f, 0.f);
-  }
-  // half layout: the lane that holds the other values of this lane's pairs
-  const int lane = tid & 31;
-  const int other = !turned ? lane : upper ? lane - lanes / 2 : lane + lanes / 2;
+  __syncwarp();
 
-  // whole passes, so that every lane of a warp takes part in the shuffles
-  for (int row = first; row - tid / LPR < end; row += U * RPP) {
+  // the query rows, then the key rows: each with its weight folded into the turn
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int r1 = part == 0 ? min(end, p.num_heads) : end;
+    const int r0 = part == 0 ? begin : max(begin, p.num_heads);
+    if (r0 >= r1) continue;
+    const __half* weight = part == 0 ? p.q_weight : p.k_weight;
+    // first  <- first * fc - second * fs,   second <- second * sc + first * ss   (two pairs a register pair)
+    float2 fc[4], fs[4], sc[4], ss[4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = row + u * RPP;
-      const bool is_q = r < p.num_heads;
-      float x[8];
-      unpack8(raw[u], x);
-      raw[u] = load(r + U * RPP);
-      if (is_q ? norm_q : norm_k) {
-        float ss = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      float w1[2] = {1.f, 1.f}, w2[2] = {1.f, 1.f};
+      if (weight != nullptr) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-        const unsigned row_lanes = (LPR == 16 ? 0xffffu : 0xffu) << (lane & ~(LPR - 1));
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o /= 2) ss += __shfl_xor_sync(row_lanes, ss, o);
-        const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= inv * (is_q ? wq[i] : wk[i]);
+        for (int j = 0; j < 2; ++j) {
+          const int e = 2 * i + j;
+          w1[j] = __half2float(weight[INTERLEAVED && turned ? c * 16 + 2 * e : first_off + e]);
+          w2[j] = __half2float(weight[INTERLEAVED && turned ? c * 16 + 2 * e + 1 : second_off + e]);
+        }
       }
-      float y[8];
-      if constexpr (INTERLEAVED) {
+      float2 cs = make_float2(1.f, 1.f), sn = make_float2(0.f, 0.f);
+      if (turned) {
+        cs = *reinterpret_cast<const float2*>(&cos_of[warp][c * 8 + 2 * i]);
+        sn = *reinterpret_cast<const float2*>(&sin_of[warp][c * 8 + 2 * i]);
+      }
+      fc[i] = make_float2(w1[0] * cs.x, w1[1] * cs.y);
+      fs[i] = make_float2(-w2[0] * sn.x, -w2[1] * sn.y);
+      sc[i] = make_float2(w2[0] * cs.x, w2[1] * cs.y);
+      ss[i] = make_float2(w1[0] * sn.x, w1[1] * sn.y);
+    }
+    __half* dst_base = part == 0 ? q_out : k_out;
+    // the prefetched rows run on from the query rows into the key rows only where a pass ends there:
+    // otherwise the key rows start anew
+    if (part == 1 && begin < p.num_heads) {
+#pragma unroll
+      for (int u = 0; u < PF; ++u) load(r0 + u * RPP + sub, raw[u]);
+    }
+    for (int row = r0; row < r1; row += PF * RPP) {
+#pragma unroll
+      for (int u = 0; u < PF; ++u) {
+        const int r = row + u * RPP + sub;
+        float2 a[4], b[4];
+        {
+          const __half2* h0 = reinterpret_cast<const __half2*>(&raw[u][0]);
+          const __half2* h1 = reinterpret_cast<const __half2*>(&raw[u][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (INTERLEAVED && turned) {
+              // pairs lie side by side: (a0 b0 a1 b1 ..)
+              const __half2* h = i < 2 ? h0 : h1;
+              const float2 x = __half22float2(h[2 * (i & 1)]), y = __half22float2(h[2 * (i & 1) + 1]);
+              a[i] = make_float2(x.x, y.x);
+              b[i] = make_float2(x.y, y.y);
+            } else {
+              a[i] = __half22float2(h0[i]);
+              b[i] = __half22float2(h1[i]);
+            }
+          }
+        }
+        load(r + PF * RPP, raw[u]);
+        float inv = 1.f;
+        if (weight != nullptr) {
+          float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s2 = fma2(b[i], b[i], fma2(a[i], a[i], s2));
+          float s = s2.x + s2.y;
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+          inv = rsqrtf(s * (1.f / D) + p.eps);
+        }
+        const float2 inv2 = make_float2(inv, inv);
+        uint4 w[2];
+        __half2* o0 = reinterpret_cast<__half2*>(&w[0]);
+        __half2* o1 = reinterpret_cast<__half2*>(&w[1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          y[2 * i] = turned ? x[2 * i] * cs[i].x - x[2 * i + 1] * cs[i].y : x[2 * i];
-          y[2 * i + 1] = turned ? x[2 * i + 1] * cs[i].x + x[2 * i] * cs[i].y : x[2 * i + 1];
+          float2 x = mul2(a[i], fc[i]), y = mul2(b[i], sc[i]);
+          if (turned) {
+            x = fma2(b[i], fs[i], x);
+            y = fma2(a[i], ss[i], y);
+          }
+          x = mul2(x, inv2);
+          y = mul2(y, inv2);
+          if (INTERLEAVED && turned) {
+            __half2* o = i < 2 ? o0 : o1;
+            o[2 * (i & 1)] = __floats2half2_rn(x.x, y.x);
+            o[2 * (i & 1) + 1] = __floats2half2_rn(x.y, y.y);
+          } else {
+            o0[i] = __floats2half2_rn(x.x, x.y);
+            o1[i] = __floats2half2_rn(y.x, y.y);
+          }
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = __shfl_sync(0xffffffffu, x[i], other);
-          const float turned_x = upper ? x[i] * cs[i].x + o * cs[i].y : x[i] * cs[i].x - o * cs[i].y;
-          y[i] = turned ? turned_x : x[i];
+        if (r < r1) {
+          __half* dst = dst_base + r * D;
+          *reinterpret_cast<uint4*>(dst + first_off) = w[0];
+          *reinterpret_cast<uint4*>(dst + second_off) = w[1];
         }
-      }
-      if (r < end) {
-        uint4 w;
-        __half2* h2 = reinterpret_cast<__half2*>(&w);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h2[e] = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
-        __half* dst = is_q ? p.q_out + t * p.q_out_stride + r * D
-                           : p.k_out + t * p.k_out_stride + (r - p.num_heads) * D;
-        *reinterpret_cast<uint4*>(dst + c * 8) = w;
       }
     }
   }
@@ -169,8 +230,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeParams
 
 template <int D>
 cudaError_t launch_rope(const RopeParams& p, bool interleaved, dim3 grid, cudaStream_t st) {
-  return interleaved ? pkv::launch_pdl(qk_norm_rope_kernel<D, true>, grid, dim3(kThreads), 0, st, p)
-                     : pkv::launch_pdl(qk_norm_rope_kernel<D, false>, grid, dim3(kThreads), 0, st, p);
+  return interleaved ? pkv::launch_pdl(qk_norm_rope_kernel<D, true>, grid, dim3(kWarps * 32), 0, st, p)
+                     : pkv::launch_pdl(qk_norm_rope_kernel<D, false>, grid, dim3(kWarps * 32), 0, st, p);
 }
 
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
@@ -246,14 +307,13 @@ int pkv_qk_norm_rope(const uint16_t* q, const uint16_t* key, const uint16_t* q_w
   p.num_heads = num_heads;
   p.num_kv_heads = num_kv_heads;
   p.eps = eps;
-  // one CTA per token; with too few tokens to give every SM a few CTAs, a token's heads are split
-  const int rpp = kThreads / (head_dim / 8), rows = num_heads + num_kv_heads;
-  const int passes = (rows + rpp - 1) / rpp;
-  int splits = num_tokens >= 1024 ? 1 : (1024 + num_tokens - 1) / num_tokens;
+  // a warp per token; where that leaves SMs short of warps, a token's heads are split
+  const int rpp = 512 / head_dim, rows = num_heads + num_kv_heads, passes = (rows + rpp - 1) / rpp;
+  int splits = num_tokens >= pkv::kFullWarps ? 1 : (pkv::kFullWarps + num_tokens - 1) / num_tokens;
   if (splits > passes) splits = passes;
   const int per = (passes + splits - 1) / splits;
-  p.rows_per_cta = per * rpp;
-  const dim3 grid(num_tokens, (passes + per - 1) / per);
+  p.rows_per_warp = per * rpp;
+  const dim3 grid((num_tokens - 1) / kWarps + 1, (passes + per - 1) / per);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = head_dim == 128 ? launch_rope<128>(p, interleaved != 0, grid, st)
                                   : launch_rope<64>(p, interleaved != 0, grid, st);
