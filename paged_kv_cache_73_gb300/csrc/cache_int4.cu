@@ -26,7 +26,7 @@ namespace {
 __device__ int g_dev_error_cache_int4 = 0;
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_cache_int4, 0, code); }
 
-constexpr int kWarps = 8;            // per CTA
+constexpr int kWarps = 4;            // per CTA
 
 struct Int4RowParams {
   const __half* key;
@@ -112,7 +112,7 @@ __device__ __forceinline__ unsigned pack8(const uint4& raw, float inv, float b, 
 
 // grid (tokens / kWarps, parts of a token's K and V rows)
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) reshape_and_cache_int4_kernel(const Int4RowParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 7) reshape_and_cache_int4_kernel(const Int4RowParams p) {
   constexpr int LPR = D / 16;                       // lanes per row
   constexpr int RPP = 32 / LPR;                     // rows a warp takes at a time
   constexpr int PF = 2;                             // of which so many are in flight
@@ -211,7 +211,7 @@ template <int D>
 __global__ void __launch_bounds__(kWarps * 32) gather_cache_int4_kernel(const Int4RowParams p) {
   constexpr int LPR = D / 16;
   constexpr int RPP = 32 / LPR;
-  constexpr int U = 4;                              // rows a lane has in flight together
+  constexpr int U = 5;                              // rows a lane has in flight together
   pkv::pdl_trigger();
   pkv::pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR;

@@ -35,7 +35,7 @@ namespace {
 __device__ int g_dev_error_rope = 0;
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_rope, 0, code); }
 
-constexpr int kWarps = 8;            // per CTA
+constexpr int kWarps = 4;            // per CTA
 constexpr int kMaxAxes = 8;
 
 struct RopeParams {
@@ -74,7 +74,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 
 // grid (tokens / kWarps, parts of a token's query and key heads)
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, INTERLEAVED ? 4 : 6) qk_norm_rope_kernel(const RopeParams p) {
   constexpr int LPR = D / 16;                       // lanes per row
   constexpr int RPP = 32 / LPR;                     // rows a warp takes at a time
   constexpr int PF = 2;                             // of which so many are in flight
