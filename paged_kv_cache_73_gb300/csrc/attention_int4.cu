@@ -29,12 +29,16 @@
 // Softmax in base 2 with a running maximum that moves only when a chunk raises it by
 // more than 2^8.  The weight that multiplies V's whole numbers is u_t = p_t s_t, rounded
 // to fp16; the maximum is kept over x_t + log2 of s_t's exponent, so that u is at most
-// 2^9 and its greatest is a normal number whatever the rows' scales.  The rounding error
-// of u times 8 is put back in fp32 (sum of p z + 8 (u - fp16(u))), so a weight's error
-// meets n - 8 and not n.
+// 2^9 and its greatest is a normal number whatever the rows' scales.  With u' = fp16(u),
+//   sum p (s n + z) = sum u' (n - 8) + sum p (z + 8 s) + (rounding of u) (n - 8):
+// the second sum is fp32, and sum u' comes from one more product, with ones, so that a
+// weight's rounding meets n - 8 and not n.
 //
-// The context is split over CTAs and over a CTA's warps, joined by the log-sum-exp
-// identity (second kernel for the CTAs' parts).
+// Each warp streams its own tokens, 32 at a time, through a ring in shared memory by
+// 16-byte cp.async: rows of any block size land in the same place, and V's rows XOR-ed so
+// that four tokens' words are read without bank conflicts.  The context is split over CTAs
+// and over a CTA's warps, joined by the log-sum-exp identity (second kernel for the CTAs'
+// parts).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -50,6 +54,9 @@ namespace {
 __device__ int g_dev_error_attention_int4 = 0;
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_attention_int4, 0, code); }
 
+#ifndef V_MINB
+#define V_MINB 3
+#endif
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int NW = 4;                 // warps per CTA
 constexpr int CHUNK = 32;             // tokens a warp handles at a time
@@ -93,9 +100,21 @@ __device__ __forceinline__ unsigned pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const unsigned*>(&h);
 }
-// exponent of a scale (a non-negative fp16 number as fp32); that of the smallest fp16 for zero
-__device__ __forceinline__ float exponent_of(float s) {
-  return static_cast<float>(max(static_cast<int>(__float_as_uint(s) >> 23) - 127, -24));
+// log2 of a scale (a non-negative fp16 number), that of the smallest fp16 for zero; it only places
+// the running maximum
+__device__ __forceinline__ float log2_of(float s) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+  return fmaxf(y, -24.f);
+}
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 template <int W>
 __device__ __forceinline__ void load_words(unsigned (&w)[W], const uint8_t* src) {
@@ -110,23 +129,166 @@ __device__ __forceinline__ void load_words(unsigned (&w)[W], const uint8_t* src)
   }
 }
 
-// A warp's running softmax over its tokens for HT = 8 NT heads; lane (g, t) holds heads 8 n + 2t,
+#ifndef V_NST
+#define V_NST 4
+#endif
+// A ring stage: 32 tokens' K rows, V rows (XOR-ed), K and V (scale, zero) pairs.
+template <int D>
+struct Ring {
+  static constexpr int ROW = D / 2;                 // bytes of a row's values
+  static constexpr int V_OFF = CHUNK * ROW;
+  static constexpr int META_OFF = 2 * CHUNK * ROW;
+  static constexpr int STAGE = META_OFF + 2 * CHUNK * 4;
+  static constexpr int NST = V_NST;
+  static constexpr int WARP = NST * STAGE;          // a warp's ring
+};
+// Byte offset of 16-byte chunk c of V row r within a stage's V rows: in each 128-byte line (2 or 4
+// rows) the chunk's place is XOR-ed with twice the line's number mod 4, so the eight lanes that read
+// rows 2t or 2t + 1 of one chunk pair, t = 0..3, reach different banks.
+template <int D>
+__device__ __forceinline__ int v_place(int r, int c) {
+  const int lin = r * (D / 32) + c, line = lin >> 3;
+  return line * 128 + (((lin & 7) ^ ((line & 3) << 1)) << 4);
+}
+
+// A warp's running softmax over its tokens for 8 NT heads; lane (g, t) holds heads 8 n + 2t,
 // 8 n + 2t + 1.
 template <int D, int NT>
 struct WarpState {
   float m[NT][2], l[NT][2], c[NT][2];   // l and c: this lane's tokens only, until the end
-  float acc[NT][D / 16][4];
+  float acc[NT][D / 16][4];             // sum u' n: {even value, heads 2t, 2t + 1; odd value x 16, the same}
+  float ones[NT][4];                    // sum u'
 };
+
+// One chunk of `valid` tokens (all 32 unless MASKED) staged at `stage`.
+template <int D, int NT, bool MASKED>
+__device__ __forceinline__ void chunk_update(const unsigned char* stage, int valid, const unsigned (&qf)[NT][D / 16][2],
+                                             const float (&ca)[NT][2], const float (&cb)[NT][2], WarpState<D, NT>& st,
+                                             int g, int t, const int (&v_off)[4]) {
+  using R = Ring<D>;
+  constexpr int WK = D / 32;            // words of a K row per lane
+  constexpr int WV = D / 64;            // words of a V row per lane
+  float x[NT][2][4];                    // tile i, {token g: heads 2t, 2t + 1; token g + 8: the same}
+  float2 vm[2][2];                      // V's scale and zero + 8 scale of those tokens
+  float top[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    unsigned ka[WK], kb[WK];
+    load_words<WK>(ka, stage + (16 * i + g) * R::ROW + t * (D / 8));
+    load_words<WK>(kb, stage + (16 * i + g + 8) * R::ROW + t * (D / 8));
+    float dot[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) dot[n][0] = dot[n][1] = dot[n][2] = dot[n][3] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const unsigned a = ka[w] >> (8 * half), b = kb[w] >> (8 * half);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          mma16816(dot[n], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qf[n][2 * w + half][0],
+                   qf[n][2 * w + half][1]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = 16 * i + g + 8 * r;
+      const bool live = !MASKED || row < valid;
+      const float2 km = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + row * 4));
+      vm[i][r] = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + CHUNK * 4 + row * 4));
+      if (!live) vm[i][r] = make_float2(0.f, 0.f);
+      const float e = log2_of(vm[i][r].x);
+      vm[i][r].y = fmaf(8.f, vm[i][r].x, vm[i][r].y);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float y = fmaf(km.x, ca[n][j] * dot[n][2 * r + j], km.y * cb[n][j]);
+          x[n][i][2 * r + j] = live ? y : -INFINITY;
+          top[n][j] = fmaxf(top[n][j], x[n][i][2 * r + j] + e);
+        }
+    }
+  }
+  bool moves = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int o = 4; o < 32; o *= 2) top[n][j] = fmaxf(top[n][j], __shfl_xor_sync(FULL, top[n][j], o));
+      moves |= top[n][j] > st.m[n][j] + kRescale;
+    }
+  if (__any_sync(FULL, moves)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float m = fmaxf(st.m[n][j], top[n][j]);
+        const float f = m == -INFINITY ? 1.f : exp2f(st.m[n][j] - m);
+        st.m[n][j] = m;
+        st.l[n][j] *= f;
+        st.c[n][j] *= f;
+        st.ones[n][j] *= f;
+        st.ones[n][2 + j] *= f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          st.acc[n][i][j] *= f;
+          st.acc[n][i][2 + j] *= f;
+        }
+      }
+  }
+  unsigned pb[NT][2][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float u[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          // the chunk has a valid token, so the maximum is not -inf (a NaN logit makes NaNs)
+          const float w = fast_exp2(x[n][i][2 * r + j] - st.m[n][j]);
+          st.l[n][j] += w;
+          u[j] = w * vm[i][r].x;
+          st.c[n][j] = fmaf(w, vm[i][r].y, st.c[n][j]);
+        }
+        pb[n][i][r] = transpose8x8(pack2(u[0], u[1]));
+      }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    unsigned va[4][WV];                 // tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the tile
+#pragma unroll
+    for (int r = 0; r < 4; ++r) load_words<WV>(va[r], stage + R::V_OFF + v_off[r] + i * 16 * R::ROW);
+#pragma unroll
+    for (int w = 0; w < WV; ++w)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const unsigned sel = 0x4400u + 0x1111u * b;          // byte b of the first token, byte b of the second
+        const unsigned e = __byte_perm(va[0][w], va[1][w], sel), f = __byte_perm(va[2][w], va[3][w], sel);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          mma16816(st.acc[n][4 * w + b], e & 0x000f000fu, e & 0x00f000f0u, f & 0x000f000fu, f & 0x00f000f0u, pb[n][i][0],
+                   pb[n][i][1]);
+      }
+    constexpr unsigned kOne2 = 0x3c003c00u;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mma16816(st.ones[n], kOne2, kOne2, kOne2, kOne2, pb[n][i][0], pb[n][i][1]);
+  }
+}
 
 // grid (parts, K/V heads x tiles of 8 NT heads of a group, sequences)
 template <int D, int NT>
-__global__ void __launch_bounds__(NW * 32) paged_attention_int4_kernel(const Int4Params p) {
+__global__ void __launch_bounds__(NW * 32, V_MINB) paged_attention_int4_kernel(const Int4Params p) {
+  using R = Ring<D>;
   constexpr int HT = 8 * NT;
   constexpr int WK = D / 32;            // words of a K row per lane
-  constexpr int WV = D / 64;            // words of a V row per lane
-  constexpr int ROW = D / 2;            // bytes of a row's values
+  constexpr int ROW = R::ROW;
   __shared__ int64_t tile_off[kMaxPartTokens / 4];
-  __shared__ float comb[NW][HT][D + 2];
+  extern __shared__ __align__(128) unsigned char smem[];     // the warps' rings
+  static_assert(HT * (D + 2) * 4 <= R::WARP, "a warp's result takes its ring's place");
 
   pkv::pdl_trigger();
   pkv::pdl_wait();
@@ -172,6 +334,43 @@ __global__ void __launch_bounds__(NW * 32) paged_attention_int4_kernel(const Int
     empty_result();
     return;
   }
+
+  // The warp takes chunks warp, warp + NW, ...; a lane copies the same pieces of every chunk: 16-byte
+  // pieces of K and V rows, and of four rows' (scale, zero) pairs.  Rows past the partition's tokens
+  // are not read.
+  unsigned char* ring = smem + warp * R::WARP;
+  constexpr int PIECES = CHUNK * ROW / 16 / 32;              // of K, and of V, per lane
+  int piece_blk[PIECES], piece_off[PIECES], v_dst[PIECES];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int at = i * 32 + lane, row = at / (ROW / 16), c = at % (ROW / 16);
+    piece_blk[i] = row >> lb;
+    piece_off[i] = (row & (B - 1)) * ROW + c * 16;
+    v_dst[i] = R::V_OFF + v_place<D>(row, c);
+  }
+  const int meta_row = 4 * (lane & 7);
+  const uint8_t* meta_src = (lane & 8 ? p.v : p.k) + (ROW << lb) + (meta_row & (B - 1)) * 4;
+  const int n_chunks = (n_tok + CHUNK - 1) / CHUNK;
+  const int my_n = n_chunks > warp ? (n_chunks - warp + NW - 1) / NW : 0;
+  auto fill = [&](int k) {
+    if (k < my_n) {
+      const int c0 = (warp + k * NW) * CHUNK, blk0 = c0 >> lb;
+      const uint32_t dst = smem_u32(ring + (k % R::NST) * R::STAGE);
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        if (c0 + (i * 32 + lane) / (ROW / 16) < n_tok) {
+          const int64_t off = tile_off[blk0 + piece_blk[i]] + piece_off[i];
+          cp_async16(dst + (i * 32 + lane) * 16, p.k + off);
+          cp_async16(dst + v_dst[i], p.v + off);
+        }
+      }
+      if (lane < 16 && c0 + meta_row < n_tok)
+        cp_async16(dst + R::META_OFF + lane * 16, meta_src + tile_off[blk0 + (meta_row >> lb)]);
+    }
+    cp_async_commit();                                       // one group a chunk, empty ones too
+  };
+#pragma unroll
+  for (int k = 0; k < R::NST - 1; ++k) fill(k);
 
   // q as the 8-column operand, laid out like a K row's half bytes: word w of a lane holds values
   // 8 w .. 8 w + 7 of its D/4; AND 0x000f000f takes values (0, 4) of it, AND 0x00f000f0 16 x (1, 5),
@@ -229,6 +428,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attention_int4_kernel(const Int
     for (int j = 0; j < 2; ++j) {
       st.m[n][j] = -INFINITY;
       st.l[n][j] = st.c[n][j] = 0.f;
+      st.ones[n][j] = st.ones[n][2 + j] = 0.f;
     }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
@@ -236,125 +436,26 @@ __global__ void __launch_bounds__(NW * 32) paged_attention_int4_kernel(const Int
       for (int j = 0; j < 4; ++j) st.acc[n][i][j] = 0.f;
   }
 
-  for (int c0 = warp * CHUNK; c0 < n_tok; c0 += NW * CHUNK) {
-    // rows past the partition's tokens are not read: they take the chunk's first row's place
-    auto row_of = [&](int r) {
-      const int at = c0 + r < n_tok ? c0 + r : c0;
-      return tile_off[at >> lb] + (at & (B - 1)) * ROW;
-    };
-    auto meta_of = [&](const uint8_t* pool, int r) {
-      const int at = c0 + r < n_tok ? c0 + r : c0;
-      return __half22float2(*reinterpret_cast<const __half2*>(pool + tile_off[at >> lb] + (ROW << lb) + (at & (B - 1)) * 4));
-    };
-    float x[NT][2][4];                  // tile i, {token g: heads 2t, 2t + 1; token g + 8: the same}
-    float2 vm[2][2];
-    float top[NT][2];
+  int v_off[4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      unsigned ka[WK], kb[WK];
-      load_words<WK>(ka, p.k + row_of(16 * i + g) + t * (D / 8));
-      load_words<WK>(kb, p.k + row_of(16 * i + g + 8) + t * (D / 8));
-      float dot[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) dot[n][0] = dot[n][1] = dot[n][2] = dot[n][3] = 0.f;
-#pragma unroll
-      for (int w = 0; w < WK; ++w) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const unsigned a = ka[w] >> (8 * half), b = kb[w] >> (8 * half);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma16816(dot[n], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qf[n][2 * w + half][0],
-                     qf[n][2 * w + half][1]);
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = 16 * i + g + 8 * r;
-        const bool live = c0 + row < n_tok;
-        const float2 km = meta_of(p.k, row);
-        const float2 v2 = meta_of(p.v, row);
-        vm[i][r] = live ? v2 : make_float2(0.f, 0.f);
-        const float e = exponent_of(vm[i][r].x);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float y = fmaf(km.x, ca[n][j] * dot[n][2 * r + j], km.y * cb[n][j]);
-            x[n][i][2 * r + j] = live ? y : -INFINITY;
-            top[n][j] = fmaxf(top[n][j], x[n][i][2 * r + j] + e);
-          }
-      }
-    }
-    bool moves = false;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int o = 4; o < 32; o *= 2) top[n][j] = fmaxf(top[n][j], __shfl_xor_sync(FULL, top[n][j], o));
-        moves |= top[n][j] > st.m[n][j] + kRescale;
-      }
-    if (__any_sync(FULL, moves)) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float m = fmaxf(st.m[n][j], top[n][j]);
-          const float f = m == -INFINITY ? 1.f : exp2f(st.m[n][j] - m);
-          st.m[n][j] = m;
-          st.l[n][j] *= f;
-          st.c[n][j] *= f;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            st.acc[n][i][j] *= f;
-            st.acc[n][i][2 + j] *= f;
-          }
-        }
-    }
-    unsigned pb[NT][2][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float u[2], z[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float m = st.m[n][j] == -INFINITY ? 0.f : st.m[n][j];
-            const float w = fast_exp2(x[n][i][2 * r + j] - m);
-            st.l[n][j] += w;
-            u[j] = w * vm[i][r].x;
-            z[j] = w * vm[i][r].y;
-          }
-          const unsigned packed = pack2(u[0], u[1]);
-          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&packed));
-          st.c[n][0] += fmaf(8.f, u[0] - back.x, z[0]);
-          st.c[n][1] += fmaf(8.f, u[1] - back.y, z[1]);
-          pb[n][i][r] = transpose8x8(packed);
-        }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      unsigned va[4][WV];               // tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the tile
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        load_words<WV>(va[r], p.v + row_of(16 * i + 2 * t + (r & 1) + 8 * (r >> 1)) + g * (D / 16));
-#pragma unroll
-      for (int w = 0; w < WV; ++w)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const unsigned sel = 0x4400u + 0x1111u * b;      // byte b of the first token, byte b of the second
-          const unsigned e = __byte_perm(va[0][w], va[1][w], sel), f = __byte_perm(va[2][w], va[3][w], sel);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma16816(st.acc[n][4 * w + b], e & 0x000f000fu, e & 0x00f000f0u, f & 0x000f000fu, f & 0x00f000f0u, pb[n][i][0],
-                     pb[n][i][1]);
-        }
-    }
+  for (int r = 0; r < 4; ++r) {
+    // lane g's D/16 bytes of V rows 2t, 2t + 1, 2t + 8, 2t + 9
+    const int at = g * (D / 16);
+    v_off[r] = v_place<D>(2 * t + (r & 1) + 8 * (r >> 1), at / 16) + at % 16;
   }
+  for (int k = 0; k < my_n; ++k) {
+    cp_async_wait<R::NST - 2>();
+    __syncwarp();                                            // every lane's copies; and stage k - 1 is read
+    fill(k + R::NST - 1);
+    const unsigned char* stage = ring + (k % R::NST) * R::STAGE;
+    const int valid = n_tok - (warp + k * NW) * CHUNK;
+    if (valid >= CHUNK)
+      chunk_update<D, NT, false>(stage, CHUNK, qf, ca, cb, st, g, t, v_off);
+    else
+      chunk_update<D, NT, true>(stage, valid, qf, ca, cb, st, g, t, v_off);
+  }
+  cp_async_wait<0>();
+  __syncwarp();                                              // the ring is free
 
   // the warps' results side by side: o in values, (m, l)
 #pragma unroll
@@ -366,12 +467,13 @@ __global__ void __launch_bounds__(NW * 32) paged_attention_int4_kernel(const Int
         st.l[n][j] += __shfl_xor_sync(FULL, st.l[n][j], o);
         st.c[n][j] += __shfl_xor_sync(FULL, st.c[n][j], o);
       }
-      float* dst = comb[warp][n * 8 + 2 * t + j];
+      float* dst = reinterpret_cast<float*>(ring) + (n * 8 + 2 * t + j) * (D + 2);
+      const float mid = fmaf(-8.f, st.ones[n][j], st.c[n][j]);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const int d = g * (D / 8) + 2 * i;                 // word i / 4, byte i % 4: values 2 i and 2 i + 1
-        dst[d] = fmaf(st.acc[n][i][j], 16777216.f, st.c[n][j]);
-        dst[d + 1] = fmaf(st.acc[n][i][2 + j], 1048576.f, st.c[n][j]);
+        dst[d] = fmaf(st.acc[n][i][j], 16777216.f, mid);
+        dst[d + 1] = fmaf(st.acc[n][i][2 + j], 1048576.f, mid);
       }
       if (g == 0) {
         dst[D] = st.m[n][j];
@@ -381,16 +483,17 @@ __global__ void __launch_bounds__(NW * 32) paged_attention_int4_kernel(const Int
   __syncthreads();
   for (int i = tid; i < nh * D; i += NW * 32) {
     const int h = i / D, d = i % D;
+    auto comb = [&](int w) { return reinterpret_cast<const float*>(smem + w * R::WARP) + h * (D + 2); };
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, comb[w][h][D]);
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, comb(w)[D]);
     float L = 0.f, o = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const float mw = comb[w][h][D];
+      const float mw = comb(w)[D];
       const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
-      L = fmaf(comb[w][h][D + 1], f, L);
-      o = fmaf(comb[w][h][d], f, o);
+      L = fmaf(comb(w)[D + 1], f, L);
+      o = fmaf(comb(w)[d], f, o);
     }
     const size_t row = static_cast<size_t>(s) * H + h0 + h;
     if (nparts == 1) {
@@ -477,6 +580,23 @@ Plan plan_for(int num_seqs, int num_heads, int num_kv_heads, int max_ctx) {
 }
 
 template <int D>
+cudaError_t prepare_kernels() {
+  static std::mutex mu;
+  static bool done[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> g(mu);
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  constexpr int smem = NW * Ring<D>::WARP;
+  e = cudaFuncSetAttribute(paged_attention_int4_kernel<D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(paged_attention_int4_kernel<D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
+template <int D>
 int launch(Int4Params p, const Plan& pl, int num_seqs, void* ws, size_t ws_bytes, cudaStream_t st) {
   p.head_tiles = pl.head_tiles;
   p.part_tokens = pl.part_tokens;
@@ -491,8 +611,11 @@ int launch(Int4Params p, const Plan& pl, int num_seqs, void* ws, size_t ws_bytes
     p.ws_o = p.ws_ml + ws_ml_floats(pairs);
   }
   const dim3 grid(p.max_parts, p.num_kv_heads * p.head_tiles, num_seqs);
-  cudaError_t e = pl.nt == 1 ? pkv::launch_pdl(paged_attention_int4_kernel<D, 1>, grid, dim3(NW * 32), 0, st, p)
-                             : pkv::launch_pdl(paged_attention_int4_kernel<D, 2>, grid, dim3(NW * 32), 0, st, p);
+  constexpr size_t smem = NW * Ring<D>::WARP;
+  cudaError_t e = prepare_kernels<D>();
+  if (e == cudaSuccess)
+    e = pl.nt == 1 ? pkv::launch_pdl(paged_attention_int4_kernel<D, 1>, grid, dim3(NW * 32), smem, st, p)
+                   : pkv::launch_pdl(paged_attention_int4_kernel<D, 2>, grid, dim3(NW * 32), smem, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess && p.max_parts > 1) {
     e = pkv::launch_pdl(paged_attention_int4_merge_kernel<D>, dim3((p.num_heads + 3) / 4, num_seqs), dim3(128), 0, st, p);
