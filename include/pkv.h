@@ -479,9 +479,10 @@ int pkv_swap_blocks_int4(const uint8_t* const* src_k_caches, const uint8_t* cons
  *   out[s,h,:] = sum_{t < ctx_s} softmax_t(scale * q[s,h,:] . k_t) v_t
  * with k_t, v_t what the pools' rows of head h / (num_heads / num_kv_heads) stand
  * for.  num_heads is a multiple of num_kv_heads.  q (device [num_seqs, num_heads,
- * head_dim] fp16), tables, lengths, out, workspace, errors and the meaning of a
- * zero length are as for pkv_paged_attention_decode, except that q, tables,
- * lengths and out must be device memory.  Products of q and the cached whole
+ * head_dim] fp16), tables, lengths, out, errors and the meaning of a zero length
+ * are as for pkv_paged_attention_decode, except that q, tables, lengths and out
+ * must be device memory, and that the workspace is always needed (at least
+ * pkv_paged_attention_int4_workspace_size(...) bytes on the current device).  Products of q and the cached whole
  * numbers are exact, sums are fp32; the softmax weights, times the rows' V scales,
  * are rounded to fp16 before they multiply V.
  * ------------------------------------------------------------------------- */

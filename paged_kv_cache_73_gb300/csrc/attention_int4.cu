@@ -34,11 +34,14 @@
 // the second sum is fp32, and sum u' comes from one more product, with ones, so that a
 // weight's rounding meets n - 8 and not n.
 //
-// Each warp streams its own tokens, 32 at a time, through a ring in shared memory by
-// 16-byte cp.async: rows of any block size land in the same place, and V's rows XOR-ed so
-// that four tokens' words are read without bank conflicts.  The context is split over CTAs
-// and over a CTA's warps, joined by the log-sum-exp identity (second kernel for the CTAs'
-// parts).
+// Every warp of a resident grid is a worker of its own.  The work is one line of chunks of
+// 32 tokens, sequence after sequence and in each cached head after cached head, cut into
+// equal pieces; a worker walks its piece through a ring in shared memory that 16-byte
+// cp.async fill some chunks ahead, across the ends of streams.  (One CTA per part of a
+// stream, with 1024 tokens each, lost a quarter of its time to starts: length, table and
+// first rows are three round trips, with three CTAs to an SM to hide them.)  Where a
+// stream is cut, its workers leave partial results that a second kernel joins by the
+// log-sum-exp identity.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -54,14 +57,11 @@ namespace {
 __device__ int g_dev_error_attention_int4 = 0;
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_attention_int4, 0, code); }
 
-#ifndef V_MINB
-#define V_MINB 3
-#endif
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int NW = 4;                 // warps per CTA
-constexpr int CHUNK = 32;             // tokens a warp handles at a time
-constexpr int kMinPartTokens = 128;   // one chunk per warp
-constexpr int kMaxPartTokens = 1024;
+constexpr int CHUNK = 32;             // tokens a worker handles at a time
+constexpr int kResident = 3;          // CTAs per SM
+constexpr int kMinChunks = 4;         // chunks a worker takes at least
 constexpr float kRescale = 8.f;       // the running maximum moves when a chunk passes it by this much
 
 struct Int4Params {
@@ -71,13 +71,26 @@ struct Int4Params {
   const int32_t* tables;
   const int32_t* lens;
   __half* out;
-  float* ws_ml;  // [S, H, max_parts, 2] (m, l), base-2 log domain
-  float* ws_o;   // [S, H, max_parts, D] unnormalised partial outputs
-  int num_heads, num_kv_heads, group, head_tiles;
+  float* ws_ml;  // [slots, rows per tile, 2] (m, l), base-2 log domain
+  float* ws_o;   // [slots, rows per tile, D] unnormalised partial outputs
+  int num_seqs, num_heads, num_kv_heads, group, head_tiles;
   int num_blocks, max_blocks, log2_block;
-  int part_tokens, max_parts;
+  int workers;
   float scale_log2;
 };
+
+// How the line of chunks is laid out and cut, from the lengths: both kernels derive it alike.  A
+// stream is one sequence's cached head (and tile of its query heads); worker w takes chunks
+// [w per, (w + 1) per) of the line.  Slot w + stream is unique to that pair: along the line one of the
+// two grows at every cut.
+__device__ __forceinline__ int chunks_of(const Int4Params& p, int s) {
+  const int len = s < p.num_seqs ? p.lens[s] : 0;
+  return len <= 0 || len > (p.max_blocks << p.log2_block) ? 0 : (len + CHUNK - 1) / CHUNK;
+}
+__device__ __forceinline__ long long per_worker(long long total, int workers) {
+  const long long per = (total + workers - 1) / workers;
+  return per > kMinChunks ? per : kMinChunks;
+}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
                                          unsigned b1) {
@@ -108,8 +121,9 @@ __device__ __forceinline__ float log2_of(float s) {
   return fmaxf(y, -24.f);
 }
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// bytes = 0 writes zeros and reads nothing
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -151,7 +165,7 @@ __device__ __forceinline__ int v_place(int r, int c) {
   return line * 128 + (((lin & 7) ^ ((line & 3) << 1)) << 4);
 }
 
-// A warp's running softmax over its tokens for 8 NT heads; lane (g, t) holds heads 8 n + 2t,
+// A worker's running softmax over one stream's tokens for 8 NT heads; lane (g, t) holds heads 8 n + 2t,
 // 8 n + 2t + 1.
 template <int D, int NT>
 struct WarpState {
@@ -173,25 +187,32 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
   float top[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
+  // the two tiles' products side by side: each is a chain of dependent accumulations
+  unsigned kw[2][2][WK];
+  float dot[2][NT][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    unsigned ka[WK], kb[WK];
-    load_words<WK>(ka, stage + (16 * i + g) * R::ROW + t * (D / 8));
-    load_words<WK>(kb, stage + (16 * i + g + 8) * R::ROW + t * (D / 8));
-    float dot[NT][4];
+    load_words<WK>(kw[i][0], stage + (16 * i + g) * R::ROW + t * (D / 8));
+    load_words<WK>(kw[i][1], stage + (16 * i + g + 8) * R::ROW + t * (D / 8));
 #pragma unroll
-    for (int n = 0; n < NT; ++n) dot[n][0] = dot[n][1] = dot[n][2] = dot[n][3] = 0.f;
+    for (int n = 0; n < NT; ++n) dot[i][n][0] = dot[i][n][1] = dot[i][n][2] = dot[i][n][3] = 0.f;
+  }
 #pragma unroll
-    for (int w = 0; w < WK; ++w) {
+  for (int w = 0; w < WK; ++w) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const unsigned a = ka[w] >> (8 * half), b = kb[w] >> (8 * half);
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const unsigned a = kw[i][0][w] >> (8 * half), b = kw[i][1][w] >> (8 * half);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          mma16816(dot[n], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qf[n][2 * w + half][0],
-                   qf[n][2 * w + half][1]);
+          mma16816(dot[i][n], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
+                   qf[n][2 * w + half][0], qf[n][2 * w + half][1]);
       }
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = 16 * i + g + 8 * r;
@@ -205,7 +226,7 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float y = fmaf(km.x, ca[n][j] * dot[n][2 * r + j], km.y * cb[n][j]);
+          const float y = fmaf(km.x, ca[n][j] * dot[i][n][2 * r + j], km.y * cb[n][j]);
           x[n][i][2 * r + j] = live ? y : -INFINITY;
           top[n][j] = fmaxf(top[n][j], x[n][i][2 * r + j] + e);
         }
@@ -215,16 +236,14 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int o = 4; o < 32; o *= 2) top[n][j] = fmaxf(top[n][j], __shfl_xor_sync(FULL, top[n][j], o));
-      moves |= top[n][j] > st.m[n][j] + kRescale;
-    }
+    for (int j = 0; j < 2; ++j) moves |= top[n][j] > st.m[n][j] + kRescale;
   if (__any_sync(FULL, moves)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) top[n][j] = fmaxf(top[n][j], __shfl_xor_sync(FULL, top[n][j], o));
         const float m = fmaxf(st.m[n][j], top[n][j]);
         const float f = m == -INFINITY ? 1.f : exp2f(st.m[n][j] - m);
         st.m[n][j] = m;
@@ -279,93 +298,140 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
   }
 }
 
-// grid (parts, K/V heads x tiles of 8 NT heads of a group, sequences)
-template <int D, int NT>
-__global__ void __launch_bounds__(NW * 32, V_MINB) paged_attention_int4_kernel(const Int4Params p) {
+// A place on the line of chunks: chunk c of the `chunks` of stream (s, y).
+struct Place {
+  int s, y, c, chunks, len;
+};
+
+template <int D, int NT, int LB>
+__global__ void __launch_bounds__(NW * 32, kResident) paged_attention_int4_kernel(const Int4Params p) {
   using R = Ring<D>;
-  constexpr int HT = 8 * NT;
-  constexpr int WK = D / 32;            // words of a K row per lane
-  constexpr int ROW = R::ROW;
-  __shared__ int64_t tile_off[kMaxPartTokens / 4];
-  extern __shared__ __align__(128) unsigned char smem[];     // the warps' rings
-  static_assert(HT * (D + 2) * 4 <= R::WARP, "a warp's result takes its ring's place");
+  constexpr int HT = 8 * NT, WK = D / 32, ROW = R::ROW, B = 1 << LB;
+  constexpr int PIECES = CHUNK * ROW / 16 / 32;              // 16-byte pieces of K, and of V, per lane and chunk
+  constexpr int RPP = 512 / ROW;                             // rows that one piece of every lane covers
+  constexpr int BPC = CHUNK / B;                             // blocks per chunk
+  extern __shared__ __align__(128) unsigned char smem[];     // the workers' rings
 
   pkv::pdl_trigger();
   pkv::pdl_wait();
-  const int part = blockIdx.x, s = blockIdx.z;
-  const int kvh = blockIdx.y / p.head_tiles, h_in_group = (blockIdx.y % p.head_tiles) * HT;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int lb = p.log2_block, B = 1 << lb;
-  const int H = p.num_heads;
-  const int h0 = kvh * p.group + h_in_group;                 // first query head of this CTA
-  const int nh = min(HT, p.group - h_in_group);              // heads that exist
-  const int ctx = p.lens[s];
-  const bool bad_len = ctx < 0 || ctx > (p.max_blocks << lb);
-  const int nparts = ctx <= 0 || bad_len ? 1 : (ctx + p.part_tokens - 1) / p.part_tokens;
-  if (part >= nparts) return;
-  auto empty_result = [&]() {
-    for (int i = tid; i < nh * D; i += NW * 32) {
-      const size_t row = static_cast<size_t>(s) * H + h0 + i / D;
-      if (nparts == 1) p.out[row * D + i % D] = __float2half_rn(0.f);
-      else p.ws_o[(row * p.max_parts + part) * D + i % D] = 0.f;
-    }
-    if (nparts > 1 && tid < nh) {
-      const size_t w = (static_cast<size_t>(s) * H + h0 + tid) * p.max_parts + part;
-      p.ws_ml[2 * w] = -INFINITY;
-      p.ws_ml[2 * w + 1] = 0.f;
-    }
-  };
-  if (ctx <= 0 || bad_len) {
-    if (bad_len && tid == 0) record_error(PKV_DEV_BAD_CONTEXT_LEN);
-    empty_result();
-    return;
-  }
-  const int begin = part * p.part_tokens, n_tok = min(p.part_tokens, ctx - begin);
-  const int64_t tile_bytes = static_cast<int64_t>(ROW + 4) << lb;
-  int bad = 0;
-  for (int i = tid; i < (n_tok + B - 1) >> lb; i += NW * 32) {
-    const int phys = p.tables[static_cast<size_t>(s) * p.max_blocks + (begin >> lb) + i];
-    const bool ok = phys >= 0 && phys < p.num_blocks;
-    bad |= !ok;
-    tile_off[i] = ok ? (static_cast<int64_t>(phys) * p.num_kv_heads + kvh) * tile_bytes : 0;
-  }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) record_error(PKV_DEV_BAD_BLOCK_ID);
-    empty_result();
-    return;
-  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int worker = blockIdx.x * NW + warp;
+  const int S = p.num_seqs, H = p.num_heads, Y = p.num_kv_heads * p.head_tiles;
 
-  // The warp takes chunks warp, warp + NW, ...; a lane copies the same pieces of every chunk: 16-byte
-  // pieces of K and V rows, and of four rows' (scale, zero) pairs.  Rows past the partition's tokens
-  // are not read.
-  unsigned char* ring = smem + warp * R::WARP;
-  constexpr int PIECES = CHUNK * ROW / 16 / 32;              // of K, and of V, per lane
-  int piece_blk[PIECES], piece_off[PIECES], v_dst[PIECES];
+  // this worker's piece of the line
+  Place at;
+  long long left;
+  {
+    long long total = 0;
+    bool bad = false;
+    for (int s = lane; s < S; s += 32) {
+      total += chunks_of(p, s);
+      bad |= p.lens[s] < 0 || p.lens[s] > (p.max_blocks << LB);
+    }
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i) {
-    const int at = i * 32 + lane, row = at / (ROW / 16), c = at % (ROW / 16);
-    piece_blk[i] = row >> lb;
-    piece_off[i] = (row & (B - 1)) * ROW + c * 16;
-    v_dst[i] = R::V_OFF + v_place<D>(row, c);
+    for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(FULL, total, o);
+    if (bad && worker == 0) record_error(PKV_DEV_BAD_CONTEXT_LEN);
+    const long long n = total * Y, per = per_worker(n, p.workers), x = worker * per;
+    if (x >= n) return;
+    left = min(per, n - x);
+    // the sequence: the first whose chunks, all heads together, reach past x
+    long long before = 0;
+    int s = S, mine = 0;
+    for (int base = 0; base < S; base += 32) {
+      mine = chunks_of(p, base + lane);
+      long long upto = mine;                                 // inclusive prefix sum over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const long long y = __shfl_up_sync(FULL, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const unsigned past = __ballot_sync(FULL, (before + upto) * Y > x);
+      if (past) {
+        const int hit = __ffs(past) - 1;
+        s = base + hit;
+        before += __shfl_sync(FULL, upto - mine, hit);
+        mine = __shfl_sync(FULL, mine, hit);
+        break;
+      }
+      before += __shfl_sync(FULL, upto, 31);
+    }
+    if (s >= S) return;                                      // the lengths changed meanwhile
+    const long long rest = x - before * Y;
+    at.s = s;
+    at.y = static_cast<int>(rest / mine);
+    at.c = static_cast<int>(rest - static_cast<long long>(at.y) * mine);
+    at.chunks = mine;
+    at.len = p.lens[s];
   }
+  auto advance = [&](Place& x) {                             // true if the stream changed
+    if (++x.c < x.chunks) return false;
+    x.c = 0;
+    if (++x.y == Y) {
+      x.y = 0;
+      do ++x.s, x.chunks = chunks_of(p, x.s);
+      while (x.chunks == 0 && x.s < S);
+      x.len = x.s < S ? p.lens[x.s] : 0;
+    }
+    return true;
+  };
+
+  // ---- the ring: a lane copies the same pieces of every chunk
+  unsigned char* ring = smem + warp * R::WARP;
+  const uint32_t ring_u32 = smem_u32(ring);
+  const int tile_bytes = (ROW + 4) * B, block_bytes = p.num_kv_heads * tile_bytes;
+  const int piece_row = lane / (ROW / 16);                   // piece i: row RPP i + piece_row
+  const int piece_col = lane % (ROW / 16) * 16;
+  const int v_lane = R::V_OFF + v_place<D>(piece_row, lane % (ROW / 16));
   const int meta_row = 4 * (lane & 7);
-  const uint8_t* meta_src = (lane & 8 ? p.v : p.k) + (ROW << lb) + (meta_row & (B - 1)) * 4;
-  const int n_chunks = (n_tok + CHUNK - 1) / CHUNK;
-  const int my_n = n_chunks > warp ? (n_chunks - warp + NW - 1) / NW : 0;
-  auto fill = [&](int k) {
-    if (k < my_n) {
-      const int c0 = (warp + k * NW) * CHUNK, blk0 = c0 >> lb;
-      const uint32_t dst = smem_u32(ring + (k % R::NST) * R::STAGE);
+  Place ahead = at;
+  long long to_fill = left;
+  // table entries of 32 blocks around `ahead`, one a lane, and of the next 32; -1 past the context or bad
+  int entry = -1, entry_next = -1;
+  auto read_entry = [&](int first) {
+    const int j = first + lane;
+    if (j * static_cast<long long>(B) >= ahead.len) return -1;
+    const int phys = p.tables[static_cast<size_t>(ahead.s) * p.max_blocks + j];
+    if (phys >= 0 && phys < p.num_blocks) return phys;
+    record_error(PKV_DEV_BAD_BLOCK_ID);
+    return -1;
+  };
+  bool fresh = true;                                         // `ahead` is at a stream's first chunk here
+  auto fill = [&](int stage) {
+    if (to_fill > 0) {
+      const int blk = ahead.c * BPC, first = blk & ~31;
+      if (fresh) {
+        entry = read_entry(first);
+        entry_next = read_entry(first + 32);
+        fresh = false;
+      } else if (blk == first) {
+        entry = entry_next;
+        entry_next = read_entry(first + 32);
+      }
+      const int valid = ahead.len - ahead.c * CHUNK;
+      const uint32_t dst = ring_u32 + stage * R::STAGE;
+      const int64_t head_off = static_cast<int64_t>(ahead.y / p.head_tiles) * tile_bytes;
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        if (c0 + (i * 32 + lane) / (ROW / 16) < n_tok) {
-          const int64_t off = tile_off[blk0 + piece_blk[i]] + piece_off[i];
-          cp_async16(dst + (i * 32 + lane) * 16, p.k + off);
-          cp_async16(dst + v_dst[i], p.v + off);
+        const int row = RPP * i + piece_row;
+        const int phys = __shfl_sync(FULL, entry, (blk & 31) + row / B);
+        if (row < valid) {
+          // a bad block's rows are zeros
+          const int64_t off = static_cast<int64_t>(max(phys, 0)) * block_bytes + head_off + (row % B) * ROW + piece_col;
+          const int bytes = phys >= 0 ? 16 : 0;
+          cp_async16(dst + lane * 16 + i * 512, p.k + off, bytes);
+          cp_async16(dst + v_lane + i * 512, p.v + off, bytes);
         }
       }
-      if (lane < 16 && c0 + meta_row < n_tok)
-        cp_async16(dst + R::META_OFF + lane * 16, meta_src + tile_off[blk0 + (meta_row >> lb)]);
+      {
+        const int phys = __shfl_sync(FULL, entry, (blk & 31) + meta_row / B);
+        if (lane < 16 && meta_row < valid)
+          cp_async16(dst + R::META_OFF + lane * 16,
+                     (lane & 8 ? p.v : p.k) + static_cast<int64_t>(max(phys, 0)) * block_bytes + head_off + ROW * B +
+                         (meta_row % B) * 4,
+                     phys >= 0 ? 16 : 0);
+      }
+      --to_fill;
+      fresh = advance(ahead);
     }
     cp_async_commit();                                       // one group a chunk, empty ones too
   };
@@ -378,166 +444,233 @@ __global__ void __launch_bounds__(NW * 32, V_MINB) paged_attention_int4_kernel(c
   // greatest value is near 2^9: q / 16 then loses nothing that matters.
   unsigned qf[NT][D / 16][2];
   float ca[NT][2], cb[NT][2];           // x = s (ca dot) + z cb, heads 2t, 2t + 1 of each tile
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float qv[WK][8];
-    float amax = 0.f, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < WK; ++w) {
-      uint4 raw = make_uint4(0, 0, 0, 0);
-      if (n * 8 + g < nh)
-        raw = *reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(s) * H + h0 + n * 8 + g) * D + t * (D / 4) + w * 8);
-      const __half2* h2 = reinterpret_cast<const __half2*>(&raw);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(h2[e]);
-        qv[w][2 * e] = f.x;
-        qv[w][2 * e + 1] = f.y;
-        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-        sum += f.x + f.y;
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o *= 2) {
-      amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
-      sum += __shfl_xor_sync(FULL, sum, o);
-    }
-    const int e = amax > 0.f ? static_cast<int>(__float_as_uint(amax) >> 23) - 127 : 9;
-    const float up = __uint_as_float(static_cast<unsigned>(9 - e + 127) << 23);
-#pragma unroll
-    for (int w = 0; w < WK; ++w) {
-      const float d = up * 0.0625f;
-      qf[n][2 * w][0] = pack2(qv[w][0] * up, qv[w][4] * up);
-      qf[n][2 * w][1] = pack2(qv[w][1] * d, qv[w][5] * d);
-      qf[n][2 * w + 1][0] = pack2(qv[w][2] * up, qv[w][6] * up);
-      qf[n][2 * w + 1][1] = pack2(qv[w][3] * d, qv[w][7] * d);
-    }
-    const float a = p.scale_log2 * 16777216.f * __uint_as_float(static_cast<unsigned>(e - 9 + 127) << 23);
-    const float b = p.scale_log2 * sum;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      ca[n][j] = __shfl_sync(FULL, a, (2 * t + j) * 4);
-      cb[n][j] = __shfl_sync(FULL, b, (2 * t + j) * 4);
-    }
-  }
-
   WarpState<D, NT> st;
+  auto begin_stream = [&]() {
+    const int in_group = at.y % p.head_tiles * HT, h0 = at.y / p.head_tiles * p.group + in_group;
+    const int nh = min(HT, p.group - in_group);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NT; ++n) {
+      float qv[WK][8];
+      float amax = 0.f, sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      st.m[n][j] = -INFINITY;
-      st.l[n][j] = st.c[n][j] = 0.f;
-      st.ones[n][j] = st.ones[n][2 + j] = 0.f;
+      for (int w = 0; w < WK; ++w) {
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (n * 8 + g < nh)
+          raw = *reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(at.s) * H + h0 + n * 8 + g) * D + t * (D / 4) + w * 8);
+        const __half2* h2 = reinterpret_cast<const __half2*>(&raw);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = __half22float2(h2[e]);
+          qv[w][2 * e] = f.x;
+          qv[w][2 * e + 1] = f.y;
+          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+          sum += f.x + f.y;
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o *= 2) {
+        amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
+        sum += __shfl_xor_sync(FULL, sum, o);
+      }
+      const int e = amax > 0.f ? static_cast<int>(__float_as_uint(amax) >> 23) - 127 : 9;
+      const float up = __uint_as_float(static_cast<unsigned>(9 - e + 127) << 23);
+#pragma unroll
+      for (int w = 0; w < WK; ++w) {
+        const float d = up * 0.0625f;
+        qf[n][2 * w][0] = pack2(qv[w][0] * up, qv[w][4] * up);
+        qf[n][2 * w][1] = pack2(qv[w][1] * d, qv[w][5] * d);
+        qf[n][2 * w + 1][0] = pack2(qv[w][2] * up, qv[w][6] * up);
+        qf[n][2 * w + 1][1] = pack2(qv[w][3] * d, qv[w][7] * d);
+      }
+      const float a = p.scale_log2 * 16777216.f * __uint_as_float(static_cast<unsigned>(e - 9 + 127) << 23);
+      const float b = p.scale_log2 * sum;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        ca[n][j] = __shfl_sync(FULL, a, (2 * t + j) * 4);
+        cb[n][j] = __shfl_sync(FULL, b, (2 * t + j) * 4);
+        st.m[n][j] = -INFINITY;
+        st.l[n][j] = st.c[n][j] = 0.f;
+        st.ones[n][j] = st.ones[n][2 + j] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st.acc[n][i][j] = 0.f;
     }
+  };
+  // the stream's result, or this worker's part of it: lane (g, t) holds values g D/8 .. of heads 2t, 2t + 1
+  auto end_stream = [&](bool whole) {
+    const int in_group = at.y % p.head_tiles * HT, h0 = at.y / p.head_tiles * p.group + in_group;
+    const int nh = min(HT, p.group - in_group), rows = min(HT, p.group);
+    const size_t slot = static_cast<size_t>(worker) + static_cast<size_t>(at.s) * Y + at.y;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) st.acc[n][i][j] = 0.f;
-  }
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) {
+          st.l[n][j] += __shfl_xor_sync(FULL, st.l[n][j], o);
+          st.c[n][j] += __shfl_xor_sync(FULL, st.c[n][j], o);
+        }
+        const int h = n * 8 + 2 * t + j;
+        if (h >= nh) continue;
+        const float mid = fmaf(-8.f, st.ones[n][j], st.c[n][j]);
+        float o[D / 8];                                      // word i / 4, byte i % 4: values 2 i and 2 i + 1
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[2 * i] = fmaf(st.acc[n][i][j], 16777216.f, mid);
+          o[2 * i + 1] = fmaf(st.acc[n][i][2 + j], 1048576.f, mid);
+        }
+        if (whole) {
+          const float inv = 1.f / st.l[n][j];
+          __half* dst = p.out + (static_cast<size_t>(at.s) * H + h0 + h) * D + g * (D / 8);
+#pragma unroll
+          for (int i = 0; i < D / 8; i += 8)
+            *reinterpret_cast<uint4*>(dst + i) =
+                make_uint4(pack2(o[i] * inv, o[i + 1] * inv), pack2(o[i + 2] * inv, o[i + 3] * inv),
+                           pack2(o[i + 4] * inv, o[i + 5] * inv), pack2(o[i + 6] * inv, o[i + 7] * inv));
+        } else {
+          const size_t w = slot * rows + h;
+          float* dst = p.ws_o + w * D + g * (D / 8);
+#pragma unroll
+          for (int i = 0; i < D / 8; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          if (g == 0) *reinterpret_cast<float2*>(p.ws_ml + 2 * w) = make_float2(st.m[n][j], st.l[n][j]);
+        }
+      }
+  };
 
   int v_off[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     // lane g's D/16 bytes of V rows 2t, 2t + 1, 2t + 8, 2t + 9
-    const int at = g * (D / 16);
-    v_off[r] = v_place<D>(2 * t + (r & 1) + 8 * (r >> 1), at / 16) + at % 16;
+    const int x = g * (D / 16);
+    v_off[r] = v_place<D>(2 * t + (r & 1) + 8 * (r >> 1), x / 16) + x % 16;
   }
-  for (int k = 0; k < my_n; ++k) {
+  bool from_start = at.c == 0;
+  begin_stream();
+  int stage = 0;
+  for (; left > 0; --left) {
     cp_async_wait<R::NST - 2>();
-    __syncwarp();                                            // every lane's copies; and stage k - 1 is read
-    fill(k + R::NST - 1);
-    const unsigned char* stage = ring + (k % R::NST) * R::STAGE;
-    const int valid = n_tok - (warp + k * NW) * CHUNK;
+    __syncwarp();                                            // every lane's copies; and the last stage is read
+    fill(stage == 0 ? R::NST - 1 : stage - 1);
+    const unsigned char* src = ring + stage * R::STAGE;
+    const int valid = at.len - at.c * CHUNK;
     if (valid >= CHUNK)
-      chunk_update<D, NT, false>(stage, CHUNK, qf, ca, cb, st, g, t, v_off);
+      chunk_update<D, NT, false>(src, CHUNK, qf, ca, cb, st, g, t, v_off);
     else
-      chunk_update<D, NT, true>(stage, valid, qf, ca, cb, st, g, t, v_off);
+      chunk_update<D, NT, true>(src, valid, qf, ca, cb, st, g, t, v_off);
+    if (++stage == R::NST) stage = 0;
+    const bool to_end = at.c + 1 == at.chunks;
+    if (to_end || left == 1) {
+      end_stream(from_start && to_end);
+      from_start = true;
+      if (left > 1) {
+        advance(at);
+        begin_stream();
+      }
+    } else {
+      ++at.c;
+    }
   }
   cp_async_wait<0>();
-  __syncwarp();                                              // the ring is free
-
-  // the warps' results side by side: o in values, (m, l)
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int o = 4; o < 32; o *= 2) {
-        st.l[n][j] += __shfl_xor_sync(FULL, st.l[n][j], o);
-        st.c[n][j] += __shfl_xor_sync(FULL, st.c[n][j], o);
-      }
-      float* dst = reinterpret_cast<float*>(ring) + (n * 8 + 2 * t + j) * (D + 2);
-      const float mid = fmaf(-8.f, st.ones[n][j], st.c[n][j]);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const int d = g * (D / 8) + 2 * i;                 // word i / 4, byte i % 4: values 2 i and 2 i + 1
-        dst[d] = fmaf(st.acc[n][i][j], 16777216.f, mid);
-        dst[d + 1] = fmaf(st.acc[n][i][2 + j], 1048576.f, mid);
-      }
-      if (g == 0) {
-        dst[D] = st.m[n][j];
-        dst[D + 1] = st.l[n][j];
-      }
-    }
-  __syncthreads();
-  for (int i = tid; i < nh * D; i += NW * 32) {
-    const int h = i / D, d = i % D;
-    auto comb = [&](int w) { return reinterpret_cast<const float*>(smem + w * R::WARP) + h * (D + 2); };
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, comb(w)[D]);
-    float L = 0.f, o = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float mw = comb(w)[D];
-      const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
-      L = fmaf(comb(w)[D + 1], f, L);
-      o = fmaf(comb(w)[d], f, o);
-    }
-    const size_t row = static_cast<size_t>(s) * H + h0 + h;
-    if (nparts == 1) {
-      p.out[row * D + d] = __float2half_rn(o / L);
-    } else {
-      const size_t w0 = row * p.max_parts + part;
-      p.ws_o[w0 * D + d] = o;
-      if (d == 0) {
-        p.ws_ml[2 * w0] = M;
-        p.ws_ml[2 * w0 + 1] = L;
-      }
-    }
-  }
 }
 
-// Joins the parts of every (sequence, head) with more than one: a warp each, a lane D/32 values.
+// Joins the parts of every cut stream, and writes the zeros of empty contexts: a warp per (sequence,
+// head), a lane D/32 values.
 template <int D>
-__global__ void __launch_bounds__(128) paged_attention_int4_merge_kernel(const Int4Params p) {
+__global__ void __launch_bounds__(128) paged_attention_int4_merge_kernel(const Int4Params p, int head_rows) {
   pkv::pdl_trigger();
   pkv::pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.x * 4 + warp, s = blockIdx.y;
+  // chunks of the sequences before s, and of all
+  long long mine[2] = {0, 0};
+  for (int i = threadIdx.x; i < p.num_seqs; i += 128) {
+    const int c = chunks_of(p, i);
+    mine[1] += c;
+    if (i < s) mine[0] += c;
+  }
+  __shared__ long long sums[4][2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) mine[k] += __shfl_xor_sync(FULL, mine[k], o);
+    if (lane == 0) sums[warp][k] = mine[k];
+  }
+  __syncthreads();
   if (h >= p.num_heads) return;
-  const int ctx = p.lens[s];
-  if (ctx <= p.part_tokens || ctx > (p.max_blocks << p.log2_block)) return;   // one part (or none): written already
-  const int nparts = (ctx + p.part_tokens - 1) / p.part_tokens;
-  const size_t w0 = (static_cast<size_t>(s) * p.num_heads + h) * p.max_parts;
+  const long long before = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
+  const long long total = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
   constexpr int V = D / 32;
+  __half* dst = p.out + (static_cast<size_t>(s) * p.num_heads + h) * D + lane * V;
+  const int chunks = chunks_of(p, s);
+  if (chunks == 0) {
+#pragma unroll
+    for (int c = 0; c < V; c += 2) *reinterpret_cast<__half2*>(dst + c) = __floats2half2_rn(0.f, 0.f);
+    return;
+  }
+  const int Y = p.num_kv_heads * p.head_tiles, tile = h % p.group / head_rows;
+  const int y = h / p.group * p.head_tiles + tile, row = h % p.group - tile * head_rows;
+  const long long first = before * Y + static_cast<long long>(y) * chunks, per = per_worker(total * Y, p.workers);
+  const long long w_first = first / per, w_last = (first + chunks - 1) / per;
+  if (w_first == w_last) return;                             // one worker wrote it
+  const int nparts = static_cast<int>(w_last - w_first) + 1, rows = min(head_rows, p.group);
+  const size_t slot0 = static_cast<size_t>(w_first) + static_cast<size_t>(s) * Y + y;
+  auto at = [&](int i) { return (slot0 + i) * rows + row; };  // part i's row of the workspace
+  // (m, l) of 32 slots at a time, one a lane; then eight slots' outputs in flight at a time
   float acc[V];
 #pragma unroll
   for (int c = 0; c < V; ++c) acc[c] = 0.f;
   float M = -INFINITY, L = 0.f;
-  for (int i = 0; i < nparts; ++i) M = fmaxf(M, p.ws_ml[2 * (w0 + i)]);
-  for (int i = 0; i < nparts; ++i) {
-    const float m = p.ws_ml[2 * (w0 + i)];
-    const float f = m == -INFINITY ? 0.f : exp2f(m - M);
-    L = fmaf(p.ws_ml[2 * (w0 + i) + 1], f, L);
+  for (int base = 0; base < nparts; base += 32) {
+    const int i = base + lane;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (i < nparts) ml = *reinterpret_cast<const float2*>(p.ws_ml + 2 * at(i));
+    float m = ml.x;
 #pragma unroll
-    for (int c = 0; c < V; ++c) acc[c] = fmaf(p.ws_o[(w0 + i) * D + lane * V + c], f, acc[c]);
+    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+    m = fmaxf(M, m);
+    const float carry = M == -INFINITY ? 0.f : exp2f(M - m);
+    M = m;
+    L *= carry;
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] *= carry;
+    const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+    L = fmaf(ml.y, f, L);
+    const int n = min(32, nparts - base);
+    for (int j0 = 0; j0 < n; j0 += 8) {
+      float x[8][V];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) x[u][c] = 0.f;
+        if (j0 + u < n) {
+          const float* src = p.ws_o + at(base + j0 + u) * D + lane * V;
+          if constexpr (V == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(src);
+            x[u][0] = y.x; x[u][1] = y.y; x[u][2] = y.z; x[u][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(src);
+            x[u][0] = y.x; x[u][1] = y.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float fu = __shfl_sync(FULL, f, (j0 + u) & 31);
+        if (j0 + u < n) {
+#pragma unroll
+          for (int c = 0; c < V; ++c) acc[c] = fmaf(x[u][c], fu, acc[c]);
+        }
+      }
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) L += __shfl_xor_sync(FULL, L, o);
   const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-  for (int c = 0; c < V; ++c)
-    p.out[(static_cast<size_t>(s) * p.num_heads + h) * D + lane * V + c] = __float2half_rn(acc[c] * inv);
+  for (int c = 0; c < V; c += 2) *reinterpret_cast<__half2*>(dst + c) = __floats2half2_rn(acc[c] * inv, acc[c + 1] * inv);
 }
 
 __host__ __device__ constexpr size_t ws_ml_floats(size_t pairs) { return (pairs * 2 + 3) / 4 * 4; }
@@ -557,70 +690,76 @@ int device_sms() {
 }
 
 // Head tiles of 8 columns, or of 16 where a group has more than 8 heads (the rows are then unpacked
-// once for both).
+// once for both); a grid that is resident at once, smaller where even the longest contexts would not
+// give every worker kMinChunks chunks.
 struct Plan {
-  int nt, head_tiles, part_tokens, max_parts;
+  int nt, head_tiles, head_rows, ctas;
+  long long slots;
 };
 Plan plan_for(int num_seqs, int num_heads, int num_kv_heads, int max_ctx) {
   Plan pl{};
   const int group = num_heads / num_kv_heads;
   pl.nt = group > 8 ? 2 : 1;
   pl.head_tiles = (group + 8 * pl.nt - 1) / (8 * pl.nt);
-  // the longest part that still gives every SM a CTA
+  pl.head_rows = group < 8 * pl.nt ? group : 8 * pl.nt;
   const long long streams = static_cast<long long>(num_seqs) * num_kv_heads * pl.head_tiles;
-  pl.part_tokens = kMinPartTokens;
-  for (int pt : {1024, 512, 256}) {
-    if (streams * ((max_ctx + pt - 1) / pt) >= device_sms()) {
-      pl.part_tokens = pt;
-      break;
-    }
-  }
-  pl.max_parts = (max_ctx + pl.part_tokens - 1) / pl.part_tokens;
+  const long long chunks = streams * ((max_ctx + CHUNK - 1) / CHUNK);
+  const long long ctas = (chunks + kMinChunks * NW - 1) / (kMinChunks * NW);
+  const long long most = static_cast<long long>(device_sms()) * kResident;
+  pl.ctas = static_cast<int>(ctas < most ? ctas : most);
+  pl.slots = streams + static_cast<long long>(pl.ctas) * NW;
   return pl;
 }
+size_t workspace_bytes_for(const Plan& pl, int head_dim) {
+  const size_t rows = static_cast<size_t>(pl.slots) * pl.head_rows;
+  return (ws_ml_floats(rows) + rows * head_dim) * sizeof(float);
+}
 
-template <int D>
-cudaError_t prepare_kernels() {
+template <int D, int NT, int LB>
+cudaError_t launch_kernel(const Int4Params& p, int ctas, cudaStream_t st) {
+  constexpr int smem = NW * Ring<D>::WARP;
   static std::mutex mu;
   static bool done[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> g(mu);
-  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
-  constexpr int smem = NW * Ring<D>::WARP;
-  e = cudaFuncSetAttribute(paged_attention_int4_kernel<D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(paged_attention_int4_kernel<D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
-  return e;
+  {
+    std::lock_guard<std::mutex> g(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+      e = cudaFuncSetAttribute(paged_attention_int4_kernel<D, NT, LB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+  }
+  e = pkv::launch_pdl(paged_attention_int4_kernel<D, NT, LB>, dim3(ctas), dim3(NW * 32), smem, st, p);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int D, int NT>
+cudaError_t launch_block_size(const Int4Params& p, int ctas, cudaStream_t st) {
+  switch (p.log2_block) {
+    case 2: return launch_kernel<D, NT, 2>(p, ctas, st);
+    case 3: return launch_kernel<D, NT, 3>(p, ctas, st);
+    case 4: return launch_kernel<D, NT, 4>(p, ctas, st);
+    default: return launch_kernel<D, NT, 5>(p, ctas, st);
+  }
 }
 
 template <int D>
-int launch(Int4Params p, const Plan& pl, int num_seqs, void* ws, size_t ws_bytes, cudaStream_t st) {
+int launch(Int4Params p, const Plan& pl, void* ws, size_t ws_bytes, cudaStream_t st) {
   p.head_tiles = pl.head_tiles;
-  p.part_tokens = pl.part_tokens;
-  p.max_parts = pl.max_parts;
-  if (p.max_parts > 1) {
-    const size_t pairs = static_cast<size_t>(num_seqs) * p.num_heads * p.max_parts;
-    const size_t need = (ws_ml_floats(pairs) + pairs * D) * sizeof(float);
-    if (ws == nullptr || ws_bytes < need)
-      return pkv::fail(PKV_ERR_WORKSPACE, "pkv_paged_attention_decode_int4: workspace of %zu bytes needed, %zu given",
-                       need, ws == nullptr ? static_cast<size_t>(0) : ws_bytes);
-    p.ws_ml = static_cast<float*>(ws);
-    p.ws_o = p.ws_ml + ws_ml_floats(pairs);
-  }
-  const dim3 grid(p.max_parts, p.num_kv_heads * p.head_tiles, num_seqs);
-  constexpr size_t smem = NW * Ring<D>::WARP;
-  cudaError_t e = prepare_kernels<D>();
+  p.workers = pl.ctas * NW;
+  const size_t need = workspace_bytes_for(pl, D);
+  if (ws == nullptr || ws_bytes < need)
+    return pkv::fail(PKV_ERR_WORKSPACE, "pkv_paged_attention_decode_int4: workspace of %zu bytes needed, %zu given", need,
+                     ws == nullptr ? static_cast<size_t>(0) : ws_bytes);
+  p.ws_ml = static_cast<float*>(ws);
+  p.ws_o = p.ws_ml + ws_ml_floats(static_cast<size_t>(pl.slots) * pl.head_rows);
+  cudaError_t e = pl.nt == 1 ? launch_block_size<D, 1>(p, pl.ctas, st) : launch_block_size<D, 2>(p, pl.ctas, st);
   if (e == cudaSuccess)
-    e = pl.nt == 1 ? pkv::launch_pdl(paged_attention_int4_kernel<D, 1>, grid, dim3(NW * 32), smem, st, p)
-                   : pkv::launch_pdl(paged_attention_int4_kernel<D, 2>, grid, dim3(NW * 32), smem, st, p);
+    e = pkv::launch_pdl(paged_attention_int4_merge_kernel<D>, dim3((p.num_heads + 3) / 4, p.num_seqs), dim3(128), 0, st,
+                        p, pl.head_rows);
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (e == cudaSuccess && p.max_parts > 1) {
-    e = pkv::launch_pdl(paged_attention_int4_merge_kernel<D>, dim3((p.num_heads + 3) / 4, num_seqs), dim3(128), 0, st, p);
-    if (e == cudaSuccess) e = cudaGetLastError();
-  }
   if (e != cudaSuccess)
     return pkv::fail(PKV_ERR_CUDA, "pkv_paged_attention_decode_int4 launch: %s", cudaGetErrorString(e));
   return PKV_OK;
@@ -651,10 +790,7 @@ size_t pkv_paged_attention_int4_workspace_size(int num_seqs, int num_heads, int 
   if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
       max_blocks_per_seq <= 0 || block_size <= 0 || static_cast<long long>(max_blocks_per_seq) * block_size > (1LL << 30))
     return 0;
-  const Plan pl = plan_for(num_seqs, num_heads, num_kv_heads, max_blocks_per_seq * block_size);
-  if (pl.max_parts <= 1) return 0;
-  const size_t pairs = static_cast<size_t>(num_seqs) * num_heads * pl.max_parts;
-  return (ws_ml_floats(pairs) + pairs * head_dim) * sizeof(float);
+  return workspace_bytes_for(plan_for(num_seqs, num_heads, num_kv_heads, max_blocks_per_seq * block_size), head_dim);
 }
 
 int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
@@ -694,6 +830,7 @@ int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, c
   p.tables = block_tables;
   p.lens = context_lens;
   p.out = reinterpret_cast<__half*>(out);
+  p.num_seqs = num_seqs;
   p.num_heads = num_heads;
   p.num_kv_heads = num_kv_heads;
   p.group = num_heads / num_kv_heads;
@@ -703,8 +840,8 @@ int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, c
   p.scale_log2 = scale * 1.4426950408889634f;
   const Plan pl = plan_for(num_seqs, num_heads, num_kv_heads, max_blocks_per_seq * block_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int rc = head_dim == 128 ? launch<128>(p, pl, num_seqs, workspace, workspace_bytes, st)
-                                 : launch<64>(p, pl, num_seqs, workspace, workspace_bytes, st);
+  const int rc = head_dim == 128 ? launch<128>(p, pl, workspace, workspace_bytes, st)
+                                 : launch<64>(p, pl, workspace, workspace_bytes, st);
   if (rc == PKV_OK) pkv::clear_error();
   return rc;
 }
