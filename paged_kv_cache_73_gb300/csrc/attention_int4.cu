@@ -60,7 +60,10 @@ __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int NW = 4;                 // warps per CTA
 constexpr int CHUNK = 32;             // tokens a worker handles at a time
-constexpr int kResident = 3;          // CTAs per SM
+#ifndef V_RES
+#define V_RES 3
+#endif
+constexpr int kResident = V_RES;          // CTAs per SM
 constexpr int kMinChunks = 4;         // chunks a worker takes at least
 constexpr float kRescale = 8.f;       // the running maximum moves when a chunk passes it by this much
 
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(NW * 32, kResident) paged_attention_int4_kerne
 
   // this worker's piece of the line
   Place at;
-  long long left;
+  int left;
   {
     long long total = 0;
     bool bad = false;
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(NW * 32, kResident) paged_attention_int4_kerne
     if (bad && worker == 0) record_error(PKV_DEV_BAD_CONTEXT_LEN);
     const long long n = total * Y, per = per_worker(n, p.workers), x = worker * per;
     if (x >= n) return;
-    left = min(per, n - x);
+    left = static_cast<int>(min(per, n - x));
     // the sequence: the first whose chunks, all heads together, reach past x
     long long before = 0;
     int s = S, mine = 0;
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(NW * 32, kResident) paged_attention_int4_kerne
   const int v_lane = R::V_OFF + v_place<D>(piece_row, lane % (ROW / 16));
   const int meta_row = 4 * (lane & 7);
   Place ahead = at;
-  long long to_fill = left;
+  int to_fill = left;
   // table entries of 32 blocks around `ahead`, one a lane, and of the next 32; -1 past the context or bad
   int entry = -1, entry_next = -1;
   auto read_entry = [&](int first) {
@@ -396,12 +399,15 @@ __global__ void __launch_bounds__(NW * 32, kResident) paged_attention_int4_kerne
     return -1;
   };
   bool fresh = true;                                         // `ahead` is at a stream's first chunk here
+  int head_off = 0;                                          // of `ahead`'s cached head in a block
+  const uint8_t* meta_src = (lane & 8 ? p.v : p.k) + ROW * B + (meta_row % B) * 4;
   auto fill = [&](int stage) {
     if (to_fill > 0) {
       const int blk = ahead.c * BPC, first = blk & ~31;
       if (fresh) {
         entry = read_entry(first);
         entry_next = read_entry(first + 32);
+        head_off = ahead.y / p.head_tiles * tile_bytes;
         fresh = false;
       } else if (blk == first) {
         entry = entry_next;
@@ -409,26 +415,29 @@ __global__ void __launch_bounds__(NW * 32, kResident) paged_attention_int4_kerne
       }
       const int valid = ahead.len - ahead.c * CHUNK;
       const uint32_t dst = ring_u32 + stage * R::STAGE;
-      const int64_t head_off = static_cast<int64_t>(ahead.y / p.head_tiles) * tile_bytes;
+      // pieces of one block (or of one pair of blocks, a half of the lanes each) share an address
+      constexpr int PPB = B * ROW / 512 > 0 ? B * ROW / 512 : 1;
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        const int row = RPP * i + piece_row;
-        const int phys = __shfl_sync(FULL, entry, (blk & 31) + row / B);
-        if (row < valid) {
-          // a bad block's rows are zeros
-          const int64_t off = static_cast<int64_t>(max(phys, 0)) * block_bytes + head_off + (row % B) * ROW + piece_col;
-          const int bytes = phys >= 0 ? 16 : 0;
-          cp_async16(dst + lane * 16 + i * 512, p.k + off, bytes);
-          cp_async16(dst + v_lane + i * 512, p.v + off, bytes);
+      for (int i0 = 0; i0 < PIECES; i0 += PPB) {
+        const int row0 = RPP * i0 + piece_row;
+        const int phys = __shfl_sync(FULL, entry, (blk & 31) + row0 / B);
+        const int bytes = phys >= 0 ? 16 : 0;                // a bad block's rows are zeros
+        const int64_t off = static_cast<int64_t>(max(phys, 0)) * block_bytes + (head_off + (row0 % B) * ROW + piece_col);
+        const uint8_t* ks = p.k + off;
+        const uint8_t* vs = p.v + off;
+#pragma unroll
+        for (int i = i0; i < i0 + PPB; ++i) {
+          if (RPP * i + piece_row < valid) {
+            cp_async16(dst + lane * 16 + i * 512, ks + (i - i0) * 512, bytes);
+            cp_async16(dst + v_lane + i * 512, vs + (i - i0) * 512, bytes);
+          }
         }
       }
       {
         const int phys = __shfl_sync(FULL, entry, (blk & 31) + meta_row / B);
         if (lane < 16 && meta_row < valid)
           cp_async16(dst + R::META_OFF + lane * 16,
-                     (lane & 8 ? p.v : p.k) + static_cast<int64_t>(max(phys, 0)) * block_bytes + head_off + ROW * B +
-                         (meta_row % B) * 4,
-                     phys >= 0 ? 16 : 0);
+                     meta_src + (static_cast<int64_t>(max(phys, 0)) * block_bytes + head_off), phys >= 0 ? 16 : 0);
       }
       --to_fill;
       fresh = advance(ahead);
@@ -694,7 +703,7 @@ int device_sms() {
 // give every worker kMinChunks chunks.
 struct Plan {
   int nt, head_tiles, head_rows, ctas;
-  long long slots;
+  long long slots, most_chunks;
 };
 Plan plan_for(int num_seqs, int num_heads, int num_kv_heads, int max_ctx) {
   Plan pl{};
@@ -704,6 +713,7 @@ Plan plan_for(int num_seqs, int num_heads, int num_kv_heads, int max_ctx) {
   pl.head_rows = group < 8 * pl.nt ? group : 8 * pl.nt;
   const long long streams = static_cast<long long>(num_seqs) * num_kv_heads * pl.head_tiles;
   const long long chunks = streams * ((max_ctx + CHUNK - 1) / CHUNK);
+  pl.most_chunks = chunks;
   const long long ctas = (chunks + kMinChunks * NW - 1) / (kMinChunks * NW);
   const long long most = static_cast<long long>(device_sms()) * kResident;
   pl.ctas = static_cast<int>(ctas < most ? ctas : most);
@@ -839,6 +849,8 @@ int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, c
   while ((1 << p.log2_block) < block_size) ++p.log2_block;
   p.scale_log2 = scale * 1.4426950408889634f;
   const Plan pl = plan_for(num_seqs, num_heads, num_kv_heads, max_blocks_per_seq * block_size);
+  if (pl.most_chunks / (pl.ctas * NW) >= (1LL << 30))
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: more than 2^30 chunks of %d tokens per warp", fn, CHUNK);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int rc = head_dim == 128 ? launch<128>(p, pl, workspace, workspace_bytes, st)
                                  : launch<64>(p, pl, workspace, workspace_bytes, st);
