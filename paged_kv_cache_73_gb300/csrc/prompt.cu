@@ -17,11 +17,13 @@
 //    see the same keys, so a short prompt fills both tiles and none computes keys that
 //    only the other needs;
 //  * otherwise 256 queries of one head; the first tile stops at its own last key.
-// Key tiles of 64 positions come by TMA through a four-slot ring.  The tiles that some
-// row of the CTA does not see whole (the diagonal, and the one that holds the sequence's
-// end) are read through registers instead where V is concerned: rows past the end become
-// zeros, and values that are not finite become zeros too and are put back in the end for
-// the rows that see them, since a masked weight of 0 would make a NaN of them.
+// Key tiles of 64 positions come by TMA through a four-slot ring.  Where some row of the
+// CTA does not see a tile whole (the diagonal, and the tile that holds the sequence's end),
+// a warp first looks V's tile over: a masked weight of 0 times a value that is not finite
+// would be a NaN, so such values become zeros, and are put back in the end for the rows
+// that see them.
+// The grid is a flat list of query tiles (each CTA finds its sequence by a prefix sum over
+// query_start), so a batch of ragged prompts launches few CTAs that have nothing to do.
 //
 // Per 64-key tile and CTA the products take 2 x (768 + 512) / 2 = 1280 clocks: S is bound
 // by shared memory (an SS product of 128 x 64 x 16 reads 6 KB), PV by math.  Two S buffers
@@ -44,7 +46,7 @@ __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_
 constexpr int BM = 128;            // queries per query tile (MMA M)
 constexpr int BN = 64;             // keys per tile (S MMA N, PV MMA K)
 constexpr int NS = 4;              // ring slots each for K and for V
-constexpr int THREADS = 384;
+constexpr int THREADS = 416;
 constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
 constexpr uint32_t TMEM_COLS = 512, O_COL = 0, S_COL = 256;
 
@@ -56,7 +58,8 @@ struct PromptParams {
   const int32_t* kstart;
   __half* out;
   int64_t k_stride, v_stride;
-  int num_heads, group, pair;           // pair: the two query tiles are two heads
+  int num_seqs, num_heads, group, pair; // pair: the two query tiles are two heads
+  int max_tiles;                        // CTAs per sequence that max_query_len covers
   int total_q, total_k;
   float scale_log2;
 };
@@ -66,19 +69,20 @@ struct Cfg {
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
   // sized as for D = 128 whatever D is, so that one CTA (with all 512 tensor-memory columns) runs per SM
-  static constexpr int SMEM = 1024 + 2 * BM * 128 * 2 + 2 * NS * BN * 128 * 2 + 256;
+  static constexpr int SMEM = 1024 + 2 * BM * 128 * 2 + 2 * NS * BN * 128 * 2 + 512;
 };
 
 __device__ __forceinline__ bool finite16(unsigned h) { return (h & 0x7c00u) != 0x7c00u; }
 
-// Warp roles (12 warps):
+// Warp roles (13 warps):
 //   0-3 / 4-7  softmax of query tile 0 / 1: waits S(j), releases K slot j % 4, masks, takes the row
 //              maximum (moving the running one, and O, only past 2^8), writes P = 2^(S - m) as fp16
 //              over the scores and arrives on p_full
 //   8          one lane issues S_g(j) = Q_g K(j)^T once K(j) landed and PV_g(j - 2), the last reader
 //              of its buffer, is done
 //   11         one lane issues O_g += P_g(j) V(j) once V(j) and P_g(j) are there, then releases V
-//   9, 10      load K, V tiles into slot j % 4 once tile j - 4 is done with it
+//   9, 10      one lane loads K, V tiles into slot j % 4 once tile j - 4 is done with it
+//   12         looks the edge tiles' V over and passes them on to the PV issuer
 // Every wait is bounded; a role that gives up records PKV_DEV_WAIT_TIMEOUT and leaves its loop, the
 // others give up in turn, and the CTA still reaches its final barrier.
 template <int D>
@@ -97,31 +101,64 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
   auto v_full = [&](int b) { return bars + 96u + 8u * (NS + b); };
   auto k_free = [&](int b) { return bars + 96u + 8u * (2 * NS + b); };
   auto v_free = [&](int b) { return bars + 96u + 8u * (3 * NS + b); };
-  const uint32_t q_full = bars + 96 + 32 * NS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + 104 + 32 * NS - base));
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + 108 + 32 * NS - base));
-  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + 112 + 32 * NS - base));
-  static_assert(116 + 32 * NS <= 256, "barrier area");
+  auto v_ok = [&](int b) { return bars + 96u + 8u * (4 * NS + b); };     // edge tiles: looked over
+  auto v_issued = [&](int b) { return bars + 96u + 8u * (5 * NS + b); };  // edge tiles: their load is on its way
+  const uint32_t q_full = bars + 96 + 48 * NS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + 104 + 48 * NS - base));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + 108 + 48 * NS - base));
+  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + 112 + 48 * NS - base));
+  static_assert(116 + 48 * NS <= 512, "barrier area");
 
-  pkv::pdl_trigger();
-  pkv::pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = blockIdx.z, H = p.num_heads;
-  const int qt = gridDim.x - 1 - blockIdx.x;                  // the tiles that see the most keys first
+  pkv::pdl_trigger();
+  if (tid == 0) {
+    prefetch_tensormap(&p.tmap_q);
+    prefetch_tensormap(&p.tmap_k);
+    prefetch_tensormap(&p.tmap_v);
+  }
+  pkv::pdl_wait();
+  const int H = p.num_heads;
   const int h0 = p.pair ? 2 * blockIdx.y : blockIdx.y;        // the first query tile's head
   const int kvh = h0 / p.group;
+  const int rows = p.pair ? BM : 2 * BM;                      // queries per CTA
+  // this CTA's sequence and query tile, from the flat index blockIdx.x.  A sequence with a bad range
+  // takes one place, to be reported.
+  auto range_ok = [&](int s) {
+    const int q0 = p.qstart[s], n = p.qstart[s + 1] - q0, k0 = p.kstart[s], m = p.kstart[s + 1] - k0;
+    return n >= 0 && n <= m && q0 >= 0 && q0 <= p.total_q - n && k0 >= 0 && k0 <= p.total_k - m;
+  };
+  int s = -1, qt = 0, before = 0;
+  for (int first = 0; first < p.num_seqs && s < 0; first += 32) {
+    const int i = first + lane;
+    int tiles = 0;
+    if (i < p.num_seqs) {
+      const int n = p.qstart[i + 1] - p.qstart[i];
+      tiles = range_ok(i) ? min((n + rows - 1) / rows, p.max_tiles) : 1;
+    }
+    int upto = tiles;                                         // inclusive prefix sum over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > static_cast<int>(blockIdx.x));
+    if (past) {
+      const int hit = __ffs(past) - 1;
+      s = first + hit;
+      qt = __shfl_sync(0xffffffffu, before + upto, hit) - 1 - static_cast<int>(blockIdx.x);   // the last, which sees
+    }                                                                                          // the most keys, first
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (s < 0) return;
   const int q0 = p.qstart[s], n = p.qstart[s + 1] - q0;
   const int k0 = p.kstart[s], m = p.kstart[s + 1] - k0;
-  const int rows = p.pair ? BM : 2 * BM;                      // queries per CTA
-  const int i0 = qt * rows;
-  if (n < 0 || n > m || q0 < 0 || q0 > p.total_q - n || k0 < 0 || k0 > p.total_k - m) {
-    if (tid == 0 && qt == 0) record_error(PKV_DEV_BAD_QUERY_RANGE);
+  if (!range_ok(s)) {
+    if (tid == 0) record_error(PKV_DEV_BAD_QUERY_RANGE);
     return;
   }
-  // more queries than the grid covers (the caller's max_query_len understated them)
-  if (tid == 0 && qt == 0 && blockIdx.y == 0 && n > static_cast<int>(gridDim.x) * rows)
-    record_error(PKV_DEV_BAD_QUERY_RANGE);
-  if (i0 >= n) return;
+  const int i0 = qt * rows;
+  // more queries than max_query_len covers
+  if (tid == 0 && qt == 0 && blockIdx.y == 0 && (n - 1) / rows >= p.max_tiles) record_error(PKV_DEV_BAD_QUERY_RANGE);
   const int ntile = p.pair || i0 + BM < n ? 2 : 1;            // query tiles with real queries
   auto tile_row = [&](int g) { return i0 + (p.pair ? 0 : g * BM); };
   auto tile_head = [&](int g) { return h0 + (p.pair ? g : 0); };
@@ -148,8 +185,10 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
         mbar_init_count(pv_done(g, u), 1);
       }
     for (int b = 0; b < NS; ++b) {
-      mbar_init_count(k_full(b), 32);
-      mbar_init_count(v_full(b), 32);
+      mbar_init_count(k_full(b), 1);
+      mbar_init_count(v_full(b), 1);
+      mbar_init_count(v_ok(b), 1);
+      mbar_init_count(v_issued(b), 1);
       mbar_init_count(k_free(b), 4 * ntile);
       mbar_init_count(v_free(b), 1);
     }
@@ -177,71 +216,78 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
   float l = 0.f, m_ref = -INFINITY;
 
   if (warp == 9 || warp == 10) {
-    // ---------------- loads: warp 9 K tiles, warp 10 V tiles ----------------
-    const bool is_k = warp == 9;
-    const CUtensorMap* map = is_k ? &p.tmap_k : &p.tmap_v;
-    if (lane == 0) prefetch_tensormap(map);
-    const __half* src = (is_k ? p.k : p.v) + static_cast<int64_t>(kvh) * D;
-    const int64_t stride = is_k ? p.k_stride : p.v_stride;
-    // K's diagonal tiles need no care (their scores are masked); V's and the one with the end do
-    const int plain = is_k ? m / BN : edge;
-    int issued = 0;
-    for (int j = 0; j < n_tiles; ++j) {
+    // ---------------- loads: warp 9 K tiles, warp 10 V tiles (one lane) ----------------
+    // Rows past the sequence's end are its neighbour's (or zeros past the tensor): K's scores are masked,
+    // V's rows are looked over.
+    if (lane == 0) {
+      const bool is_k = warp == 9;
+      const CUtensorMap* map = is_k ? &p.tmap_k : &p.tmap_v;
+      int issued = 0;
+      for (int j = 0; j < n_tiles; ++j) {
+        const int b = j % NS;
+        if (j >= NS && !wait(is_k ? k_free(b) : v_free(b), (j / NS - 1) & 1)) {
+          failed = true;
+          break;
+        }
+        const uint32_t full = is_k ? k_full(b) : v_full(b);
+        const uint32_t dst = (is_k ? sk : sv) + b * C::KV_BYTES;
+        mbar_arrive_expect_tx(full, C::KV_BYTES);
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half)
+          tma_load_3d(dst + half * (BN * 128), map, half * 64, kvh, k0 + j * BN, full);
+        if (!is_k && j >= edge) mbar_arrive(v_issued(b));
+        ++issued;
+      }
+      if (failed) give_up();
+      if (*abort_flag) {
+        // let the copies this lane issued land (bounded) before the CTA's shared memory is released
+        for (int t = max(0, issued - NS); t < issued; ++t)
+          mbar_wait(is_k ? k_full(t % NS) : v_full(t % NS), (t / NS) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 12) {
+    // ---------------- the edge tiles' V: values that are not finite, and what is past the end ----------------
+    for (int j = edge; j < n_tiles; ++j) {
       const int b = j % NS;
-      if (j >= NS && !wait(is_k ? k_free(b) : v_free(b), (j / NS - 1) & 1)) {
+      // v_full's phase is this tile's only once its load is issued (tile j - 4 has landed by then): a
+      // wait for it before that could be for an earlier tile of the same parity
+      if (!__all_sync(0xffffffffu, wait(v_issued(b), ((j - edge) / NS) & 1) && wait(v_full(b), (j / NS) & 1))) {
         failed = true;
         break;
       }
-      const uint32_t full = is_k ? k_full(b) : v_full(b);
-      const uint32_t dst = (is_k ? sk : sv) + b * C::KV_BYTES;
-      if (j < plain) {
-        if (lane == 0) {
-          mbar_expect_tx(full, C::KV_BYTES);
+      unsigned char* tile = smem + (sv + b * C::KV_BYTES - base);
+      // 0 times a value is a NaN if the value is not finite; sums of those are NaN
+      const __half2 zero = __float2half2_rn(0.f);
+      __half2 acc[4] = {zero, zero, zero, zero};
+#pragma unroll 8
+      for (int c = lane; c < C::KV_BYTES / 16; c += 32) {
+        const uint4 x = *reinterpret_cast<const uint4*>(tile + c * 16);
+        acc[0] = __hfma2(*reinterpret_cast<const __half2*>(&x.x), zero, acc[0]);
+        acc[1] = __hfma2(*reinterpret_cast<const __half2*>(&x.y), zero, acc[1]);
+        acc[2] = __hfma2(*reinterpret_cast<const __half2*>(&x.z), zero, acc[2]);
+        acc[3] = __hfma2(*reinterpret_cast<const __half2*>(&x.w), zero, acc[3]);
+      }
+      const __half2 sum = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+      if (__any_sync(0xffffffffu, __hisnan(__low2half(sum)) || __hisnan(__high2half(sum)))) {
+        for (int c = lane; c < C::KV_BYTES / 16; c += 32) {
+          const int key = j * BN + (c / 8) % BN;              // 128-byte rows, a half of the head dimension each
+          unsigned* w = reinterpret_cast<unsigned*>(tile + c * 16);
 #pragma unroll
-          for (int half = 0; half < D / 64; ++half)
-            tma_load_3d(dst + half * (BN * 128), map, half * 64, kvh, k0 + j * BN, full);
-        }
-        __syncwarp();
-      } else {
-        constexpr int RPW = 32 / CPR;                         // rows per warp-wide load
-        constexpr int U = 16;                                 // loads in flight per lane
-        const int c = lane % CPR;
-        unsigned char* tile = smem + (dst - base);
-        for (int r0 = 0; r0 < BN; r0 += U * RPW) {
-          uint4 x[U];
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int t = j * BN + r0 + u * RPW + lane / CPR;
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (r0 + u * RPW < BN && t < m) x[u] = *reinterpret_cast<const uint4*>(src + (k0 + t) * stride + c * 8);
-          }
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (r0 + u * RPW >= BN) break;
-            if (!is_k) {
-              unsigned w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (!finite16(w[e]) || !finite16(w[e] >> 16)) {
-                  *not_finite = 1;
-                  w[e] = (finite16(w[e]) ? w[e] & 0xffffu : 0u) | (finite16(w[e] >> 16) ? w[e] & 0xffff0000u : 0u);
-                }
-              }
-              x[u] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int e = 0; e < 4; ++e) {
+            const unsigned x = w[e];
+            if (!finite16(x) || !finite16(x >> 16)) {
+              if (key < m) *not_finite = 1;
+              w[e] = (finite16(x) ? x & 0xffffu : 0u) | (finite16(x >> 16) ? x & 0xffff0000u : 0u);
             }
-            *reinterpret_cast<uint4*>(tile + sw128(r0 + u * RPW + lane / CPR, c, BN)) = x[u];
           }
         }
         fence_proxy_async_smem();                             // these stores -> tensor-core reads
       }
-      mbar_arrive(full);
-      ++issued;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_ok(b));
     }
     if (failed) give_up();
-    if (*abort_flag) {
-      // let the copies this warp issued land (bounded) before the CTA's shared memory is released
-      for (int t = max(0, issued - NS); t < issued; ++t) mbar_wait(is_k ? k_full(t % NS) : v_full(t % NS), (t / NS) & 1);
-    }
   } else if (warp == 8) {
     // ---------------- S = Q K^T issue (one lane) ----------------
     if (lane == 0) {
@@ -288,7 +334,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
       constexpr uint32_t IDESC_PV = umma_idesc_f16(BM, D, true);
       int issued[2] = {0, 0};
       for (int j = 0; j < n_tiles && !failed; ++j) {
-        if (!wait(v_full(j % NS), (j / NS) & 1)) {
+        if (!wait(v_full(j % NS), (j / NS) & 1) || (j >= edge && !wait(v_ok(j % NS), ((j - edge) / NS) & 1))) {
           failed = true;
           break;
         }
@@ -491,7 +537,7 @@ int encode_rows_map(CUtensorMap* map, const void* x, int D, int H, int T, int64_
 }
 
 template <int D>
-int launch(const PromptParams& p, int num_seqs, int max_query_len, cudaStream_t st) {
+int launch(PromptParams p, int max_query_len, cudaStream_t st) {
   static std::mutex mu;
   static bool done[64] = {false};
   int dev = 0;
@@ -505,7 +551,12 @@ int launch(const PromptParams& p, int num_seqs, int max_query_len, cudaStream_t 
   }
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention setup: %s", cudaGetErrorString(e));
   const int rows = p.pair ? BM : 2 * BM;
-  const dim3 grid((max_query_len - 1) / rows + 1, p.pair ? p.num_heads / 2 : p.num_heads, num_seqs);
+  p.max_tiles = (max_query_len - 1) / rows + 1;
+  // the tiles of num_seqs sequences that have total_q queries together, at most
+  const long long by_total = static_cast<long long>(p.total_q) / rows + p.num_seqs;
+  const long long by_longest = static_cast<long long>(p.max_tiles) * p.num_seqs;
+  const dim3 grid(static_cast<unsigned>(by_total < by_longest ? by_total : by_longest),
+                  p.pair ? p.num_heads / 2 : p.num_heads);
   e = pkv::launch_pdl(prompt_attention_kernel<D>, grid, dim3(THREADS), Cfg<D>::SMEM, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention launch: %s", cudaGetErrorString(e));
@@ -573,6 +624,7 @@ int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t*
   p.out = reinterpret_cast<__half*>(out);
   p.k_stride = key_stride;
   p.v_stride = value_stride;
+  p.num_seqs = num_seqs;
   p.num_heads = num_heads;
   p.group = num_heads / num_kv_heads;
   p.pair = p.group % 2 == 0 ? 1 : 0;
@@ -580,7 +632,7 @@ int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t*
   p.total_k = total_k;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  rc = head_dim == 128 ? launch<128>(p, num_seqs, max_query_len, st) : launch<64>(p, num_seqs, max_query_len, st);
+  rc = head_dim == 128 ? launch<128>(p, max_query_len, st) : launch<64>(p, max_query_len, st);
   if (rc == PKV_OK) pkv::clear_error();
   return rc;
 }
