@@ -11,23 +11,24 @@
 // 4 D flops per (query, key) pair that the mask leaves, against two rows read per
 // 128-query tile: bound by the tensor cores.  Scores and outputs live in tensor memory
 // (tcgen05.mma, fp16 in, fp32 accumulation); a softmax thread owns a query row, which is
-// a tensor-memory lane.  One CTA has two query tiles of 128 rows that share every K/V tile
-// it loads:
-//  * in a group with an even number of heads, two heads of the same 128 queries: both
-//    see the same keys, so a short prompt fills both tiles and none computes keys that
-//    only the other needs;
-//  * otherwise 256 queries of one head; the first tile stops at its own last key.
-// Key tiles of 64 positions come by TMA through a four-slot ring.  Where some row of the
-// CTA does not see a tile whole (the diagonal, and the tile that holds the sequence's end),
-// a warp first looks V's tile over: a masked weight of 0 times a value that is not finite
-// would be a NaN, so such values become zeros, and are put back in the end for the rows
-// that see them.
-// The grid is a flat list of query tiles (each CTA finds its sequence by a prefix sum over
-// query_start), so a batch of ragged prompts launches few CTAs that have nothing to do.
+// a tensor-memory lane.
+//  * One CTA takes 128 queries of one head, with a half of the tensor memory and of the
+//    shared memory, so two run on an SM: each hides the other's start, end and hand-offs.
+//    One CTA with two query tiles that share every K/V tile took 1187 us against 1074 for
+//    eight 4096-token prompts (40 heads on 8), and 126 against 101 for ragged short ones,
+//    where starts and ends are most of the time.
+//  * Key tiles of 64 positions come by TMA through a ring.  Where some row of the CTA does
+//    not see a tile whole (the diagonal, and the tile that holds the sequence's end), a
+//    warp first looks V's tile over: a masked weight of 0 times a value that is not finite
+//    would be a NaN, so such values become zeros, and are put back in the end for the rows
+//    that see them.
+//  * The grid is a flat list of query tiles (each CTA finds its sequence by a prefix sum
+//    over query_start), so a batch of ragged prompts launches few CTAs that have nothing
+//    to do.
 //
-// Per 64-key tile and CTA the products take 2 x (768 + 512) / 2 = 1280 clocks: S is bound
-// by shared memory (an SS product of 128 x 64 x 16 reads 6 KB), PV by math.  Two S buffers
-// per query tile keep S(j + 1) running under the softmax of tile j.
+// Per 128 x 64 tile the products take 384 + 256 clocks: S is bound by shared memory (an SS
+// product of 128 x 64 x 16 reads 6 KB), PV by math.  Two S buffers keep S(j + 1) running
+// under the softmax of tile j.
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -45,10 +46,7 @@ __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_
 
 constexpr int BM = 128;            // queries per query tile (MMA M)
 constexpr int BN = 64;             // keys per tile (S MMA N, PV MMA K)
-constexpr int NS = 4;              // ring slots each for K and for V
-constexpr int THREADS = 416;
 constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
-constexpr uint32_t TMEM_COLS = 512, O_COL = 0, S_COL = 256;
 
 struct PromptParams {
   CUtensorMap tmap_q, tmap_k, tmap_v;   // (D, heads, tokens), boxes of 64 x 1 x 128 (q) or 64, 128-byte swizzle
@@ -58,8 +56,8 @@ struct PromptParams {
   const int32_t* kstart;
   __half* out;
   int64_t k_stride, v_stride;
-  int num_seqs, num_heads, group, pair; // pair: the two query tiles are two heads
-  int max_tiles;                        // CTAs per sequence that max_query_len covers
+  int num_seqs, num_heads, group;
+  int max_tiles;                        // query tiles per sequence that max_query_len covers
   int total_q, total_k;
   float scale_log2;
 };
@@ -68,46 +66,54 @@ template <int D>
 struct Cfg {
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
-  // sized as for D = 128 whatever D is, so that one CTA (with all 512 tensor-memory columns) runs per SM
-  static constexpr int SMEM = 1024 + 2 * BM * 128 * 2 + 2 * NS * BN * 128 * 2 + 512;
+  static constexpr int NS = D == 64 ? 4 : 2;                  // ring slots each for K and for V
+  static constexpr int BYTES = 1024 + Q_BYTES + 2 * NS * KV_BYTES + 512;
+  // so much that no third CTA, which would wait for tensor memory, fits an SM
+  static constexpr int SMEM = BYTES > 80 * 1024 ? BYTES : 80 * 1024;
 };
+// Tensor memory: the O accumulator and two S buffers of 64 columns, a half of the SM's 512 columns.
+constexpr uint32_t TMEM_COLS = 256, O_COL = 0, S_COL = 128;
+constexpr int W_S = 4, W_LOAD = 5, W_CHECK = 6, W_PV = 7;     // warps 0 to 3: softmax
+constexpr int THREADS = 256;
 
 __device__ __forceinline__ bool finite16(unsigned h) { return (h & 0x7c00u) != 0x7c00u; }
 
-// Warp roles (13 warps):
-//   0-3 / 4-7  softmax of query tile 0 / 1: waits S(j), releases K slot j % 4, masks, takes the row
-//              maximum (moving the running one, and O, only past 2^8), writes P = 2^(S - m) as fp16
-//              over the scores and arrives on p_full
-//   8          one lane issues S_g(j) = Q_g K(j)^T once K(j) landed and PV_g(j - 2), the last reader
-//              of its buffer, is done
-//   11         one lane issues O_g += P_g(j) V(j) once V(j) and P_g(j) are there, then releases V
-//   9, 10      one lane loads K, V tiles into slot j % 4 once tile j - 4 is done with it
-//   12         looks the edge tiles' V over and passes them on to the PV issuer
+// Warp roles:
+//   0-3      softmax: waits S(j), releases K slot j % NS, masks, takes the row maximum (moving the
+//            running one, and O, only past 2^8), writes P = 2^(S - m) as fp16 over the scores and
+//            arrives on p_full
+//   W_S      one lane issues S(j) = Q K(j)^T once K(j) landed and PV(j - 2), the last reader of its
+//            buffer, is done
+//   W_PV     one lane issues O += P(j) V(j) once V(j) and P(j) are there, then releases V
+//   W_LOAD   one lane loads K and V tiles into slot j % NS once tile j - NS is done with it
+//   W_CHECK  looks the edge tiles' V over and passes them on to the PV issuer
 // Every wait is bounded; a role that gives up records PKV_DEV_WAIT_TIMEOUT and leaves its loop, the
 // others give up in turn, and the CTA still reaches its final barrier.
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __grid_constant__ PromptParams p) {
+__global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   using C = Cfg<D>;
+  constexpr int NS = C::NS;
   constexpr int CPR = D / 8;                                  // 16-byte chunks per row
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - raw);
-  const uint32_t sq = base, sk = sq + 2 * C::Q_BYTES, sv = sk + NS * C::KV_BYTES, bars = sv + NS * C::KV_BYTES;
-  auto s_full = [&](int g, int u) { return bars + 8u * (2 * g + u); };
-  auto p_full = [&](int g, int u) { return bars + 32u + 8u * (2 * g + u); };
-  auto pv_done = [&](int g, int u) { return bars + 64u + 8u * (2 * g + u); };
-  auto k_full = [&](int b) { return bars + 96u + 8u * b; };
-  auto v_full = [&](int b) { return bars + 96u + 8u * (NS + b); };
-  auto k_free = [&](int b) { return bars + 96u + 8u * (2 * NS + b); };
-  auto v_free = [&](int b) { return bars + 96u + 8u * (3 * NS + b); };
-  auto v_ok = [&](int b) { return bars + 96u + 8u * (4 * NS + b); };     // edge tiles: looked over
-  auto v_issued = [&](int b) { return bars + 96u + 8u * (5 * NS + b); };  // edge tiles: their load is on its way
-  const uint32_t q_full = bars + 96 + 48 * NS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + 104 + 48 * NS - base));
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + 108 + 48 * NS - base));
-  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + 112 + 48 * NS - base));
-  static_assert(116 + 48 * NS <= 512, "barrier area");
+  const uint32_t sq = base, sk = sq + C::Q_BYTES, sv = sk + NS * C::KV_BYTES, bars = sv + NS * C::KV_BYTES;
+  // per S buffer u (key tile j uses j % 2) and per ring slot b
+  auto s_full = [&](int u) { return bars + 8u * u; };
+  auto p_full = [&](int u) { return bars + 16u + 8u * u; };
+  auto pv_done = [&](int u) { return bars + 32u + 8u * u; };
+  auto k_full = [&](int b) { return bars + 48u + 8u * b; };
+  auto v_full = [&](int b) { return bars + 48u + 8u * (NS + b); };
+  auto k_free = [&](int b) { return bars + 48u + 8u * (2 * NS + b); };
+  auto v_free = [&](int b) { return bars + 48u + 8u * (3 * NS + b); };
+  auto v_ok = [&](int b) { return bars + 48u + 8u * (4 * NS + b); };     // edge tiles: looked over
+  auto v_issued = [&](int b) { return bars + 48u + 8u * (5 * NS + b); };  // edge tiles: their load is on its way
+  const uint32_t q_full = bars + 48 + 48 * NS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + 56 + 48 * NS - base));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + 60 + 48 * NS - base));
+  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + 64 + 48 * NS - base));
+  static_assert(68 + 48 * NS <= 512, "barrier area");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pkv::pdl_trigger();
@@ -118,9 +124,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
   }
   pkv::pdl_wait();
   const int H = p.num_heads;
-  const int h0 = p.pair ? 2 * blockIdx.y : blockIdx.y;        // the first query tile's head
-  const int kvh = h0 / p.group;
-  const int rows = p.pair ? BM : 2 * BM;                      // queries per CTA
+  const int h = blockIdx.y, kvh = h / p.group;
   // this CTA's sequence and query tile, from the flat index blockIdx.x.  A sequence with a bad range
   // takes one place, to be reported.
   auto range_ok = [&](int s) {
@@ -133,7 +137,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
     int tiles = 0;
     if (i < p.num_seqs) {
       const int n = p.qstart[i + 1] - p.qstart[i];
-      tiles = range_ok(i) ? min((n + rows - 1) / rows, p.max_tiles) : 1;
+      tiles = range_ok(i) ? min((n + BM - 1) / BM, p.max_tiles) : 1;
     }
     int upto = tiles;                                         // inclusive prefix sum over the lanes
 #pragma unroll
@@ -156,17 +160,11 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
     if (tid == 0) record_error(PKV_DEV_BAD_QUERY_RANGE);
     return;
   }
-  const int i0 = qt * rows;
+  const int i0 = qt * BM;
   // more queries than max_query_len covers
-  if (tid == 0 && qt == 0 && blockIdx.y == 0 && (n - 1) / rows >= p.max_tiles) record_error(PKV_DEV_BAD_QUERY_RANGE);
-  const int ntile = p.pair || i0 + BM < n ? 2 : 1;            // query tiles with real queries
-  auto tile_row = [&](int g) { return i0 + (p.pair ? 0 : g * BM); };
-  auto tile_head = [&](int g) { return h0 + (p.pair ? g : 0); };
-  // key tiles that query tile g sees, and the CTA's (those of its last query tile)
-  auto tiles_of = [&](int g) { return (m - n + min(tile_row(g) + BM, n) - 1) / BN + 1; };
-  const int n_tiles = tiles_of(ntile - 1);
-  const int tiles0 = tiles_of(0);
-  const int first_pos = m - n + i0;                           // the CTA's first query's position
+  if (tid == 0 && qt == 0 && blockIdx.y == 0 && (n - 1) / BM >= p.max_tiles) record_error(PKV_DEV_BAD_QUERY_RANGE);
+  const int first_pos = m - n + i0;                           // the first query's position
+  const int n_tiles = (m - n + min(i0 + BM, n) - 1) / BN + 1;
   // tiles from here on hold keys that some row does not see, or the sequence's end
   const int edge = min((first_pos + 1) / BN, m / BN);
 
@@ -178,35 +176,33 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
     tc_fence_before();
   }
   if (tid == 0) {
-    for (int g = 0; g < 2; ++g)
-      for (int u = 0; u < 2; ++u) {
-        mbar_init_count(s_full(g, u), 1);
-        mbar_init_count(p_full(g, u), 128);
-        mbar_init_count(pv_done(g, u), 1);
-      }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init_count(s_full(u), 1);
+      mbar_init_count(p_full(u), 128);
+      mbar_init_count(pv_done(u), 1);
+    }
     for (int b = 0; b < NS; ++b) {
       mbar_init_count(k_full(b), 1);
       mbar_init_count(v_full(b), 1);
       mbar_init_count(v_ok(b), 1);
       mbar_init_count(v_issued(b), 1);
-      mbar_init_count(k_free(b), 4 * ntile);
+      mbar_init_count(k_free(b), 4);
       mbar_init_count(v_free(b), 1);
     }
     *abort_flag = 0;
     *not_finite = 0;
     mbar_init_count(q_full, 1);
-    mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(ntile) * C::Q_BYTES);
+    mbar_arrive_expect_tx(q_full, C::Q_BYTES);
     // rows past the sequence's queries read the next one's (or zeros past the tensor): never stored
-    for (int g = 0; g < ntile; ++g)
 #pragma unroll
-      for (int half = 0; half < D / 64; ++half)
-        tma_load_3d(sq + g * C::Q_BYTES + half * (BM * 128), &p.tmap_q, half * 64, tile_head(g), q0 + tile_row(g), q_full);
+    for (int half = 0; half < D / 64; ++half)
+      tma_load_3d(sq + half * (BM * 128), &p.tmap_q, half * 64, h, q0 + i0, q_full);
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto t_s = [&](int g, int u) { return tmem + S_COL + 128u * g + 64u * u; };
-  auto t_o = [&](int g) { return tmem + O_COL + 128u * g; };
+  auto t_s = [&](int u) { return tmem + S_COL + 64u * u; };
+  const uint32_t t_o = tmem + O_COL;
   auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_or_abort(bar, parity, abort_flag); };
   auto give_up = [&]() {
     if (!*abort_flag) record_error(PKV_DEV_WAIT_TIMEOUT);
@@ -215,42 +211,47 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
   bool failed = false;
   float l = 0.f, m_ref = -INFINITY;
 
-  if (warp == 9 || warp == 10) {
-    // ---------------- loads: warp 9 K tiles, warp 10 V tiles (one lane) ----------------
+  if (warp == W_LOAD) {
+    // ---------------- loads (one lane) ----------------
     // Rows past the sequence's end are its neighbour's (or zeros past the tensor): K's scores are masked,
     // V's rows are looked over.
     if (lane == 0) {
-      const bool is_k = warp == 9;
-      const CUtensorMap* map = is_k ? &p.tmap_k : &p.tmap_v;
-      int issued = 0;
+      int k_issued = 0, v_issued_n = 0;
       for (int j = 0; j < n_tiles; ++j) {
         const int b = j % NS;
-        if (j >= NS && !wait(is_k ? k_free(b) : v_free(b), (j / NS - 1) & 1)) {
+        if (j >= NS && !wait(k_free(b), (j / NS - 1) & 1)) {
           failed = true;
           break;
         }
-        const uint32_t full = is_k ? k_full(b) : v_full(b);
-        const uint32_t dst = (is_k ? sk : sv) + b * C::KV_BYTES;
-        mbar_arrive_expect_tx(full, C::KV_BYTES);
+        mbar_arrive_expect_tx(k_full(b), C::KV_BYTES);
 #pragma unroll
         for (int half = 0; half < D / 64; ++half)
-          tma_load_3d(dst + half * (BN * 128), map, half * 64, kvh, k0 + j * BN, full);
-        if (!is_k && j >= edge) mbar_arrive(v_issued(b));
-        ++issued;
+          tma_load_3d(sk + b * C::KV_BYTES + half * (BN * 128), &p.tmap_k, half * 64, kvh, k0 + j * BN, k_full(b));
+        ++k_issued;
+        if (j >= NS && !wait(v_free(b), (j / NS - 1) & 1)) {
+          failed = true;
+          break;
+        }
+        mbar_arrive_expect_tx(v_full(b), C::KV_BYTES);
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half)
+          tma_load_3d(sv + b * C::KV_BYTES + half * (BN * 128), &p.tmap_v, half * 64, kvh, k0 + j * BN, v_full(b));
+        if (j >= edge) mbar_arrive(v_issued(b));
+        ++v_issued_n;
       }
       if (failed) give_up();
       if (*abort_flag) {
         // let the copies this lane issued land (bounded) before the CTA's shared memory is released
-        for (int t = max(0, issued - NS); t < issued; ++t)
-          mbar_wait(is_k ? k_full(t % NS) : v_full(t % NS), (t / NS) & 1);
+        for (int t = max(0, k_issued - NS); t < k_issued; ++t) mbar_wait(k_full(t % NS), (t / NS) & 1);
+        for (int t = max(0, v_issued_n - NS); t < v_issued_n; ++t) mbar_wait(v_full(t % NS), (t / NS) & 1);
       }
     }
     __syncwarp();
-  } else if (warp == 12) {
+  } else if (warp == W_CHECK) {
     // ---------------- the edge tiles' V: values that are not finite, and what is past the end ----------------
     for (int j = edge; j < n_tiles; ++j) {
       const int b = j % NS;
-      // v_full's phase is this tile's only once its load is issued (tile j - 4 has landed by then): a
+      // v_full's phase is this tile's only once its load is issued (tile j - NS has landed by then): a
       // wait for it before that could be for an earlier tile of the same parity
       if (!__all_sync(0xffffffffu, wait(v_issued(b), ((j - edge) / NS) & 1) && wait(v_full(b), (j / NS) & 1))) {
         failed = true;
@@ -288,111 +289,85 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
       if (lane == 0) mbar_arrive(v_ok(b));
     }
     if (failed) give_up();
-  } else if (warp == 8) {
+  } else if (warp == W_S) {
     // ---------------- S = Q K^T issue (one lane) ----------------
     if (lane == 0) {
       constexpr uint32_t IDESC_QK = umma_idesc_f16(BM, BN, false);
-      const uint64_t a_desc0 = umma_smem_desc(sq, 16, 1024), a_desc1 = umma_smem_desc(sq + C::Q_BYTES, 16, 1024);
-      int issued[2] = {0, 0};
+      const uint64_t a0 = umma_smem_desc(sq, 16, 1024);
+      int issued = 0;
       failed = !wait(q_full, 0);
       for (int j = 0; j < n_tiles && !failed; ++j) {
-        if (!wait(k_full(j % NS), (j / NS) & 1)) {
+        const int u = j & 1;
+        if (!wait(k_full(j % NS), (j / NS) & 1) || (j >= 2 && !wait(pv_done(u), ((j - 2) >> 1) & 1))) {
           failed = true;
           break;
         }
-        const int u = j & 1;
+        tc_fence_after();
         const uint64_t b0 = umma_smem_desc(sk + (j % NS) * C::KV_BYTES, 16, 1024);
-        for (int g = 0; g < ntile; ++g) {
-          if (j >= 2 && !wait(pv_done(g, u), ((j - 2) >> 1) & 1)) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
-          if (g != 0 || j < tiles0) {                         // past its last key, tile 0 only keeps step
-            const uint64_t a0 = g == 0 ? a_desc0 : a_desc1;
-            const uint32_t d = t_s(g, u);
-            umma_ss(d, a0, b0, IDESC_QK, 0u);
+        const uint32_t d = t_s(u);
+        umma_ss(d, a0, b0, IDESC_QK, 0u);
 #pragma unroll
-            for (int kk = 1; kk < D / 16; ++kk)
-              umma_ss(d, a0 + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4),
-                      b0 + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), IDESC_QK, 1u);
-          }
-          umma_commit(s_full(g, u));
-          ++issued[g];
-        }
+        for (int kk = 1; kk < D / 16; ++kk)
+          umma_ss(d, a0 + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4), b0 + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4),
+                  IDESC_QK, 1u);
+        umma_commit(s_full(u));
+        ++issued;
       }
       if (failed) {
         give_up();
-        for (int g = 0; g < ntile; ++g)
-          if (issued[g] > 0) mbar_wait(s_full(g, (issued[g] - 1) & 1), ((issued[g] - 1) >> 1) & 1);
+        if (issued > 0) mbar_wait(s_full((issued - 1) & 1), ((issued - 1) >> 1) & 1);
       }
     }
     __syncwarp();
-  } else if (warp == 11) {
+  } else if (warp == W_PV) {
     // ---------------- O += P V issue (one lane) ----------------
     if (lane == 0) {
       constexpr uint32_t IDESC_PV = umma_idesc_f16(BM, D, true);
-      int issued[2] = {0, 0};
-      for (int j = 0; j < n_tiles && !failed; ++j) {
-        if (!wait(v_full(j % NS), (j / NS) & 1) || (j >= edge && !wait(v_ok(j % NS), ((j - edge) / NS) & 1))) {
+      int issued = 0;
+      for (int j = 0; j < n_tiles; ++j) {
+        const int u = j & 1;
+        if (!wait(v_full(j % NS), (j / NS) & 1) || (j >= edge && !wait(v_ok(j % NS), ((j - edge) / NS) & 1)) ||
+            !wait(p_full(u), (j >> 1) & 1)) {
           failed = true;
           break;
         }
-        const int u = j & 1;
+        tc_fence_after();
         const uint64_t v0 = umma_smem_desc(sv + (j % NS) * C::KV_BYTES, BN * 128, 1024);
-        for (int g = 0; g < ntile; ++g) {
-          if (!wait(p_full(g, u), (j >> 1) & 1)) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
-          if (g != 0 || j < tiles0) {
-            const uint32_t o = t_o(g), pa = t_s(g, u);
-            umma_ts(o, pa, v0, IDESC_PV, j > 0 ? 1u : 0u);
+        const uint32_t pa = t_s(u);
+        umma_ts(t_o, pa, v0, IDESC_PV, j > 0 ? 1u : 0u);
 #pragma unroll
-            for (int kk = 1; kk < BN / 16; ++kk) umma_ts(o, pa + kk * 8, v0 + ((kk * 16 * 128) >> 4), IDESC_PV, 1u);
-          }
-          umma_commit(pv_done(g, u));
-          ++issued[g];
-        }
-        if (failed) break;
+        for (int kk = 1; kk < BN / 16; ++kk) umma_ts(t_o, pa + kk * 8, v0 + ((kk * 16 * 128) >> 4), IDESC_PV, 1u);
+        umma_commit(pv_done(u));
+        ++issued;
         umma_commit(v_free(j % NS));
       }
       if (failed) {
         give_up();
-        for (int g = 0; g < ntile; ++g)
-          if (issued[g] > 0) mbar_wait(pv_done(g, (issued[g] - 1) & 1), ((issued[g] - 1) >> 1) & 1);
+        if (issued > 0) mbar_wait(pv_done((issued - 1) & 1), ((issued - 1) >> 1) & 1);
       }
     }
     __syncwarp();
-  } else if (warp < 4 * ntile) {
+  } else {
     // ---------------- softmax ----------------
-    const int g = warp >> 2;
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t to = t_o(g);
-    const int tile_first = m - n + tile_row(g);               // the query tile's first position
-    const int pos = tile_first + (tid & (BM - 1));
-    const int my_tiles = g == 0 ? tiles0 : n_tiles;
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t to = t_o;
+    const int pos = first_pos + tid;
     for (int j = 0; j < n_tiles; ++j) {
       // decisions stay warp-uniform: the tcgen05.ld/st below are warp-collective
       const int u = j & 1;
-      const uint32_t ts = t_s(g, u);
-      if (!__all_sync(0xffffffffu, wait(s_full(g, u), (j >> 1) & 1))) {
+      const uint32_t ts = t_s(u);
+      if (!__all_sync(0xffffffffu, wait(s_full(u), (j >> 1) & 1))) {
         failed = true;
         break;
       }
       tc_fence_after();
       if (lane == 0) mbar_arrive(k_free(j % NS));
-      if (j >= my_tiles) {                                    // no product was issued
-        mbar_arrive(p_full(g, u));
-        continue;
-      }
       float sv_[BN];
       tmem_ld32_nowait(ts + lane_off, *reinterpret_cast<float(*)[32]>(sv_));
       tmem_ld32_nowait(ts + lane_off + 32, *reinterpret_cast<float(*)[32]>(sv_ + 32));
       tmem_ld_wait();
       const int key0 = j * BN;
-      if (key0 + BN - 1 > tile_first) {                       // keys after the query (and past the end)
+      if (key0 + BN - 1 > first_pos) {                       // keys after the query (and past the end)
 #pragma unroll
         for (int c = 0; c < BN; ++c)
           if (key0 + c > pos) sv_[c] = -INFINITY;
@@ -414,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
       }
       const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
       if (__any_sync(0xffffffffu, rescale && j > 0)) {
-        if (!__all_sync(0xffffffffu, wait(pv_done(g, (j - 1) & 1), ((j - 1) >> 1) & 1))) {
+        if (!__all_sync(0xffffffffu, wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1))) {
           failed = true;
           break;
         }
@@ -446,10 +421,10 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
       l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(p_full(g, u));
+      mbar_arrive(p_full(u));
     }
     if (!failed) {
-      failed = !__all_sync(0xffffffffu, wait(pv_done(g, (n_tiles - 1) & 1), ((n_tiles - 1) >> 1) & 1));
+      failed = !__all_sync(0xffffffffu, wait(pv_done((n_tiles - 1) & 1), ((n_tiles - 1) >> 1) & 1));
       tc_fence_after();
     }
     if (failed) give_up();
@@ -458,23 +433,22 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
   // ---------------- epilogue ----------------
   __syncthreads();
   const bool aborted = *abort_flag != 0;
-  if (warp < 4 * ntile && !aborted) {
+  if (warp < 4 && !aborted) {
     // each thread normalises its O row and stages it in the K/V ring (every MMA is done), chunks XOR-ed
     // with the row's low bits; the warp then stores whole rows
-    const int g = warp >> 2;
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     const float inv = 1.f / l;                                // a query sees its own key at least
-    unsigned char* stage = smem + (sk - base);                // [256 rows][D * 2 bytes]
+    unsigned char* stage = smem + (sk - base);                // [128 rows][D * 2 bytes]
     constexpr int RB = D * 2;
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       float o[32];
-      tmem_ld32(t_o(g) + lane_off + c * 32, o);
+      tmem_ld32(t_o + lane_off + c * 32, o);
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] *= inv;
       if (*not_finite) {
         // values that are not finite in the edge tiles were left out: add them where they are seen
-        const int pos = min(m - n + tile_row(g) + (tid & (BM - 1)), m - 1);
+        const int pos = min(first_pos + tid, m - 1);
         for (int t = edge * BN; t <= pos; ++t) {
           const __half* row = p.v + (k0 + t) * p.v_stride + static_cast<int64_t>(kvh) * D + c * 32;
 #pragma unroll
@@ -501,10 +475,10 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_attention_kernel(const __gr
 #pragma unroll 4
     for (int r0 = 0; r0 < 32; r0 += RPI) {
       const int row = warp * 32 + r0 + lane / CPR;            // CTA row
-      const int i = tile_row(g) + (row & (BM - 1));
+      const int i = i0 + row;
       if (i < n) {
         const uint4 w = *reinterpret_cast<const uint4*>(stage + row * RB + ((c ^ (row & (CPR - 1))) << 4));
-        *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(q0 + i) * H + tile_head(g)) * D + c * 8) = w;
+        *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(q0 + i) * H + h) * D + c * 8) = w;
       }
     }
   }
@@ -538,6 +512,7 @@ int encode_rows_map(CUtensorMap* map, const void* x, int D, int H, int T, int64_
 
 template <int D>
 int launch(PromptParams p, int max_query_len, cudaStream_t st) {
+  using C = Cfg<D>;
   static std::mutex mu;
   static bool done[64] = {false};
   int dev = 0;
@@ -545,19 +520,18 @@ int launch(PromptParams p, int max_query_len, cudaStream_t st) {
   if (e == cudaSuccess) {
     std::lock_guard<std::mutex> g(mu);
     if (dev < 0 || dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(prompt_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+      e = cudaFuncSetAttribute(prompt_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
       if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
     }
   }
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention setup: %s", cudaGetErrorString(e));
-  const int rows = p.pair ? BM : 2 * BM;
-  p.max_tiles = (max_query_len - 1) / rows + 1;
+  p.max_tiles = (max_query_len - 1) / BM + 1;
   // the tiles of num_seqs sequences that have total_q queries together, at most
-  const long long by_total = static_cast<long long>(p.total_q) / rows + p.num_seqs;
+  const long long by_total = static_cast<long long>(p.total_q) / BM + p.num_seqs;
   const long long by_longest = static_cast<long long>(p.max_tiles) * p.num_seqs;
   const dim3 grid(static_cast<unsigned>(by_total < by_longest ? by_total : by_longest),
-                  p.pair ? p.num_heads / 2 : p.num_heads);
-  e = pkv::launch_pdl(prompt_attention_kernel<D>, grid, dim3(THREADS), Cfg<D>::SMEM, st, p);
+                  p.num_heads);
+  e = pkv::launch_pdl(prompt_attention_kernel<D>, grid, dim3(THREADS), C::SMEM, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention launch: %s", cudaGetErrorString(e));
   return PKV_OK;
@@ -627,7 +601,6 @@ int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t*
   p.num_seqs = num_seqs;
   p.num_heads = num_heads;
   p.group = num_heads / num_kv_heads;
-  p.pair = p.group % 2 == 0 ? 1 : 0;
   p.total_q = total_q;
   p.total_k = total_k;
   p.scale_log2 = scale * 1.4426950408889634f;
