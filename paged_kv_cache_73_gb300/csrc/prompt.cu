@@ -22,9 +22,12 @@
 //    warp first looks V's tile over: a masked weight of 0 times a value that is not finite
 //    would be a NaN, so such values become zeros, and are put back in the end for the rows
 //    that see them.
-//  * The grid is a flat list of query tiles (each CTA finds its sequence by a prefix sum
-//    over query_start), so a batch of ragged prompts launches few CTAs that have nothing
-//    to do.
+//  * The grid is a flat list of query tiles (a tile's sequence is found by a prefix sum over
+//    query_start), so a batch of ragged prompts launches few CTAs that have nothing to do.
+//  * A CTA that runs takes over tiles of CTAs not launched yet (clusterlaunchcontrol), and its
+//    roles pass from one tile to the next on their own: the next tile's K and V are loaded
+//    and its first scores computed while the softmax warps write the last tile's output.
+//    One launch per tile spent 4.3 us of 7.7 on starts and ends where prompts are short.
 //
 // Per 128 x 64 tile the products take 384 + 256 clocks: S is bound by shared memory (an SS
 // product of 128 x 64 x 16 reads 6 KB), PV by math.  Two S buffers keep S(j + 1) running
@@ -62,12 +65,14 @@ struct PromptParams {
   float scale_log2;
 };
 
+constexpr int STAGE_BYTES = 32 * 64;                          // a warp's staging of 32 rows x 32 output columns
+
 template <int D>
 struct Cfg {
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
   static constexpr int NS = D == 64 ? 4 : 2;                  // ring slots each for K and for V
-  static constexpr int BYTES = 1024 + Q_BYTES + 2 * NS * KV_BYTES + 512;
+  static constexpr int BYTES = 1024 + Q_BYTES + 2 * NS * KV_BYTES + 4 * STAGE_BYTES + 512;
   // so much that no third CTA, which would wait for tensor memory, fits an SM
   static constexpr int SMEM = BYTES > 80 * 1024 ? BYTES : 80 * 1024;
 };
@@ -78,96 +83,84 @@ constexpr int THREADS = 256;
 
 __device__ __forceinline__ bool finite16(unsigned h) { return (h & 0x7c00u) != 0x7c00u; }
 
+// A query tile: its first row of q and out, the rows that are its sequence's, the first one's position
+// among the keys; the sequence's first key and their number; key tiles to visit, the first edge tile.
+struct Item {
+  int q_row, rows, first_pos, k_row, keys, n_tiles, edge, head;
+};
+
+// ---- taking over a CTA that was not launched yet -------------------------------------------------
+// The answer, 16 bytes at `answer`, arrives as a transaction on `bar`.
+__device__ __forceinline__ void try_cancel(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   answer),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool cancelled(uint32_t answer, int& x, int& y) {
+  uint32_t ok, cx, cy;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%3];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, r;\n\t}"
+      : "=r"(ok), "=r"(cx), "=r"(cy)
+      : "r"(answer)
+      : "memory");
+  x = static_cast<int>(cx);
+  y = static_cast<int>(cy);
+  return ok != 0;
+}
+
 // Warp roles:
-//   0-3      softmax: waits S(j), releases K slot j % NS, masks, takes the row maximum (moving the
-//            running one, and O, only past 2^8), writes P = 2^(S - m) as fp16 over the scores and
-//            arrives on p_full
+//   0-3      softmax: waits S(j), releases K slot, masks, takes the row maximum (moving the running
+//            one, and O, only past 2^8), writes P = 2^(S - m) as fp16 over the scores and arrives on
+//            p_full; after an item's last tile, its output
 //   W_S      one lane issues S(j) = Q K(j)^T once K(j) landed and PV(j - 2), the last reader of its
 //            buffer, is done
 //   W_PV     one lane issues O += P(j) V(j) once V(j) and P(j) are there, then releases V
-//   W_LOAD   one lane loads K and V tiles into slot j % NS once tile j - NS is done with it
+//   W_LOAD   finds the next item and one lane loads its Q and its K and V tiles into the ring
 //   W_CHECK  looks the edge tiles' V over and passes them on to the PV issuer
-// Every wait is bounded; a role that gives up records PKV_DEV_WAIT_TIMEOUT and leaves its loop, the
-// others give up in turn, and the CTA still reaches its final barrier.
+// Key tiles are numbered through all of a CTA's items (j above), items too; every hand-off is an
+// mbarrier, and no waiter is more than one phase behind the barrier it waits on.  Every wait is
+// bounded; a role that gives up records PKV_DEV_WAIT_TIMEOUT and leaves its loop, the others give up
+// in turn, and the CTA still reaches its final barrier.
 template <int D>
 __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   using C = Cfg<D>;
   constexpr int NS = C::NS;
-  constexpr int CPR = D / 8;                                  // 16-byte chunks per row
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - raw);
-  const uint32_t sq = base, sk = sq + C::Q_BYTES, sv = sk + NS * C::KV_BYTES, bars = sv + NS * C::KV_BYTES;
-  // per S buffer u (key tile j uses j % 2) and per ring slot b
+  const uint32_t sq = base, sk = sq + C::Q_BYTES, sv = sk + NS * C::KV_BYTES, so = sv + NS * C::KV_BYTES;
+  const uint32_t bars = so + 4 * STAGE_BYTES;
+  // per S buffer u (key tile j uses j % 2), per ring slot b, per item slot i (item number % 2)
   auto s_full = [&](int u) { return bars + 8u * u; };
   auto p_full = [&](int u) { return bars + 16u + 8u * u; };
   auto pv_done = [&](int u) { return bars + 32u + 8u * u; };
-  auto k_full = [&](int b) { return bars + 48u + 8u * b; };
-  auto v_full = [&](int b) { return bars + 48u + 8u * (NS + b); };
-  auto k_free = [&](int b) { return bars + 48u + 8u * (2 * NS + b); };
-  auto v_free = [&](int b) { return bars + 48u + 8u * (3 * NS + b); };
-  auto v_ok = [&](int b) { return bars + 48u + 8u * (4 * NS + b); };     // edge tiles: looked over
-  auto v_issued = [&](int b) { return bars + 48u + 8u * (5 * NS + b); };  // edge tiles: their load is on its way
-  const uint32_t q_full = bars + 48 + 48 * NS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + 56 + 48 * NS - base));
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + 60 + 48 * NS - base));
-  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + 64 + 48 * NS - base));
-  static_assert(68 + 48 * NS <= 512, "barrier area");
+  auto item_full = [&](int i) { return bars + 48u + 8u * i; };
+  auto item_free = [&](int i) { return bars + 64u + 8u * i; };
+  const uint32_t q_full = bars + 80, q_free = bars + 88, o_free = bars + 96, answered = bars + 104;
+  auto k_full = [&](int b) { return bars + 112u + 8u * b; };
+  auto v_full = [&](int b) { return bars + 112u + 8u * (NS + b); };
+  auto k_free = [&](int b) { return bars + 112u + 8u * (2 * NS + b); };
+  auto v_free = [&](int b) { return bars + 112u + 8u * (3 * NS + b); };
+  auto v_ok = [&](int b) { return bars + 112u + 8u * (4 * NS + b); };     // edge tiles: looked over
+  auto v_issued = [&](int b) { return bars + 112u + 8u * (5 * NS + b); };  // edge tiles: their load is on its way
+  constexpr uint32_t AT = 112 + 48 * NS;                      // 16-byte aligned
+  const uint32_t answer = bars + AT;
+  volatile Item* items = reinterpret_cast<volatile Item*>(smem + (bars + AT + 16 - base));            // [2]
+  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + AT + 80 - base));         // [2]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + AT + 88 - base));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + AT + 92 - base));
+  static_assert(sizeof(Item) == 32 && AT % 16 == 0 && AT + 96 <= 512, "barrier area");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pkv::pdl_trigger();
-  if (tid == 0) {
-    prefetch_tensormap(&p.tmap_q);
-    prefetch_tensormap(&p.tmap_k);
-    prefetch_tensormap(&p.tmap_v);
-  }
-  pkv::pdl_wait();
-  const int H = p.num_heads;
-  const int h = blockIdx.y, kvh = h / p.group;
-  // this CTA's sequence and query tile, from the flat index blockIdx.x.  A sequence with a bad range
-  // takes one place, to be reported.
-  auto range_ok = [&](int s) {
-    const int q0 = p.qstart[s], n = p.qstart[s + 1] - q0, k0 = p.kstart[s], m = p.kstart[s + 1] - k0;
-    return n >= 0 && n <= m && q0 >= 0 && q0 <= p.total_q - n && k0 >= 0 && k0 <= p.total_k - m;
-  };
-  int s = -1, qt = 0, before = 0;
-  for (int first = 0; first < p.num_seqs && s < 0; first += 32) {
-    const int i = first + lane;
-    int tiles = 0;
-    if (i < p.num_seqs) {
-      const int n = p.qstart[i + 1] - p.qstart[i];
-      tiles = range_ok(i) ? min((n + BM - 1) / BM, p.max_tiles) : 1;
-    }
-    int upto = tiles;                                         // inclusive prefix sum over the lanes
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, before + upto > static_cast<int>(blockIdx.x));
-    if (past) {
-      const int hit = __ffs(past) - 1;
-      s = first + hit;
-      qt = __shfl_sync(0xffffffffu, before + upto, hit) - 1 - static_cast<int>(blockIdx.x);   // the last, which sees
-    }                                                                                          // the most keys, first
-    before += __shfl_sync(0xffffffffu, upto, 31);
-  }
-  if (s < 0) return;
-  const int q0 = p.qstart[s], n = p.qstart[s + 1] - q0;
-  const int k0 = p.kstart[s], m = p.kstart[s + 1] - k0;
-  if (!range_ok(s)) {
-    if (tid == 0) record_error(PKV_DEV_BAD_QUERY_RANGE);
-    return;
-  }
-  const int i0 = qt * BM;
-  // more queries than max_query_len covers
-  if (tid == 0 && qt == 0 && blockIdx.y == 0 && (n - 1) / BM >= p.max_tiles) record_error(PKV_DEV_BAD_QUERY_RANGE);
-  const int first_pos = m - n + i0;                           // the first query's position
-  const int n_tiles = (m - n + min(i0 + BM, n) - 1) / BN + 1;
-  // tiles from here on hold keys that some row does not see, or the sequence's end
-  const int edge = min((first_pos + 1) / BN, m / BN);
-
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(TMEM_COLS)
@@ -175,29 +168,34 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
-  if (tid == 0) {
+  if (tid == 32) {
     for (int u = 0; u < 2; ++u) {
       mbar_init_count(s_full(u), 1);
       mbar_init_count(p_full(u), 128);
       mbar_init_count(pv_done(u), 1);
+      mbar_init_count(item_full(u), 1);
+      mbar_init_count(item_free(u), 7);                       // 4 softmax warps, both issuers, the checker
     }
+    mbar_init_count(q_full, 1);
+    mbar_init_count(q_free, 1);
+    mbar_init_count(o_free, 4);
+    mbar_init_count(answered, 1);
     for (int b = 0; b < NS; ++b) {
       mbar_init_count(k_full(b), 1);
       mbar_init_count(v_full(b), 1);
-      mbar_init_count(v_ok(b), 1);
-      mbar_init_count(v_issued(b), 1);
       mbar_init_count(k_free(b), 4);
       mbar_init_count(v_free(b), 1);
+      mbar_init_count(v_ok(b), 1);
+      mbar_init_count(v_issued(b), 1);
     }
     *abort_flag = 0;
-    *not_finite = 0;
-    mbar_init_count(q_full, 1);
-    mbar_arrive_expect_tx(q_full, C::Q_BYTES);
-    // rows past the sequence's queries read the next one's (or zeros past the tensor): never stored
-#pragma unroll
-    for (int half = 0; half < D / 64; ++half)
-      tma_load_3d(sq + half * (BM * 128), &p.tmap_q, half * 64, h, q0 + i0, q_full);
   }
+  if (tid == 64) {
+    prefetch_tensormap(&p.tmap_q);
+    prefetch_tensormap(&p.tmap_k);
+    prefetch_tensormap(&p.tmap_v);
+  }
+  pkv::pdl_wait();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -208,85 +206,225 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
     if (!*abort_flag) record_error(PKV_DEV_WAIT_TIMEOUT);
     *abort_flag = 1;
   };
+  // the next item, once it is there; n_tiles 0 ends the loop
+  auto take_item = [&](int it, Item& item) {
+    if (!wait(item_full(it & 1), (it >> 1) & 1)) return false;
+    const volatile Item& x = items[it & 1];
+    item.q_row = x.q_row;
+    item.rows = x.rows;
+    item.first_pos = x.first_pos;
+    item.k_row = x.k_row;
+    item.keys = x.keys;
+    item.n_tiles = x.n_tiles;
+    item.edge = x.edge;
+    item.head = x.head;
+    return true;
+  };
   bool failed = false;
-  float l = 0.f, m_ref = -INFINITY;
 
   if (warp == W_LOAD) {
-    // ---------------- loads (one lane) ----------------
-    // Rows past the sequence's end are its neighbour's (or zeros past the tensor): K's scores are masked,
-    // V's rows are looked over.
+    // ---------------- items and loads ----------------
+    auto range_ok = [&](int s) {
+      const int q0 = p.qstart[s], n = p.qstart[s + 1] - q0, k0 = p.kstart[s], m = p.kstart[s + 1] - k0;
+      return n >= 0 && n <= m && q0 >= 0 && q0 <= p.total_q - n && k0 >= 0 && k0 <= p.total_k - m;
+    };
+    // The query tile of flat index x: its sequence by a prefix sum of the sequences' tiles.  A sequence
+    // with a bad range takes one place, to be reported.
+    auto find_item = [&](int x, int h, Item& item) {
+      int s = -1, qt = 0, before = 0;
+      for (int first = 0; first < p.num_seqs && s < 0; first += 32) {
+        const int i = first + lane;
+        int tiles = 0;
+        if (i < p.num_seqs) {
+          const int n = p.qstart[i + 1] - p.qstart[i];
+          tiles = range_ok(i) ? min((n + BM - 1) / BM, p.max_tiles) : 1;
+        }
+        int upto = tiles;                                     // inclusive prefix sum over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + upto > x);
+        if (past) {
+          const int hit = __ffs(past) - 1;
+          s = first + hit;
+          qt = __shfl_sync(0xffffffffu, before + upto, hit) - 1 - x;    // the last, which sees the most keys, first
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+      }
+      if (s < 0) return false;
+      const int q0 = p.qstart[s], n = p.qstart[s + 1] - q0, k0 = p.kstart[s], m = p.kstart[s + 1] - k0;
+      if (!range_ok(s)) {
+        if (lane == 0) record_error(PKV_DEV_BAD_QUERY_RANGE);
+        return false;
+      }
+      // more queries than max_query_len covers
+      if (lane == 0 && qt == 0 && (n - 1) / BM >= p.max_tiles) record_error(PKV_DEV_BAD_QUERY_RANGE);
+      const int i0 = qt * BM;
+      item.q_row = q0 + i0;
+      item.rows = min(n - i0, BM);
+      item.first_pos = m - n + i0;
+      item.k_row = k0;
+      item.keys = m;
+      item.n_tiles = (item.first_pos + item.rows - 1) / BN + 1;
+      // tiles from here on hold keys that some row does not see, or the sequence's end
+      item.edge = min((item.first_pos + 1) / BN, m / BN);
+      item.head = h;
+      return true;
+    };
+    int x = blockIdx.x, y = blockIdx.y, j = 0, it = 0, asked = 0;
+    int k_issued = 0, v_issued_n = 0, q_issued = 0;
+    while (true) {
+      Item item;
+      const bool real = find_item(x, y, item);
+      if (lane == 0) {
+        // ask for the next item now; its answer is looked at after this one's loads
+        mbar_arrive_expect_tx(answered, 16);
+        try_cancel(answer, answered);
+      }
+      ++asked;
+      if (real) {
+        if (lane == 0) {
+          const int slot = it & 1;
+          if (it >= 2 && !wait(item_free(slot), ((it >> 1) - 1) & 1)) failed = true;
+          if (!failed) {
+            volatile Item& out = items[slot];
+            out.q_row = item.q_row;
+            out.rows = item.rows;
+            out.first_pos = item.first_pos;
+            out.k_row = item.k_row;
+            out.keys = item.keys;
+            out.n_tiles = item.n_tiles;
+            out.edge = item.edge;
+            out.head = item.head;
+            not_finite[slot] = 0;
+            mbar_arrive(item_full(slot));
+          }
+          const int kvh = item.head / p.group;
+          for (int i = 0; i < item.n_tiles && !failed; ++i, ++j) {
+            const int b = j % NS;
+            // Rows past the sequence's end are its neighbour's (or zeros past the tensor): K's scores are
+            // masked, V's rows are looked over.
+            if (j >= NS && !wait(k_free(b), (j / NS - 1) & 1)) {
+              failed = true;
+              break;
+            }
+            mbar_arrive_expect_tx(k_full(b), C::KV_BYTES);
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half)
+              tma_load_3d(sk + b * C::KV_BYTES + half * (BN * 128), &p.tmap_k, half * 64, kvh, item.k_row + i * BN, k_full(b));
+            ++k_issued;
+            if (i == 0) {
+              // Q, once the last item's scores are computed.  Rows past the sequence's queries read the
+              // next one's (or zeros past the tensor): never stored.
+              if (it >= 1 && !wait(q_free, (it - 1) & 1)) {
+                failed = true;
+                break;
+              }
+              mbar_arrive_expect_tx(q_full, C::Q_BYTES);
+#pragma unroll
+              for (int half = 0; half < D / 64; ++half)
+                tma_load_3d(sq + half * (BM * 128), &p.tmap_q, half * 64, item.head, item.q_row, q_full);
+              ++q_issued;
+            }
+            if (j >= NS && !wait(v_free(b), (j / NS - 1) & 1)) {
+              failed = true;
+              break;
+            }
+            mbar_arrive_expect_tx(v_full(b), C::KV_BYTES);
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half)
+              tma_load_3d(sv + b * C::KV_BYTES + half * (BN * 128), &p.tmap_v, half * 64, kvh, item.k_row + i * BN, v_full(b));
+            if (i >= item.edge) mbar_arrive(v_issued(b));
+            ++v_issued_n;
+          }
+        }
+        ++it;
+      }
+      j = __shfl_sync(0xffffffffu, j, 0);
+      failed = __shfl_sync(0xffffffffu, failed, 0);
+      // the answer: another CTA's place, or none left (after which none may be asked for)
+      if (!__all_sync(0xffffffffu, mbar_wait(answered, (asked - 1) & 1))) failed = true;
+      const bool more = !failed && cancelled(answer, x, y);
+      fence_proxy_async_smem();                               // the answer is read before the next one is written
+      __syncwarp();
+      if (!more) break;
+    }
     if (lane == 0) {
-      int k_issued = 0, v_issued_n = 0;
-      for (int j = 0; j < n_tiles; ++j) {
-        const int b = j % NS;
-        if (j >= NS && !wait(k_free(b), (j / NS - 1) & 1)) {
+      if (!failed) {
+        const int slot = it & 1;
+        if (it >= 2 && !wait(item_free(slot), ((it >> 1) - 1) & 1)) {
           failed = true;
-          break;
+        } else {
+          items[slot].n_tiles = 0;
+          mbar_arrive(item_full(slot));
         }
-        mbar_arrive_expect_tx(k_full(b), C::KV_BYTES);
-#pragma unroll
-        for (int half = 0; half < D / 64; ++half)
-          tma_load_3d(sk + b * C::KV_BYTES + half * (BN * 128), &p.tmap_k, half * 64, kvh, k0 + j * BN, k_full(b));
-        ++k_issued;
-        if (j >= NS && !wait(v_free(b), (j / NS - 1) & 1)) {
-          failed = true;
-          break;
-        }
-        mbar_arrive_expect_tx(v_full(b), C::KV_BYTES);
-#pragma unroll
-        for (int half = 0; half < D / 64; ++half)
-          tma_load_3d(sv + b * C::KV_BYTES + half * (BN * 128), &p.tmap_v, half * 64, kvh, k0 + j * BN, v_full(b));
-        if (j >= edge) mbar_arrive(v_issued(b));
-        ++v_issued_n;
       }
       if (failed) give_up();
       if (*abort_flag) {
         // let the copies this lane issued land (bounded) before the CTA's shared memory is released
         for (int t = max(0, k_issued - NS); t < k_issued; ++t) mbar_wait(k_full(t % NS), (t / NS) & 1);
         for (int t = max(0, v_issued_n - NS); t < v_issued_n; ++t) mbar_wait(v_full(t % NS), (t / NS) & 1);
+        if (q_issued > 0) mbar_wait(q_full, (q_issued - 1) & 1);
       }
     }
     __syncwarp();
   } else if (warp == W_CHECK) {
     // ---------------- the edge tiles' V: values that are not finite, and what is past the end ----------------
-    for (int j = edge; j < n_tiles; ++j) {
-      const int b = j % NS;
-      // v_full's phase is this tile's only once its load is issued (tile j - NS has landed by then): a
-      // wait for it before that could be for an earlier tile of the same parity
-      if (!__all_sync(0xffffffffu, wait(v_issued(b), ((j - edge) / NS) & 1) && wait(v_full(b), (j / NS) & 1))) {
+    uint32_t edge_phase = 0;                                  // bit b: parity of slot b's next edge tile
+    int j0 = 0;
+    for (int it = 0;; ++it) {
+      Item item;
+      if (!__all_sync(0xffffffffu, take_item(it, item))) {
         failed = true;
         break;
       }
-      unsigned char* tile = smem + (sv + b * C::KV_BYTES - base);
-      // 0 times a value is a NaN if the value is not finite; sums of those are NaN
-      const __half2 zero = __float2half2_rn(0.f);
-      __half2 acc[4] = {zero, zero, zero, zero};
+      if (item.n_tiles == 0) break;
+      for (int i = item.edge; i < item.n_tiles; ++i) {
+        const int j = j0 + i, b = j % NS;
+        // v_full's phase is this tile's only once its load is issued (tile j - NS has landed by then): a
+        // wait for it before that could be for an earlier tile of the same parity
+        if (!__all_sync(0xffffffffu, wait(v_issued(b), (edge_phase >> b) & 1) && wait(v_full(b), (j / NS) & 1))) {
+          failed = true;
+          break;
+        }
+        edge_phase ^= 1u << b;
+        unsigned char* tile = smem + (sv + b * C::KV_BYTES - base);
+        // 0 times a value is a NaN if the value is not finite; sums of those are NaN
+        const __half2 zero = __float2half2_rn(0.f);
+        __half2 acc[4] = {zero, zero, zero, zero};
 #pragma unroll 8
-      for (int c = lane; c < C::KV_BYTES / 16; c += 32) {
-        const uint4 x = *reinterpret_cast<const uint4*>(tile + c * 16);
-        acc[0] = __hfma2(*reinterpret_cast<const __half2*>(&x.x), zero, acc[0]);
-        acc[1] = __hfma2(*reinterpret_cast<const __half2*>(&x.y), zero, acc[1]);
-        acc[2] = __hfma2(*reinterpret_cast<const __half2*>(&x.z), zero, acc[2]);
-        acc[3] = __hfma2(*reinterpret_cast<const __half2*>(&x.w), zero, acc[3]);
-      }
-      const __half2 sum = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
-      if (__any_sync(0xffffffffu, __hisnan(__low2half(sum)) || __hisnan(__high2half(sum)))) {
         for (int c = lane; c < C::KV_BYTES / 16; c += 32) {
-          const int key = j * BN + (c / 8) % BN;              // 128-byte rows, a half of the head dimension each
-          unsigned* w = reinterpret_cast<unsigned*>(tile + c * 16);
+          const uint4 x = *reinterpret_cast<const uint4*>(tile + c * 16);
+          acc[0] = __hfma2(*reinterpret_cast<const __half2*>(&x.x), zero, acc[0]);
+          acc[1] = __hfma2(*reinterpret_cast<const __half2*>(&x.y), zero, acc[1]);
+          acc[2] = __hfma2(*reinterpret_cast<const __half2*>(&x.z), zero, acc[2]);
+          acc[3] = __hfma2(*reinterpret_cast<const __half2*>(&x.w), zero, acc[3]);
+        }
+        const __half2 sum = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+        if (__any_sync(0xffffffffu, __hisnan(__low2half(sum)) || __hisnan(__high2half(sum)))) {
+          for (int c = lane; c < C::KV_BYTES / 16; c += 32) {
+            const int key = i * BN + (c / 8) % BN;            // 128-byte rows, a half of the head dimension each
+            unsigned* w = reinterpret_cast<unsigned*>(tile + c * 16);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const unsigned x = w[e];
-            if (!finite16(x) || !finite16(x >> 16)) {
-              if (key < m) *not_finite = 1;
-              w[e] = (finite16(x) ? x & 0xffffu : 0u) | (finite16(x >> 16) ? x & 0xffff0000u : 0u);
+            for (int e = 0; e < 4; ++e) {
+              const unsigned x = w[e];
+              if (!finite16(x) || !finite16(x >> 16)) {
+                if (key < item.keys) not_finite[it & 1] = 1;
+                w[e] = (finite16(x) ? x & 0xffffu : 0u) | (finite16(x >> 16) ? x & 0xffff0000u : 0u);
+              }
             }
           }
+          __threadfence_block();
+          fence_proxy_async_smem();                           // these stores -> tensor-core reads
         }
-        fence_proxy_async_smem();                             // these stores -> tensor-core reads
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_ok(b));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_ok(b));
+      if (failed) break;
+      j0 += item.n_tiles;
+      if (lane == 0) mbar_arrive(item_free(it & 1));
     }
     if (failed) give_up();
   } else if (warp == W_S) {
@@ -294,28 +432,33 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
     if (lane == 0) {
       constexpr uint32_t IDESC_QK = umma_idesc_f16(BM, BN, false);
       const uint64_t a0 = umma_smem_desc(sq, 16, 1024);
-      int issued = 0;
-      failed = !wait(q_full, 0);
-      for (int j = 0; j < n_tiles && !failed; ++j) {
-        const int u = j & 1;
-        if (!wait(k_full(j % NS), (j / NS) & 1) || (j >= 2 && !wait(pv_done(u), ((j - 2) >> 1) & 1))) {
-          failed = true;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t b0 = umma_smem_desc(sk + (j % NS) * C::KV_BYTES, 16, 1024);
-        const uint32_t d = t_s(u);
-        umma_ss(d, a0, b0, IDESC_QK, 0u);
+      int j = 0;
+      for (int it = 0; !failed; ++it) {
+        Item item;
+        if (!take_item(it, item) || (item.n_tiles > 0 && !wait(q_full, it & 1))) failed = true;
+        if (failed || item.n_tiles == 0) break;
+        mbar_arrive(item_free(it & 1));
+        for (int i = 0; i < item.n_tiles; ++i, ++j) {
+          const int u = j & 1;
+          if (!wait(k_full(j % NS), (j / NS) & 1) || (j >= 2 && !wait(pv_done(u), ((j - 2) >> 1) & 1))) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t b0 = umma_smem_desc(sk + (j % NS) * C::KV_BYTES, 16, 1024);
+          const uint32_t d = t_s(u);
+          umma_ss(d, a0, b0, IDESC_QK, 0u);
 #pragma unroll
-        for (int kk = 1; kk < D / 16; ++kk)
-          umma_ss(d, a0 + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4), b0 + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4),
-                  IDESC_QK, 1u);
-        umma_commit(s_full(u));
-        ++issued;
+          for (int kk = 1; kk < D / 16; ++kk)
+            umma_ss(d, a0 + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4),
+                    b0 + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), IDESC_QK, 1u);
+          umma_commit(s_full(u));
+        }
+        if (!failed) umma_commit(q_free);
       }
       if (failed) {
         give_up();
-        if (issued > 0) mbar_wait(s_full((issued - 1) & 1), ((issued - 1) >> 1) & 1);
+        if (j > 0) mbar_wait(s_full((j - 1) & 1), ((j - 1) >> 1) & 1);
       }
     }
     __syncwarp();
@@ -323,166 +466,180 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
     // ---------------- O += P V issue (one lane) ----------------
     if (lane == 0) {
       constexpr uint32_t IDESC_PV = umma_idesc_f16(BM, D, true);
-      int issued = 0;
-      for (int j = 0; j < n_tiles; ++j) {
-        const int u = j & 1;
-        if (!wait(v_full(j % NS), (j / NS) & 1) || (j >= edge && !wait(v_ok(j % NS), ((j - edge) / NS) & 1)) ||
-            !wait(p_full(u), (j >> 1) & 1)) {
-          failed = true;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t v0 = umma_smem_desc(sv + (j % NS) * C::KV_BYTES, BN * 128, 1024);
-        const uint32_t pa = t_s(u);
-        umma_ts(t_o, pa, v0, IDESC_PV, j > 0 ? 1u : 0u);
+      uint32_t edge_phase = 0;
+      int j = 0;
+      for (int it = 0; !failed; ++it) {
+        Item item;
+        if (!take_item(it, item)) failed = true;
+        if (failed || item.n_tiles == 0) break;
+        mbar_arrive(item_free(it & 1));
+        for (int i = 0; i < item.n_tiles; ++i, ++j) {
+          const int u = j & 1, b = j % NS;
+          bool ok = wait(v_full(b), (j / NS) & 1);
+          if (ok && i >= item.edge) {
+            ok = wait(v_ok(b), (edge_phase >> b) & 1);
+            edge_phase ^= 1u << b;
+          }
+          // the first product overwrites the accumulator: the last item's output has been read
+          if (ok && i == 0 && it > 0) ok = wait(o_free, (it - 1) & 1);
+          if (!ok || !wait(p_full(u), (j >> 1) & 1)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t v0 = umma_smem_desc(sv + b * C::KV_BYTES, BN * 128, 1024);
+          const uint32_t pa = t_s(u);
+          umma_ts(t_o, pa, v0, IDESC_PV, i > 0 ? 1u : 0u);
 #pragma unroll
-        for (int kk = 1; kk < BN / 16; ++kk) umma_ts(t_o, pa + kk * 8, v0 + ((kk * 16 * 128) >> 4), IDESC_PV, 1u);
-        umma_commit(pv_done(u));
-        ++issued;
-        umma_commit(v_free(j % NS));
+          for (int kk = 1; kk < BN / 16; ++kk) umma_ts(t_o, pa + kk * 8, v0 + ((kk * 16 * 128) >> 4), IDESC_PV, 1u);
+          umma_commit(pv_done(u));
+          umma_commit(v_free(b));
+        }
       }
       if (failed) {
         give_up();
-        if (issued > 0) mbar_wait(pv_done((issued - 1) & 1), ((issued - 1) >> 1) & 1);
+        if (j > 0) mbar_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1);
       }
     }
     __syncwarp();
   } else {
-    // ---------------- softmax ----------------
+    // ---------------- softmax and output ----------------
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t to = t_o;
-    const int pos = first_pos + tid;
-    for (int j = 0; j < n_tiles; ++j) {
+    unsigned char* stage = smem + (so + warp * STAGE_BYTES - base);       // [32 rows][64 bytes]
+    int j = 0;
+    for (int it = 0; !failed; ++it) {
+      Item item;
       // decisions stay warp-uniform: the tcgen05.ld/st below are warp-collective
-      const int u = j & 1;
-      const uint32_t ts = t_s(u);
-      if (!__all_sync(0xffffffffu, wait(s_full(u), (j >> 1) & 1))) {
-        failed = true;
-        break;
-      }
-      tc_fence_after();
-      if (lane == 0) mbar_arrive(k_free(j % NS));
-      float sv_[BN];
-      tmem_ld32_nowait(ts + lane_off, *reinterpret_cast<float(*)[32]>(sv_));
-      tmem_ld32_nowait(ts + lane_off + 32, *reinterpret_cast<float(*)[32]>(sv_ + 32));
-      tmem_ld_wait();
-      const int key0 = j * BN;
-      if (key0 + BN - 1 > first_pos) {                       // keys after the query (and past the end)
-#pragma unroll
-        for (int c = 0; c < BN; ++c)
-          if (key0 + c > pos) sv_[c] = -INFINITY;
-      }
-      float m8[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m8[i] = fmaxf(sv_[i], sv_[8 + i]);
-#pragma unroll
-      for (int c = 16; c < BN; c += 16)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m8[i] = max3(m8[i], sv_[c + i], sv_[c + 8 + i]);
-      float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-      mx *= p.scale_log2;
-      const bool rescale = mx > m_ref + kRescale;             // also the first finite maximum
-      float alpha = 1.f;
-      if (rescale) {
-        alpha = exp2f(m_ref - mx);
-        m_ref = mx;
-      }
-      const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
-      if (__any_sync(0xffffffffu, rescale && j > 0)) {
-        if (!__all_sync(0xffffffffu, wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1))) {
+      if (!__all_sync(0xffffffffu, take_item(it, item))) failed = true;
+      if (failed || item.n_tiles == 0) break;
+      const int pos = item.first_pos + tid;
+      float l = 0.f, m_ref = -INFINITY;
+      for (int i = 0; i < item.n_tiles; ++i, ++j) {
+        const int u = j & 1;
+        const uint32_t ts = t_s(u);
+        if (!__all_sync(0xffffffffu, wait(s_full(u), (j >> 1) & 1))) {
           failed = true;
           break;
         }
         tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          tmem_ld32(to + lane_off + c * 32, o);
-          uint32_t ob[32];
+        if (lane == 0) mbar_arrive(k_free(j % NS));
+        float sv_[BN];
+        tmem_ld32_nowait(ts + lane_off, *reinterpret_cast<float(*)[32]>(sv_));
+        tmem_ld32_nowait(ts + lane_off + 32, *reinterpret_cast<float(*)[32]>(sv_ + 32));
+        tmem_ld_wait();
+        const int key0 = i * BN;
+        if (key0 + BN - 1 > item.first_pos) {                 // keys after the query (and past the end)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e] * alpha);
-          tmem_st32(to + lane_off + c * 32, ob);
+          for (int c = 0; c < BN; ++c)
+            if (key0 + c > pos) sv_[c] = -INFINITY;
         }
-      }
-      // P as fp16; the row sum adds the rounded weights, the ones that multiply V
-      float sum8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      uint32_t pk[BN / 2];
+        float m8[8];
 #pragma unroll
-      for (int e = 0; e < BN / 2; ++e) {
-        float x0, x1;
-        fma2(x0, x1, sv_[2 * e], sv_[2 * e + 1], p.scale_log2, nref);
-        pk[e] = pack_half2(fast_exp2(x0), fast_exp2(x1));
-        add_half2(sum8[2 * (e & 3)], sum8[2 * (e & 3) + 1], pk[e]);
-      }
-      float sum4[4];
+        for (int e = 0; e < 8; ++e) m8[e] = fmaxf(sv_[e], sv_[8 + e]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum4[i] = sum8[2 * i] + sum8[2 * i + 1];
-      tmem_st32(ts + lane_off, pk);
-      l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(p_full(u));
-    }
-    if (!failed) {
-      failed = !__all_sync(0xffffffffu, wait(pv_done((n_tiles - 1) & 1), ((n_tiles - 1) >> 1) & 1));
-      tc_fence_after();
-    }
-    if (failed) give_up();
-  }
-
-  // ---------------- epilogue ----------------
-  __syncthreads();
-  const bool aborted = *abort_flag != 0;
-  if (warp < 4 && !aborted) {
-    // each thread normalises its O row and stages it in the K/V ring (every MMA is done), chunks XOR-ed
-    // with the row's low bits; the warp then stores whole rows
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    const float inv = 1.f / l;                                // a query sees its own key at least
-    unsigned char* stage = smem + (sk - base);                // [128 rows][D * 2 bytes]
-    constexpr int RB = D * 2;
+        for (int c = 16; c < BN; c += 16)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m8[e] = max3(m8[e], sv_[c + e], sv_[c + 8 + e]);
+        float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        mx *= p.scale_log2;
+        const bool rescale = mx > m_ref + kRescale;           // also the first finite maximum
+        float alpha = 1.f;
+        if (rescale) {
+          alpha = exp2f(m_ref - mx);
+          m_ref = mx;
+        }
+        const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
+        if (__any_sync(0xffffffffu, rescale && i > 0)) {
+          if (!__all_sync(0xffffffffu, wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1))) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      float o[32];
-      tmem_ld32(t_o + lane_off + c * 32, o);
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld32(t_o + lane_off + c * 32, o);
+            uint32_t ob[32];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] *= inv;
-      if (*not_finite) {
-        // values that are not finite in the edge tiles were left out: add them where they are seen
-        const int pos = min(first_pos + tid, m - 1);
-        for (int t = edge * BN; t <= pos; ++t) {
-          const __half* row = p.v + (k0 + t) * p.v_stride + static_cast<int64_t>(kvh) * D + c * 32;
+            for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e] * alpha);
+            tmem_st32(t_o + lane_off + c * 32, ob);
+          }
+        }
+        // P as fp16; the row sum adds the rounded weights, the ones that multiply V
+        float sum8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[BN / 2];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const __half x = row[e];
-            if (!finite16(__half_as_ushort(x))) o[e] += __half2float(x);
+        for (int e = 0; e < BN / 2; ++e) {
+          float x0, x1;
+          fma2(x0, x1, sv_[2 * e], sv_[2 * e + 1], p.scale_log2, nref);
+          pk[e] = pack_half2(fast_exp2(x0), fast_exp2(x1));
+          add_half2(sum8[2 * (e & 3)], sum8[2 * (e & 3) + 1], pk[e]);
+        }
+        float sum4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum4[e] = sum8[2 * e] + sum8[2 * e + 1];
+        tmem_st32(ts + lane_off, pk);
+        l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_full(u));
+      }
+      if (!failed) failed = !__all_sync(0xffffffffu, wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1));
+      if (failed) break;
+      tc_fence_after();
+      // the output, 32 columns at a time: each thread normalises its row and stages it, chunks XOR-ed with
+      // the row; four lanes then store 64 bytes of a row
+      const float inv = 1.f / l;                              // a query sees its own key at least
+      const bool fix = not_finite[it & 1] != 0;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        tmem_ld32(t_o + lane_off + c * 32, o);
+        if (c == D / 32 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(o_free);
+            mbar_arrive(item_free(it & 1));
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= inv;
+        if (fix) {
+          // values that are not finite in the edge tiles were left out: add them where they are seen
+          const int last = min(pos, item.keys - 1);
+          for (int t = item.edge * BN; t <= last; ++t) {
+            const __half* row = p.v + (item.k_row + t) * p.v_stride + static_cast<int64_t>(item.head / p.group) * D + c * 32;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const __half x = row[e];
+              if (!finite16(__half_as_ushort(x))) o[e] += __half2float(x);
+            }
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(pack_half2(o[8 * k], o[8 * k + 1]), pack_half2(o[8 * k + 2], o[8 * k + 3]),
+                         pack_half2(o[8 * k + 4], o[8 * k + 5]), pack_half2(o[8 * k + 6], o[8 * k + 7]));
+        __syncwarp();
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 8) {
+          const int row = r0 + lane / 4, k = lane % 4;
+          if (warp * 32 + row < item.rows) {
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + row * 64 + ((k ^ ((row >> 1) & 3)) << 4));
+            *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(item.q_row + warp * 32 + row) * p.num_heads + item.head) * D +
+                                      c * 32 + k * 8) = w;
           }
         }
         __syncwarp();
       }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint4 w;
-        w.x = pack_half2(o[8 * k], o[8 * k + 1]);
-        w.y = pack_half2(o[8 * k + 2], o[8 * k + 3]);
-        w.z = pack_half2(o[8 * k + 4], o[8 * k + 5]);
-        w.w = pack_half2(o[8 * k + 6], o[8 * k + 7]);
-        *reinterpret_cast<uint4*>(stage + tid * RB + (((c * 4 + k) ^ (tid & (CPR - 1))) << 4)) = w;
-      }
     }
-    __syncwarp();
-    constexpr int RPI = 32 / CPR;
-    const int c = lane % CPR;
-#pragma unroll 4
-    for (int r0 = 0; r0 < 32; r0 += RPI) {
-      const int row = warp * 32 + r0 + lane / CPR;            // CTA row
-      const int i = i0 + row;
-      if (i < n) {
-        const uint4 w = *reinterpret_cast<const uint4*>(stage + row * RB + ((c ^ (row & (CPR - 1))) << 4));
-        *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(q0 + i) * H + h) * D + c * 8) = w;
-      }
-    }
+    if (failed) give_up();
   }
-  if (tid == 0) mbar_wait(q_full, 0);                         // landed, unless the CTA gave up early: bounded
+
+  // every tensor-memory access is done (tcgen05.ld and .st wait inline, the products are committed)
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
