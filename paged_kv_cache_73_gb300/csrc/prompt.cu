@@ -28,10 +28,14 @@
 //    roles pass from one tile to the next on their own: the next tile's K and V are loaded
 //    and its first scores computed while the softmax warps write the last tile's output.
 //    One launch per tile spent 4.3 us of 7.7 on starts and ends where prompts are short.
+//  * Five kinds of warps run different code at once and share the instruction cache, so code
+//    is kept small where it is not hot: waits in one loop instead of two took ragged short
+//    prompts from 94 us to 74, an unrolled staging of the output had them at 107.
 //
-// Per 128 x 64 tile the products take 384 + 256 clocks: S is bound by shared memory (an SS
-// product of 128 x 64 x 16 reads 6 KB), PV by math.  Two S buffers keep S(j + 1) running
-// under the softmax of tile j.
+// Per 128 x 64 tile (D = 128) the products take 384 + 256 clocks: S is bound by shared memory
+// (an SS product of 128 x 64 x 16 reads 6 KB), PV by math; both with the loads come to 750
+// clocks of shared-memory traffic, and 685 a tile are measured on long prompts.  Two S buffers
+// keep S(j + 1) running under the softmax of tile j (about 1000 clocks).
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -62,17 +66,16 @@ struct PromptParams {
   int num_seqs, num_heads, group;
   int max_tiles;                        // query tiles per sequence that max_query_len covers
   int total_q, total_k;
+  int out_sectors;                      // out is 32-byte aligned
   float scale_log2;
 };
-
-constexpr int STAGE_BYTES = 32 * 64;                          // a warp's staging of 32 rows x 32 output columns
 
 template <int D>
 struct Cfg {
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
   static constexpr int NS = D == 64 ? 4 : 2;                  // ring slots each for K and for V
-  static constexpr int BYTES = 1024 + Q_BYTES + 2 * NS * KV_BYTES + 4 * STAGE_BYTES + 512;
+  static constexpr int BYTES = 1024 + Q_BYTES + 2 * NS * KV_BYTES + 512;
   // so much that no third CTA, which would wait for tensor memory, fits an SM
   static constexpr int SMEM = BYTES > 80 * 1024 ? BYTES : 80 * 1024;
 };
@@ -88,6 +91,19 @@ __device__ __forceinline__ bool finite16(unsigned h) { return (h & 0x7c00u) != 0
 struct Item {
   int q_row, rows, first_pos, k_row, keys, n_tiles, edge, head;
 };
+
+// Sixteen fp16 values to out: one 32-byte store where out's rows are whole sectors, else two of 16.
+__device__ __forceinline__ void store16(__half* dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                        uint32_t g, uint32_t h, bool sectors) {
+  if (sectors) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e),
+                 "r"(f), "r"(g), "r"(h)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(a, b, c, d);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(e, f, g, h);
+  }
+}
 
 // ---- taking over a CTA that was not launched yet -------------------------------------------------
 // The answer, 16 bytes at `answer`, arrives as a transaction on `bar`.
@@ -115,6 +131,17 @@ __device__ __forceinline__ bool cancelled(uint32_t answer, int& x, int& y) {
   return ok != 0;
 }
 
+// A wait for the phase of `parity`, false once another role has raised the abort flag or after 2^26
+// tries (a second or so).  Small, because it is in a dozen places of roles that share the instruction
+// cache; the flag is looked at only now and then, for a shared-memory read in a thread that issues
+// products stalls it until they are done.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_try_wait_parity(bar, parity); ++i)
+    if ((i & 1023u) == 0 && (*abort_flag != 0 || i >= (1u << 26))) return false;
+  return true;
+}
+
 // Warp roles:
 //   0-3      softmax: waits S(j), releases K slot, masks, takes the row maximum (moving the running
 //            one, and O, only past 2^8), writes P = 2^(S - m) as fp16 over the scores and arrives on
@@ -136,8 +163,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - raw);
-  const uint32_t sq = base, sk = sq + C::Q_BYTES, sv = sk + NS * C::KV_BYTES, so = sv + NS * C::KV_BYTES;
-  const uint32_t bars = so + 4 * STAGE_BYTES;
+  const uint32_t sq = base, sk = sq + C::Q_BYTES, sv = sk + NS * C::KV_BYTES, bars = sv + NS * C::KV_BYTES;
   // per S buffer u (key tile j uses j % 2), per ring slot b, per item slot i (item number % 2)
   auto s_full = [&](int u) { return bars + 8u * u; };
   auto p_full = [&](int u) { return bars + 16u + 8u * u; };
@@ -201,7 +227,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
   const uint32_t tmem = *tmem_slot;
   auto t_s = [&](int u) { return tmem + S_COL + 64u * u; };
   const uint32_t t_o = tmem + O_COL;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_or_abort(bar, parity, abort_flag); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag); };
   auto give_up = [&]() {
     if (!*abort_flag) record_error(PKV_DEV_WAIT_TIMEOUT);
     *abort_flag = 1;
@@ -224,54 +250,65 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
 
   if (warp == W_LOAD) {
     // ---------------- items and loads ----------------
-    auto range_ok = [&](int s) {
-      const int q0 = p.qstart[s], n = p.qstart[s + 1] - q0, k0 = p.kstart[s], m = p.kstart[s + 1] - k0;
-      return n >= 0 && n <= m && q0 >= 0 && q0 <= p.total_q - n && k0 >= 0 && k0 <= p.total_k - m;
-    };
-    // The query tile of flat index x: its sequence by a prefix sum of the sequences' tiles.  A sequence
-    // with a bad range takes one place, to be reported.
-    auto find_item = [&](int x, int h, Item& item) {
-      int s = -1, qt = 0, before = 0;
-      for (int first = 0; first < p.num_seqs && s < 0; first += 32) {
-        const int i = first + lane;
-        int tiles = 0;
-        if (i < p.num_seqs) {
-          const int n = p.qstart[i + 1] - p.qstart[i];
-          tiles = range_ok(i) ? min((n + BM - 1) / BM, p.max_tiles) : 1;
-        }
-        int upto = tiles;                                     // inclusive prefix sum over the lanes
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const int y = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += y;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, before + upto > x);
-        if (past) {
-          const int hit = __ffs(past) - 1;
-          s = first + hit;
-          qt = __shfl_sync(0xffffffffu, before + upto, hit) - 1 - x;    // the last, which sees the most keys, first
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+    // 32 sequences at a time, one a lane: where they start, their lengths and query tiles, and the tiles
+    // of all before (a prefix sum).  A sequence with a bad range takes one place, to be reported.
+    int q0 = 0, n = 0, k0 = 0, m = 0, upto = 0;               // upto: inclusive, from the batch's first
+    bool range_ok = true;
+    int batch = -32, before = 0, batch_tiles = 0;             // the batch's first sequence, the tiles before it
+    auto read_batch = [&](int first) {
+      before = first == 0 ? 0 : before + batch_tiles;
+      batch = first;
+      const int i = first + lane;
+      int tiles = 0;
+      if (i < p.num_seqs) {
+        q0 = p.qstart[i];
+        n = p.qstart[i + 1] - q0;
+        k0 = p.kstart[i];
+        m = p.kstart[i + 1] - k0;
+        range_ok = n >= 0 && n <= m && q0 >= 0 && q0 <= p.total_q - n && k0 >= 0 && k0 <= p.total_k - m;
+        tiles = range_ok ? min((n + BM - 1) / BM, p.max_tiles) : 1;
       }
-      if (s < 0) return false;
-      const int q0 = p.qstart[s], n = p.qstart[s + 1] - q0, k0 = p.kstart[s], m = p.kstart[s + 1] - k0;
-      if (!range_ok(s)) {
+      upto = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      batch_tiles = __shfl_sync(0xffffffffu, upto, 31);
+    };
+    // The query tile of flat index x, the tiles of a sequence from its last, which sees the most keys.  The
+    // batch is kept: a CTA's indices mostly rise.
+    auto find_item = [&](int x, int h, Item& item) {
+      if (batch < 0 || x < before) read_batch(0);
+      while (x >= before + batch_tiles) {
+        if (batch + 32 >= p.num_seqs) return false;
+        read_batch(batch + 32);
+      }
+      const int hit = __ffs(__ballot_sync(0xffffffffu, before + upto > x)) - 1;
+      const int qt = __shfl_sync(0xffffffffu, before + upto, hit) - 1 - x;
+      const int s_n = __shfl_sync(0xffffffffu, n, hit), s_m = __shfl_sync(0xffffffffu, m, hit);
+      const int s_q0 = __shfl_sync(0xffffffffu, q0, hit), s_k0 = __shfl_sync(0xffffffffu, k0, hit);
+      if (!__shfl_sync(0xffffffffu, static_cast<int>(range_ok), hit)) {
         if (lane == 0) record_error(PKV_DEV_BAD_QUERY_RANGE);
         return false;
       }
       // more queries than max_query_len covers
-      if (lane == 0 && qt == 0 && (n - 1) / BM >= p.max_tiles) record_error(PKV_DEV_BAD_QUERY_RANGE);
+      if (lane == 0 && qt == 0 && (s_n - 1) / BM >= p.max_tiles) record_error(PKV_DEV_BAD_QUERY_RANGE);
       const int i0 = qt * BM;
-      item.q_row = q0 + i0;
-      item.rows = min(n - i0, BM);
-      item.first_pos = m - n + i0;
-      item.k_row = k0;
-      item.keys = m;
+      item.q_row = s_q0 + i0;
+      item.rows = min(s_n - i0, BM);
+      item.first_pos = s_m - s_n + i0;
+      item.k_row = s_k0;
+      item.keys = s_m;
       item.n_tiles = (item.first_pos + item.rows - 1) / BN + 1;
       // tiles from here on hold keys that some row does not see, or the sequence's end
-      item.edge = min((item.first_pos + 1) / BN, m / BN);
+      item.edge = min((item.first_pos + 1) / BN, s_m / BN);
       item.head = h;
       return true;
+    };
+    auto ask = [&]() {
+      mbar_arrive_expect_tx(answered, 16);
+      try_cancel(answer, answered);
     };
     int x = blockIdx.x, y = blockIdx.y, j = 0, it = 0, asked = 0;
     int k_issued = 0, v_issued_n = 0, q_issued = 0;
@@ -279,13 +316,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
       Item item;
       const bool real = find_item(x, y, item);
       if (lane == 0) {
-        // ask for the next item now; its answer is looked at after this one's loads
-        mbar_arrive_expect_tx(answered, 16);
-        try_cancel(answer, answered);
-      }
-      ++asked;
-      if (real) {
-        if (lane == 0) {
+        if (real) {
           const int slot = it & 1;
           if (it >= 2 && !wait(item_free(slot), ((it >> 1) - 1) & 1)) failed = true;
           if (!failed) {
@@ -328,6 +359,12 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
                 tma_load_3d(sq + half * (BM * 128), &p.tmap_q, half * 64, item.head, item.q_row, q_full);
               ++q_issued;
             }
+            // the next item is asked for as late as its answer still comes in time (0.4 us): one taken
+            // early is not there for a CTA that runs dry
+            if (i == item.n_tiles - 1) {
+              ask();
+              ++asked;
+            }
             if (j >= NS && !wait(v_free(b), (j / NS - 1) & 1)) {
               failed = true;
               break;
@@ -339,18 +376,28 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
             if (i >= item.edge) mbar_arrive(v_issued(b));
             ++v_issued_n;
           }
+        } else {
+          ask();
+          ++asked;
         }
-        ++it;
       }
+      it += real;
       j = __shfl_sync(0xffffffffu, j, 0);
+      asked = __shfl_sync(0xffffffffu, asked, 0);
       failed = __shfl_sync(0xffffffffu, failed, 0);
+      if (failed) break;
       // the answer: another CTA's place, or none left (after which none may be asked for)
-      if (!__all_sync(0xffffffffu, mbar_wait(answered, (asked - 1) & 1))) failed = true;
-      const bool more = !failed && cancelled(answer, x, y);
+      if (!__all_sync(0xffffffffu, wait(answered, (asked - 1) & 1))) {
+        failed = true;
+        break;
+      }
+      const bool more = cancelled(answer, x, y);
       fence_proxy_async_smem();                               // the answer is read before the next one is written
       __syncwarp();
       if (!more) break;
     }
+    // (a role gave up) an answer on its way lands before the CTA's shared memory is released: bounded
+    if (failed && asked > 0) mbar_wait(answered, (asked - 1) & 1);
     if (lane == 0) {
       if (!failed) {
         const int slot = it & 1;
@@ -505,7 +552,6 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
   } else {
     // ---------------- softmax and output ----------------
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    unsigned char* stage = smem + (so + warp * STAGE_BYTES - base);       // [32 rows][64 bytes]
     int j = 0;
     for (int it = 0; !failed; ++it) {
       Item item;
@@ -528,7 +574,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
         tmem_ld32_nowait(ts + lane_off + 32, *reinterpret_cast<float(*)[32]>(sv_ + 32));
         tmem_ld_wait();
         const int key0 = i * BN;
-        if (key0 + BN - 1 > item.first_pos) {                 // keys after the query (and past the end)
+        if (__any_sync(0xffffffffu, key0 + BN - 1 > pos)) {                 // keys after the query (and past the end)
 #pragma unroll
           for (int c = 0; c < BN; ++c)
             if (key0 + c > pos) sv_[c] = -INFINITY;
@@ -587,14 +633,15 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
       if (!failed) failed = !__all_sync(0xffffffffu, wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1));
       if (failed) break;
       tc_fence_after();
-      // the output, 32 columns at a time: each thread normalises its row and stages it, chunks XOR-ed with
-      // the row; four lanes then store 64 bytes of a row
+      // the output, 32 columns at a time: each thread normalises and stores its own row, whole 32-byte
+      // sectors at once; the next columns are read meanwhile
       const float inv = 1.f / l;                              // a query sees its own key at least
       const bool fix = not_finite[it & 1] != 0;
+      __half* dst = p.out + (static_cast<size_t>(item.q_row + tid) * p.num_heads + item.head) * D;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
-        float o[32];
-        tmem_ld32(t_o + lane_off + c * 32, o);
+        float x[32];
+        tmem_ld32(t_o + lane_off + c * 32, x);
         if (c == D / 32 - 1) {
           tc_fence_before();
           __syncwarp();
@@ -604,35 +651,26 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
           }
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= inv;
-        if (fix) {
-          // values that are not finite in the edge tiles were left out: add them where they are seen
-          const int last = min(pos, item.keys - 1);
-          for (int t = item.edge * BN; t <= last; ++t) {
-            const __half* row = p.v + (item.k_row + t) * p.v_stride + static_cast<int64_t>(item.head / p.group) * D + c * 32;
+        for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], x[e], x[e + 1], inv, 0.f);
+        if (tid < item.rows) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const __half x = row[e];
-              if (!finite16(__half_as_ushort(x))) o[e] += __half2float(x);
-            }
-          }
+          for (int e = 0; e < 32; e += 16)
+            store16(dst + c * 32 + e, pack_half2(x[e], x[e + 1]), pack_half2(x[e + 2], x[e + 3]), pack_half2(x[e + 4], x[e + 5]),
+                    pack_half2(x[e + 6], x[e + 7]), pack_half2(x[e + 8], x[e + 9]), pack_half2(x[e + 10], x[e + 11]),
+                    pack_half2(x[e + 12], x[e + 13]), pack_half2(x[e + 14], x[e + 15]), p.out_sectors);
         }
         __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint4*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
-              make_uint4(pack_half2(o[8 * k], o[8 * k + 1]), pack_half2(o[8 * k + 2], o[8 * k + 3]),
-                         pack_half2(o[8 * k + 4], o[8 * k + 5]), pack_half2(o[8 * k + 6], o[8 * k + 7]));
-        __syncwarp();
-#pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += 8) {
-          const int row = r0 + lane / 4, k = lane % 4;
-          if (warp * 32 + row < item.rows) {
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + row * 64 + ((k ^ ((row >> 1) & 3)) << 4));
-            *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(item.q_row + warp * 32 + row) * p.num_heads + item.head) * D +
-                                      c * 32 + k * 8) = w;
-          }
-        }
+      }
+      if (fix) {
+        // values that are not finite in the edge tiles were left out: added to the stored row where the
+        // query sees them (rare, so its code is small rather than fast)
+        const int last = tid < item.rows ? min(pos, item.keys - 1) : -1;
+        const __half* v = p.v + (item.k_row + static_cast<int64_t>(item.edge) * BN) * p.v_stride + static_cast<int64_t>(item.head / p.group) * D;
+#pragma unroll 1
+        for (int t = item.edge * BN; t <= last; ++t, v += p.v_stride)
+#pragma unroll 1
+          for (int e = 0; e < D; ++e)
+            if (!finite16(__half_as_ushort(v[e]))) dst[e] = __float2half_rn(__half2float(dst[e]) + __half2float(v[e]));
         __syncwarp();
       }
     }
@@ -760,6 +798,7 @@ int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t*
   p.group = num_heads / num_kv_heads;
   p.total_q = total_q;
   p.total_k = total_k;
+  p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = head_dim == 128 ? launch<128>(p, max_query_len, st) : launch<64>(p, max_query_len, st);

@@ -79,6 +79,22 @@ def test_chunks_over_cached_context(cuda_device, D, H, Hk):
     check(make(D + H + 1, NEWS, [0, 5, 64, 1, 63, 130, 7, 400, 9, 33, 2, 129], H, Hk, D), cuda_device)
 
 
+@pytest.mark.parametrize("D,H,Hk", [(128, 24, 24), (64, 30, 6)])
+def test_more_tiles_than_run_at_once(cuda_device, D, H, Hk):
+    # CTAs take over tiles: 29 tiles a head, some sequences without any
+    check(make(D + H + 2, [130, 1, 0, 600, 64, 3, 300, 0, 257, 129, 5, 700], [0, 0, 3, 100, 1, 70, 0, 9, 5, 0, 0, 64], H, Hk, D),
+          cuda_device)
+
+
+def test_output_at_a_16_byte_boundary(cuda_device):
+    q, k, v, qs, ks = (torch.from_numpy(x).to(cuda_device) for x in make(16, [200], 0, 2, 1, 128))
+    buf = torch.zeros(200 * 2 * 128 + 8, dtype=torch.float16, device=cuda_device)
+    out = buf[8:].view(200, 2, 128)
+    assert out.data_ptr() % 32 == 16
+    pkv.prompt_attention(q, k, v, qs, 0.1, 200, out=out)
+    assert torch.equal(out, pkv.prompt_attention(q, k, v, qs, 0.1, 200)) and not buf[:8].any()
+
+
 def test_one_query_each_over_long_contexts(cuda_device):
     check(make(5, [1] * 5, [0, 62, 63, 64, 1000], 4, 2, 128), cuda_device)
 
