@@ -58,12 +58,8 @@ __device__ int g_dev_error_attention_int4 = 0;
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_attention_int4, 0, code); }
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int NW = 4;                 // warps per CTA
+constexpr int NW = 12;                // warps on an SM, in one CTA; a small grid has CTAs of four
 constexpr int CHUNK = 32;             // tokens a worker handles at a time
-#ifndef V_RES
-#define V_RES 3
-#endif
-constexpr int kResident = V_RES;          // CTAs per SM
 constexpr int kMinChunks = 4;         // chunks a worker takes at least
 constexpr float kRescale = 8.f;       // the running maximum moves when a chunk passes it by this much
 
@@ -146,9 +142,6 @@ __device__ __forceinline__ void load_words(unsigned (&w)[W], const uint8_t* src)
   }
 }
 
-#ifndef V_NST
-#define V_NST 4
-#endif
 // A ring stage: 32 tokens' K rows, V rows (XOR-ed), K and V (scale, zero) pairs.
 template <int D>
 struct Ring {
@@ -156,7 +149,7 @@ struct Ring {
   static constexpr int V_OFF = CHUNK * ROW;
   static constexpr int META_OFF = 2 * CHUNK * ROW;
   static constexpr int STAGE = META_OFF + 2 * CHUNK * 4;
-  static constexpr int NST = V_NST;
+  static constexpr int NST = 3;
   static constexpr int WARP = NST * STAGE;          // a warp's ring
 };
 // Byte offset of 16-byte chunk c of V row r within a stage's V rows: in each 128-byte line (2 or 4
@@ -177,8 +170,8 @@ struct WarpState {
   float ones[NT][4];                    // sum u'
 };
 
-// One chunk of `valid` tokens (all 32 unless MASKED) staged at `stage`.
-template <int D, int NT, bool MASKED>
+// One chunk of `valid` tokens (32 or more: all) staged at `stage`.
+template <int D, int NT>
 __device__ __forceinline__ void chunk_update(const unsigned char* stage, int valid, const unsigned (&qf)[NT][D / 16][2],
                                              const float (&ca)[NT][2], const float (&cb)[NT][2], WarpState<D, NT>& st,
                                              int g, int t, const int (&v_off)[4]) {
@@ -219,22 +212,38 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = 16 * i + g + 8 * r;
-      const bool live = !MASKED || row < valid;
       const float2 km = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + row * 4));
       vm[i][r] = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + CHUNK * 4 + row * 4));
-      if (!live) vm[i][r] = make_float2(0.f, 0.f);
-      const float e = log2_of(vm[i][r].x);
       vm[i][r].y = fmaf(8.f, vm[i][r].x, vm[i][r].y);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float y = fmaf(km.x, ca[n][j] * dot[i][n][2 * r + j], km.y * cb[n][j]);
-          x[n][i][2 * r + j] = live ? y : -INFINITY;
-          top[n][j] = fmaxf(top[n][j], x[n][i][2 * r + j] + e);
-        }
+        for (int j = 0; j < 2; ++j)
+          x[n][i][2 * r + j] = fmaf(km.x, ca[n][j] * dot[i][n][2 * r + j], km.y * cb[n][j]);
     }
   }
+  if (valid < CHUNK) {                  // rows past the context: no weight, whatever is there
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (16 * i + g + 8 * r >= valid) {
+          vm[i][r] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) x[n][i][2 * r] = x[n][i][2 * r + 1] = -INFINITY;
+        }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float e = log2_of(vm[i][r].x);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) top[n][j] = fmaxf(top[n][j], x[n][i][2 * r + j] + e);
+    }
   bool moves = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -307,7 +316,7 @@ struct Place {
 };
 
 template <int D, int NT, int LB>
-__global__ void __launch_bounds__(NW * 32, kResident) paged_attention_int4_kernel(const Int4Params p) {
+__global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const Int4Params p) {
   using R = Ring<D>;
   constexpr int HT = 8 * NT, WK = D / 32, ROW = R::ROW, B = 1 << LB;
   constexpr int PIECES = CHUNK * ROW / 16 / 32;              // 16-byte pieces of K, and of V, per lane and chunk
@@ -315,10 +324,12 @@ __global__ void __launch_bounds__(NW * 32, kResident) paged_attention_int4_kerne
   constexpr int BPC = CHUNK / B;                             // blocks per chunk
   extern __shared__ __align__(128) unsigned char smem[];     // the workers' rings
 
-  pkv::pdl_trigger();
+  // the joining kernel may start once all of this grid has come here: it reads the lengths before it
+  // waits for this grid, so they have to be there
   pkv::pdl_wait();
+  pkv::pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int worker = blockIdx.x * NW + warp;
+  const int worker = warp * gridDim.x + blockIdx.x;
   const int S = p.num_seqs, H = p.num_heads, Y = p.num_kv_heads * p.head_tiles;
 
   // this worker's piece of the line
@@ -565,10 +576,7 @@ __global__ void __launch_bounds__(NW * 32, kResident) paged_attention_int4_kerne
     fill(stage == 0 ? R::NST - 1 : stage - 1);
     const unsigned char* src = ring + stage * R::STAGE;
     const int valid = at.len - at.c * CHUNK;
-    if (valid >= CHUNK)
-      chunk_update<D, NT, false>(src, CHUNK, qf, ca, cb, st, g, t, v_off);
-    else
-      chunk_update<D, NT, true>(src, valid, qf, ca, cb, st, g, t, v_off);
+    chunk_update<D, NT>(src, valid, qf, ca, cb, st, g, t, v_off);
     if (++stage == R::NST) stage = 0;
     const bool to_end = at.c + 1 == at.chunks;
     if (to_end || left == 1) {
@@ -588,9 +596,8 @@ __global__ void __launch_bounds__(NW * 32, kResident) paged_attention_int4_kerne
 // Joins the parts of every cut stream, and writes the zeros of empty contexts: a warp per (sequence,
 // head), a lane D/32 values.
 template <int D>
-__global__ void __launch_bounds__(128) paged_attention_int4_merge_kernel(const Int4Params p, int head_rows) {
+__global__ void __launch_bounds__(128, 10) paged_attention_int4_merge_kernel(const Int4Params p, int head_rows) {
   pkv::pdl_trigger();
-  pkv::pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.x * 4 + warp, s = blockIdx.y;
   // chunks of the sequences before s, and of all
@@ -608,26 +615,31 @@ __global__ void __launch_bounds__(128) paged_attention_int4_merge_kernel(const I
     if (lane == 0) sums[warp][k] = mine[k];
   }
   __syncthreads();
-  if (h >= p.num_heads) return;
+  if (h >= p.num_heads) {
+    pkv::pdl_wait();
+    return;
+  }
   const long long before = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
   const long long total = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
   constexpr int V = D / 32;
   __half* dst = p.out + (static_cast<size_t>(s) * p.num_heads + h) * D + lane * V;
   const int chunks = chunks_of(p, s);
   if (chunks == 0) {
+    pkv::pdl_wait();
 #pragma unroll
     for (int c = 0; c < V; c += 2) *reinterpret_cast<__half2*>(dst + c) = __floats2half2_rn(0.f, 0.f);
     return;
   }
   const int Y = p.num_kv_heads * p.head_tiles, tile = h % p.group / head_rows;
   const int y = h / p.group * p.head_tiles + tile, row = h % p.group - tile * head_rows;
-  const long long first = before * Y + static_cast<long long>(y) * chunks, per = per_worker(total * Y, p.workers);
-  const long long w_first = first / per, w_last = (first + chunks - 1) / per;
+  const long long first = before * Y + static_cast<long long>(y) * chunks;
+  const long long per = per_worker(total * Y, p.workers), w_first = first / per, w_last = (first + chunks - 1) / per;
+  pkv::pdl_wait();                                           // the parts
   if (w_first == w_last) return;                             // one worker wrote it
   const int nparts = static_cast<int>(w_last - w_first) + 1, rows = min(head_rows, p.group);
   const size_t slot0 = static_cast<size_t>(w_first) + static_cast<size_t>(s) * Y + y;
   auto at = [&](int i) { return (slot0 + i) * rows + row; };  // part i's row of the workspace
-  // (m, l) of 32 slots at a time, one a lane; then eight slots' outputs in flight at a time
+  // (m, l) of 32 slots at a time, one a lane; then four slots' outputs in flight at a time
   float acc[V];
 #pragma unroll
   for (int c = 0; c < V; ++c) acc[c] = 0.f;
@@ -648,10 +660,10 @@ __global__ void __launch_bounds__(128) paged_attention_int4_merge_kernel(const I
     const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
     L = fmaf(ml.y, f, L);
     const int n = min(32, nparts - base);
-    for (int j0 = 0; j0 < n; j0 += 8) {
-      float x[8][V];
+    for (int j0 = 0; j0 < n; j0 += 4) {
+      float x[4][V];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 4; ++u) {
 #pragma unroll
         for (int c = 0; c < V; ++c) x[u][c] = 0.f;
         if (j0 + u < n) {
@@ -666,7 +678,7 @@ __global__ void __launch_bounds__(128) paged_attention_int4_merge_kernel(const I
         }
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 4; ++u) {
         const float fu = __shfl_sync(FULL, f, (j0 + u) & 31);
         if (j0 + u < n) {
 #pragma unroll
@@ -699,10 +711,11 @@ int device_sms() {
 }
 
 // Head tiles of 8 columns, or of 16 where a group has more than 8 heads (the rows are then unpacked
-// once for both); a grid that is resident at once, smaller where even the longest contexts would not
-// give every worker kMinChunks chunks.
+// once for both).  One CTA of twelve warps to an SM, or, where even the longest contexts would not give
+// each of those kMinChunks chunks, as many CTAs of four warps as that takes (smaller CTAs start sooner:
+// 14.4 against 16.3 us for one sequence of 2048 tokens and 40 heads).
 struct Plan {
-  int nt, head_tiles, head_rows, ctas;
+  int nt, head_tiles, head_rows, ctas, warps;
   long long slots, most_chunks;
 };
 Plan plan_for(int num_seqs, int num_heads, int num_kv_heads, int max_ctx) {
@@ -712,12 +725,12 @@ Plan plan_for(int num_seqs, int num_heads, int num_kv_heads, int max_ctx) {
   pl.head_tiles = (group + 8 * pl.nt - 1) / (8 * pl.nt);
   pl.head_rows = group < 8 * pl.nt ? group : 8 * pl.nt;
   const long long streams = static_cast<long long>(num_seqs) * num_kv_heads * pl.head_tiles;
-  const long long chunks = streams * ((max_ctx + CHUNK - 1) / CHUNK);
-  pl.most_chunks = chunks;
-  const long long ctas = (chunks + kMinChunks * NW - 1) / (kMinChunks * NW);
-  const long long most = static_cast<long long>(device_sms()) * kResident;
-  pl.ctas = static_cast<int>(ctas < most ? ctas : most);
-  pl.slots = streams + static_cast<long long>(pl.ctas) * NW;
+  pl.most_chunks = streams * ((max_ctx + CHUNK - 1) / CHUNK);
+  const long long workers = (pl.most_chunks + kMinChunks - 1) / kMinChunks, sms = device_sms();
+  const bool full = workers >= sms * NW;
+  pl.warps = full ? NW : 4;
+  pl.ctas = static_cast<int>(full ? sms : (workers + 3) / 4);
+  pl.slots = streams + static_cast<long long>(pl.ctas) * pl.warps;
   return pl;
 }
 size_t workspace_bytes_for(const Plan& pl, int head_dim) {
@@ -726,7 +739,7 @@ size_t workspace_bytes_for(const Plan& pl, int head_dim) {
 }
 
 template <int D, int NT, int LB>
-cudaError_t launch_kernel(const Int4Params& p, int ctas, cudaStream_t st) {
+cudaError_t launch_kernel(const Int4Params& p, const Plan& pl, cudaStream_t st) {
   constexpr int smem = NW * Ring<D>::WARP;
   static std::mutex mu;
   static bool done[64] = {false};
@@ -741,31 +754,32 @@ cudaError_t launch_kernel(const Int4Params& p, int ctas, cudaStream_t st) {
       if (dev >= 0 && dev < 64) done[dev] = true;
     }
   }
-  e = pkv::launch_pdl(paged_attention_int4_kernel<D, NT, LB>, dim3(ctas), dim3(NW * 32), smem, st, p);
+  e = pkv::launch_pdl(paged_attention_int4_kernel<D, NT, LB>, dim3(pl.ctas), dim3(pl.warps * 32),
+                      static_cast<size_t>(pl.warps) * Ring<D>::WARP, st, p);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 template <int D, int NT>
-cudaError_t launch_block_size(const Int4Params& p, int ctas, cudaStream_t st) {
+cudaError_t launch_block_size(const Int4Params& p, const Plan& pl, cudaStream_t st) {
   switch (p.log2_block) {
-    case 2: return launch_kernel<D, NT, 2>(p, ctas, st);
-    case 3: return launch_kernel<D, NT, 3>(p, ctas, st);
-    case 4: return launch_kernel<D, NT, 4>(p, ctas, st);
-    default: return launch_kernel<D, NT, 5>(p, ctas, st);
+    case 2: return launch_kernel<D, NT, 2>(p, pl, st);
+    case 3: return launch_kernel<D, NT, 3>(p, pl, st);
+    case 4: return launch_kernel<D, NT, 4>(p, pl, st);
+    default: return launch_kernel<D, NT, 5>(p, pl, st);
   }
 }
 
 template <int D>
 int launch(Int4Params p, const Plan& pl, void* ws, size_t ws_bytes, cudaStream_t st) {
   p.head_tiles = pl.head_tiles;
-  p.workers = pl.ctas * NW;
+  p.workers = pl.ctas * pl.warps;
   const size_t need = workspace_bytes_for(pl, D);
   if (ws == nullptr || ws_bytes < need)
     return pkv::fail(PKV_ERR_WORKSPACE, "pkv_paged_attention_decode_int4: workspace of %zu bytes needed, %zu given", need,
                      ws == nullptr ? static_cast<size_t>(0) : ws_bytes);
   p.ws_ml = static_cast<float*>(ws);
   p.ws_o = p.ws_ml + ws_ml_floats(static_cast<size_t>(pl.slots) * pl.head_rows);
-  cudaError_t e = pl.nt == 1 ? launch_block_size<D, 1>(p, pl.ctas, st) : launch_block_size<D, 2>(p, pl.ctas, st);
+  cudaError_t e = pl.nt == 1 ? launch_block_size<D, 1>(p, pl, st) : launch_block_size<D, 2>(p, pl, st);
   if (e == cudaSuccess)
     e = pkv::launch_pdl(paged_attention_int4_merge_kernel<D>, dim3((p.num_heads + 3) / 4, p.num_seqs), dim3(128), 0, st,
                         p, pl.head_rows);
@@ -849,7 +863,7 @@ int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, c
   while ((1 << p.log2_block) < block_size) ++p.log2_block;
   p.scale_log2 = scale * 1.4426950408889634f;
   const Plan pl = plan_for(num_seqs, num_heads, num_kv_heads, max_blocks_per_seq * block_size);
-  if (pl.most_chunks / (pl.ctas * NW) >= (1LL << 30))
+  if (pl.most_chunks / (pl.ctas * pl.warps) >= (1LL << 30))
     return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: more than 2^30 chunks of %d tokens per warp", fn, CHUNK);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int rc = head_dim == 128 ? launch<128>(p, pl, workspace, workspace_bytes, st)
