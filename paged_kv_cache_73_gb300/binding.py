@@ -9,6 +9,7 @@ or a call fails, a ``PkvError`` is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -674,6 +675,12 @@ def paged_attention_int4_workspace_size(num_seqs: int, num_heads: int, num_kv_he
                                                               max_blocks_per_seq, block_size))
 
 
+@functools.lru_cache(maxsize=1024)
+def _int4_workspace_size(device: int, *sizes: int) -> int:
+    """The size for a device's SM count and these sizes, as the library gives it."""
+    return paged_attention_int4_workspace_size(*sizes)
+
+
 def paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                 block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
                                 block_size: int, out: Optional[torch.Tensor] = None,
@@ -700,7 +707,7 @@ def paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
         if out.shape != q.shape:
             raise PkvError(PKV_ERR_INVALID_ARG, "paged_attention_decode_int4: out must be shaped like q")
     if workspace is None:
-        n = paged_attention_int4_workspace_size(S, H, Hk, D, max_blocks, block_size)
+        n = _int4_workspace_size(dev, S, H, Hk, D, max_blocks, block_size)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load().pkv_paged_attention_decode_int4(
