@@ -26,6 +26,11 @@
 // joins a byte of two tokens' words into two fp16 pairs.  P^T comes from S^T's
 // accumulator by an 8x8 transpose in registers (movmatrix).
 //
+// Where each cached head has one query head, the products' other seven columns are idle, and
+// so would be most of the softmax: a warp then deals the 32 logits of its one column out,
+// one to a lane, and brings the weights back by one transpose and three shuffles (a fifth of
+// the chunk's instructions saved).
+//
 // Softmax in base 2 with a running maximum that moves only when a chunk raises it by
 // more than 2^8.  The weight that multiplies V's whole numbers is u_t = p_t s_t, rounded
 // to fp16; the maximum is kept over x_t + log2 of s_t's exponent, so that u is at most
@@ -162,7 +167,8 @@ __device__ __forceinline__ int v_place(int r, int c) {
 }
 
 // A worker's running softmax over one stream's tokens for 8 NT heads; lane (g, t) holds heads 8 n + 2t,
-// 8 n + 2t + 1.
+// 8 n + 2t + 1.  With a lone head (SOLO) only [0][0] is used: m by all lanes alike, l and c for the one
+// token of each chunk that a lane takes, acc and ones in lanes with t = 0.
 template <int D, int NT>
 struct WarpState {
   float m[NT][2], l[NT][2], c[NT][2];   // l and c: this lane's tokens only, until the end
@@ -171,18 +177,13 @@ struct WarpState {
 };
 
 // One chunk of `valid` tokens (32 or more: all) staged at `stage`.
-template <int D, int NT>
+template <int D, int NT, bool SOLO>
 __device__ __forceinline__ void chunk_update(const unsigned char* stage, int valid, const unsigned (&qf)[NT][D / 16][2],
                                              const float (&ca)[NT][2], const float (&cb)[NT][2], WarpState<D, NT>& st,
                                              int g, int t, const int (&v_off)[4]) {
   using R = Ring<D>;
   constexpr int WK = D / 32;            // words of a K row per lane
   constexpr int WV = D / 64;            // words of a V row per lane
-  float x[NT][2][4];                    // tile i, {token g: heads 2t, 2t + 1; token g + 8: the same}
-  float2 vm[2][2];                      // V's scale and zero + 8 scale of those tokens
-  float top[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
   // the two tiles' products side by side: each is a chain of dependent accumulations
   unsigned kw[2][2][WK];
   float dot[2][NT][4];
@@ -207,87 +208,132 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = 16 * i + g + 8 * r;
-      const float2 km = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + row * 4));
-      vm[i][r] = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + CHUNK * 4 + row * 4));
-      vm[i][r].y = fmaf(8.f, vm[i][r].x, vm[i][r].y);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          x[n][i][2 * r + j] = fmaf(km.x, ca[n][j] * dot[i][n][2 * r + j], km.y * cb[n][j]);
+  unsigned pb[NT][2][2];                // P^T: tile i, rows 2t, 2t + 1 and those + 8
+  if constexpr (SOLO) {
+    // lane (g, t) takes the token of tile t / 2, row g + 8 (t % 2), whose dot lane (g, 0) holds
+    const int from = 4 * g, row = 16 * (t >> 1) + g + 8 * (t & 1);
+    const float d00 = __shfl_sync(FULL, dot[0][0][0], from), d01 = __shfl_sync(FULL, dot[0][0][2], from);
+    const float d10 = __shfl_sync(FULL, dot[1][0][0], from), d11 = __shfl_sync(FULL, dot[1][0][2], from);
+    const float d = t < 2 ? (t == 0 ? d00 : d01) : (t == 2 ? d10 : d11);
+    const float2 km = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + row * 4));
+    float2 vm = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + CHUNK * 4 + row * 4));
+    float x = fmaf(km.x, ca[0][0] * d, km.y * cb[0][0]);
+    if (row >= valid) {                 // past the context: no weight, whatever is there
+      vm = make_float2(0.f, 0.f);
+      x = -INFINITY;
     }
-  }
-  if (valid < CHUNK) {                  // rows past the context: no weight, whatever is there
+    float top = x + log2_of(vm.x);
+    if (__any_sync(FULL, top > st.m[0][0] + kRescale)) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int o = 1; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+      const float m = fmaxf(st.m[0][0], top), f = m == -INFINITY ? 1.f : exp2f(st.m[0][0] - m);
+      st.m[0][0] = m;
+      st.l[0][0] *= f;
+      st.c[0][0] *= f;
+      st.ones[0][0] *= f;
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        if (16 * i + g + 8 * r >= valid) {
-          vm[i][r] = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) x[n][i][2 * r] = x[n][i][2 * r + 1] = -INFINITY;
-        }
-    __syncwarp();
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float e = log2_of(vm[i][r].x);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) top[n][j] = fmaxf(top[n][j], x[n][i][2 * r + j] + e);
-    }
-  bool moves = false;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) moves |= top[n][j] > st.m[n][j] + kRescale;
-  if (__any_sync(FULL, moves)) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int o = 4; o < 32; o *= 2) top[n][j] = fmaxf(top[n][j], __shfl_xor_sync(FULL, top[n][j], o));
-        const float m = fmaxf(st.m[n][j], top[n][j]);
-        const float f = m == -INFINITY ? 1.f : exp2f(st.m[n][j] - m);
-        st.m[n][j] = m;
-        st.l[n][j] *= f;
-        st.c[n][j] *= f;
-        st.ones[n][j] *= f;
-        st.ones[n][2 + j] *= f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          st.acc[n][i][j] *= f;
-          st.acc[n][i][2 + j] *= f;
-        }
+      for (int i = 0; i < D / 16; ++i) {
+        st.acc[0][i][0] *= f;
+        st.acc[0][i][2] *= f;
       }
-  }
-  unsigned pb[NT][2][2];
+    }
+    const float w = fast_exp2(x - st.m[0][0]);
+    st.l[0][0] += w;
+    st.c[0][0] = fmaf(w, fmaf(8.f, vm.x, vm.y), st.c[0][0]);
+    // transposed, lane (2k, t) holds the weights of rows 2t, 2t + 1 of the k-th eight tokens: column 0 of the
+    // products wants all four in lane (0, t); what other columns hold does not matter
+    const unsigned u = transpose8x8(static_cast<unsigned>(__half_as_ushort(__float2half_rn(w * vm.x))));
+    pb[0][0][0] = u;
+    pb[0][0][1] = __shfl_sync(FULL, u, 8 + t);
+    pb[0][1][0] = __shfl_sync(FULL, u, 16 + t);
+    pb[0][1][1] = __shfl_sync(FULL, u, 24 + t);
+  } else {
+    float x[NT][2][4];                    // tile i, {token g: heads 2t, 2t + 1; token g + 8: the same}
+    float2 vm[2][2];                      // V's scale and zero + 8 scale of those tokens
+    float top[NT][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = 16 * i + g + 8 * r;
+        const float2 km = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + row * 4));
+        vm[i][r] = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + CHUNK * 4 + row * 4));
+        vm[i][r].y = fmaf(8.f, vm[i][r].x, vm[i][r].y);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            x[n][i][2 * r + j] = fmaf(km.x, ca[n][j] * dot[i][n][2 * r + j], km.y * cb[n][j]);
+      }
+    }
+    if (valid < CHUNK) {                  // rows past the context: no weight, whatever is there
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (16 * i + g + 8 * r >= valid) {
+            vm[i][r] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n][i][2 * r] = x[n][i][2 * r + 1] = -INFINITY;
+          }
+      __syncwarp();
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float u[2];
+        const float e = log2_of(vm[i][r].x);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) top[n][j] = fmaxf(top[n][j], x[n][i][2 * r + j] + e);
+      }
+    bool moves = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) moves |= top[n][j] > st.m[n][j] + kRescale;
+    if (__any_sync(FULL, moves)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          // the chunk has a valid token, so the maximum is not -inf (a NaN logit makes NaNs)
-          const float w = fast_exp2(x[n][i][2 * r + j] - st.m[n][j]);
-          st.l[n][j] += w;
-          u[j] = w * vm[i][r].x;
-          st.c[n][j] = fmaf(w, vm[i][r].y, st.c[n][j]);
+#pragma unroll
+          for (int o = 4; o < 32; o *= 2) top[n][j] = fmaxf(top[n][j], __shfl_xor_sync(FULL, top[n][j], o));
+          const float m = fmaxf(st.m[n][j], top[n][j]);
+          const float f = m == -INFINITY ? 1.f : exp2f(st.m[n][j] - m);
+          st.m[n][j] = m;
+          st.l[n][j] *= f;
+          st.c[n][j] *= f;
+          st.ones[n][j] *= f;
+          st.ones[n][2 + j] *= f;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            st.acc[n][i][j] *= f;
+            st.acc[n][i][2 + j] *= f;
+          }
         }
-        pb[n][i][r] = transpose8x8(pack2(u[0], u[1]));
-      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float u[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            // the chunk has a valid token, so the maximum is not -inf (a NaN logit makes NaNs)
+            const float w = fast_exp2(x[n][i][2 * r + j] - st.m[n][j]);
+            st.l[n][j] += w;
+            u[j] = w * vm[i][r].x;
+            st.c[n][j] = fmaf(w, vm[i][r].y, st.c[n][j]);
+          }
+          pb[n][i][r] = transpose8x8(pack2(u[0], u[1]));
+        }
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     unsigned va[4][WV];                 // tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the tile
@@ -315,7 +361,7 @@ struct Place {
   int s, y, c, chunks, len;
 };
 
-template <int D, int NT, int LB>
+template <int D, int NT, bool SOLO, int LB>
 __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const Int4Params p) {
   using R = Ring<D>;
   constexpr int HT = 8 * NT, WK = D / 32, ROW = R::ROW, B = 1 << LB;
@@ -506,8 +552,8 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
       const float b = p.scale_log2 * sum;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        ca[n][j] = __shfl_sync(FULL, a, (2 * t + j) * 4);
-        cb[n][j] = __shfl_sync(FULL, b, (2 * t + j) * 4);
+        ca[n][j] = __shfl_sync(FULL, a, SOLO ? 0 : (2 * t + j) * 4);
+        cb[n][j] = __shfl_sync(FULL, b, SOLO ? 0 : (2 * t + j) * 4);
         st.m[n][j] = -INFINITY;
         st.l[n][j] = st.c[n][j] = 0.f;
         st.ones[n][j] = st.ones[n][2 + j] = 0.f;
@@ -526,9 +572,9 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < (SOLO ? 1 : 2); ++j) {
 #pragma unroll
-        for (int o = 4; o < 32; o *= 2) {
+        for (int o = SOLO ? 1 : 4; o < 32; o *= 2) {
           st.l[n][j] += __shfl_xor_sync(FULL, st.l[n][j], o);
           st.c[n][j] += __shfl_xor_sync(FULL, st.c[n][j], o);
         }
@@ -576,7 +622,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
     fill(stage == 0 ? R::NST - 1 : stage - 1);
     const unsigned char* src = ring + stage * R::STAGE;
     const int valid = at.len - at.c * CHUNK;
-    chunk_update<D, NT>(src, valid, qf, ca, cb, st, g, t, v_off);
+    chunk_update<D, NT, SOLO>(src, valid, qf, ca, cb, st, g, t, v_off);
     if (++stage == R::NST) stage = 0;
     const bool to_end = at.c + 1 == at.chunks;
     if (to_end || left == 1) {
@@ -738,7 +784,7 @@ size_t workspace_bytes_for(const Plan& pl, int head_dim) {
   return (ws_ml_floats(rows) + rows * head_dim) * sizeof(float);
 }
 
-template <int D, int NT, int LB>
+template <int D, int NT, bool SOLO, int LB>
 cudaError_t launch_kernel(const Int4Params& p, const Plan& pl, cudaStream_t st) {
   constexpr int smem = NW * Ring<D>::WARP;
   static std::mutex mu;
@@ -749,23 +795,23 @@ cudaError_t launch_kernel(const Int4Params& p, const Plan& pl, cudaStream_t st) 
   {
     std::lock_guard<std::mutex> g(mu);
     if (dev < 0 || dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(paged_attention_int4_kernel<D, NT, LB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      e = cudaFuncSetAttribute(paged_attention_int4_kernel<D, NT, SOLO, LB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) done[dev] = true;
     }
   }
-  e = pkv::launch_pdl(paged_attention_int4_kernel<D, NT, LB>, dim3(pl.ctas), dim3(pl.warps * 32),
+  e = pkv::launch_pdl(paged_attention_int4_kernel<D, NT, SOLO, LB>, dim3(pl.ctas), dim3(pl.warps * 32),
                       static_cast<size_t>(pl.warps) * Ring<D>::WARP, st, p);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SOLO>
 cudaError_t launch_block_size(const Int4Params& p, const Plan& pl, cudaStream_t st) {
   switch (p.log2_block) {
-    case 2: return launch_kernel<D, NT, 2>(p, pl, st);
-    case 3: return launch_kernel<D, NT, 3>(p, pl, st);
-    case 4: return launch_kernel<D, NT, 4>(p, pl, st);
-    default: return launch_kernel<D, NT, 5>(p, pl, st);
+    case 2: return launch_kernel<D, NT, SOLO, 2>(p, pl, st);
+    case 3: return launch_kernel<D, NT, SOLO, 3>(p, pl, st);
+    case 4: return launch_kernel<D, NT, SOLO, 4>(p, pl, st);
+    default: return launch_kernel<D, NT, SOLO, 5>(p, pl, st);
   }
 }
 
@@ -779,7 +825,8 @@ int launch(Int4Params p, const Plan& pl, void* ws, size_t ws_bytes, cudaStream_t
                      ws == nullptr ? static_cast<size_t>(0) : ws_bytes);
   p.ws_ml = static_cast<float*>(ws);
   p.ws_o = p.ws_ml + ws_ml_floats(static_cast<size_t>(pl.slots) * pl.head_rows);
-  cudaError_t e = pl.nt == 1 ? launch_block_size<D, 1>(p, pl, st) : launch_block_size<D, 2>(p, pl, st);
+  cudaError_t e = p.group == 1 ? launch_block_size<D, 1, true>(p, pl, st)
+                  : pl.nt == 1 ? launch_block_size<D, 1, false>(p, pl, st) : launch_block_size<D, 2, false>(p, pl, st);
   if (e == cudaSuccess)
     e = pkv::launch_pdl(paged_attention_int4_merge_kernel<D>, dim3((p.num_heads + 3) / 4, p.num_seqs), dim3(128), 0, st,
                         p, pl.head_rows);
