@@ -484,7 +484,8 @@ int pkv_swap_blocks_int4(const uint8_t* const* src_k_caches, const uint8_t* cons
  * must be device memory, and that the workspace is always needed (at least
  * pkv_paged_attention_int4_workspace_size(...) bytes on the current device).  Products of q and the cached whole
  * numbers are exact, sums are fp32; the softmax weights, times the rows' V scales,
- * are rounded to fp16 before they multiply V.
+ * are rounded to fp16 before they multiply V (with one query head to a K/V head
+ * what the rounding leaves multiplies V too).
  * ------------------------------------------------------------------------- */
 size_t pkv_paged_attention_int4_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                                int max_blocks_per_seq, int block_size);

@@ -29,7 +29,8 @@
 // Where each cached head has one query head, the products' other seven columns are idle, and
 // so would be most of the softmax: a warp then deals the 32 logits of its one column out,
 // one to a lane, and brings the weights back by one transpose and three shuffles (a fifth of
-// the chunk's instructions saved).
+// the chunk's instructions saved).  Its second column takes what the weights' rounding to fp16
+// left, which costs nothing there.
 //
 // Softmax in base 2 with a running maximum that moves only when a chunk raises it by
 // more than 2^8.  The weight that multiplies V's whole numbers is u_t = p_t s_t, rounded
@@ -167,8 +168,9 @@ __device__ __forceinline__ int v_place(int r, int c) {
 }
 
 // A worker's running softmax over one stream's tokens for 8 NT heads; lane (g, t) holds heads 8 n + 2t,
-// 8 n + 2t + 1.  With a lone head (SOLO) only [0][0] is used: m by all lanes alike, l and c for the one
-// token of each chunk that a lane takes, acc and ones in lanes with t = 0.
+// 8 n + 2t + 1.  With a lone head (SOLO) m, l and c use [0][0]: m by all lanes alike, l and c for the one token
+// of each chunk that a lane takes; acc and ones in lanes with t = 0 (columns 0 and 1: the weights
+// and what their rounding left).
 template <int D, int NT>
 struct WarpState {
   float m[NT][2], l[NT][2], c[NT][2];   // l and c: this lane's tokens only, until the end
@@ -231,22 +233,26 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
       st.l[0][0] *= f;
       st.c[0][0] *= f;
       st.ones[0][0] *= f;
+      st.ones[0][1] *= f;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        st.acc[0][i][0] *= f;
-        st.acc[0][i][2] *= f;
-      }
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st.acc[0][i][j] *= f;
     }
     const float w = fast_exp2(x - st.m[0][0]);
     st.l[0][0] += w;
     st.c[0][0] = fmaf(w, fmaf(8.f, vm.x, vm.y), st.c[0][0]);
-    // transposed, lane (2k, t) holds the weights of rows 2t, 2t + 1 of the k-th eight tokens: column 0 of the
-    // products wants all four in lane (0, t); what other columns hold does not matter
-    const unsigned u = transpose8x8(static_cast<unsigned>(__half_as_ushort(__float2half_rn(w * vm.x))));
-    pb[0][0][0] = u;
-    pb[0][0][1] = __shfl_sync(FULL, u, 8 + t);
-    pb[0][1][0] = __shfl_sync(FULL, u, 16 + t);
-    pb[0][1][1] = __shfl_sync(FULL, u, 24 + t);
+    // The weight in two halves, u' and what its rounding left: columns 0 and 1.  Transposed, lane (2k, t)
+    // holds u' of rows 2t, 2t + 1 of the k-th eight tokens and lane (2k + 1, t) the rest; the products want
+    // the four in lanes (0, t) and (1, t), and what other columns hold does not matter.
+    const float u = w * vm.x;
+    const __half hi = __float2half_rn(u), rest = __float2half_rn(u - __half2float(hi));
+    const unsigned both = transpose8x8(static_cast<unsigned>(__half_as_ushort(hi)) | static_cast<unsigned>(__half_as_ushort(rest)) << 16);
+    const int column = (4 * g + t) & 7;
+    pb[0][0][0] = both;
+    pb[0][0][1] = __shfl_sync(FULL, both, 8 + column);
+    pb[0][1][0] = __shfl_sync(FULL, both, 16 + column);
+    pb[0][1][1] = __shfl_sync(FULL, both, 24 + column);
   } else {
     float x[NT][2][4];                    // tile i, {token g: heads 2t, 2t + 1; token g + 8: the same}
     float2 vm[2][2];                      // V's scale and zero + 8 scale of those tokens
@@ -465,6 +471,12 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
         entry = read_entry(first);
         entry_next = read_entry(first + 32);
         head_off = ahead.y / p.head_tiles * tile_bytes;
+        // its queries, for when the products come to it
+        const int in_group = ahead.y % p.head_tiles * HT, h0 = ahead.y / p.head_tiles * p.group + in_group;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          if (n * 8 + g < min(HT, p.group - in_group))
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + (static_cast<size_t>(ahead.s) * H + h0 + n * 8 + g) * D + t * (D / 4)));
         fresh = false;
       } else if (blk == first) {
         entry = entry_next;
@@ -580,6 +592,14 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
         }
         const int h = n * 8 + 2 * t + j;
         if (h >= nh) continue;
+        if constexpr (SOLO) {                                // the weights' two halves
+          st.ones[0][0] += st.ones[0][1];
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            st.acc[0][i][0] += st.acc[0][i][1];
+            st.acc[0][i][2] += st.acc[0][i][3];
+          }
+        }
         const float mid = fmaf(-8.f, st.ones[n][j], st.c[n][j]);
         float o[D / 8];                                      // word i / 4, byte i % 4: values 2 i and 2 i + 1
 #pragma unroll
