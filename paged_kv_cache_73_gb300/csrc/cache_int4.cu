@@ -5,14 +5,16 @@
 // 68 bytes for D = 128 where fp16 takes 256.  It stands for lo + s * n.
 //
 // Both kernels are HBM-bound.  A warp takes a token's rows (or a part of them, where there
-// are few tokens), D/16 lanes a row, 16 values a lane in two 16-byte chunks half a row
-// apart, so that every access of a row is contiguous over its lanes.
+// are few tokens), so that every access of a row is contiguous over its lanes in whole
+// sectors.  The read-back has 16 values to a lane in two 16-byte chunks half a row apart.
 //
-// The write has about 4.5 values to handle per clock and SM at HBM rate, so it counts
-// instructions: minimum and maximum on packed fp16 pairs, and the quotients two to an
-// instruction.  u = x / s - lo / s is rounded by adding and taking off 1.5 * 2^23; only
-// where u comes nearer to a half than its error bound (some 2^-16 of all values) is n
-// decided by the exact remainder.
+// The write has about 9 values to handle per clock and SM at HBM rate, so it counts
+// instructions: 32 values to a lane, which halves what a row costs beside its values (150 ->
+// 143 us for the write and read-back of 16 411 tokens of 2 x 40 rows of 128); minimum and
+// maximum on packed fp16 pairs; the quotients two to an instruction.  u = x / s - lo / s is
+// rounded by adding and taking off 1.5 * 2^23, whose low bytes are then gathered; only where
+// u comes nearer to a half than its error bound (some 2^-16 of all values) is n decided by
+// the exact remainder.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -82,23 +84,24 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // Eight values' n, four bits each.  d / s = u + e with u = x inv + b, b = -lo inv: inv is off by 2^-23
 // relative and the sum by 2^-24 of it, so e is below 2^-18 + 2^-23 |b|; `sure` is one half less more
 // than that.
-__device__ __forceinline__ unsigned pack8(const uint4& raw, float inv, float b, float lo, float s, float sure, bool past) {
-  constexpr float kMagic = 12582912.f;              // 1.5 * 2^23: the sum's low bits are the whole number
+__device__ __forceinline__ unsigned pack8(const uint4& raw, float inv, float b, float lo, float s, float sure) {
+  constexpr float kMagic = 12582912.f;              // 1.5 * 2^23: the sum's low byte is the whole number
   const __half2* h2 = reinterpret_cast<const __half2*>(&raw);
-  unsigned word = 0;
-  float most = 0.f, least = 0.f;
+  unsigned m[8];
+  float far = 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 u = fma2(__half22float2(h2[e]), inv, make_float2(b, b));
-    const float2 m = add2(u, kMagic);
-    const float2 r = fma2(add2(m, -kMagic), -1.f, u);
-    most = fmaxf(most, fmaxf(r.x, r.y));
-    least = fminf(least, fminf(r.x, r.y));
-    word += __float_as_uint(m.x) << (8 * e);
-    word += __float_as_uint(m.y) << (8 * e + 4);
+    const float2 n = add2(u, kMagic);
+    const float2 r = fma2(add2(n, -kMagic), -1.f, u);
+    far = fmaxf(far, fmaxf(fabsf(r.x), fabsf(r.y)));
+    m[2 * e] = __float_as_uint(n.x);
+    m[2 * e + 1] = __float_as_uint(n.y);
   }
-  word -= 0x4B400000u * 0x11111111u;                // the magic number's own bits, eight times
-  if (past || most >= sure || least <= -sure) {
+  const unsigned even = __byte_perm(__byte_perm(m[0], m[2], 0x0040), __byte_perm(m[4], m[6], 0x0040), 0x5410);
+  const unsigned odd = __byte_perm(__byte_perm(m[1], m[3], 0x0040), __byte_perm(m[5], m[7], 0x0040), 0x5410);
+  unsigned word = even + (odd << 4);
+  if (!(far < sure)) {
     word = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -113,9 +116,8 @@ __device__ __forceinline__ unsigned pack8(const uint4& raw, float inv, float b, 
 // grid (tokens / kWarps, parts of a token's K and V rows)
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32, 7) reshape_and_cache_int4_kernel(const Int4RowParams p) {
-  constexpr int LPR = D / 16;                       // lanes per row
+  constexpr int LPR = D / 32;                       // lanes per row: 16 values of each half of it to a lane
   constexpr int RPP = 32 / LPR;                     // rows a warp takes at a time
-  constexpr int PF = 2;                             // of which so many are in flight
   pkv::pdl_trigger();
   pkv::pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR;
@@ -123,21 +125,21 @@ __global__ void __launch_bounds__(kWarps * 32, 7) reshape_and_cache_int4_kernel(
   if (t >= p.num_tokens) return;
   const int H = p.num_heads;
   const int begin = blockIdx.y * p.rows_per_warp, end = min(2 * H, begin + p.rows_per_warp);
-  const __half* key = p.key + t * p.key_stride + c * 8;
-  const __half* value = p.value + t * p.value_stride + c * 8 - static_cast<int64_t>(H) * D;
-  uint4 raw[PF][2];
-  auto load = [&](int r, uint4 (&x)[2]) {
+  const __half* key = p.key + t * p.key_stride + c * 16;
+  const __half* value = p.value + t * p.value_stride + c * 16 - static_cast<int64_t>(H) * D;
+  uint4 raw[4];
+  auto load = [&](int r, uint4 (&x)[4]) {
     if (r < end) {
       const __half* src = (r < H ? key : value) + r * D;
-      x[0] = *reinterpret_cast<const uint4*>(src);
-      x[1] = *reinterpret_cast<const uint4*>(src + D / 2);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const uint4*>(src + (k >> 1) * (D / 2) + (k & 1) * 8);
     } else {
-      x[0] = x[1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = make_uint4(0, 0, 0, 0);
     }
   };
   const int first = begin + lane / LPR;
-#pragma unroll
-  for (int u = 0; u < PF; ++u) load(first + u * RPP, raw[u]);
+  load(first, raw);
   const int64_t slot = p.slots[t];
   if (slot < 0) return;                             // padding token
   if (slot >= p.num_slots) {
@@ -148,45 +150,47 @@ __global__ void __launch_bounds__(kWarps * 32, 7) reshape_and_cache_int4_kernel(
   const int64_t block_base = (slot >> p.log2_block) * H * p.tile_bytes;
   uint8_t* k_block = p.k_cache + block_base;
   uint8_t* v_block = p.v_cache + block_base - static_cast<int64_t>(H) * p.tile_bytes;
-  const int data_off = in_block * (D / 2) + c * 4;
+  const int data_off = in_block * (D / 2) + c * 8;
   const int meta_off = ((D / 2) << p.log2_block) + in_block * 4;
-  for (int row = first; row - lane / LPR < end; row += PF * RPP) {
+  for (int r = first; r - lane / LPR < end; r += RPP) {
+    uint4 x[4];
 #pragma unroll
-    for (int u = 0; u < PF; ++u) {
-      const int r = row + u * RPP;
-      const uint4 x0 = raw[u][0], x1 = raw[u][1];
-      load(r + PF * RPP, raw[u]);
-      // NaN-keeping minimum and maximum: a row that holds a NaN gets a NaN scale
-      const __half2* h0 = reinterpret_cast<const __half2*>(&x0);
-      const __half2* h1 = reinterpret_cast<const __half2*>(&x1);
-      __half2 lo2 = h0[0], hi2 = h0[0];
+    for (int k = 0; k < 4; ++k) x[k] = raw[k];
+    load(r + RPP, raw);
+    // NaN-keeping minimum and maximum: a row that holds a NaN gets a NaN scale
+    __half2 lo2 = *reinterpret_cast<const __half2*>(&x[0]), hi2 = lo2;
 #pragma unroll
-      for (int e = 1; e < 8; ++e) {
-        lo2 = __hmin2_nan(lo2, e < 4 ? h0[e] : h1[e - 4]);
-        hi2 = __hmax2_nan(hi2, e < 4 ? h0[e] : h1[e - 4]);
+    for (int k = 0; k < 4; ++k) {
+      const __half2* h2 = reinterpret_cast<const __half2*>(&x[k]);
+#pragma unroll
+      for (int e = k == 0 ? 1 : 0; e < 4; ++e) {
+        lo2 = __hmin2_nan(lo2, h2[e]);
+        hi2 = __hmax2_nan(hi2, h2[e]);
       }
-      // lowest and negated highest side by side: one shuffle a step
-      __half2 both = __hmin2_nan(__lows2half2(lo2, __hneg2(hi2)), __highs2half2(lo2, __hneg2(hi2)));
+    }
+    // lowest and negated highest side by side: one shuffle a step
+    __half2 both = __hmin2_nan(__lows2half2(lo2, __hneg2(hi2)), __highs2half2(lo2, __hneg2(hi2)));
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o /= 2) both = __hmin2_nan(both, __shfl_xor_sync(0xffffffffu, both, o));
-      const float lo = __low2float(both), span = -__high2float(both) - lo;
-      // span / 15 correctly rounded: one step of Markstein's division by a constant
-      constexpr float kFifteenth = 1.f / 15.f;
-      const float s0 = span * kFifteenth;
-      __half s_h = __float2half_rn(fmaf(fmaf(-s0, 15.f, span), kFifteenth, s0));
-      const float s = __half2float(s_h);
-      if (!(s <= 65504.f)) s_h = __ushort_as_half(0x7fff);   // a row that is not finite stands for NaNs
-      const float inv = s > 0.f ? rcp_approx(s) : 0.f;
-      const float b = -lo * inv;
-      const float sure = 0.5f - 0x1p-17f - fabsf(b) * 0x1p-22f;
-      const bool past = span * inv > 15.25f;        // only where a scale below 2^-14 was rounded down
-      const unsigned w0 = pack8(x0, inv, b, lo, s, sure, past), w1 = pack8(x1, inv, b, lo, s, sure, past);
-      if (r < end) {
-        uint8_t* tile = (r < H ? k_block : v_block) + static_cast<int64_t>(r) * p.tile_bytes;
-        *reinterpret_cast<unsigned*>(tile + data_off) = w0;
-        *reinterpret_cast<unsigned*>(tile + data_off + D / 4) = w1;
-        if (c == 0) *reinterpret_cast<__half2*>(tile + meta_off) = __halves2half2(s_h, __low2half(both));
-      }
+    for (int o = LPR / 2; o > 0; o /= 2) both = __hmin2_nan(both, __shfl_xor_sync(0xffffffffu, both, o));
+    const float lo = __low2float(both), span = -__high2float(both) - lo;
+    // span / 15 correctly rounded: one step of Markstein's division by a constant
+    constexpr float kFifteenth = 1.f / 15.f;
+    const float s0 = span * kFifteenth;
+    __half s_h = __float2half_rn(fmaf(fmaf(-s0, 15.f, span), kFifteenth, s0));
+    const float s = __half2float(s_h);
+    if (!(s <= 65504.f)) s_h = __ushort_as_half(0x7fff);   // a row that is not finite stands for NaNs
+    const float inv = s > 0.f ? rcp_approx(s) : 0.f;
+    const float b = -lo * inv;
+    // past: only where a scale below 2^-14 was rounded down
+    const float sure = span * inv > 15.25f ? -1.f : 0.5f - 0x1p-17f - fabsf(b) * 0x1p-22f;
+    unsigned w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = pack8(x[k], inv, b, lo, s, sure);
+    if (r < end) {
+      uint8_t* tile = (r < H ? k_block : v_block) + static_cast<int64_t>(r) * p.tile_bytes;
+      *reinterpret_cast<uint2*>(tile + data_off) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(tile + data_off + D / 4) = make_uint2(w[2], w[3]);
+      if (c == 0) *reinterpret_cast<__half2*>(tile + meta_off) = __halves2half2(s_h, __low2half(both));
     }
   }
 }
@@ -275,15 +279,15 @@ int check_shape(const char* fn, int num_tokens, int num_heads, int head_dim, int
 
 // A warp per token; where that leaves SMs short of warps, a token's 2 H rows are split.
 template <typename Kernel>
-int launch_rows(const char* fn, Kernel k64, Kernel k128, Int4RowParams p, int num_tokens, int head_dim, int block_size,
-                int num_blocks, void* stream) {
+int launch_rows(const char* fn, Kernel k64, Kernel k128, int values_per_lane, Int4RowParams p, int num_tokens, int head_dim,
+                int block_size, int num_blocks, void* stream) {
   int lb = 0;
   while ((1 << lb) < block_size) ++lb;
   p.log2_block = lb;
   p.tile_bytes = block_size * (head_dim / 2 + 4);
   p.num_slots = static_cast<int64_t>(num_blocks) * block_size;
   p.num_tokens = num_tokens;
-  const int rpp = 512 / head_dim, passes = (2 * p.num_heads + rpp - 1) / rpp;
+  const int rpp = 32 * values_per_lane / head_dim, passes = (2 * p.num_heads + rpp - 1) / rpp;
   int splits = num_tokens >= pkv::kFullWarps ? 1 : (pkv::kFullWarps + num_tokens - 1) / num_tokens;
   if (splits > passes) splits = passes;
   const int per = (passes + splits - 1) / splits;
@@ -342,7 +346,7 @@ int pkv_reshape_and_cache_int4(const uint16_t* key, const uint16_t* value, uint8
   p.key_stride = key_stride;
   p.value_stride = value_stride;
   p.num_heads = num_kv_heads;
-  return launch_rows(fn, reshape_and_cache_int4_kernel<64>, reshape_and_cache_int4_kernel<128>, p, num_tokens, head_dim,
+  return launch_rows(fn, reshape_and_cache_int4_kernel<64>, reshape_and_cache_int4_kernel<128>, 32, p, num_tokens, head_dim,
                      block_size, num_blocks, stream);
 }
 
@@ -367,7 +371,7 @@ int pkv_gather_cache_int4(const uint8_t* k_cache, const uint8_t* v_cache, const 
   p.key_out = reinterpret_cast<__half*>(key);
   p.value_out = reinterpret_cast<__half*>(value);
   p.num_heads = num_kv_heads;
-  return launch_rows(fn, gather_cache_int4_kernel<64>, gather_cache_int4_kernel<128>, p, num_tokens, head_dim, block_size,
+  return launch_rows(fn, gather_cache_int4_kernel<64>, gather_cache_int4_kernel<128>, 16, p, num_tokens, head_dim, block_size,
                      num_blocks, stream);
 }
 
