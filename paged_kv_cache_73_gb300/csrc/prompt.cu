@@ -24,6 +24,8 @@
 //    that see them.
 //  * The grid is a flat list of query tiles (a tile's sequence is found by a prefix sum over
 //    query_start), so a batch of ragged prompts launches few CTAs that have nothing to do.
+//    Head after head, so that a head's K/V stay in L2; only the last heads' tiles go from long
+//    to short, so that the CTAs end together.
 //  * A CTA that runs takes over tiles of CTAs not launched yet (clusterlaunchcontrol), and its
 //    roles pass from one tile to the next on their own: the next tile's K and V are loaded
 //    and its first scores computed while the softmax warps write the last tile's output.
@@ -36,6 +38,7 @@
 // (an SS product of 128 x 64 x 16 reads 6 KB), PV by math; both with the loads come to 750
 // clocks of shared-memory traffic, and 685 a tile are measured on long prompts.  Two S buffers
 // keep S(j + 1) running under the softmax of tile j (about 1000 clocks).
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -53,6 +56,10 @@ __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_
 
 constexpr int BM = 128;            // queries per query tile (MMA M)
 constexpr int BN = 64;             // keys per tile (S MMA N, PV MMA K)
+// The last kLate items (as many as CTAs run at once) come by length, in kParts steps from long to short: 69.5
+// -> 67 us for chunks over cached contexts (17 to 24 key tiles an item), 1072 -> 1062 for long prompts; 912 and
+// 1824 items, or 4 steps, do no better.
+constexpr int kLate = 304, kParts = 8;
 constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
 
 struct PromptParams {
@@ -65,6 +72,7 @@ struct PromptParams {
   int64_t k_stride, v_stride;
   int num_seqs, num_heads, group;
   int max_tiles;                        // query tiles per sequence that max_query_len covers
+  int late;                             // heads whose query tiles come last and by length
   int total_q, total_k;
   int out_sectors;                      // out is 32-byte aligned
   float scale_log2;
@@ -250,50 +258,71 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
 
   if (warp == W_LOAD) {
     // ---------------- items and loads ----------------
-    // 32 sequences at a time, one a lane: where they start, their lengths and query tiles, and the tiles
-    // of all before (a prefix sum).  A sequence with a bad range takes one place, to be reported.
-    int q0 = 0, n = 0, k0 = 0, m = 0, upto = 0;               // upto: inclusive, from the batch's first
-    bool range_ok = true;
-    int batch = -32, before = 0, batch_tiles = 0;             // the batch's first sequence, the tiles before it
-    auto read_batch = [&](int first) {
-      before = first == 0 ? 0 : before + batch_tiles;
-      batch = first;
-      const int i = first + lane;
-      int tiles = 0;
-      if (i < p.num_seqs) {
-        q0 = p.qstart[i];
-        n = p.qstart[i + 1] - q0;
-        k0 = p.kstart[i];
-        m = p.kstart[i + 1] - k0;
-        range_ok = n >= 0 && n <= m && q0 >= 0 && q0 <= p.total_q - n && k0 >= 0 && k0 <= p.total_k - m;
-        tiles = range_ok ? min((n + BM - 1) / BM, p.max_tiles) : 1;
+    // 32 sequences at a time, one a lane: where they start, their lengths, their query tiles and the key
+    // tiles that the last of those visits.  A sequence with a bad range has none; some CTA gets to each
+    // batch and reports it.
+    // A batch's items come in parts: part 0 has all query tiles of the first heads; each further part those
+    // of the last p.late heads that visit more than `few` key tiles and are in no part before.
+    int q0 = 0, n = 0, k0 = 0, m = 0, tiles = 0, own = 0;
+    int batch = 0, part = -1, most = 0;                       // most: the largest `own`
+    int upto = 0, per_head = 0, end = 0, begin = 0;           // a head's items up to the lane's, all; the lane's tiles
+    int64_t part_base = 0;                                    // the part's first item
+    // Item x.  Batch and part are kept: a CTA's items mostly rise.
+    auto find_item = [&](int x, Item& item) {
+      if (x < part_base) {
+        batch = part_base = 0;
+        part = -1;
       }
-      upto = tiles;
+      while (true) {
+        const int heads = part <= 0 ? p.num_heads - p.late : p.late;
+        if (part >= 0) {
+          const int64_t size = static_cast<int64_t>(per_head) * heads;
+          if (x - part_base < size) break;
+          part_base += size;
+          if (part == kParts) {
+            batch += 32;
+            if (batch >= p.num_seqs) return false;
+            part = -1;
+          }
+        }
+        if (++part == 0) {
+          const int i = batch + lane;
+          tiles = own = 0;
+          if (i < p.num_seqs) {
+            q0 = p.qstart[i];
+            n = p.qstart[i + 1] - q0;
+            k0 = p.kstart[i];
+            m = p.kstart[i + 1] - k0;
+            const bool ok = n >= 0 && n <= m && q0 >= 0 && q0 <= p.total_q - n && k0 >= 0 && k0 <= p.total_k - m;
+            if (!ok || n > p.max_tiles * static_cast<int64_t>(BM)) record_error(PKV_DEV_BAD_QUERY_RANGE);
+            tiles = ok ? min((n + BM - 1) / BM, p.max_tiles) : 0;
+            if (tiles > 0) own = (m - n + min(n, tiles * BM) - 1) / BN + 1;
+          }
+          most = __reduce_max_sync(0xffffffffu, own);
+          begin = 0;
+          end = tiles;
+        } else {
+          // begin: the lane's first query tile that visits more than `few` key tiles
+          const int few = most - part * ((most + kParts - 1) / kParts);
+          const int rows = few * BN + 1 - (m - n);            // so many queries of the sequence see at most that
+          end = part == 1 ? tiles : begin;
+          begin = part == kParts || rows <= 0 ? 0 : few >= own ? tiles : min(tiles, (rows - 1) / BM);
+        }
+        upto = end - begin;
 #pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
+        for (int o = 1; o < 32; o *= 2) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        per_head = __shfl_sync(0xffffffffu, upto, 31);
       }
-      batch_tiles = __shfl_sync(0xffffffffu, upto, 31);
-    };
-    // The query tile of flat index x, the tiles of a sequence from its last, which sees the most keys.  The
-    // batch is kept: a CTA's indices mostly rise.
-    auto find_item = [&](int x, int h, Item& item) {
-      if (batch < 0 || x < before) read_batch(0);
-      while (x >= before + batch_tiles) {
-        if (batch + 32 >= p.num_seqs) return false;
-        read_batch(batch + 32);
-      }
-      const int hit = __ffs(__ballot_sync(0xffffffffu, before + upto > x)) - 1;
-      const int qt = __shfl_sync(0xffffffffu, before + upto, hit) - 1 - x;
+      const unsigned in_part = static_cast<unsigned>(x - part_base), h = in_part / static_cast<unsigned>(per_head);
+      const int w = static_cast<int>(in_part - h * per_head);
+      const int hit = __ffs(__ballot_sync(0xffffffffu, upto > w)) - 1;
+      // a sequence's tiles from the last, which visits the most key tiles
+      const int qt = __shfl_sync(0xffffffffu, begin + upto, hit) - 1 - w;
       const int s_n = __shfl_sync(0xffffffffu, n, hit), s_m = __shfl_sync(0xffffffffu, m, hit);
       const int s_q0 = __shfl_sync(0xffffffffu, q0, hit), s_k0 = __shfl_sync(0xffffffffu, k0, hit);
-      if (!__shfl_sync(0xffffffffu, static_cast<int>(range_ok), hit)) {
-        if (lane == 0) record_error(PKV_DEV_BAD_QUERY_RANGE);
-        return false;
-      }
-      // more queries than max_query_len covers
-      if (lane == 0 && qt == 0 && (s_n - 1) / BM >= p.max_tiles) record_error(PKV_DEV_BAD_QUERY_RANGE);
       const int i0 = qt * BM;
       item.q_row = s_q0 + i0;
       item.rows = min(s_n - i0, BM);
@@ -303,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
       item.n_tiles = (item.first_pos + item.rows - 1) / BN + 1;
       // tiles from here on hold keys that some row does not see, or the sequence's end
       item.edge = min((item.first_pos + 1) / BN, s_m / BN);
-      item.head = h;
+      item.head = static_cast<int>(h) + (part == 0 ? 0 : p.num_heads - p.late);
       return true;
     };
     auto ask = [&]() {
@@ -314,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
     int k_issued = 0, v_issued_n = 0, q_issued = 0;
     while (true) {
       Item item;
-      const bool real = find_item(x, y, item);
+      const bool real = find_item(y * static_cast<int>(gridDim.x) + x, item);
       if (lane == 0) {
         if (real) {
           const int slot = it & 1;
@@ -724,8 +753,12 @@ int launch(PromptParams p, int max_query_len, cudaStream_t st) {
   // the tiles of num_seqs sequences that have total_q queries together, at most
   const long long by_total = static_cast<long long>(p.total_q) / BM + p.num_seqs;
   const long long by_longest = static_cast<long long>(p.max_tiles) * p.num_seqs;
-  const dim3 grid(static_cast<unsigned>(by_total < by_longest ? by_total : by_longest),
-                  p.num_heads);
+  const long long per_head = by_total < by_longest ? by_total : by_longest;
+  const long long late = kLate / per_head + 1;
+  p.late = static_cast<int>(late < p.num_heads ? late : p.num_heads);
+  if (per_head * p.num_heads > INT_MAX)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "pkv_prompt_attention: more than 2^31 - 1 query tiles over all heads");
+  const dim3 grid(static_cast<unsigned>(per_head), p.num_heads);
   e = pkv::launch_pdl(prompt_attention_kernel<D>, grid, dim3(THREADS), C::SMEM, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention launch: %s", cudaGetErrorString(e));
