@@ -497,6 +497,18 @@ def _rows(t: torch.Tensor, name: str, device: int) -> Tuple[int, int, int, int]:
                    f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} device={t.device}")
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """Memory for a call on `stream` (None: the current one).  It belongs to that stream, so neither work that
+    the current stream has yet to do with the memory's last owner, nor its next owner, meets the call's."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def rope_frequencies(inv_freq: Sequence[float], device="cuda") -> torch.Tensor:
     """The int64 ``frequencies`` of qk_norm_rope from angular frequencies in radians per position
     (``base ** (-2 i / rotary_dim)``, or any scaled variant), one per rotated pair."""
@@ -546,13 +558,13 @@ def qk_norm_rope(q: torch.Tensor, key: torch.Tensor, positions: torch.Tensor, fr
                 raise PkvError(PKV_ERR_INVALID_ARG, f"qk_norm_rope: {name} must have head_dim entries")
     qos, kos = H * D, Hk * D
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=torch.float16, device=q.device)
+        q_out = _empty((T, H, D), torch.float16, q.device, stream)
     else:
         *shape, qos = _rows(q_out, "q_out", dev)
         if shape != [T, H, D]:
             raise PkvError(PKV_ERR_INVALID_ARG, "qk_norm_rope: q_out must be shaped like q")
     if k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=torch.float16, device=q.device)
+        k_out = _empty((T, Hk, D), torch.float16, q.device, stream)
     else:
         *shape, kos = _rows(k_out, "k_out", dev)
         if shape != [T, Hk, D]:
@@ -616,7 +628,7 @@ def gather_cache_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping
     outs = []
     for t, name in ((key, "key"), (value, "value")):
         if t is None:
-            t = torch.empty(shape, dtype=torch.float16, device=k_cache.device)
+            t = _empty(shape, torch.float16, k_cache.device, stream)
         else:
             _need(t, name, torch.float16, 3)
             if tuple(t.shape) != shape:
@@ -701,14 +713,16 @@ def paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     if rows != S or context_lens.shape[0] != S:
         raise PkvError(PKV_ERR_INVALID_ARG, "block_tables / context_lens rows != num_seqs")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     else:
         _need(out, "out", torch.float16, 3)
         if out.shape != q.shape:
             raise PkvError(PKV_ERR_INVALID_ARG, "paged_attention_decode_int4: out must be shaped like q")
     if workspace is None:
         n = _int4_workspace_size(dev, S, H, Hk, D, max_blocks, block_size)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        workspace = _empty((n,), torch.uint8, q.device, stream) if n else None
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _need(workspace, "workspace", workspace.dtype, workspace.dim())
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load().pkv_paged_attention_decode_int4(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
@@ -743,7 +757,7 @@ def prompt_attention(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, qu
         if key_start.shape[0] != S + 1:
             raise PkvError(PKV_ERR_INVALID_ARG, "prompt_attention: query_start and key_start differ in length")
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.float16, device=q.device)
+        out = _empty((T, H, D), torch.float16, q.device, stream)
     else:
         _need(out, "out", torch.float16, 3)
         if out.shape != q.shape:
