@@ -449,7 +449,8 @@ int pkv_rope_frequencies(const double* inv_freq, int n, int64_t* frequencies_out
  * [num_tokens, num_kv_heads, head_dim] fp16, 16-byte aligned, a token's heads
  * contiguous, tokens key_stride / value_stride elements apart (multiples of 8, at
  * least a token's length).  Negative slots are skipped; a slot outside the pool
- * records PKV_DEV_BAD_SLOT and is not written. */
+ * records PKV_DEV_BAD_SLOT and is not written.  No two tokens may have the same
+ * slot: its row could mix theirs. */
 int pkv_reshape_and_cache_int4(const uint16_t* key, const uint16_t* value, uint8_t* k_cache, uint8_t* v_cache,
                                const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
                                int block_size, int num_blocks, int64_t key_stride, int64_t value_stride,
@@ -481,11 +482,12 @@ int pkv_swap_blocks_int4(const uint8_t* const* src_k_caches, const uint8_t* cons
  * for.  num_heads is a multiple of num_kv_heads.  q (device [num_seqs, num_heads,
  * head_dim] fp16), tables, lengths, out, errors and the meaning of a zero length
  * are as for pkv_paged_attention_decode, except that q, tables, lengths and out
- * must be device memory, and that the workspace is always needed (at least
- * pkv_paged_attention_int4_workspace_size(...) bytes on the current device).  Products of q and the cached whole
- * numbers are exact, sums are fp32; the softmax weights, times the rows' V scales,
- * are rounded to fp16 before they multiply V (with one query head to a K/V head
- * what the rounding leaves multiplies V too).
+ * must be device memory, and that the workspace is always needed: at least
+ * pkv_paged_attention_int4_workspace_size(...) bytes, asked for with the device
+ * current.  Calls that may run at the same time need workspaces of their own.
+ * Products of q and the cached whole numbers are exact, sums are fp32; the softmax
+ * weights, times the rows' V scales, are rounded to fp16 before they multiply V
+ * (with one query head to a K/V head what the rounding leaves multiplies V too).
  * ------------------------------------------------------------------------- */
 size_t pkv_paged_attention_int4_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                                int max_blocks_per_seq, int block_size);
@@ -520,7 +522,8 @@ int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, c
  *                 written.
  *   out           device [total_q, num_heads, head_dim] fp16, contiguous, 16-byte
  *                 aligned; must not overlap the inputs
- * scale must be positive.  A sequence without queries is skipped; n_s > m_s or
+ * scale must be positive; at most 2^26 queries and 2^26 keys.  A sequence without
+ * queries is skipped; n_s > m_s or
  * rows outside q or key record PKV_DEV_BAD_QUERY_RANGE and the sequence's rows are
  * not written.  Rows of out in no sequence are left as they were.  Keys and values
  * that a query does not see (after it, or after its sequence's end) do not reach its

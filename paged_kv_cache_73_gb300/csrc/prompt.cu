@@ -139,14 +139,15 @@ __device__ __forceinline__ bool cancelled(uint32_t answer, int& x, int& y) {
   return ok != 0;
 }
 
-// A wait for the phase of `parity`, false once another role has raised the abort flag or after 2^26
-// tries (a second or so).  Small, because it is in a dozen places of roles that share the instruction
-// cache; the flag is looked at only now and then, for a shared-memory read in a thread that issues
-// products stalls it until they are done.
+// A wait for the phase of `parity`, false once another role has raised the abort flag or after 2^19
+// tries (2 s: a failed try takes 3.9 us).  Some role may wait for the whole of another's item, which
+// 2^26 keys, the most that a call takes, keep under 0.8 s.  Small, because it is in a dozen places of
+// roles that share the instruction cache; the flag is looked at only now and then, for a shared-memory
+// read in a thread that issues products stalls it until they are done.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
 #pragma unroll 1
   for (uint32_t i = 1; !mbar_try_wait_parity(bar, parity); ++i)
-    if ((i & 1023u) == 0 && (*abort_flag != 0 || i >= (1u << 26))) return false;
+    if ((i & 1023u) == 0 && (*abort_flag != 0 || i >= (1u << 19))) return false;
   return true;
 }
 
@@ -735,7 +736,7 @@ int encode_rows_map(CUtensorMap* map, const void* x, int D, int H, int T, int64_
 }
 
 template <int D>
-int launch(PromptParams p, int max_query_len, cudaStream_t st) {
+int launch(const PromptParams& p, long long tiles, cudaStream_t st) {
   using C = Cfg<D>;
   static std::mutex mu;
   static bool done[64] = {false};
@@ -749,16 +750,7 @@ int launch(PromptParams p, int max_query_len, cudaStream_t st) {
     }
   }
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention setup: %s", cudaGetErrorString(e));
-  p.max_tiles = (max_query_len - 1) / BM + 1;
-  // the tiles of num_seqs sequences that have total_q queries together, at most
-  const long long by_total = static_cast<long long>(p.total_q) / BM + p.num_seqs;
-  const long long by_longest = static_cast<long long>(p.max_tiles) * p.num_seqs;
-  const long long per_head = by_total < by_longest ? by_total : by_longest;
-  const long long late = kLate / per_head + 1;
-  p.late = static_cast<int>(late < p.num_heads ? late : p.num_heads);
-  if (per_head * p.num_heads > INT_MAX)
-    return pkv::fail(PKV_ERR_UNSUPPORTED, "pkv_prompt_attention: more than 2^31 - 1 query tiles over all heads");
-  const dim3 grid(static_cast<unsigned>(per_head), p.num_heads);
+  const dim3 grid(static_cast<unsigned>(tiles), p.num_heads);
   e = pkv::launch_pdl(prompt_attention_kernel<D>, grid, dim3(THREADS), C::SMEM, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention launch: %s", cudaGetErrorString(e));
@@ -803,8 +795,8 @@ int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t*
   }
   if (num_seqs > 65535 || num_heads > 65535)
     return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: num_seqs/num_heads above 65535", fn);
-  if (total_q > (1 << 30) || total_k > (1 << 30) || max_query_len > (1 << 30))
-    return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: more than 2^30 tokens", fn);
+  if (total_q > (1 << 26) || total_k > (1 << 26))
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: more than 2^26 tokens", fn);
   if (total_k == 0) return pkv::fail(PKV_ERR_INVALID_ARG, "%s: queries but no keys", fn);
   if (!q || !key || !value || !query_start || !out) return pkv::fail(PKV_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (!aligned16(q) || !aligned16(key) || !aligned16(value) || !aligned16(out))
@@ -815,6 +807,13 @@ int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t*
   if (!std::isfinite(scale) || !(scale > 0.f))
     return pkv::fail(PKV_ERR_INVALID_ARG, "%s: scale must be finite and positive", fn);
   PromptParams p{};
+  p.max_tiles = (max_query_len - 1) / BM + 1;
+  // the query tiles of num_seqs sequences that have total_q queries together, at most
+  const long long by_total = total_q / BM + num_seqs, by_longest = static_cast<long long>(p.max_tiles) * num_seqs;
+  const long long tiles = by_total < by_longest ? by_total : by_longest, late = kLate / tiles + 1;
+  if (tiles * num_heads > INT_MAX)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 query tiles over all heads", fn);
+  p.late = static_cast<int>(late < num_heads ? late : num_heads);
   int rc = encode_rows_map(&p.tmap_q, q, head_dim, num_heads, total_q, q_stride, BM);
   if (rc == PKV_OK) rc = encode_rows_map(&p.tmap_k, key, head_dim, num_kv_heads, total_k, key_stride, BN);
   if (rc == PKV_OK) rc = encode_rows_map(&p.tmap_v, value, head_dim, num_kv_heads, total_k, value_stride, BN);
@@ -834,7 +833,7 @@ int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t*
   p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  rc = head_dim == 128 ? launch<128>(p, max_query_len, st) : launch<64>(p, max_query_len, st);
+  rc = head_dim == 128 ? launch<128>(p, tiles, st) : launch<64>(p, tiles, st);
   if (rc == PKV_OK) pkv::clear_error();
   return rc;
 }

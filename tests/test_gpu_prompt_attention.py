@@ -195,3 +195,51 @@ def test_shapes_refused(cuda_device):
                 dict(query_start=qs.long()), dict(q=q[:, :3]), dict(scale=-1.0)):
         with pytest.raises(pkv.PkvError):
             pkv.prompt_attention(**{**dict(q=q, key=k, value=v, query_start=qs, scale=0.1, max_query_len=10), **bad})
+
+
+def test_more_sequences_than_a_warp_holds(cuda_device):
+    # 70 sequences, some empty, in three batches of lanes; few and many heads
+    rng = np.random.default_rng(20)
+    news = [int(x) for x in rng.choice([0, 1, 5, 64, 130, 200], 70)]
+    past = [int(x) for x in rng.choice([0, 3, 64, 150], 70)]
+    check(make(21, news, past, 2, 1, 64), cuda_device)
+    check(make(22, [0] * 40 + [150] * 3, 0, 24, 24, 128), cuda_device)
+
+
+def test_a_bad_range_in_a_later_batch_is_recorded(cuda_device):
+    # sequences 40, 42 and 44 go back to row 0 and the ones between overlap: more tiles than the grid has
+    starts = list(range(0, 41 * 30, 30)) + [0, 1200, 0, 1200, 0, 1200]
+    q, k, v = (torch.randn(1230, 2, 64, device=cuda_device).half() for _ in range(3))
+    pkv.prompt_attention(q, k, v, torch.tensor(starts, dtype=torch.int32, device=cuda_device), 0.1, 1200)
+    assert pkv.device_error() == 6
+
+
+def test_long_wait_for_a_long_context(cuda_device):
+    # one query over 2^24 keys, about 0.2 s in which some roles wait for others.  With q = 0 each weight is
+    # 1; whole values in [-1, 1] keep every partial sum below 2^24, exact in fp32: only the division and the
+    # fp16 rounding remain
+    m = 1 << 24
+    v = (torch.arange(m, device=cuda_device, dtype=torch.int32)[:, None, None] * torch.arange(1, 65, device=cuda_device,
+                                                                                             dtype=torch.int32))
+    v = (v % 3 - (torch.arange(64, device=cuda_device) % 2)).half()
+    k = torch.zeros_like(v)
+    q = torch.zeros(1, 1, 64, dtype=torch.float16, device=cuda_device)
+    start = lambda n: torch.tensor([0, n], dtype=torch.int32, device=cuda_device)
+    v.clamp_(-1, 1)
+    got = pkv.prompt_attention(q, k, v, start(1), 1.0, 1, key_start=start(m))
+    assert pkv.device_error() == 0
+    want = v.sum(0, dtype=torch.float64) / m
+    assert ((got[0].double() - want).abs() <= want.abs() * (2.0 ** -11 + 2.0 ** -22) + 2.0 ** -25).all()
+
+
+def test_rows_past_2_31_elements(cuda_device):
+    # the last sequence's rows lie past element 2^31 of q, key, value and out
+    T, H, D, n = 360000, 48, 128, 200
+    big = torch.empty(T, H, D, dtype=torch.float16, device=cuda_device)
+    big[T - n:] = torch.randn(n, H, D, device=cuda_device)
+    out = torch.empty_like(big)
+    start = torch.tensor([T - n, T], dtype=torch.int32, device=cuda_device)
+    pkv.prompt_attention(big, big[:, :24], big[:, 24:], start, 0.1, n, out=out)
+    small = big[T - n:].clone()
+    want = pkv.prompt_attention(small, small[:, :24], small[:, 24:], start - (T - n), 0.1, n)
+    assert pkv.device_error() == 0 and torch.equal(out[T - n:], want)

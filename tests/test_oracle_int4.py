@@ -235,3 +235,12 @@ def test_prompt_attention_refuses(lib, kw, status):
     assert _prompt(lib, **kw) == status
     if status != pkv.PKV_OK:
         assert lib.pkv_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=(1 << 26) + 1),
+    dict(Tk=(1 << 26) + 1),
+    dict(T=1 << 26, Tk=1 << 26, maxq=1 << 26, H=65535, Hk=1, sq=65535 * 64, sk=64, sv=64),     # query tiles of all heads
+])
+def test_prompt_attention_refuses_what_is_too_large(lib, kw):
+    assert _prompt(lib, **kw) == pkv.PKV_ERR_UNSUPPORTED and b"more than" in lib.pkv_last_error()
