@@ -225,3 +225,23 @@ def test_a_pool_past_4_gib(cuda_device):
     assert pkv.device_error() == 0
     want = o4.paged_decode_attention(*case, 0.1, 32)
     assert (np.abs(got.cpu().numpy() - want) <= tolerance(case, want, 0.1, 32)).all()
+
+
+@pytest.mark.parametrize("H,Hk", [(3, 3), (4, 1)])
+def test_many_sequences(cuda_device, H, Hk):
+    # more sequences than the joining kernel's threads, a third of them empty
+    rng = np.random.default_rng(31)
+    lens = [int(x) for x in rng.choice([0, 1, 40, 300], 300)]
+    check(make(31, lens, H, Hk, 64, 16, cuda_device), 16, cuda_device)
+
+
+def test_two_streams_at_once(cuda_device):
+    cases = [make(32 + i, [900, 33, 1500, 5], 8, 8 >> (2 * i), 128, 16, cuda_device) for i in range(2)]
+    dev = [[torch.from_numpy(x).to(cuda_device) for x in c] for c in cases]
+    alone = [pkv.paged_attention_decode_int4(*d, 0.1, 16) for d in dev]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in dev]
+    got = [[pkv.paged_attention_decode_int4(*d, 0.1, 16, stream=st) for d, st in zip(dev, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    assert pkv.device_error() == 0
+    assert all(torch.equal(g, a) for pair in got for g, a in zip(pair, alone))

@@ -122,3 +122,33 @@ def test_copy_and_swap_blocks(cuda_device, D, B, H):
         assert torch.equal(p, w)
     pkv.copy_blocks_int4(pools[:1], pools[1:2], torch.tensor([[0, 9]], device=cuda_device), B)
     assert pkv.device_error() == 4
+
+
+def test_rows_and_pools_past_32_bits(cuda_device):
+    # rows past element 2^31 of key, value and the outputs; slots in the last blocks of a pool past 4 GiB
+    T, H, D, B, n = 700000, 24, 128, 32, 150
+    N = (5 << 30) // (H * B * (D // 2 + 4))
+    kv = torch.empty(T, 2 * H, D, dtype=torch.float16, device=cuda_device)
+    kv[T - n:] = torch.randn(n, 2 * H, D, device=cuda_device)
+    pools = [torch.zeros(pkv.int4_cache_shape(N, H, B, D), dtype=torch.uint8, device=cuda_device) for _ in range(2)]
+    slots = torch.full((T,), -1, dtype=torch.int64, device=cuda_device)
+    slots[T - n:] = N * B - 1 - torch.arange(n, device=cuda_device)
+    pkv.reshape_and_cache_int4(kv[:, :H], kv[:, H:], *pools, slots, B)
+    outs = pkv.gather_cache_int4(*pools, slots, B)
+    assert outs[0].numel() > 1 << 31
+    small = [torch.zeros(pkv.int4_cache_shape(8, H, B, D), dtype=torch.uint8, device=cuda_device) for _ in range(2)]
+    low, x = slots[T - n:] - (N - 8) * B, kv[T - n:].clone()
+    pkv.reshape_and_cache_int4(x[:, :H], x[:, H:], *small, low, B)
+    assert pkv.device_error() == 0
+    assert all(torch.equal(p[N - 8:], s) and not p[:N - 8].any() for p, s in zip(pools, small))
+    assert all(torch.equal(o[T - n:], s) for o, s in zip(outs, pkv.gather_cache_int4(*small, low, B)))
+
+
+def test_a_slot_read_many_times(cuda_device):
+    x = torch.randn(8, 2, 64, device=cuda_device).half()
+    pools = [torch.zeros(pkv.int4_cache_shape(2, 2, 4, 64), dtype=torch.uint8, device=cuda_device) for _ in range(2)]
+    pkv.reshape_and_cache_int4(x, x, *pools, torch.arange(8, device=cuda_device), 4)
+    one = pkv.gather_cache_int4(*pools, torch.arange(8, device=cuda_device), 4)
+    sl = torch.tensor([5, 5, 0, 5, 7, 0, 5], device=cuda_device)
+    for got, o in zip(pkv.gather_cache_int4(*pools, sl, 4), one):
+        assert torch.equal(got, o[sl])

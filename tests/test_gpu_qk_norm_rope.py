@@ -122,3 +122,16 @@ def test_binding_refuses(cuda_device, change):
               "weight": dict(q_weight=w[0][:32].contiguous()), "axis": dict(pair_axis=torch.zeros(5, dtype=torch.int32, device=cuda_device))}[change])
     with pytest.raises(pkv.PkvError):
         pkv.qk_norm_rope(**a)
+
+
+def test_rows_past_2_31_elements(cuda_device):
+    T, H, D, n = 360000, 48, 128, 50
+    big = torch.zeros(T, H, D, dtype=torch.float16, device=cuda_device)
+    big[T - n:] = torch.randn(n, H, D, device=cuda_device)
+    pos = torch.arange(T, dtype=torch.int32, device=cuda_device)
+    f = pkv.rope_frequencies([10000.0 ** (-i / 64) for i in range(64)], cuda_device)
+    small = big[T - n:].clone()
+    want = pkv.qk_norm_rope(small[:, :40], small[:, 40:], pos[T - n:].clone(), f)
+    pkv.qk_norm_rope(big[:, :40], big[:, 40:], pos, f, q_out=big[:, :40], k_out=big[:, 40:])
+    assert pkv.device_error() == 0
+    assert torch.equal(big[T - n:, :40], want[0]) and torch.equal(big[T - n:, 40:], want[1])
