@@ -245,3 +245,33 @@ def test_two_streams_at_once(cuda_device):
     torch.cuda.synchronize()
     assert pkv.device_error() == 0
     assert all(torch.equal(g, a) for pair in got for g, a in zip(pair, alone))
+
+
+@pytest.mark.parametrize("H,Hk", [(8, 1), (2, 2)])
+def test_error_does_not_grow_with_the_context(cuda_device, H, Hk):
+    # A rounding's error is uniform within half a step, 2^-11 of the value at most: 2^-11 / sqrt(3) of it in
+    # the 2-norm.  The output has one; each weight has one of its own (with a lone head 2^-11 less), which
+    # meets s (n - 8) of its row: the 2-norm of p s (n - 8) over the tokens against the output's.  A fifth
+    # more for the spread of 512 or 128 values' norms, 2^-16 for fp32.
+    case = make(33, [40000], H, Hk, 64, 16, cuda_device)
+    q, kc, vc, tables, lens = case
+    want = o4.paged_decode_attention(*case, 0.125, 16)
+    got = run(case, 0.125, 16, cuda_device).cpu().numpy().astype(np.float64)
+    assert pkv.device_error() == 0
+    t = np.arange(40000)
+    blk, row = tables[0][t // 16], t % 16
+    k, v = (o4.pool_values(x, 16)[blk, :, row] for x in (kc, vc))
+    meta = np.ascontiguousarray(vc[:, :, 16 * 32:]).view(np.float16).reshape(vc.shape[0], Hk, 16, 2)[blk, :, row]
+    sc, zero = meta[..., 0].astype(np.float64), meta[..., 1].astype(np.float64)
+    part = 0.0
+    for h in range(H):
+        g = h * Hk // H
+        x = 0.125 * k[:, g] @ q[0, h].astype(np.float64)
+        p = np.exp(x - x.max())
+        p /= p.sum()
+        part += ((p[:, None] * (v[:, g] - zero[:, g, None] - 8 * sc[:, g, None])) ** 2).sum()
+    part /= (want ** 2).sum()
+    rounding = 2.0 ** -11 / 3 ** 0.5
+    limit = 1.2 * rounding * (1 + (part if H > Hk else 0)) ** 0.5 + 2.0 ** -16
+    off = np.linalg.norm(got - want) / np.linalg.norm(want)
+    assert off <= limit, (off, limit)
