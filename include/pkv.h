@@ -529,7 +529,9 @@ int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, c
  * that a query does not see (after it, or after its sequence's end) do not reach its
  * row, whatever they hold.
  * Tensor cores: fp16 products, fp32 sums; the softmax weights are rounded to fp16
- * before they multiply V.  No workspace.
+ * before they multiply V.  The tensor cores cut their sums off at the last bit: a
+ * row over n keys loses up to n 2^-27 of itself to that, as much as the output's
+ * own rounding from 2^16 keys on.  No workspace.
  * ------------------------------------------------------------------------- */
 int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t* value, const int32_t* query_start,
                          const int32_t* key_start, int num_seqs, int total_q, int total_k, int max_query_len,

@@ -6,7 +6,8 @@
 //
 // Both kernels are HBM-bound.  A warp takes a token's rows (or a part of them, where there
 // are few tokens), so that every access of a row is contiguous over its lanes in whole
-// sectors.  The read-back has 16 values to a lane in two 16-byte chunks half a row apart.
+// sectors.  The read-back has 16 values to a lane in two 16-byte chunks half a row apart, and
+// runs at 98 % of the copy rate (160k tokens of 8 + 8 rows of 128: 124 us).
 //
 // The write has about 9 values to handle per clock and SM at HBM rate, so it counts
 // instructions: 32 values to a lane, which halves what a row costs beside its values (150 ->
