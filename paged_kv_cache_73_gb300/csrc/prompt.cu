@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
   if (tid == 32) {
     for (int u = 0; u < 2; ++u) {
       mbar_init_count(s_full(u), 1);
-      mbar_init_count(p_full(u), 128);
+      mbar_init_count(p_full(u), 4);
       mbar_init_count(pv_done(u), 1);
       mbar_init_count(item_full(u), 1);
       mbar_init_count(item_free(u), 7);                       // 4 softmax warps, both issuers, the checker
@@ -243,6 +243,15 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
   auto give_up = [&]() {
     if (!*abort_flag) record_error(PKV_DEV_WAIT_TIMEOUT);
     *abort_flag = 1;
+  };
+  // The same for a softmax warp: its lanes leave the loop together (with one arrival a warp on p_full, 66.9 ->
+  // 65.8 us for chunks at D = 64; one lane that waits for the others took 72, and in the loader's and the
+  // checker's waits the larger code costs more than it saves).
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t i = 1; !__all_sync(0xffffffffu, mbar_try_wait_parity(bar, parity)); ++i)
+      if ((i & 1023u) == 0 && (__any_sync(0xffffffffu, *abort_flag != 0) || i >= (1u << 19))) return false;
+    return true;
   };
   // the next item, once it is there; n_tiles 0 ends the loop
   auto take_item = [&](int it, Item& item) {
@@ -596,7 +605,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
       for (int i = 0; i < item.n_tiles; ++i, ++j) {
         const int u = j & 1;
         const uint32_t ts = t_s(u);
-        if (!__all_sync(0xffffffffu, wait(s_full(u), (j >> 1) & 1))) {
+        if (!warp_wait(s_full(u), (j >> 1) & 1)) {
           failed = true;
           break;
         }
@@ -629,7 +638,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
         }
         const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
         if (__any_sync(0xffffffffu, rescale && i > 0)) {
-          if (!__all_sync(0xffffffffu, wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1))) {
+          if (!warp_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1)) {
             failed = true;
             break;
           }
@@ -661,9 +670,10 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
         l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(p_full(u));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(u));
       }
-      if (!failed) failed = !__all_sync(0xffffffffu, wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1));
+      if (!failed) failed = !warp_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1);
       if (failed) break;
       tc_fence_after();
       // the output, 32 columns at a time: each thread normalises and stores its own row, whole 32-byte
