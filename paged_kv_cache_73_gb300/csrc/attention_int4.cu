@@ -122,6 +122,13 @@ __device__ __forceinline__ unsigned transpose8x8(unsigned x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+// four 8x8 matrices of 16-bit elements, transposed: lane (g, t) gets rows 2t, 2t + 1 of column g of each
+__device__ __forceinline__ void load_transposed(unsigned (&w)[4], uint32_t row) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(row)
+               : "memory");
+}
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -172,12 +179,12 @@ struct Ring {
   static constexpr int WARP = NST * STAGE;          // a warp's ring
 };
 // Byte offset of 16-byte chunk c of V row r within a stage's V rows: in each 128-byte line (2 or 4
-// rows) the chunk's place is XOR-ed with twice the line's number mod 4, so the eight lanes that read
-// rows 2t or 2t + 1 of one chunk pair, t = 0..3, reach different banks.
+// rows) the chunk's place is XOR-ed with the line's number mod 4, so one chunk of eight rows lies in
+// different banks.
 template <int D>
 __device__ __forceinline__ int v_place(int r, int c) {
   const int lin = r * (D / 32) + c, line = lin >> 3;
-  return line * 128 + (((lin & 7) ^ ((line & 3) << 1)) << 4);
+  return line * 128 + (((lin & 7) ^ (line & 3)) << 4);
 }
 
 // A worker's running softmax over one stream's tokens for 8 NT heads; lane (g, t) holds heads 8 n + 2t,
@@ -196,10 +203,9 @@ struct WarpState {
 template <int D, int NT, bool SOLO>
 __device__ __forceinline__ void chunk_update(const unsigned char* stage, int valid, const unsigned (&qf)[NT][D / 16][2],
                                              const float (&ca)[NT][2], const float (&cb)[NT][2], WarpState<D, NT>& st,
-                                             int g, int t, const int (&v_off)[4]) {
+                                             int g, int t, uint32_t v_row) {
   using R = Ring<D>;
   constexpr int WK = D / 32;            // words of a K row per lane
-  constexpr int WV = D / 64;            // words of a V row per lane
   // the two tiles' products side by side: each is a chain of dependent accumulations
   unsigned kw[2][2][WK];
   float dot[2][NT][4];
@@ -371,20 +377,21 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    unsigned va[4][WV];                 // tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the tile
 #pragma unroll
-    for (int r = 0; r < 4; ++r) load_words<WV>(va[r], stage + R::V_OFF + v_off[r] + i * 16 * R::ROW);
+    for (int pair = 0; pair < D / 64; ++pair) {              // 16-byte chunks 2 pair, 2 pair + 1 of the rows
+      unsigned v[4];                                         // of each: tokens 2t, 2t + 1, then those + 8
+      load_transposed(v, v_row + i * 16 * R::ROW ^ pair * 32);
 #pragma unroll
-    for (int w = 0; w < WV; ++w)
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const unsigned sel = 0x4400u + 0x1111u * b;          // byte b of the first token, byte b of the second
-        const unsigned e = __byte_perm(va[0][w], va[1][w], sel), f = __byte_perm(va[2][w], va[3][w], sel);
+        for (int h = 0; h < 2; ++h) {
+          const unsigned e = v[2 * c] >> (8 * h), f = v[2 * c + 1] >> (8 * h);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          mma16816(st.acc[n][4 * w + b], e & 0x000f000fu, e & 0x00f000f0u, f & 0x000f000fu, f & 0x00f000f0u, pb[n][i][0],
-                   pb[n][i][1]);
-      }
+          for (int n = 0; n < NT; ++n)
+            mma16816(st.acc[n][4 * pair + 2 * c + h], e & 0x000f000fu, e & 0x00f000f0u, f & 0x000f000fu, f & 0x00f000f0u,
+                     pb[n][i][0], pb[n][i][1]);
+        }
+    }
     constexpr unsigned kOne2 = 0x3c003c00u;
 #pragma unroll
     for (int n = 0; n < NT; ++n) mma16816(st.ones[n], kOne2, kOne2, kOne2, kOne2, pb[n][i][0], pb[n][i][1]);
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
         for (int j = 0; j < 4; ++j) st.acc[n][i][j] = 0.f;
     }
   };
-  // the stream's result, or this worker's part of it: lane (g, t) holds values g D/8 .. of heads 2t, 2t + 1
+  // the stream's result, or this worker's part of it: lane (g, t) holds values 32 k + 4 g .. of heads 2t, 2t + 1
   auto end_stream = [&](bool whole) {
     const int in_group = at.y % p.head_tiles * HT, h0 = at.y / p.head_tiles * p.group + in_group;
     const int nh = min(HT, p.group - in_group), rows = min(HT, p.group);
@@ -630,7 +637,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
           }
         }
         const float mid = fmaf(-8.f, st.ones[n][j], st.c[n][j]);
-        float o[D / 8];                                      // word i / 4, byte i % 4: values 2 i and 2 i + 1
+        float o[D / 8];                                      // o[4 k ..]: values 32 k + 4 g ..
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           o[2 * i] = fmaf(st.acc[n][i][j], 16777216.f, mid);
@@ -638,30 +645,24 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
         }
         if (whole) {
           const float inv = 1.f / st.l[n][j];
-          __half* dst = p.out + (static_cast<size_t>(at.s) * H + h0 + h) * D + g * (D / 8);
-#pragma unroll
-          for (int i = 0; i < D / 8; i += 8)
-            *reinterpret_cast<uint4*>(dst + i) =
-                make_uint4(pack2(o[i] * inv, o[i + 1] * inv), pack2(o[i + 2] * inv, o[i + 3] * inv),
-                           pack2(o[i + 4] * inv, o[i + 5] * inv), pack2(o[i + 6] * inv, o[i + 7] * inv));
-        } else {
-          const size_t w = slot * rows + h;
-          float* dst = p.ws_o + w * D + g * (D / 8);
+          __half* dst = p.out + (static_cast<size_t>(at.s) * H + h0 + h) * D + g * 4;
 #pragma unroll
           for (int i = 0; i < D / 8; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            *reinterpret_cast<uint2*>(dst + 8 * i) = make_uint2(pack2(o[i] * inv, o[i + 1] * inv), pack2(o[i + 2] * inv, o[i + 3] * inv));
+        } else {
+          const size_t w = slot * rows + h;
+          float* dst = p.ws_o + w * D + g * 4;
+#pragma unroll
+          for (int i = 0; i < D / 8; i += 4)
+            *reinterpret_cast<float4*>(dst + 8 * i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           if (g == 0) *reinterpret_cast<float2*>(p.ws_ml + 2 * w) = make_float2(st.m[n][j], st.l[n][j]);
         }
       }
   };
 
-  int v_off[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    // lane g's D/16 bytes of V rows 2t, 2t + 1, 2t + 8, 2t + 9
-    const int x = g * (D / 16);
-    v_off[r] = v_place<D>(2 * t + (r & 1) + 8 * (r >> 1), x / 16) + x % 16;
-  }
+  // the V row and chunk whose address this lane gives: matrices are (first, second eight tokens) of a chunk,
+  // then of the next
+  const uint32_t v_row = ring_u32 + R::V_OFF + v_place<D>((lane & 8) + (lane & 7), lane >> 4);
   bool from_start = at.c == 0;
   begin_stream();
   int stage = 0;
@@ -671,7 +672,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
     fill(stage == 0 ? R::NST - 1 : stage - 1);
     const unsigned char* src = ring + stage * R::STAGE;
     const int valid = at.len - at.c * CHUNK;
-    chunk_update<D, NT, SOLO>(src, valid, qf, ca, cb, st, g, t, v_off);
+    chunk_update<D, NT, SOLO>(src, valid, qf, ca, cb, st, g, t, v_row + stage * R::STAGE);
     if (++stage == R::NST) stage = 0;
     const bool to_end = at.c + 1 == at.chunks;
     if (to_end || left == 1) {
