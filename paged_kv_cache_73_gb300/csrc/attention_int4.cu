@@ -368,10 +368,11 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
   for (int n = 0; n < NT; ++n) {
     const float2 even = make_float2(st.ones[n][0] * -0x1p-21f, st.ones[n][1] * -0x1p-21f);
     const float2 odd = make_float2(st.ones[n][0] * -0x1p-17f, st.ones[n][1] * -0x1p-17f);
+    const float2 both = make_float2(even.x + odd.x, even.y + odd.y);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       add2(st.acc[n][i][0], st.acc[n][i][1], even);
-      add2(st.acc[n][i][2], st.acc[n][i][3], odd);
+      add2(st.acc[n][i][2], st.acc[n][i][3], i & 1 ? both : odd);
     }
     st.ones[n][0] = st.ones[n][1] = st.ones[n][2] = st.ones[n][3] = 0.f;
   }
@@ -385,11 +386,13 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const unsigned e = v[2 * c] >> (8 * h), f = v[2 * c + 1] >> (8 * h);
+          // the low bytes' halves apart; of the high bytes the low half and the whole (which holds 17 n at most)
+          const unsigned e = h ? __byte_perm(v[2 * c], 0, 0x4341) : v[2 * c];
+          const unsigned f = h ? __byte_perm(v[2 * c + 1], 0, 0x4341) : v[2 * c + 1];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            mma16816(st.acc[n][4 * pair + 2 * c + h], e & 0x000f000fu, e & 0x00f000f0u, f & 0x000f000fu, f & 0x00f000f0u,
-                     pb[n][i][0], pb[n][i][1]);
+            mma16816(st.acc[n][4 * pair + 2 * c + h], e & 0x000f000fu, h ? e : e & 0x00f000f0u, f & 0x000f000fu,
+                     h ? f : f & 0x00f000f0u, pb[n][i][0], pb[n][i][1]);
         }
     }
     constexpr unsigned kOne2 = 0x3c003c00u;
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           o[2 * i] = fmaf(st.acc[n][i][j], 16777216.f, mid);
-          o[2 * i + 1] = fmaf(st.acc[n][i][2 + j], 1048576.f, mid);
+          o[2 * i + 1] = fmaf(st.acc[n][i][2 + j] - (i & 1 ? st.acc[n][i][j] : 0.f), 1048576.f, mid);
         }
         if (whole) {
           const float inv = 1.f / st.l[n][j];
