@@ -21,10 +21,12 @@
 //
 // Layout within a warp (lane = 4 g + t): for S^T, lane (g, t) holds D/4 values of token
 // rows g and g + 8; which of the row's values a lane takes is free as long as q is laid
-// out the same, so a lane reads D/8 contiguous bytes.  For O^T, it holds two pairs of
-// tokens (2t, 2t + 1 and those + 8) and D/8 values g D/8 .., of each; a byte permute
-// joins a byte of two tokens' words into two fp16 pairs.  P^T comes from S^T's
-// accumulator by an 8x8 transpose in registers (movmatrix).
+// out the same, so a lane reads D/8 contiguous bytes.  For O^T a transposing matrix load takes
+// V's rows as 16-bit elements: a lane gets tokens 2t, 2t + 1 of one element, that is of four
+// values, in the two halves of a register.  Of the low bytes both half bytes are masked out; of the
+// high bytes the low half is, and the whole byte enters as n + 16 n', whose n comes off in the
+// end (byte permutes of row words and four masks: 130 us for long grouped contexts, now 122).
+// P^T comes from S^T's accumulator by an 8x8 transpose in registers (movmatrix).
 //
 // Where each cached head has one query head, the products' other seven columns are idle, and
 // so would be most of the softmax: a warp then deals the 32 logits of its one column out,
@@ -51,9 +53,10 @@
 // log-sum-exp identity.
 //
 // Measured (D = 128): 64 sequences of 128 to 2048 tokens, 40 heads, 72 us = 5.3 TB/s of cached
-// rows; 32 sequences of 8192 to 32768, 64 heads on 8, 127 us = 5.7 TB/s, where copies alone take
-// 117 and everything but the copies 126; one sequence of 2048 tokens, 40 heads, 14.2 us, of which
-// 9 are there at 128 tokens too.
+// rows; 32 sequences of 8192 to 32768, 64 heads on 8, 120 us = 6.1 TB/s.  Copies alone take 94 and
+// 96 % of that; one sequence of 2048 tokens, 40 heads, 14.1 us, of which 9
+// are there at 128 tokens too.  Small blocks cost: 64 sequences of 1088 tokens take 69 us with
+// blocks of 32 tokens, 74 with 16 and 83 with 8 (tiles of 2176, 1088 and 544 bytes).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -194,8 +197,9 @@ __device__ __forceinline__ int v_place(int r, int c) {
 template <int D, int NT>
 struct WarpState {
   float m[NT][2], l[NT][2], c[NT][2];   // l and c: this lane's tokens only, until the end
-  float acc[NT][D / 16][4];             // {even value, heads 2t, 2t + 1; odd value x 16, the same}: sum u' (n - 8)
-                                        // over the chunks before the last, sum u' n over that
+  // Value pair i: {even value, heads 2t, 2t + 1; 16 times the odd value, the same, plus the even one where i is
+  // odd}, as sum u' (n - 8) over the chunks before the last and sum u' n over that.
+  float acc[NT][D / 16][4];
   float ones[NT][4];                    // sum u' over the last chunk
 };
 
