@@ -54,7 +54,7 @@
 //
 // Measured (D = 128): 64 sequences of 128 to 2048 tokens, 40 heads, 72 us = 5.3 TB/s of cached
 // rows; 32 sequences of 8192 to 32768, 64 heads on 8, 120 us = 6.1 TB/s.  Copies alone take 94 and
-// 96 % of that; one sequence of 2048 tokens, 40 heads, 14.1 us, of which 9
+// 96 % of that; one sequence of 2048 tokens, 40 heads, 12.6 us, of which 9
 // are there at 128 tokens too.  Small blocks cost: 64 sequences of 1088 tokens take 69 us with
 // blocks of 32 tokens, 74 with 16 and 83 with 8 (tiles of 2176, 1088 and 544 bytes).
 #include <cuda_fp16.h>
@@ -76,6 +76,10 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int NW = 12;                // warps on an SM, in one CTA; a small grid has CTAs of four
 constexpr int CHUNK = 32;             // tokens a worker handles at a time
 constexpr int kMinChunks = 4;         // chunks a worker takes at least
+// Sixteen warps join a head's parts where there are at most kFewHeads heads in all and equal streams would be
+// cut into more than kManyParts: one sequence of 131072 tokens, 8 heads on 1, 87 -> 25 us, 32 on 8, 55 -> 36;
+// elsewhere one warp does: 8 sequences of 512 tokens, 40 heads, 16.5 us against 22.6, one of 128 9.4 against 10.5.
+constexpr int kFewHeads = 256, kManyParts = 32;
 constexpr float kRescale = 8.f;       // the running maximum moves when a chunk passes it by this much
 
 struct Int4Params {
@@ -696,21 +700,23 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
   cp_async_wait<0>();
 }
 
-// Joins the parts of every cut stream, and writes the zeros of empty contexts: a warp per (sequence,
-// head), a lane D/32 values.
-template <int D>
-__global__ void __launch_bounds__(128, 10) paged_attention_int4_merge_kernel(const Int4Params p, int head_rows) {
+// Joins the parts of every cut stream, and writes the zeros of empty contexts: WPH warps per (sequence,
+// head), a lane D/32 values.  Where there are few heads in all, each may have been cut into a thousand
+// parts, and sixteen warps share them.
+template <int D, int WPH>
+__global__ void __launch_bounds__(WPH == 1 ? 128 : WPH * 32) paged_attention_int4_merge_kernel(const Int4Params p, int head_rows) {
+  constexpr int WARPS = WPH == 1 ? 4 : WPH, FLY = 8;         // warps of a CTA; parts in flight to a warp
   pkv::pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x * 4 + warp, s = blockIdx.y;
+  const int h = WPH == 1 ? blockIdx.x * 4 + warp : blockIdx.x, s = blockIdx.y;
   // chunks of the sequences before s, and of all
   long long mine[2] = {0, 0};
-  for (int i = threadIdx.x; i < p.num_seqs; i += 128) {
+  for (int i = threadIdx.x; i < p.num_seqs; i += WARPS * 32) {
     const int c = chunks_of(p, i);
     mine[1] += c;
     if (i < s) mine[0] += c;
   }
-  __shared__ long long sums[4][2];
+  __shared__ long long sums[WARPS][2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -722,27 +728,34 @@ __global__ void __launch_bounds__(128, 10) paged_attention_int4_merge_kernel(con
     pkv::pdl_wait();
     return;
   }
-  const long long before = sums[0][0] + sums[1][0] + sums[2][0] + sums[3][0];
-  const long long total = sums[0][1] + sums[1][1] + sums[2][1] + sums[3][1];
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) {
+    before += sums[i][0];
+    total += sums[i][1];
+  }
   constexpr int V = D / 32;
   __half* dst = p.out + (static_cast<size_t>(s) * p.num_heads + h) * D + lane * V;
   const int chunks = chunks_of(p, s);
-  if (chunks == 0) {
-    pkv::pdl_wait();
-#pragma unroll
-    for (int c = 0; c < V; c += 2) *reinterpret_cast<__half2*>(dst + c) = __floats2half2_rn(0.f, 0.f);
-    return;
-  }
   const int Y = p.num_kv_heads * p.head_tiles, tile = h % p.group / head_rows;
   const int y = h / p.group * p.head_tiles + tile, row = h % p.group - tile * head_rows;
   const long long first = before * Y + static_cast<long long>(y) * chunks;
   const long long per = per_worker(total * Y, p.workers), w_first = first / per, w_last = (first + chunks - 1) / per;
   pkv::pdl_wait();                                           // the parts
+  if (chunks == 0) {
+    if (WPH == 1 || warp == 0) {
+#pragma unroll
+      for (int c = 0; c < V; c += 2) *reinterpret_cast<__half2*>(dst + c) = __floats2half2_rn(0.f, 0.f);
+    }
+    return;
+  }
   if (w_first == w_last) return;                             // one worker wrote it
-  const int nparts = static_cast<int>(w_last - w_first) + 1, rows = min(head_rows, p.group);
-  const size_t slot0 = static_cast<size_t>(w_first) + static_cast<size_t>(s) * Y + y;
+  const int all = static_cast<int>(w_last - w_first) + 1, rows = min(head_rows, p.group);
+  // this warp's parts
+  const int share = (all + WPH - 1) / WPH, part0 = WPH == 1 ? 0 : warp * share, nparts = min(share, all - part0);
+  const size_t slot0 = static_cast<size_t>(w_first) + part0 + static_cast<size_t>(s) * Y + y;
   auto at = [&](int i) { return (slot0 + i) * rows + row; };  // part i's row of the workspace
-  // (m, l) of 32 slots at a time, one a lane; then four slots' outputs in flight at a time
+  // (m, l) of 32 slots at a time, one a lane; then some slots' outputs in flight at a time
   float acc[V];
 #pragma unroll
   for (int c = 0; c < V; ++c) acc[c] = 0.f;
@@ -763,25 +776,25 @@ __global__ void __launch_bounds__(128, 10) paged_attention_int4_merge_kernel(con
     const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
     L = fmaf(ml.y, f, L);
     const int n = min(32, nparts - base);
-    for (int j0 = 0; j0 < n; j0 += 4) {
-      float x[4][V];
+    for (int j0 = 0; j0 < n; j0 += FLY) {
+      float x[FLY][V];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < FLY; ++u) {
 #pragma unroll
         for (int c = 0; c < V; ++c) x[u][c] = 0.f;
         if (j0 + u < n) {
           const float* src = p.ws_o + at(base + j0 + u) * D + lane * V;
           if constexpr (V == 4) {
-            const float4 y = *reinterpret_cast<const float4*>(src);
-            x[u][0] = y.x; x[u][1] = y.y; x[u][2] = y.z; x[u][3] = y.w;
+            const float4 z = *reinterpret_cast<const float4*>(src);
+            x[u][0] = z.x; x[u][1] = z.y; x[u][2] = z.z; x[u][3] = z.w;
           } else {
-            const float2 y = *reinterpret_cast<const float2*>(src);
-            x[u][0] = y.x; x[u][1] = y.y;
+            const float2 z = *reinterpret_cast<const float2*>(src);
+            x[u][0] = z.x; x[u][1] = z.y;
           }
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < FLY; ++u) {
         const float fu = __shfl_sync(FULL, f, (j0 + u) & 31);
         if (j0 + u < n) {
 #pragma unroll
@@ -792,6 +805,31 @@ __global__ void __launch_bounds__(128, 10) paged_attention_int4_merge_kernel(con
   }
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) L += __shfl_xor_sync(FULL, L, o);
+  if constexpr (WPH > 1) {
+    __shared__ float warp_m[WPH], warp_l[WPH];
+    __shared__ __align__(16) float warp_o[WPH][D];
+    if (lane == 0) {
+      warp_m[warp] = M;
+      warp_l[warp] = L;
+    }
+#pragma unroll
+    for (int c = 0; c < V; ++c) warp_o[warp][lane * V + c] = acc[c];
+    __syncthreads();
+    if (warp != 0) return;
+    M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < WPH; ++i) M = fmaxf(M, warp_m[i]);
+    L = 0.f;
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] = 0.f;
+#pragma unroll
+    for (int i = 0; i < WPH; ++i) {
+      const float f = warp_m[i] == -INFINITY ? 0.f : exp2f(warp_m[i] - M);
+      L = fmaf(warp_l[i], f, L);
+#pragma unroll
+      for (int c = 0; c < V; ++c) acc[c] = fmaf(warp_o[i][lane * V + c], f, acc[c]);
+    }
+  }
   const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
   for (int c = 0; c < V; c += 2) *reinterpret_cast<__half2*>(dst + c) = __floats2half2_rn(acc[c] * inv, acc[c + 1] * inv);
@@ -884,9 +922,15 @@ int launch(Int4Params p, const Plan& pl, void* ws, size_t ws_bytes, cudaStream_t
   p.ws_o = p.ws_ml + ws_ml_floats(static_cast<size_t>(pl.slots) * pl.head_rows);
   cudaError_t e = p.group == 1 ? launch_block_size<D, 1, true>(p, pl, st)
                   : pl.nt == 1 ? launch_block_size<D, 1, false>(p, pl, st) : launch_block_size<D, 2, false>(p, pl, st);
-  if (e == cudaSuccess)
-    e = pkv::launch_pdl(paged_attention_int4_merge_kernel<D>, dim3((p.num_heads + 3) / 4, p.num_seqs), dim3(128), 0, st,
-                        p, pl.head_rows);
+  if (e == cudaSuccess) {
+    const long long streams = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.head_tiles;
+    if (static_cast<long long>(p.num_heads) * p.num_seqs <= kFewHeads && p.workers > kManyParts * streams)
+      e = pkv::launch_pdl(paged_attention_int4_merge_kernel<D, 16>, dim3(p.num_heads, p.num_seqs), dim3(512), 0, st, p,
+                          pl.head_rows);
+    else
+      e = pkv::launch_pdl(paged_attention_int4_merge_kernel<D, 1>, dim3((p.num_heads + 3) / 4, p.num_seqs), dim3(128), 0,
+                          st, p, pl.head_rows);
+  }
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess)
     return pkv::fail(PKV_ERR_CUDA, "pkv_paged_attention_decode_int4 launch: %s", cudaGetErrorString(e));

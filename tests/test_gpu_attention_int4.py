@@ -275,3 +275,10 @@ def test_error_does_not_grow_with_the_context(cuda_device, H, Hk):
     limit = 1.2 * rounding * (1 + (part if H > Hk else 0)) ** 0.5 + 2.0 ** -16
     off = np.linalg.norm(got - want) / np.linalg.norm(want)
     assert off <= limit, (off, limit)
+
+
+@pytest.mark.parametrize("lens,H,Hk,D,B", [([140000], 2, 1, 128, 16), ([0, 50000, 3, 30000], 8, 2, 64, 32),
+                                           ([100] * 40 + [60000], 4, 1, 128, 16), ([20000], 40, 1, 64, 16)])
+def test_streams_cut_into_many_parts(cuda_device, lens, H, Hk, D, B):
+    # a stream over a thousand warps; beside empty and short ones; many heads on one
+    check(make(34, lens, H, Hk, D, B, cuda_device), B, cuda_device)
