@@ -531,7 +531,10 @@ int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, c
  * Tensor cores: fp16 products, fp32 sums; the softmax weights are rounded to fp16
  * before they multiply V.  The tensor cores cut their sums off at the last bit: a
  * row over n keys loses up to n 2^-27 of itself to that, as much as the output's
- * own rounding from 2^16 keys on.  No workspace.
+ * own rounding from 2^16 keys on.  Few queries over many keys are shared out to
+ * clusters of blocks, by num_seqs, total_q, total_k and max_query_len, so rows may
+ * differ in their last bits between calls with other buffers around them.  No
+ * workspace.
  * ------------------------------------------------------------------------- */
 int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t* value, const int32_t* query_start,
                          const int32_t* key_start, int num_seqs, int total_q, int total_k, int max_query_len,

@@ -30,6 +30,10 @@
 //    roles pass from one tile to the next on their own: the next tile's K and V are loaded
 //    and its first scores computed while the softmax warps write the last tile's output.
 //    One launch per tile spent 4.3 us of 7.7 on starts and ends where prompts are short.
+//  * Few queries over many keys (a chunk of one long request) would leave most SMs idle: there the CTAs
+//    of a cluster share a query tile's keys, and each then joins a slice of the columns from all
+//    parts by the log-sum-exp identity, read through distributed shared memory: no workspace and no
+//    second kernel.
 //  * Five kinds of warps run different code at once and share the instruction cache, so code
 //    is kept small where it is not hot: waits in one loop instead of two took ragged short
 //    prompts from 94 us to 74, an unrolled staging of the output had them at 107.
@@ -63,6 +67,12 @@ constexpr int BN = 64;             // keys per tile (S MMA N, PV MMA K)
 // -> 67 us for chunks over cached contexts (17 to 24 key tiles an item), 1072 -> 1062 for long prompts; 912 and
 // 1824 items, or 4 steps, do no better.
 constexpr int kLate = 304, kParts = 8;
+// Where the query tiles of all heads fill at most half of the resident CTAs and a query sees kSplitTiles key
+// tiles or more on average, clusters of two to eight CTAs take an item each and share its key tiles (at least
+// two to a CTA, and none shared below half of kSplitTiles): 128 queries over 131072 keys, 32 heads on 8, 1400
+// -> 256 us; 64 over 8192, 96 -> 29; 128 over 1128, 8 heads, 18.5 -> 12.7.  Below, the clusters' start and the
+// joining cost more than they save: 1024 tokens over themselves, 8 heads, 17.2 -> 18.7 us.
+constexpr int kResident = 304, kSplitTiles = 12, kMostParts = 8;
 constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
 
 struct PromptParams {
@@ -86,7 +96,7 @@ struct Cfg {
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
   static constexpr int NS = D == 64 ? 4 : 2;                  // ring slots each for K and for V
-  static constexpr int BYTES = 1024 + Q_BYTES + 2 * NS * KV_BYTES + 512;
+  static constexpr int BYTES = 1024 + Q_BYTES + 2 * NS * KV_BYTES + 512 + 8 * BM;
   // so much that no third CTA, which would wait for tensor memory, fits an SM
   static constexpr int SMEM = BYTES > 80 * 1024 ? BYTES : 80 * 1024;
 };
@@ -114,6 +124,42 @@ __device__ __forceinline__ void store16(__half* dst, uint32_t a, uint32_t b, uin
     reinterpret_cast<uint4*>(dst)[0] = make_uint4(a, b, c, d);
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(e, f, g, h);
   }
+}
+
+// ---- a cluster's CTAs ----------------------------------------------------------------------------
+__device__ __forceinline__ int cluster_rank() {
+  int r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int cluster_size() {
+  int n;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, int rank) {
+  uint32_t out;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(rank));
+  return out;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void st_shared(uint32_t addr, float a) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(a) : "memory");
+}
+__device__ __forceinline__ void st_shared(uint32_t addr, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
 // ---- taking over a CTA that was not launched yet -------------------------------------------------
@@ -167,7 +213,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
 // mbarrier, and no waiter is more than one phase behind the barrier it waits on.  Every wait is
 // bounded; a role that gives up records PKV_DEV_WAIT_TIMEOUT and leaves its loop, the others give up
 // in turn, and the CTA still reaches its final barrier.
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   using C = Cfg<D>;
   constexpr int NS = C::NS;
@@ -196,6 +242,11 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + AT + 88 - base));
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + AT + 92 - base));
   static_assert(sizeof(Item) == 32 && AT % 16 == 0 && AT + 96 <= 512, "barrier area");
+  // SPLIT: this CTA's place in its cluster, and its part of the item for the others to read: each row's
+  // maximum and sum, and O as [D][BM] floats where the K and V rings were
+  const int rank = SPLIT ? cluster_rank() : 0, parts = SPLIT ? cluster_size() : 1;
+  const uint32_t part_ml = bars + 512, part_o = sk;
+  static_assert(D * BM * 4 <= 2 * NS * C::KV_BYTES, "O fits in the rings");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pkv::pdl_trigger();
@@ -227,7 +278,9 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
       mbar_init_count(v_issued(b), 1);
     }
     *abort_flag = 0;
+    if (SPLIT) items[0].rows = 0;
   }
+  if (SPLIT && tid < BM) st_shared(part_ml + tid * 8, -INFINITY, 0.f);
   if (tid == 64) {
     prefetch_tensormap(&p.tmap_q);
     prefetch_tensormap(&p.tmap_k);
@@ -352,11 +405,21 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
       mbar_arrive_expect_tx(answered, 16);
       try_cancel(answer, answered);
     };
-    int x = blockIdx.x, y = blockIdx.y, j = 0, it = 0, asked = 0;
+    int x = blockIdx.x / parts, y = blockIdx.y, j = 0, it = 0, asked = 0;
     int k_issued = 0, v_issued_n = 0, q_issued = 0;
     while (true) {
       Item item;
-      const bool real = find_item(y * static_cast<int>(gridDim.x) + x, item);
+      const bool real = find_item(y * (static_cast<int>(gridDim.x) / parts) + x, item);
+      if (SPLIT && real) {
+        // this CTA's key tiles
+        const int use = item.n_tiles < kSplitTiles / 2 ? 1 : min(parts, item.n_tiles / 2);
+        const int t0 = item.n_tiles * min(rank, use) / use;
+        item.n_tiles = item.n_tiles * min(rank + 1, use) / use - t0;
+        item.first_pos -= t0 * BN;
+        item.k_row += t0 * BN;
+        item.keys -= t0 * BN;
+        item.edge = max(0, item.edge - t0);
+      }
       if (lane == 0) {
         if (real) {
           const int slot = it & 1;
@@ -403,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
             }
             // the next item is asked for as late as its answer still comes in time (0.4 us): one taken
             // early is not there for a CTA that runs dry
-            if (i == item.n_tiles - 1) {
+            if (!SPLIT && i == item.n_tiles - 1) {
               ask();
               ++asked;
             }
@@ -418,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
             if (i >= item.edge) mbar_arrive(v_issued(b));
             ++v_issued_n;
           }
-        } else {
+        } else if (!SPLIT) {
           ask();
           ++asked;
         }
@@ -427,7 +490,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
       j = __shfl_sync(0xffffffffu, j, 0);
       asked = __shfl_sync(0xffffffffu, asked, 0);
       failed = __shfl_sync(0xffffffffu, failed, 0);
-      if (failed) break;
+      if (failed || SPLIT) break;
       // the answer: another CTA's place, or none left (after which none may be asked for)
       if (!__all_sync(0xffffffffu, wait(answered, (asked - 1) & 1))) {
         failed = true;
@@ -693,6 +756,22 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
             mbar_arrive(item_free(it & 1));
           }
         }
+        if constexpr (SPLIT) {
+          if (fix) {
+            const int last = tid < item.rows ? min(pos, item.keys - 1) : -1;
+            const __half* v = p.v + (item.k_row + static_cast<int64_t>(item.edge) * BN) * p.v_stride +
+                              static_cast<int64_t>(item.head / p.group) * D + c * 32;
+#pragma unroll 1
+            for (int t = item.edge * BN; t <= last; ++t, v += p.v_stride)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!finite16(__half_as_ushort(v[e]))) x[e] += __half2float(v[e]);
+            __syncwarp();
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) st_shared(part_o + ((c * 32 + e) * BM + tid) * 4, x[e]);
+          continue;
+        }
 #pragma unroll
         for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], x[e], x[e + 1], inv, 0.f);
         if (tid < item.rows) {
@@ -704,7 +783,9 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
         }
         __syncwarp();
       }
-      if (fix) {
+      if constexpr (SPLIT) {
+        st_shared(part_ml + tid * 8, m_ref, l);
+      } else if (fix) {
         // values that are not finite in the edge tiles were left out: added to the stored row where the
         // query sees them (rare, so its code is small rather than fast)
         const int last = tid < item.rows ? min(pos, item.keys - 1) : -1;
@@ -720,6 +801,52 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
     if (failed) give_up();
   }
 
+  if constexpr (SPLIT) {
+    __syncwarp();
+    cluster_sync();                                           // every CTA's part is there
+    const int rows = items[0].rows;
+    if (tid < rows) {
+      // a row to a thread, this CTA's D / parts columns of it, by the log-sum-exp identity
+      const int columns = D / parts;
+      float f[kMostParts];                                    // the parts' factors
+      uint32_t o_of[kMostParts];
+      bool has[kMostParts];                                   // not where a part saw no key, or had none
+      float M = -INFINITY, L = 0.f;
+      float2 ml[kMostParts];
+#pragma unroll
+      for (int r = 0; r < kMostParts; ++r)
+        ml[r] = r < parts ? ld_cluster2(map_to_rank(part_ml + tid * 8, r)) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int r = 0; r < kMostParts; ++r) M = fmaxf(M, ml[r].x);
+#pragma unroll
+      for (int r = 0; r < kMostParts; ++r) {
+        has[r] = ml[r].x != -INFINITY || ml[r].y != 0.f;
+        f[r] = exp2f(ml[r].x - M);
+        if (has[r]) L = fmaf(ml[r].y, f[r], L);
+        o_of[r] = map_to_rank(part_o + (rank * columns * BM + tid) * 4, r < parts ? r : 0);
+      }
+      const float inv = 1.f / L;
+      __half* dst = p.out + (static_cast<size_t>(items[0].q_row + tid) * p.num_heads + items[0].head) * D + rank * columns;
+#pragma unroll 1
+      for (int c = 0; c < columns; c += 8) {
+        float v[kMostParts][8], o[8];
+#pragma unroll
+        for (int r = 0; r < kMostParts; ++r)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[r][e] = has[r] ? ld_cluster(o_of[r] + (c + e) * BM * 4) : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          o[e] = 0.f;
+#pragma unroll
+          for (int r = 0; r < kMostParts; ++r) o[e] = has[r] ? fmaf(v[r][e], f[r], o[e]) : o[e];
+        }
+        *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack_half2(o[0] * inv, o[1] * inv), pack_half2(o[2] * inv, o[3] * inv),
+                                                        pack_half2(o[4] * inv, o[5] * inv), pack_half2(o[6] * inv, o[7] * inv));
+      }
+    }
+    __syncwarp();
+    cluster_sync();                                           // nobody reads this CTA's part any more
+  }
   // every tensor-memory access is done (tcgen05.ld and .st wait inline, the products are committed)
   tc_fence_before();
   __syncthreads();
@@ -748,8 +875,8 @@ int encode_rows_map(CUtensorMap* map, const void* x, int D, int H, int T, int64_
   return PKV_OK;
 }
 
-template <int D>
-int launch(const PromptParams& p, long long tiles, cudaStream_t st) {
+template <int D, bool SPLIT>
+int launch(const PromptParams& p, long long tiles, int parts, cudaStream_t st) {
   using C = Cfg<D>;
   static std::mutex mu;
   static bool done[64] = {false};
@@ -758,13 +885,14 @@ int launch(const PromptParams& p, long long tiles, cudaStream_t st) {
   if (e == cudaSuccess) {
     std::lock_guard<std::mutex> g(mu);
     if (dev < 0 || dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(prompt_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+      e = cudaFuncSetAttribute(prompt_attention_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
       if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
     }
   }
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention setup: %s", cudaGetErrorString(e));
-  const dim3 grid(static_cast<unsigned>(tiles), p.num_heads);
-  e = pkv::launch_pdl(prompt_attention_kernel<D>, grid, dim3(THREADS), C::SMEM, st, p);
+  const dim3 grid(static_cast<unsigned>(tiles * parts), p.num_heads);
+  e = SPLIT ? pkv::launch_pdl_cluster(prompt_attention_kernel<D, SPLIT>, grid, dim3(THREADS), C::SMEM, st, parts, p)
+            : pkv::launch_pdl(prompt_attention_kernel<D, SPLIT>, grid, dim3(THREADS), C::SMEM, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention launch: %s", cudaGetErrorString(e));
   return PKV_OK;
@@ -846,7 +974,11 @@ int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t*
   p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  rc = head_dim == 128 ? launch<128>(p, tiles, st) : launch<64>(p, tiles, st);
+  int parts = 1;
+  while (parts < kMostParts && tiles * num_heads * parts * 2 <= kResident && (total_k - total_q / 2) / num_seqs >= kSplitTiles * BN)
+    parts *= 2;
+  if (parts > 1) rc = head_dim == 128 ? launch<128, true>(p, tiles, parts, st) : launch<64, true>(p, tiles, parts, st);
+  else rc = head_dim == 128 ? launch<128, false>(p, tiles, 1, st) : launch<64, false>(p, tiles, 1, st);
   if (rc == PKV_OK) pkv::clear_error();
   return rc;
 }

@@ -243,3 +243,59 @@ def test_rows_past_2_31_elements(cuda_device):
     small = big[T - n:].clone()
     want = pkv.prompt_attention(small, small[:, :24], small[:, 24:], start - (T - n), 0.1, n)
     assert pkv.device_error() == 0 and torch.equal(out[T - n:], want)
+
+
+@pytest.mark.parametrize("news,past,H,Hk,D", [
+    ([1], [5000], 4, 1, 128), ([130], [4000], 2, 2, 64), ([300, 40], [2000, 3000], 3, 1, 128),
+    ([1, 1, 0, 128], [0, 9000, 70, 3], 4, 2, 64), ([700], [0], 2, 1, 128), ([64, 65], [960, 1100], 8, 2, 128)])
+def test_few_tiles_over_many_keys(cuda_device, news, past, H, Hk, D):
+    # the keys of a query tile are shared out to the CTAs of a cluster; some have none of a short sequence
+    check(make(40 + D + H, news, past, H, Hk, D), cuda_device)
+
+
+def test_few_tiles_unseen_values_and_padding(cuda_device):
+    # as above with NaNs and infinities behind the queries, past the sequence, and seen by some rows
+    case = make(41, [100, 60], [3000, 1500], 2, 1, 128)
+    q, k, v, qs, ks = case
+    clean = run(case, 0.1, cuda_device)
+    k2, v2 = k.copy(), v.copy()
+    for x in (k2, v2):
+        x[ks[1] - 1], x[ks[2] - 30] = np.nan, -np.inf
+    got = run((q, k2, v2, qs, ks), 0.1, cuda_device)
+    assert pkv.device_error() == 0
+    same = np.ones(qs[-1], bool)
+    same[qs[1] - 1] = False
+    same[qs[2] - 30:] = False
+    assert torch.equal(got[torch.from_numpy(same)], clean[torch.from_numpy(same)])
+    assert torch.isnan(got[qs[1] - 1]).all()
+    v3 = v.copy()
+    v3[ks[2] - 20, 0, 3], v3[ks[2] - 2, 0, 3], v3[ks[2] - 5, 0, 9], v3[5, 0, 70] = np.inf, -np.inf, np.nan, np.inf
+    got = run((q, k, v3, qs, ks), 0.1, cuda_device).float().cpu().numpy()
+    rows = got[qs[2] - 30:, 0]
+    assert (rows[10:28, 3] == np.inf).all() and np.isnan(rows[28:, 3]).all() and np.isfinite(rows[:10, 3]).all()
+    assert np.isnan(rows[25:, 9]).all() and np.isfinite(rows[:25, 9]).all()
+    assert (got[:100, :, 70] == np.inf).all()                # seen by every query of the first sequence
+    # rows behind the last sequence stay, and the call replays from a graph
+    out = torch.full((170, 2, 128), 5.0, dtype=torch.float16, device=cuda_device)
+    d = [torch.from_numpy(x).to(cuda_device) for x in case]
+    qq = torch.cat([d[0], torch.full((10, 2, 128), float("nan"), dtype=torch.float16, device=cuda_device)])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkv.prompt_attention(qq, d[1], d[2], d[3], 0.1, 100, key_start=d[4], out=out)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[:160], clean) and (out[160:] == 5).all()
+
+
+def test_two_streams_at_once(cuda_device):
+    # shared-out keys on one stream, a full grid of D = 64 on another
+    cases = [make(42, [100], [6000], 8, 2, 128), make(43, [700, 900, 300], 100, 30, 6, 64)]
+    dev = [[torch.from_numpy(x).to(cuda_device) for x in c] for c in cases]
+    call = lambda d, **kw: pkv.prompt_attention(d[0], d[1], d[2], d[3], 0.1, 900, key_start=d[4], **kw)
+    alone = [call(d) for d in dev]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in dev]
+    got = [[call(d, stream=st) for d, st in zip(dev, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    assert pkv.device_error() == 0
+    assert all(torch.equal(g, a) for pair in got for g, a in zip(pair, alone))
