@@ -203,7 +203,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
 // Warp roles:
 //   0-3      softmax: waits S(j), releases K slot, masks, takes the row maximum (moving the running
 //            one, and O, only past 2^8), writes P = 2^(S - m) as fp16 over the scores and arrives on
-//            p_full; after an item's last tile, its output
+//            p_full; after an item's last tile, its output (with SPLIT the part of it for the cluster)
 //   W_S      one lane issues S(j) = Q K(j)^T once K(j) landed and PV(j - 2), the last reader of its
 //            buffer, is done
 //   W_PV     one lane issues O += P(j) V(j) once V(j) and P(j) are there, then releases V
