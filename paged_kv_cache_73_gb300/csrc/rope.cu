@@ -10,9 +10,9 @@
 // HBM-bound: each value is read once and written once, 8 flops between, so the
 // kernel is 16-byte loads, a reduction over the lanes that hold a head, and
 // 16-byte stores.
-//  * One warp takes one token (or a part of its heads, where there are few tokens): it
-//    computes the token's R/2 sines and cosines once, two a lane, and uses them for all
-//    of its heads.  No CTA barrier: warps run free of one another.
+//  * One warp takes one token (or a part of its heads, where there are few tokens, or two
+//    tokens of few heads): it computes the token's R/2 sines and cosines once and uses them
+//    for all of its heads.  No CTA barrier: warps run free of one another.
 //  * The angle is computed in whole numbers: f is given in units of 2^-64 turns, so
 //    position * f wraps modulo one turn by itself, exactly, however far the
 //    position; its top 32 bits then go to sincospif.  A product in fp32 would be off
@@ -39,6 +39,10 @@ __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_
 
 constexpr int kWarps = 4;            // per CTA
 constexpr int kMaxAxes = 8;
+// From kPairTokens tokens of at most kPairPasses warps' worth of rows each, half a warp takes a token: there a
+// warp's time is its chain of loads, angles and stores, and two chains share it (32768 tokens, 8 + 1 heads of
+// 64, 37 -> 26 us, of 128, 43 -> 36).  8192 tokens of 32 + 8 heads of 128 would go from 33 to 40 us.
+constexpr int kPairTokens = 2 * pkv::kFullWarps, kPairPasses = 4;
 
 struct RopeParams {
   const __half* q;
@@ -74,18 +78,21 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// grid (tokens / kWarps, parts of a token's query and key heads)
-template <int D, bool INTERLEAVED>
+// grid (tokens / (kWarps TPW), parts of a token's query and key heads); TPW tokens to a warp
+template <int D, bool INTERLEAVED, int TPW>
 __global__ void __launch_bounds__(kWarps * 32, INTERLEAVED ? 4 : 6) qk_norm_rope_kernel(const RopeParams p) {
   constexpr int LPR = D / 16;                       // lanes per row
-  constexpr int RPP = 32 / LPR;                     // rows a warp takes at a time
+  constexpr int LANES = 32 / TPW;                   // lanes per token
+  constexpr int RPP = LANES / LPR;                  // rows they take at a time
   constexpr int PF = 2;                             // of which so many are in flight
-  __shared__ __align__(16) float cos_of[kWarps][D / 2], sin_of[kWarps][D / 2];
+  __shared__ __align__(16) float cos_tab[kWarps * TPW][D / 2], sin_tab[kWarps * TPW][D / 2];
   pkv::pdl_trigger();
   pkv::pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR;
-  const int t = blockIdx.x * kWarps + warp;
-  if (t >= p.num_tokens) return;
+  const int lane = threadIdx.x & (LANES - 1), c = lane % LPR, slot = threadIdx.x / LANES;
+  const int wanted = blockIdx.x * kWarps * TPW + slot;
+  if (wanted - slot % TPW >= p.num_tokens) return;  // a whole warp
+  const bool live = TPW == 1 || wanted < p.num_tokens;
+  const int t = TPW == 1 ? wanted : min(wanted, p.num_tokens - 1);
   const int total = p.num_heads + p.num_kv_heads;
   const int begin = blockIdx.y * p.rows_per_warp, end = min(total, begin + p.rows_per_warp);
   // this lane's values of a row: eight from first_off and eight from second_off.  The lanes past the
@@ -112,7 +119,7 @@ __global__ void __launch_bounds__(kWarps * 32, INTERLEAVED ? 4 : 6) qk_norm_rope
 #pragma unroll
   for (int u = 0; u < PF; ++u) load(begin + u * RPP + sub, raw[u]);
 
-  for (int pair = lane; pair < p.rotary_dim / 2; pair += 32) {
+  for (int pair = lane; pair < p.rotary_dim / 2; pair += LANES) {
     const int axis = p.pair_axis == nullptr ? 0 : p.pair_axis[pair];
     float cs = 1.f, sn = 0.f;
     if (axis >= 0 && axis < p.num_axes) {
@@ -123,8 +130,8 @@ __global__ void __launch_bounds__(kWarps * 32, INTERLEAVED ? 4 : 6) qk_norm_rope
     } else if (blockIdx.y == 0) {
       record_error(PKV_DEV_BAD_AXIS);
     }
-    cos_of[warp][pair] = cs;
-    sin_of[warp][pair] = sn;
+    cos_tab[slot][pair] = cs;
+    sin_tab[slot][pair] = sn;
   }
   __syncwarp();
 
@@ -150,8 +157,8 @@ __global__ void __launch_bounds__(kWarps * 32, INTERLEAVED ? 4 : 6) qk_norm_rope
       }
       float2 cs = make_float2(1.f, 1.f), sn = make_float2(0.f, 0.f);
       if (turned) {
-        cs = *reinterpret_cast<const float2*>(&cos_of[warp][c * 8 + 2 * i]);
-        sn = *reinterpret_cast<const float2*>(&sin_of[warp][c * 8 + 2 * i]);
+        cs = *reinterpret_cast<const float2*>(&cos_tab[slot][c * 8 + 2 * i]);
+        sn = *reinterpret_cast<const float2*>(&sin_tab[slot][c * 8 + 2 * i]);
       }
       fc[i] = make_float2(w1[0] * cs.x, w1[1] * cs.y);
       fs[i] = make_float2(-w2[0] * sn.x, -w2[1] * sn.y);
@@ -220,7 +227,7 @@ __global__ void __launch_bounds__(kWarps * 32, INTERLEAVED ? 4 : 6) qk_norm_rope
             o1[i] = __floats2half2_rn(y.x, y.y);
           }
         }
-        if (r < r1) {
+        if (r < r1 && live) {
           __half* dst = dst_base + r * D;
           *reinterpret_cast<uint4*>(dst + first_off) = w[0];
           *reinterpret_cast<uint4*>(dst + second_off) = w[1];
@@ -230,10 +237,10 @@ __global__ void __launch_bounds__(kWarps * 32, INTERLEAVED ? 4 : 6) qk_norm_rope
   }
 }
 
-template <int D>
+template <int D, int TPW>
 cudaError_t launch_rope(const RopeParams& p, bool interleaved, dim3 grid, cudaStream_t st) {
-  return interleaved ? pkv::launch_pdl(qk_norm_rope_kernel<D, true>, grid, dim3(kWarps * 32), 0, st, p)
-                     : pkv::launch_pdl(qk_norm_rope_kernel<D, false>, grid, dim3(kWarps * 32), 0, st, p);
+  return interleaved ? pkv::launch_pdl(qk_norm_rope_kernel<D, true, TPW>, grid, dim3(kWarps * 32), 0, st, p)
+                     : pkv::launch_pdl(qk_norm_rope_kernel<D, false, TPW>, grid, dim3(kWarps * 32), 0, st, p);
 }
 
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
@@ -309,16 +316,18 @@ int pkv_qk_norm_rope(const uint16_t* q, const uint16_t* key, const uint16_t* q_w
   p.num_heads = num_heads;
   p.num_kv_heads = num_kv_heads;
   p.eps = eps;
-  // a warp per token; where that leaves SMs short of warps, a token's heads are split
+  // a warp per token, or half a one; where that leaves SMs short of warps, a token's heads are split
   const int rpp = 512 / head_dim, rows = num_heads + num_kv_heads, passes = (rows + rpp - 1) / rpp;
   int splits = num_tokens >= pkv::kFullWarps ? 1 : (pkv::kFullWarps + num_tokens - 1) / num_tokens;
   if (splits > passes) splits = passes;
   const int per = (passes + splits - 1) / splits;
   p.rows_per_warp = per * rpp;
-  const dim3 grid((num_tokens - 1) / kWarps + 1, (passes + per - 1) / per);
+  const int tpw = passes <= kPairPasses && num_tokens >= kPairTokens ? 2 : 1;
+  const dim3 grid((num_tokens - 1) / (kWarps * tpw) + 1, (passes + per - 1) / per);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = head_dim == 128 ? launch_rope<128>(p, interleaved != 0, grid, st)
-                                  : launch_rope<64>(p, interleaved != 0, grid, st);
+  const bool inter = interleaved != 0;
+  cudaError_t e = head_dim == 128 ? (tpw == 2 ? launch_rope<128, 2>(p, inter, grid, st) : launch_rope<128, 1>(p, inter, grid, st))
+                                  : (tpw == 2 ? launch_rope<64, 2>(p, inter, grid, st) : launch_rope<64, 1>(p, inter, grid, st));
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_qk_norm_rope launch: %s", cudaGetErrorString(e));
   pkv::clear_error();

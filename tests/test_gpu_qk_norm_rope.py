@@ -135,3 +135,10 @@ def test_rows_past_2_31_elements(cuda_device):
     pkv.qk_norm_rope(big[:, :40], big[:, 40:], pos, f, q_out=big[:, :40], k_out=big[:, 40:])
     assert pkv.device_error() == 0
     assert torch.equal(big[T - n:, :40], want[0]) and torch.equal(big[T - n:, 40:], want[1])
+
+
+@pytest.mark.parametrize("T,H,Hk,D,R,axes,inter,norm", [(5001, 3, 1, 128, 128, 1, False, True), (4865, 1, 1, 64, 32, 3, True, True),
+                                                        (4864, 8, 8, 128, 64, 2, True, False)])
+def test_many_tokens_of_few_heads(cuda_device, T, H, Hk, D, R, axes, inter, norm):
+    # two tokens to a warp, the last one alone
+    test_against_oracle(cuda_device, T, H, Hk, D, R, axes, inter, norm)
