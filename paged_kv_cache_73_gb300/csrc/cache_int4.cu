@@ -114,16 +114,19 @@ __device__ __forceinline__ unsigned pack8(const uint4& raw, float inv, float b, 
   return word;
 }
 
-// grid (tokens / kWarps, parts of a token's K and V rows)
-template <int D>
+// grid (tokens / (kWarps TPW), parts of a token's K and V rows); TPW tokens to a warp
+template <int D, int TPW>
 __global__ void __launch_bounds__(kWarps * 32, 7) reshape_and_cache_int4_kernel(const Int4RowParams p) {
   constexpr int LPR = D / 32;                       // lanes per row: 16 values of each half of it to a lane
-  constexpr int RPP = 32 / LPR;                     // rows a warp takes at a time
+  constexpr int LANES = 32 / TPW;                   // lanes per token
+  constexpr int RPP = LANES / LPR;                  // rows they take at a time
   pkv::pdl_trigger();
   pkv::pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR;
-  const int t = blockIdx.x * kWarps + warp;
-  if (t >= p.num_tokens) return;
+  const int lane = threadIdx.x & (LANES - 1), c = lane % LPR, place = threadIdx.x / LANES;
+  const int wanted = blockIdx.x * kWarps * TPW + place;
+  if (wanted - place % TPW >= p.num_tokens) return;  // a whole warp
+  bool live = TPW == 1 || wanted < p.num_tokens;
+  const int t = TPW == 1 ? wanted : min(wanted, p.num_tokens - 1);
   const int H = p.num_heads;
   const int begin = blockIdx.y * p.rows_per_warp, end = min(2 * H, begin + p.rows_per_warp);
   const __half* key = p.key + t * p.key_stride + c * 16;
@@ -141,11 +144,12 @@ __global__ void __launch_bounds__(kWarps * 32, 7) reshape_and_cache_int4_kernel(
   };
   const int first = begin + lane / LPR;
   load(first, raw);
-  const int64_t slot = p.slots[t];
-  if (slot < 0) return;                             // padding token
-  if (slot >= p.num_slots) {
-    if (lane == 0 && blockIdx.y == 0) record_error(PKV_DEV_BAD_SLOT);
-    return;
+  int64_t slot = p.slots[t];
+  if (slot < 0 || slot >= p.num_slots) {
+    if (slot >= 0 && live && lane == 0 && blockIdx.y == 0) record_error(PKV_DEV_BAD_SLOT);
+    if (TPW == 1) return;
+    live = false;                                   // padding token or bad slot, beside others in its warp
+    slot = 0;
   }
   const int in_block = static_cast<int>(slot & ((1 << p.log2_block) - 1));
   const int64_t block_base = (slot >> p.log2_block) * H * p.tile_bytes;
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kWarps * 32, 7) reshape_and_cache_int4_kernel(
     unsigned w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = pack8(x[k], inv, b, lo, s, sure);
-    if (r < end) {
+    if (r < end && live) {
       uint8_t* tile = (r < H ? k_block : v_block) + static_cast<int64_t>(r) * p.tile_bytes;
       *reinterpret_cast<uint2*>(tile + data_off) = make_uint2(w[0], w[1]);
       *reinterpret_cast<uint2*>(tile + data_off + D / 4) = make_uint2(w[2], w[3]);
@@ -211,16 +215,17 @@ __device__ __forceinline__ uint4 unpack8(unsigned word, __half2 s2, __half2 z2) 
                     __byte_perm(pair[0], pair[1], 0x7632), __byte_perm(pair[2], pair[3], 0x7632));
 }
 
-// grid (tokens / kWarps, parts of a token's K and V rows)
-template <int D>
+// grid (tokens / (kWarps TPW), parts of a token's K and V rows)
+template <int D, int TPW>
 __global__ void __launch_bounds__(kWarps * 32) gather_cache_int4_kernel(const Int4RowParams p) {
   constexpr int LPR = D / 16;
-  constexpr int RPP = 32 / LPR;
+  constexpr int LANES = 32 / TPW;
+  constexpr int RPP = LANES / LPR;
   constexpr int U = 5;                              // rows a lane has in flight together
   pkv::pdl_trigger();
   pkv::pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR;
-  const int t = blockIdx.x * kWarps + warp;
+  const int lane = threadIdx.x & (LANES - 1), c = lane % LPR;
+  const int t = blockIdx.x * kWarps * TPW + threadIdx.x / LANES;
   if (t >= p.num_tokens) return;
   const int H = p.num_heads;
   const int begin = blockIdx.y * p.rows_per_warp, end = min(2 * H, begin + p.rows_per_warp);
@@ -278,10 +283,13 @@ int check_shape(const char* fn, int num_tokens, int num_heads, int head_dim, int
   return PKV_OK;
 }
 
-// A warp per token; where that leaves SMs short of warps, a token's 2 H rows are split.
+// A warp per token; where that leaves SMs short of warps, a token's 2 H rows are split.  Many tokens of so few
+// rows that a quarter of a warp has them in two passes go four to a warp: a warp's time is its chain of
+// loads and stores there (16384 tokens of one head of 128: write 12.4 -> 8.3 us, read-back 8.3 -> 6.2).  Kernels:
+// for D = 64 and 128, one and four tokens to a warp.
 template <typename Kernel>
-int launch_rows(const char* fn, Kernel k64, Kernel k128, int values_per_lane, Int4RowParams p, int num_tokens, int head_dim,
-                int block_size, int num_blocks, void* stream) {
+int launch_rows(const char* fn, const Kernel (&kernels)[2][2], int values_per_lane, Int4RowParams p, int num_tokens,
+                int head_dim, int block_size, int num_blocks, void* stream) {
   int lb = 0;
   while ((1 << lb) < block_size) ++lb;
   p.log2_block = lb;
@@ -293,8 +301,9 @@ int launch_rows(const char* fn, Kernel k64, Kernel k128, int values_per_lane, In
   if (splits > passes) splits = passes;
   const int per = (passes + splits - 1) / splits;
   p.rows_per_warp = per * rpp;
-  const dim3 grid((num_tokens - 1) / kWarps + 1, (passes + per - 1) / per);
-  cudaError_t e = pkv::launch_pdl(head_dim == 128 ? k128 : k64, grid, dim3(kWarps * 32), 0,
+  const bool four = 4 * p.num_heads <= rpp && num_tokens >= 4 * pkv::kFullWarps;
+  const dim3 grid((num_tokens - 1) / (kWarps * (four ? 4 : 1)) + 1, (passes + per - 1) / per);
+  cudaError_t e = pkv::launch_pdl(kernels[head_dim == 128][four], grid, dim3(kWarps * 32), 0,
                                   static_cast<cudaStream_t>(stream), p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
@@ -347,8 +356,10 @@ int pkv_reshape_and_cache_int4(const uint16_t* key, const uint16_t* value, uint8
   p.key_stride = key_stride;
   p.value_stride = value_stride;
   p.num_heads = num_kv_heads;
-  return launch_rows(fn, reshape_and_cache_int4_kernel<64>, reshape_and_cache_int4_kernel<128>, 32, p, num_tokens, head_dim,
-                     block_size, num_blocks, stream);
+  using Kernel = void (*)(Int4RowParams);
+  static constexpr Kernel kernels[2][2] = {{reshape_and_cache_int4_kernel<64, 1>, reshape_and_cache_int4_kernel<64, 4>},
+                                           {reshape_and_cache_int4_kernel<128, 1>, reshape_and_cache_int4_kernel<128, 4>}};
+  return launch_rows(fn, kernels, 32, p, num_tokens, head_dim, block_size, num_blocks, stream);
 }
 
 int pkv_gather_cache_int4(const uint8_t* k_cache, const uint8_t* v_cache, const int64_t* slot_mapping,
@@ -372,8 +383,10 @@ int pkv_gather_cache_int4(const uint8_t* k_cache, const uint8_t* v_cache, const 
   p.key_out = reinterpret_cast<__half*>(key);
   p.value_out = reinterpret_cast<__half*>(value);
   p.num_heads = num_kv_heads;
-  return launch_rows(fn, gather_cache_int4_kernel<64>, gather_cache_int4_kernel<128>, 16, p, num_tokens, head_dim, block_size,
-                     num_blocks, stream);
+  using Kernel = void (*)(Int4RowParams);
+  static constexpr Kernel kernels[2][2] = {{gather_cache_int4_kernel<64, 1>, gather_cache_int4_kernel<64, 4>},
+                                           {gather_cache_int4_kernel<128, 1>, gather_cache_int4_kernel<128, 4>}};
+  return launch_rows(fn, kernels, 16, p, num_tokens, head_dim, block_size, num_blocks, stream);
 }
 
 }  // extern "C"

@@ -152,3 +152,31 @@ def test_a_slot_read_many_times(cuda_device):
     sl = torch.tensor([5, 5, 0, 5, 7, 0, 5], device=cuda_device)
     for got, o in zip(pkv.gather_cache_int4(*pools, sl, 4), one):
         assert torch.equal(got, o[sl])
+
+
+@pytest.mark.parametrize("D,H,T", [(128, 1, 9729), (128, 2, 10001), (64, 4, 9731), (64, 1, 9728)])
+def test_many_tokens_of_few_heads(cuda_device, D, H, T):
+    # four tokens to a warp: the last warp's not all there, padding and bad slots beside others
+    B, rng = 16, np.random.default_rng(D + H)
+    kv = _rows(rng, T, 2 * H, D)
+    N = -(-T // B) + 1
+    slots = rng.permutation(N * B)[:T].astype(np.int64)
+    slots[3::7] = -1
+    slots[5] = slots[T - 1] = N * B
+    kc, vc = o4.empty_pool(N, H, B, D), o4.empty_pool(N, H, B, D)
+    kd, vd = (torch.from_numpy(p.copy()).to(cuda_device) for p in (kc, vc))
+    dev = torch.from_numpy(kv).to(cuda_device)
+    sl = torch.from_numpy(slots).to(cuda_device)
+    pkv.reshape_and_cache_int4(dev[:, :H], dev[:, H:], kd, vd, sl, B)
+    assert pkv.device_error() == 3
+    good = np.where(slots >= N * B, -1, slots)
+    o4.store(kc, kv[:, :H], good, B)
+    o4.store(vc, kv[:, H:], good, B)
+    assert np.array_equal(kd.cpu().numpy(), kc) and np.array_equal(vd.cpu().numpy(), vc)
+    ko, vo = (torch.full((T, H, D), 7.0, dtype=torch.float16, device=cuda_device) for _ in range(2))
+    pkv.gather_cache_int4(kd, vd, sl, B, ko, vo)
+    assert pkv.device_error() == 3
+    for got, pool in ((ko, kc), (vo, vc)):
+        want = o4.pool_values(pool, B)[good // B, :, good % B].astype(np.float16)
+        want[good < 0] = 7.0
+        assert np.array_equal(got.cpu().numpy().view(np.uint16), want.view(np.uint16))
