@@ -140,10 +140,10 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device: Optional[int] = None) -> Optional[int]:
     if stream is None:
         # the raw handle: building torch's Stream object takes as long as a small launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -497,16 +497,16 @@ def _rows(t: torch.Tensor, name: str, device: int) -> Tuple[int, int, int, int]:
                    f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} device={t.device}")
 
 
-def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
-    """Memory for a call on `stream` (None: the current one).  It belongs to that stream, so neither work that
-    the current stream has yet to do with the memory's last owner, nor its next owner, meets the call's."""
+def _empty(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """Memory beside `like` for a call on `stream` (None: the current one).  It belongs to that stream, so neither
+    work that the current stream has yet to do with the memory's last owner, nor its next owner, meets the call's."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
         handle = _stream(stream)
         stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def rope_frequencies(inv_freq: Sequence[float], device="cuda") -> torch.Tensor:
@@ -558,13 +558,13 @@ def qk_norm_rope(q: torch.Tensor, key: torch.Tensor, positions: torch.Tensor, fr
                 raise PkvError(PKV_ERR_INVALID_ARG, f"qk_norm_rope: {name} must have head_dim entries")
     qos, kos = H * D, Hk * D
     if q_out is None:
-        q_out = _empty((T, H, D), torch.float16, q.device, stream)
+        q_out = _empty((T, H, D), torch.float16, q, stream)
     else:
         *shape, qos = _rows(q_out, "q_out", dev)
         if shape != [T, H, D]:
             raise PkvError(PKV_ERR_INVALID_ARG, "qk_norm_rope: q_out must be shaped like q")
     if k_out is None:
-        k_out = _empty((T, Hk, D), torch.float16, q.device, stream)
+        k_out = _empty((T, Hk, D), torch.float16, q, stream)
     else:
         *shape, kos = _rows(k_out, "k_out", dev)
         if shape != [T, Hk, D]:
@@ -572,7 +572,7 @@ def qk_norm_rope(q: torch.Tensor, key: torch.Tensor, positions: torch.Tensor, fr
     _check(load().pkv_qk_norm_rope(
         q.data_ptr(), key.data_ptr(), _ptr(q_weight), _ptr(k_weight), eps, positions.data_ptr(), axes,
         frequencies.data_ptr(), _ptr(pair_axis), 2 * pairs, int(interleaved), T, H, Hk, D, qs, ks,
-        q_out.data_ptr(), k_out.data_ptr(), qos, kos, _stream(stream)))
+        q_out.data_ptr(), k_out.data_ptr(), qos, kos, _stream(stream, dev)))
     return q_out, k_out
 
 
@@ -584,9 +584,8 @@ def int4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_d
     return num_blocks, num_kv_heads, block_size * (head_dim // 2 + 4)
 
 
-def _need_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, block_size: int) -> Tuple[int, int, int]:
-    """(num_blocks, num_kv_heads, head_dim) of two four-bit pools."""
-    dev = torch.cuda.current_device()
+def _need_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, block_size: int, dev: int) -> Tuple[int, int, int]:
+    """(num_blocks, num_kv_heads, head_dim) of two four-bit pools on the current device, dev."""
     if not (_is(k_cache, torch.uint8, 3, dev) and _is(v_cache, torch.uint8, 3, dev)):
         _need(k_cache, "k_cache", torch.uint8, 3)
         _need(v_cache, "v_cache", torch.uint8, 3)
@@ -604,7 +603,7 @@ def reshape_and_cache_int4(key: torch.Tensor, value: torch.Tensor, k_cache: torc
     dev = torch.cuda.current_device()
     *rows, ks = _rows(key, "key", dev)
     *vrows, vs = _rows(value, "value", dev)
-    N, H, D = _need_int4(k_cache, v_cache, block_size)
+    N, H, D = _need_int4(k_cache, v_cache, block_size, dev)
     if not _is(slot_mapping, torch.int64, 1, dev):
         _need(slot_mapping, "slot_mapping", torch.int64, 1)
     T = slot_mapping.shape[0]
@@ -612,7 +611,7 @@ def reshape_and_cache_int4(key: torch.Tensor, value: torch.Tensor, k_cache: torc
         raise PkvError(PKV_ERR_INVALID_ARG, "reshape_and_cache_int4: inconsistent shapes")
     _check(load().pkv_reshape_and_cache_int4(key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                              slot_mapping.data_ptr(), T, H, D, block_size, N, ks, vs,
-                                             _stream(stream)))
+                                             _stream(stream, dev)))
 
 
 def gather_cache_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor, block_size: int,
@@ -620,23 +619,25 @@ def gather_cache_int4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping
                       stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """fp16 rows [T, H, D] of what slots slot_mapping[t] of the pools stand for (rows with a negative
     slot are left as they were)."""
-    N, H, D = _need_int4(k_cache, v_cache, block_size)
-    if not _is(slot_mapping, torch.int64, 1, torch.cuda.current_device()):
+    dev = torch.cuda.current_device()
+    N, H, D = _need_int4(k_cache, v_cache, block_size, dev)
+    if not _is(slot_mapping, torch.int64, 1, dev):
         _need(slot_mapping, "slot_mapping", torch.int64, 1)
     shape = (slot_mapping.shape[0], H, D)
     T = shape[0]
     outs = []
     for t, name in ((key, "key"), (value, "value")):
         if t is None:
-            t = _empty(shape, torch.float16, k_cache.device, stream)
+            t = _empty(shape, torch.float16, k_cache, stream)
         else:
-            _need(t, name, torch.float16, 3)
-            if tuple(t.shape) != shape:
+            if not _is(t, torch.float16, 3, dev):
+                _need(t, name, torch.float16, 3)
+            if t.shape != shape:
                 raise PkvError(PKV_ERR_INVALID_ARG, f"gather_cache_int4: {name} must be [{T}, {H}, {D}]")
         outs.append(t)
     key, value = outs
     _check(load().pkv_gather_cache_int4(k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
-                                        key.data_ptr(), value.data_ptr(), T, H, D, block_size, N, _stream(stream)))
+                                        key.data_ptr(), value.data_ptr(), T, H, D, block_size, N, _stream(stream, dev)))
     return key, value
 
 
@@ -644,10 +645,11 @@ def copy_blocks_int4(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.
                      block_size: int, stream=None) -> None:
     """copy_blocks on four-bit pools."""
     L = len(k_caches)
+    dev = torch.cuda.current_device()
     if len(v_caches) != L or L == 0:
         raise PkvError(PKV_ERR_INVALID_ARG, "copy_blocks_int4: need as many K as V pools, at least one")
     for k, v in zip(k_caches, v_caches):
-        N, H, D = _need_int4(k, v, block_size)
+        N, H, D = _need_int4(k, v, block_size, dev)
         if k.shape != k_caches[0].shape:
             raise PkvError(PKV_ERR_INVALID_ARG, "copy_blocks_int4: pools differ in shape")
     _need(block_mapping, "block_mapping", torch.int64, 2, host_ok=True)
@@ -655,7 +657,7 @@ def copy_blocks_int4(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.
         raise PkvError(PKV_ERR_INVALID_ARG, "copy_blocks_int4: block_mapping must be [P, 2]")
     arr = lambda ts: ctypes.cast((ctypes.c_void_p * L)(*[t.data_ptr() for t in ts]), ctypes.c_void_p)
     _check(load().pkv_copy_blocks_int4(arr(k_caches), arr(v_caches), L, block_mapping.data_ptr(),
-                                       block_mapping.shape[0], H, D, block_size, N, _stream(stream)))
+                                       block_mapping.shape[0], H, D, block_size, N, _stream(stream, dev)))
 
 
 def swap_blocks_int4(src_k: Sequence[torch.Tensor], src_v: Sequence[torch.Tensor], dst_k: Sequence[torch.Tensor],
@@ -700,7 +702,7 @@ def paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     """out[s, h] = softmax attention of q[s, h] over the sequence's rows of four-bit pools; num_heads
     may be a multiple of the pools' heads (grouped heads)."""
     dev = torch.cuda.current_device()
-    N, Hk, D = _need_int4(k_cache, v_cache, block_size)
+    N, Hk, D = _need_int4(k_cache, v_cache, block_size, dev)
     if not (_is(q, torch.float16, 3, dev) and _is(block_tables, torch.int32, 2, dev)
             and _is(context_lens, torch.int32, 1, dev)):
         _need(q, "q", torch.float16, 3)
@@ -713,21 +715,22 @@ def paged_attention_decode_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     if rows != S or context_lens.shape[0] != S:
         raise PkvError(PKV_ERR_INVALID_ARG, "block_tables / context_lens rows != num_seqs")
     if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
+        out = _empty((S, H, D), torch.float16, q, stream)
     else:
-        _need(out, "out", torch.float16, 3)
+        if not _is(out, torch.float16, 3, dev):
+            _need(out, "out", torch.float16, 3)
         if out.shape != q.shape:
             raise PkvError(PKV_ERR_INVALID_ARG, "paged_attention_decode_int4: out must be shaped like q")
     if workspace is None:
         n = _int4_workspace_size(dev, S, H, Hk, D, max_blocks, block_size)
-        workspace = _empty((n,), torch.uint8, q.device, stream) if n else None
+        workspace = _empty((n,), torch.uint8, k_cache, stream) if n else None
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         _need(workspace, "workspace", workspace.dtype, workspace.dim())
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load().pkv_paged_attention_decode_int4(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
         S, H, Hk, D, N, max_blocks, float(scale), block_size, out.data_ptr(), _ptr(workspace), ws_bytes,
-        _stream(stream)))
+        _stream(stream, dev)))
     return out
 
 
@@ -757,14 +760,15 @@ def prompt_attention(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, qu
         if key_start.shape[0] != S + 1:
             raise PkvError(PKV_ERR_INVALID_ARG, "prompt_attention: query_start and key_start differ in length")
     if out is None:
-        out = _empty((T, H, D), torch.float16, q.device, stream)
+        out = _empty((T, H, D), torch.float16, q, stream)
     else:
-        _need(out, "out", torch.float16, 3)
+        if not _is(out, torch.float16, 3, dev):
+            _need(out, "out", torch.float16, 3)
         if out.shape != q.shape:
             raise PkvError(PKV_ERR_INVALID_ARG, "prompt_attention: out must be shaped like q")
     _check(load().pkv_prompt_attention(
         q.data_ptr(), key.data_ptr(), value.data_ptr(), query_start.data_ptr(), _ptr(key_start), S, T, Tk,
-        int(max_query_len), H, Hk, D, qs, ks, vs, float(scale), out.data_ptr(), _stream(stream)))
+        int(max_query_len), H, Hk, D, qs, ks, vs, float(scale), out.data_ptr(), _stream(stream, dev)))
     return out
 
 
