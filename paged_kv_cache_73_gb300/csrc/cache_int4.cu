@@ -48,14 +48,19 @@ struct Int4RowParams {
   int rows_per_warp;
 };
 
-// n of one value by the definition, from the estimate n0 (off by at most one): n s against d = x - lo,
-// halves to even.  n s is exact in fp32 (4 + 11 bits), and so is 2 (d - n s) next to a border.
-__device__ __forceinline__ unsigned nearest_exact(float d, float s, float n0) {
-  float n = fminf(fmaxf(n0, 0.f), 15.f);
+// n of one value by the definition, from the estimate n0 (off by at most one): n s against x - lo, halves to
+// even.  n s is exact in fp32 (4 + 11 bits).  x - lo can take 40 bits: d is its rounding to fp32 and rest, by
+// a two-sum, exactly what that left.  Next to a border r = d - n s is exact too.  d is below 16 s (below
+// 22 s where s is below the normals, and exact there), so its last place is 2^-19 of s's leading bit at most:
+// 2 r and s are multiples of twice d's last place, 2 rest is at most one, and rest decides where 2 r meets s.
+__device__ __forceinline__ unsigned nearest_exact(float x, float lo, float s, float inv) {
+  const float d = x - lo, back = d - x, rest = (x - (d - back)) - (lo + back);
+  float n = fminf(fmaxf(rintf(d * inv), 0.f), 15.f);
   const float r2 = 2.f * fmaf(-n, s, d);
   const bool odd = (static_cast<int>(n) & 1) != 0;
-  if (r2 > s || (r2 == s && odd)) n += 1.f;
-  if (r2 < -s || (r2 == -s && odd)) n -= 1.f;
+  const bool up = r2 > s || (r2 == s && (rest > 0.f || (rest == 0.f && odd)));
+  const bool down = r2 < -s || (r2 == -s && (rest < 0.f || (rest == 0.f && odd)));
+  n += up ? 1.f : down ? -1.f : 0.f;
   return static_cast<unsigned>(fminf(fmaxf(n, 0.f), 15.f));
 }
 
@@ -107,8 +112,7 @@ __device__ __forceinline__ unsigned pack8(const uint4& raw, float inv, float b, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float x = (i & 1) ? __high2float(h2[i / 2]) : __low2float(h2[i / 2]);
-      const float d = x - lo;
-      word |= s > 0.f ? nearest_exact(d, s, rintf(d * inv)) << (4 * i) : 0u;
+      word |= s > 0.f ? nearest_exact(x, lo, s, inv) << (4 * i) : 0u;
     }
   }
   return word;

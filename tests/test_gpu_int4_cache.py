@@ -180,3 +180,25 @@ def test_many_tokens_of_few_heads(cuda_device, D, H, T):
         want = o4.pool_values(pool, B)[good // B, :, good % B].astype(np.float16)
         want[good < 0] = 7.0
         assert np.array_equal(got.cpu().numpy().view(np.uint16), want.view(np.uint16))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_halves_beside_a_tiny_minimum(cuda_device, D):
+    # x - min takes more than the 24 bits of fp32: rounded to them, it lands on a half that it is not on
+    rng = np.random.default_rng(D)
+    x = np.zeros((400, 2, D), np.float16)
+    step = 2.0 ** rng.integers(-6, 12, (400, 2, 1))
+    x[...] = step * rng.integers(0, 31, x.shape) / 2
+    x[..., 0], x[..., 1] = 0, 15 * step[..., 0]
+    x[:, 0, 0] = -rng.integers(1, 64, 400) * 2.0 ** -24      # below 0: the values lie just past the halves
+    x[:, 1, 2] = x[:, 1, 0] = 2.0 ** -24                     # above 0: just before them
+    x[:, 1, 3:] = np.maximum(x[:, 1, 3:], 2.0 ** -24)
+    x[0, 0, :3], x[0, 0, 3:] = [-65504, 19936, -2.0 ** -24], 0
+    pools = [torch.zeros(pkv.int4_cache_shape(100, 2, 4, D), dtype=torch.uint8, device=cuda_device) for _ in range(2)]
+    dev = torch.from_numpy(x).to(cuda_device)
+    pkv.reshape_and_cache_int4(dev, dev.flip(1), *pools, torch.arange(400, device=cuda_device), 4)
+    assert pkv.device_error() == 0
+    for pool, rows in zip(pools, (x, x[:, ::-1])):
+        want = o4.empty_pool(100, 2, 4, D)
+        o4.store(want, rows, np.arange(400), 4)
+        assert np.array_equal(pool.cpu().numpy(), want)
