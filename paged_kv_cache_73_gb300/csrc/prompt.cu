@@ -52,21 +52,17 @@
 
 #include "launch.cuh"
 #include "pkv_internal.h"
+#include "prompt_items.cuh"
 #include "tcgen05.cuh"
 
 namespace {
 
 using namespace pkv::tc;
+using namespace pkv::prompt;
 
 __device__ int g_dev_error_prompt = 0;
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_prompt, 0, code); }
 
-constexpr int BM = 128;            // queries per query tile (MMA M)
-constexpr int BN = 64;             // keys per tile (S MMA N, PV MMA K)
-// The last kLate items (as many as CTAs run at once) come by length, in kParts steps from long to short: 69.5
-// -> 67 us for chunks over cached contexts (17 to 24 key tiles an item), 1072 -> 1062 for long prompts; 912 and
-// 1824 items, or 4 steps, do no better.
-constexpr int kLate = 304, kParts = 8;
 // Where the query tiles of all heads fill at most half of the resident CTAs and a query sees kSplitTiles key
 // tiles or more on average, clusters of two to eight CTAs take an item each and share its key tiles (at least
 // two to a CTA, and none shared below half of kSplitTiles): 128 queries over 131072 keys, 32 heads on 8, 1400
@@ -79,14 +75,10 @@ struct PromptParams {
   CUtensorMap tmap_q, tmap_k, tmap_v;   // (D, heads, tokens), boxes of 64 x 1 x 128 (q) or 64, 128-byte swizzle
   const __half* k;
   const __half* v;
-  const int32_t* qstart;
-  const int32_t* kstart;
   __half* out;
   int64_t k_stride, v_stride;
-  int num_seqs, num_heads, group;
-  int max_tiles;                        // query tiles per sequence that max_query_len covers
-  int late;                             // heads whose query tiles come last and by length
-  int total_q, total_k;
+  Layout layout;
+  int group;
   int out_sectors;                      // out is 32-byte aligned
   float scale_log2;
 };
@@ -106,12 +98,6 @@ constexpr int W_S = 4, W_LOAD = 5, W_CHECK = 6, W_PV = 7;     // warps 0 to 3: s
 constexpr int THREADS = 256;
 
 __device__ __forceinline__ bool finite16(unsigned h) { return (h & 0x7c00u) != 0x7c00u; }
-
-// A query tile: its first row of q and out, the rows that are its sequence's, the first one's position
-// among the keys; the sequence's first key and their number; key tiles to visit, the first edge tile.
-struct Item {
-  int q_row, rows, first_pos, k_row, keys, n_tiles, edge, head;
-};
 
 // Sixteen fp16 values to out: one 32-byte store where out's rows are whole sectors, else two of 16.
 __device__ __forceinline__ void store16(__half* dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
@@ -324,83 +310,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
 
   if (warp == W_LOAD) {
     // ---------------- items and loads ----------------
-    // 32 sequences at a time, one a lane: where they start, their lengths, their query tiles and the key
-    // tiles that the last of those visits.  A sequence with a bad range has none; some CTA gets to each
-    // batch and reports it.
-    // A batch's items come in parts: part 0 has all query tiles of the first heads; each further part those
-    // of the last p.late heads that visit more than `few` key tiles and are in no part before.
-    int q0 = 0, n = 0, k0 = 0, m = 0, tiles = 0, own = 0;
-    int batch = 0, part = -1, most = 0;                       // most: the largest `own`
-    int upto = 0, per_head = 0, end = 0, begin = 0;           // a head's items up to the lane's, all; the lane's tiles
-    int64_t part_base = 0;                                    // the part's first item
-    // Item x.  Batch and part are kept: a CTA's items mostly rise.
-    auto find_item = [&](int x, Item& item) {
-      if (x < part_base) {
-        batch = part_base = 0;
-        part = -1;
-      }
-      while (true) {
-        const int heads = part <= 0 ? p.num_heads - p.late : p.late;
-        if (part >= 0) {
-          const int64_t size = static_cast<int64_t>(per_head) * heads;
-          if (x - part_base < size) break;
-          part_base += size;
-          if (part == kParts) {
-            batch += 32;
-            if (batch >= p.num_seqs) return false;
-            part = -1;
-          }
-        }
-        if (++part == 0) {
-          const int i = batch + lane;
-          tiles = own = 0;
-          if (i < p.num_seqs) {
-            q0 = p.qstart[i];
-            n = p.qstart[i + 1] - q0;
-            k0 = p.kstart[i];
-            m = p.kstart[i + 1] - k0;
-            const bool ok = n >= 0 && n <= m && q0 >= 0 && q0 <= p.total_q - n && k0 >= 0 && k0 <= p.total_k - m;
-            if (!ok || n > p.max_tiles * static_cast<int64_t>(BM)) record_error(PKV_DEV_BAD_QUERY_RANGE);
-            tiles = ok ? min((n + BM - 1) / BM, p.max_tiles) : 0;
-            if (tiles > 0) own = (m - n + min(n, tiles * BM) - 1) / BN + 1;
-          }
-          most = __reduce_max_sync(0xffffffffu, own);
-          begin = 0;
-          end = tiles;
-        } else {
-          // begin: the lane's first query tile that visits more than `few` key tiles
-          const int few = most - part * ((most + kParts - 1) / kParts);
-          const int rows = few * BN + 1 - (m - n);            // so many queries of the sequence see at most that
-          end = part == 1 ? tiles : begin;
-          begin = part == kParts || rows <= 0 ? 0 : few >= own ? tiles : min(tiles, (rows - 1) / BM);
-        }
-        upto = end - begin;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const int y = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += y;
-        }
-        per_head = __shfl_sync(0xffffffffu, upto, 31);
-      }
-      const unsigned in_part = static_cast<unsigned>(x - part_base), h = in_part / static_cast<unsigned>(per_head);
-      const int w = static_cast<int>(in_part - h * per_head);
-      const int hit = __ffs(__ballot_sync(0xffffffffu, upto > w)) - 1;
-      // a sequence's tiles from the last, which visits the most key tiles
-      const int qt = __shfl_sync(0xffffffffu, begin + upto, hit) - 1 - w;
-      const int s_n = __shfl_sync(0xffffffffu, n, hit), s_m = __shfl_sync(0xffffffffu, m, hit);
-      const int s_q0 = __shfl_sync(0xffffffffu, q0, hit), s_k0 = __shfl_sync(0xffffffffu, k0, hit);
-      const int i0 = qt * BM;
-      item.q_row = s_q0 + i0;
-      item.rows = min(s_n - i0, BM);
-      item.first_pos = s_m - s_n + i0;
-      item.k_row = s_k0;
-      item.keys = s_m;
-      item.n_tiles = (item.first_pos + item.rows - 1) / BN + 1;
-      // tiles from here on hold keys that some row does not see, or the sequence's end
-      item.edge = min((item.first_pos + 1) / BN, s_m / BN);
-      item.head = static_cast<int>(h) + (part == 0 ? 0 : p.num_heads - p.late);
-      return true;
-    };
+    ItemFinder finder;
     auto ask = [&]() {
       mbar_arrive_expect_tx(answered, 16);
       try_cancel(answer, answered);
@@ -409,7 +319,8 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
     int k_issued = 0, v_issued_n = 0, q_issued = 0;
     while (true) {
       Item item;
-      const bool real = find_item(y * (static_cast<int>(gridDim.x) / parts) + x, item);
+      const bool real = finder.find(p.layout, y * (static_cast<int>(gridDim.x) / parts) + x, lane, item,
+                                    [](int code) { record_error(code); });
       if (SPLIT && real) {
         // this CTA's key tiles
         const int use = item.n_tiles < kSplitTiles / 2 ? 1 : min(parts, item.n_tiles / 2);
@@ -743,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
       // sectors at once; the next columns are read meanwhile
       const float inv = 1.f / l;                              // a query sees its own key at least
       const bool fix = not_finite[it & 1] != 0;
-      __half* dst = p.out + (static_cast<size_t>(item.q_row + tid) * p.num_heads + item.head) * D;
+      __half* dst = p.out + (static_cast<size_t>(item.q_row + tid) * p.layout.num_heads + item.head) * D;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float x[32];
@@ -826,7 +737,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
         o_of[r] = map_to_rank(part_o + (rank * columns * BM + tid) * 4, r < parts ? r : 0);
       }
       const float inv = 1.f / L;
-      __half* dst = p.out + (static_cast<size_t>(items[0].q_row + tid) * p.num_heads + items[0].head) * D + rank * columns;
+      __half* dst = p.out + (static_cast<size_t>(items[0].q_row + tid) * p.layout.num_heads + items[0].head) * D + rank * columns;
 #pragma unroll 1
       for (int c = 0; c < columns; c += 8) {
         float v[kMostParts][8], o[8];
@@ -890,7 +801,7 @@ int launch(const PromptParams& p, long long tiles, int parts, cudaStream_t st) {
     }
   }
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "pkv_prompt_attention setup: %s", cudaGetErrorString(e));
-  const dim3 grid(static_cast<unsigned>(tiles * parts), p.num_heads);
+  const dim3 grid(static_cast<unsigned>(tiles * parts), p.layout.num_heads);
   e = SPLIT ? pkv::launch_pdl_cluster(prompt_attention_kernel<D, SPLIT>, grid, dim3(THREADS), C::SMEM, st, parts, p)
             : pkv::launch_pdl(prompt_attention_kernel<D, SPLIT>, grid, dim3(THREADS), C::SMEM, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
@@ -948,29 +859,25 @@ int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t*
   if (!std::isfinite(scale) || !(scale > 0.f))
     return pkv::fail(PKV_ERR_INVALID_ARG, "%s: scale must be finite and positive", fn);
   PromptParams p{};
-  p.max_tiles = (max_query_len - 1) / BM + 1;
-  // the query tiles of num_seqs sequences that have total_q queries together, at most
-  const long long by_total = total_q / BM + num_seqs, by_longest = static_cast<long long>(p.max_tiles) * num_seqs;
-  const long long tiles = by_total < by_longest ? by_total : by_longest, late = kLate / tiles + 1;
+  p.layout.qstart = query_start;
+  p.layout.kstart = key_start ? key_start : query_start;
+  p.layout.num_seqs = num_seqs;
+  p.layout.num_heads = num_heads;
+  p.layout.total_q = total_q;
+  p.layout.total_k = total_k;
+  const long long tiles = lay_out(p.layout, max_query_len);
   if (tiles * num_heads > INT_MAX)
     return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 query tiles over all heads", fn);
-  p.late = static_cast<int>(late < num_heads ? late : num_heads);
   int rc = encode_rows_map(&p.tmap_q, q, head_dim, num_heads, total_q, q_stride, BM);
   if (rc == PKV_OK) rc = encode_rows_map(&p.tmap_k, key, head_dim, num_kv_heads, total_k, key_stride, BN);
   if (rc == PKV_OK) rc = encode_rows_map(&p.tmap_v, value, head_dim, num_kv_heads, total_k, value_stride, BN);
   if (rc != PKV_OK) return rc;
   p.k = reinterpret_cast<const __half*>(key);
   p.v = reinterpret_cast<const __half*>(value);
-  p.qstart = query_start;
-  p.kstart = key_start ? key_start : query_start;
   p.out = reinterpret_cast<__half*>(out);
   p.k_stride = key_stride;
   p.v_stride = value_stride;
-  p.num_seqs = num_seqs;
-  p.num_heads = num_heads;
   p.group = num_heads / num_kv_heads;
-  p.total_q = total_q;
-  p.total_k = total_k;
   p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
