@@ -249,8 +249,9 @@ int pkv_paged_attention_decode_shared_prefix(const uint16_t* q, const uint16_t* 
  *                 out must not overlap the inputs
  *   query_start   device [num_seqs + 1] int32, non-decreasing, last = total_q
  *   max_query_len host: the largest n_s (sizes the grid).  A larger n_s records
- *                 PKV_DEV_BAD_QUERY_RANGE, and its rows past the grid are not
- *                 written.
+ *                 PKV_DEV_BAD_QUERY_RANGE, and its rows from max_query_len on,
+ *                 rounded up to 128, are not written.  0: nothing
+ *                 runs, and nothing is recorded.
  *   pools, tables, context_lens as for pkv_paged_attention_decode.
  * scale must be positive.  A sequence with n_s = 0 is skipped; n_s > ctx_s or
  * rows outside q record PKV_DEV_BAD_QUERY_RANGE; a table entry outside
@@ -518,8 +519,9 @@ int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, c
  *   query_start   device [num_seqs + 1] int32, non-decreasing
  *   key_start     device [num_seqs + 1] int32, non-decreasing, or NULL: query_start
  *   max_query_len host: the largest n_s (sizes the grid).  A larger n_s records
- *                 PKV_DEV_BAD_QUERY_RANGE, and its rows past the grid are not
- *                 written.
+ *                 PKV_DEV_BAD_QUERY_RANGE, and its rows from max_query_len on,
+ *                 rounded up to 128, are not written.  0: nothing
+ *                 runs, and nothing is recorded.
  *   out           device [total_q, num_heads, head_dim] fp16, contiguous, 16-byte
  *                 aligned; must not overlap the inputs
  * scale must be positive; at most 2^26 queries and 2^26 keys.  A sequence without

@@ -28,14 +28,16 @@ struct Layout {
   const int32_t* qstart;
   const int32_t* kstart;
   int num_seqs, num_heads;
+  int max_query_len;
   int max_tiles;                        // query tiles per sequence that max_query_len covers
   int late;                             // heads whose query tiles come last and by length
   int total_q, total_k;
 };
 
-// Sets max_tiles and late; returns the places per head that the grid needs: the query tiles of num_seqs
+// Sets what follows from max_query_len; returns the places per head that the grid needs: the query tiles of num_seqs
 // sequences that have total_q queries together and max_query_len at most each.
 inline long long lay_out(Layout& p, int max_query_len) {
+  p.max_query_len = max_query_len;
   p.max_tiles = (max_query_len - 1) / BM + 1;
   const long long by_total = p.total_q / BM + p.num_seqs, by_longest = static_cast<long long>(p.max_tiles) * p.num_seqs;
   const long long tiles = by_total < by_longest ? by_total : by_longest, late = kLate / tiles + 1;
@@ -85,7 +87,7 @@ struct ItemFinder {
           k0 = p.kstart[i];
           m = p.kstart[i + 1] - k0;
           const bool ok = n >= 0 && n <= m && q0 >= 0 && q0 <= p.total_q - n && k0 >= 0 && k0 <= p.total_k - m;
-          if (!ok || n > p.max_tiles * static_cast<int64_t>(BM)) report(PKV_DEV_BAD_QUERY_RANGE);
+          if (!ok || n > p.max_query_len) report(PKV_DEV_BAD_QUERY_RANGE);
           tiles = ok ? min((n + BM - 1) / BM, p.max_tiles) : 0;
           if (tiles > 0) own = (m - n + min(n, tiles * BM) - 1) / BN + 1;
         }

@@ -299,3 +299,15 @@ def test_two_streams_at_once(cuda_device):
     torch.cuda.synchronize()
     assert pkv.device_error() == 0
     assert all(torch.equal(g, a) for pair in got for g, a in zip(pair, alone))
+
+
+def test_more_queries_than_announced_are_recorded(cuda_device):
+    # within the first tile and past it; only rows past the announced length's tiles are not written
+    for n, announced, written in ((100, 10, 100), (128, 127, 128), (300, 200, 256)):
+        q, k, v, qs, _ = (torch.from_numpy(x).to(cuda_device) for x in make(44 + n, [n], 0, 2, 1, 64))
+        want = pkv.prompt_attention(q, k, v, qs, 0.1, n)
+        assert pkv.device_error() == 0
+        out = torch.full_like(q, 3.0)
+        pkv.prompt_attention(q, k, v, qs, 0.1, announced, out=out)
+        assert pkv.device_error() == 6
+        assert torch.equal(out[:written], want[:written]) and (out[written:] == 3).all()

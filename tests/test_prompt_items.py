@@ -109,3 +109,10 @@ def test_bad_ranges_are_reported(program):
     assert codes > 0 and sorted(x[2] for x in items) == [0, 400]
     _, items, codes = run(program, 1, 300, [0, 100, 400], [0, 100, 400], [[0, 1, 2, 3, 4]], total_k=399)
     assert codes > 0 and [x[2] for x in items] == [0]
+
+
+@pytest.mark.parametrize("max_len", [10, 59, 99, 100])
+def test_more_queries_than_announced_are_reported(program, max_len):
+    qs = starts([100, 60, 5])
+    _, items, codes = run(program, 1, max_len, qs, qs, [[0, 1, 2, 3]])
+    assert (codes > 0) == (max_len < 100) and sorted(x[3] for x in items) == [5, 60, 100]
