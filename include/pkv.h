@@ -482,8 +482,9 @@ int pkv_swap_blocks_int4(const uint8_t* const* src_k_caches, const uint8_t* cons
  * with k_t, v_t what the pools' rows of head h / (num_heads / num_kv_heads) stand
  * for.  num_heads is a multiple of num_kv_heads.  q (device [num_seqs, num_heads,
  * head_dim] fp16), tables, lengths, out, errors and the meaning of a zero length
- * are as for pkv_paged_attention_decode, except that q, tables, lengths and out
- * must be device memory, and that the workspace is always needed: at least
+ * are as for pkv_paged_attention_decode (a table entry outside the pool records
+ * PKV_DEV_BAD_BLOCK_ID and its tokens get no weight), except that q, tables, lengths
+ * and out must be device memory, and that the workspace is always needed: at least
  * pkv_paged_attention_int4_workspace_size(...) bytes, asked for with the device
  * current.  Calls that may run at the same time need workspaces of their own.
  * Products of q and the cached whole numbers are exact, sums are fp32; the softmax

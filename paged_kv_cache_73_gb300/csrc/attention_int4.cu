@@ -81,6 +81,7 @@ constexpr int kMinChunks = 4;         // chunks a worker takes at least
 // elsewhere one warp does: 8 sequences of 512 tokens, 40 heads, 16.5 us against 22.6, one of 128 9.4 against 10.5.
 constexpr int kFewHeads = 256, kManyParts = 32;
 constexpr float kRescale = 8.f;       // the running maximum moves when a chunk passes it by this much
+constexpr float kLowest = -3.4028235e38f;  // its start: finite, so that a chunk without a live row gives weights of 0
 
 struct Int4Params {
   const __half* q;
@@ -207,9 +208,10 @@ struct WarpState {
   float ones[NT][4];                    // sum u' over the last chunk
 };
 
-// One chunk of `valid` tokens (32 or more: all) staged at `stage`.
+// One chunk staged at `stage`.  live: the rows that count; the others (past the context, or of a block outside the
+// pool) get no weight, whatever is there.
 template <int D, int NT, bool SOLO>
-__device__ __forceinline__ void chunk_update(const unsigned char* stage, int valid, const unsigned (&qf)[NT][D / 16][2],
+__device__ __forceinline__ void chunk_update(const unsigned char* stage, unsigned live, const unsigned (&qf)[NT][D / 16][2],
                                              const float (&ca)[NT][2], const float (&cb)[NT][2], WarpState<D, NT>& st,
                                              int g, int t, uint32_t v_row) {
   using R = Ring<D>;
@@ -248,7 +250,7 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
     const float2 km = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + row * 4));
     float2 vm = __half22float2(*reinterpret_cast<const __half2*>(stage + R::META_OFF + CHUNK * 4 + row * 4));
     float x = fmaf(km.x, ca[0][0] * d, km.y * cb[0][0]);
-    if (row >= valid) {                 // past the context: no weight, whatever is there
+    if (!(live >> row & 1)) {
       vm = make_float2(0.f, 0.f);
       x = -INFINITY;
     }
@@ -256,7 +258,7 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
     if (__any_sync(FULL, top > st.m[0][0] + kRescale)) {
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-      const float m = fmaxf(st.m[0][0], top), f = m == -INFINITY ? 1.f : exp2f(st.m[0][0] - m);
+      const float m = fmaxf(st.m[0][0], top), f = exp2f(st.m[0][0] - m);
       st.m[0][0] = m;
       st.l[0][0] *= f;
       st.c[0][0] *= f;
@@ -302,12 +304,12 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
             x[n][i][2 * r + j] = fmaf(km.x, ca[n][j] * dot[i][n][2 * r + j], km.y * cb[n][j]);
       }
     }
-    if (valid < CHUNK) {                  // rows past the context: no weight, whatever is there
+    if (const unsigned mine = live >> g; live != FULL) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          if (16 * i + g + 8 * r >= valid) {
+          if (!(mine >> (16 * i + 8 * r) & 1)) {
             vm[i][r] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int n = 0; n < NT; ++n) x[n][i][2 * r] = x[n][i][2 * r + 1] = -INFINITY;
@@ -337,7 +339,7 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
 #pragma unroll
           for (int o = 4; o < 32; o *= 2) top[n][j] = fmaxf(top[n][j], __shfl_xor_sync(FULL, top[n][j], o));
           const float m = fmaxf(st.m[n][j], top[n][j]);
-          const float f = m == -INFINITY ? 1.f : exp2f(st.m[n][j] - m);
+          const float f = exp2f(st.m[n][j] - m);
           st.m[n][j] = m;
           st.l[n][j] *= f;
           st.c[n][j] *= f;
@@ -359,8 +361,7 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, int val
           float u[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            // the chunk has a valid token, so the maximum is not -inf (a NaN logit makes NaNs)
-            const float w = fast_exp2(x[n][i][2 * r + j] - st.m[n][j]);
+            const float w = fast_exp2(x[n][i][2 * r + j] - st.m[n][j]);    // a NaN logit makes NaNs
             st.l[n][j] += w;
             u[j] = w * vm[i][r].x;
             st.c[n][j] = fmaf(w, vm[i][r].y, st.c[n][j]);
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
   const int meta_row = 4 * (lane & 7);
   Place ahead = at;
   int to_fill = left;
-  // table entries of 32 blocks around `ahead`, one a lane, and of the next 32; -1 past the context or bad
+  // table entries of 32 blocks around `ahead`, one a lane, and of the next 32; -1 past the context, -2 bad
   int entry = -1, entry_next = -1;
   auto read_entry = [&](int first) {
     const int j = first + lane;
@@ -506,8 +507,9 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
     const int phys = p.tables[static_cast<size_t>(ahead.s) * p.max_blocks + j];
     if (phys >= 0 && phys < p.num_blocks) return phys;
     record_error(PKV_DEV_BAD_BLOCK_ID);
-    return -1;
+    return -2;
   };
+  unsigned gone = 0;                                         // per stage eight bits: its chunk's bad blocks
   bool fresh = true;                                         // `ahead` is at a stream's first chunk here
   int head_off = 0;                                          // of `ahead`'s cached head in a block
   const uint8_t* meta_src = (lane & 8 ? p.v : p.k) + ROW * B + (meta_row % B) * 4;
@@ -529,6 +531,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
         entry = entry_next;
         entry_next = read_entry(first + 32);
       }
+      gone = (gone & ~(0xffu << 8 * stage)) | (__ballot_sync(FULL, entry == -2) >> (blk & 31) & ((1u << BPC) - 1)) << 8 * stage;
       const int valid = ahead.len - ahead.c * CHUNK;
       const uint32_t dst = ring_u32 + stage * R::STAGE;
       // pieces of one block (or of one pair of blocks, a half of the lanes each) share an address
@@ -537,7 +540,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
       for (int i0 = 0; i0 < PIECES; i0 += PPB) {
         const int row0 = RPP * i0 + piece_row;
         const int phys = __shfl_sync(FULL, entry, (blk & 31) + row0 / B);
-        const int bytes = phys >= 0 ? 16 : 0;                // a bad block's rows are zeros
+        const int bytes = phys >= 0 ? 16 : 0;                // nothing of a bad block is read
         const int64_t off = static_cast<int64_t>(max(phys, 0)) * block_bytes + (head_off + (row0 % B) * ROW + piece_col);
         const uint8_t* ks = p.k + off;
         const uint8_t* vs = p.v + off;
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
       for (int j = 0; j < 2; ++j) {
         ca[n][j] = __shfl_sync(FULL, a, SOLO ? 0 : (2 * t + j) * 4);
         cb[n][j] = __shfl_sync(FULL, b, SOLO ? 0 : (2 * t + j) * 4);
-        st.m[n][j] = -INFINITY;
+        st.m[n][j] = kLowest;
         st.l[n][j] = st.c[n][j] = 0.f;
         st.ones[n][j] = st.ones[n][2 + j] = 0.f;
       }
@@ -655,7 +658,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
           o[2 * i + 1] = fmaf(st.acc[n][i][2 + j] - (i & 1 ? st.acc[n][i][j] : 0.f), 1048576.f, mid);
         }
         if (whole) {
-          const float inv = 1.f / st.l[n][j];
+          const float inv = st.l[n][j] == 0.f ? 0.f : 1.f / st.l[n][j];   // 0: every block is bad
           __half* dst = p.out + (static_cast<size_t>(at.s) * H + h0 + h) * D + g * 4;
 #pragma unroll
           for (int i = 0; i < D / 8; i += 4)
@@ -683,7 +686,10 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
     fill(stage == 0 ? R::NST - 1 : stage - 1);
     const unsigned char* src = ring + stage * R::STAGE;
     const int valid = at.len - at.c * CHUNK;
-    chunk_update<D, NT, SOLO>(src, valid, qf, ca, cb, st, g, t, v_row + stage * R::STAGE);
+    // the rows before the context's end, of blocks that are in the pool
+    unsigned live = valid < CHUNK ? (1u << valid) - 1 : FULL;
+    for (unsigned bad = gone >> 8 * stage & 0xffu; bad; bad &= bad - 1) live &= ~((FULL >> (32 - B)) << (__ffs(bad) - 1) * B);
+    chunk_update<D, NT, SOLO>(src, live, qf, ca, cb, st, g, t, v_row + stage * R::STAGE);
     if (++stage == R::NST) stage = 0;
     const bool to_end = at.c + 1 == at.chunks;
     if (to_end || left == 1) {

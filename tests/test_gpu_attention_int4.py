@@ -282,3 +282,30 @@ def test_error_does_not_grow_with_the_context(cuda_device, H, Hk):
 def test_streams_cut_into_many_parts(cuda_device, lens, H, Hk, D, B):
     # a stream over a thousand warps; beside empty and short ones; many heads on one
     check(make(34, lens, H, Hk, D, B, cuda_device), B, cuda_device)
+
+
+@pytest.mark.parametrize("H,Hk", [(2, 2), (6, 2), (12, 1), (40, 2)])
+@pytest.mark.parametrize("D,B", [(64, 4), (128, 8), (128, 16), (64, 32)])
+def test_bad_blocks_have_no_weight(cuda_device, H, Hk, D, B):
+    # scattered bad blocks, whole chunks of them, the first, the last, every one of a sequence; one short
+    # sequence without any and a long one that many warps share
+    rng = np.random.default_rng(D + B + H)
+    case = make(D + B + H, [300, 70, 5, 33, 4000, 31], H, Hk, D, B, cuda_device)
+    q, kc, vc, tables, lens = case
+    blocks = [-(-int(n) // B) for n in lens]
+    bad = [rng.random(b) < 0.2 for b in blocks]
+    bad[0][0] = bad[1][-1] = True
+    bad[2][:] = False
+    bad[3][:] = True
+    bad[4][500 // B:3000 // B] = True
+    broken, kept, left = tables.copy(), np.full_like(tables, -1), []
+    for s, b in enumerate(bad):
+        broken[s, :blocks[s]][b] = rng.choice([-1, -7, kc.shape[0], 2 ** 31 - 1], b.sum())
+        good = tables[s, :blocks[s]][~b]
+        kept[s, :len(good)] = good
+        left.append(int(lens[s]) - B * int(b.sum()) + (b[-1] and B * blocks[s] - int(lens[s])))
+    fair = (q, kc, vc, kept, np.array(left, np.int32))
+    want = o4.paged_decode_attention(*fair, 0.2, B)
+    got = run((q, kc, vc, broken, lens), 0.2, B, cuda_device).cpu().numpy().astype(np.float64)
+    assert pkv.device_error() == 1 and pkv.device_error() == 0
+    assert (np.abs(got - want) <= tolerance(fair, want, 0.2, B)).all() and not got[3].any()
