@@ -102,8 +102,11 @@ struct Int4Params {
 // stream is one sequence's cached head (and tile of its query heads); worker w takes chunks
 // [w per, (w + 1) per) of the line.  Slot w + stream is unique to that pair: along the line one of the
 // two grows at every cut.
+// AHEAD: read before the caller's wait for the kernels before it, and so from L2, where those that are done
+// have left them.
+template <bool AHEAD>
 __device__ __forceinline__ int chunks_of(const Int4Params& p, int s) {
-  const int len = s < p.num_seqs ? p.lens[s] : 0;
+  const int len = s >= p.num_seqs ? 0 : AHEAD ? __ldcg(p.lens + s) : p.lens[s];
   return len <= 0 || len > (p.max_blocks << p.log2_block) ? 0 : (len + CHUNK - 1) / CHUNK;
 }
 __device__ __forceinline__ long long per_worker(long long total, int workers) {
@@ -424,8 +427,9 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
   constexpr int BPC = CHUNK / B;                             // blocks per chunk
   extern __shared__ __align__(128) unsigned char smem[];     // the workers' rings
 
-  // the joining kernel may start once all of this grid has come here: it reads the lengths before it
-  // waits for this grid, so they have to be there
+  // Every thread waits before it triggers, unlike in the other kernels: the joining kernel, launched next, may
+  // start once all of this grid has triggered, and reads the lengths before it waits for this grid.  The
+  // kernels before this one are done by then, so the lengths are there.
   pkv::pdl_wait();
   pkv::pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
     long long total = 0;
     bool bad = false;
     for (int s = lane; s < S; s += 32) {
-      total += chunks_of(p, s);
+      total += chunks_of<false>(p, s);
       bad |= p.lens[s] < 0 || p.lens[s] > (p.max_blocks << LB);
     }
 #pragma unroll
@@ -452,7 +456,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
     long long before = 0;
     int s = S, mine = 0;
     for (int base = 0; base < S; base += 32) {
-      mine = chunks_of(p, base + lane);
+      mine = chunks_of<false>(p, base + lane);
       long long upto = mine;                                 // inclusive prefix sum over the lanes
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
     x.c = 0;
     if (++x.y == Y) {
       x.y = 0;
-      do ++x.s, x.chunks = chunks_of(p, x.s);
+      do ++x.s, x.chunks = chunks_of<false>(p, x.s);
       while (x.chunks == 0 && x.s < S);
       x.len = x.s < S ? p.lens[x.s] : 0;
     }
@@ -708,7 +712,9 @@ __global__ void __launch_bounds__(NW * 32, 1) paged_attention_int4_kernel(const 
 
 // Joins the parts of every cut stream, and writes the zeros of empty contexts: WPH warps per (sequence,
 // head), a lane D/32 values.  Where there are few heads in all, each may have been cut into a thousand
-// parts, and sixteen warps share them.
+// parts, and sixteen warps share them.  The lengths are read before the wait: this kernel's launch has to
+// follow that of paged_attention_int4_kernel, whose every thread waits for the kernels before it and then
+// triggers; no other kernel may come between the two.
 template <int D, int WPH>
 __global__ void __launch_bounds__(WPH == 1 ? 128 : WPH * 32) paged_attention_int4_merge_kernel(const Int4Params p, int head_rows) {
   constexpr int WARPS = WPH == 1 ? 4 : WPH, FLY = 8;         // warps of a CTA; parts in flight to a warp
@@ -718,7 +724,7 @@ __global__ void __launch_bounds__(WPH == 1 ? 128 : WPH * 32) paged_attention_int
   // chunks of the sequences before s, and of all
   long long mine[2] = {0, 0};
   for (int i = threadIdx.x; i < p.num_seqs; i += WARPS * 32) {
-    const int c = chunks_of(p, i);
+    const int c = chunks_of<true>(p, i);
     mine[1] += c;
     if (i < s) mine[0] += c;
   }
@@ -742,7 +748,7 @@ __global__ void __launch_bounds__(WPH == 1 ? 128 : WPH * 32) paged_attention_int
   }
   constexpr int V = D / 32;
   __half* dst = p.out + (static_cast<size_t>(s) * p.num_heads + h) * D + lane * V;
-  const int chunks = chunks_of(p, s);
+  const int chunks = chunks_of<true>(p, s);
   const int Y = p.num_kv_heads * p.head_tiles, tile = h % p.group / head_rows;
   const int y = h / p.group * p.head_tiles + tile, row = h % p.group - tile * head_rows;
   const long long first = before * Y + static_cast<long long>(y) * chunks;

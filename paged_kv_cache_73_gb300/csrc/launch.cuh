@@ -5,6 +5,9 @@
 // griddepcontrol.wait before it reads any input (which waits for the previous
 // grid to complete and its writes to be visible) and griddepcontrol.launch_dependents
 // at its start, so the next kernel's launch overlaps this one's tail.
+//
+// The exception is the four-bit decode's pair of kernels: the joining one reads the context
+// lengths before its wait, and so the one before it triggers only after its own.
 #pragma once
 
 #include <cuda_runtime.h>
