@@ -70,6 +70,9 @@ __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_
 // joining cost more than they save: 1024 tokens over themselves, 8 heads, 17.2 -> 18.7 us.
 constexpr int kResident = 304, kSplitTiles = 12, kMostParts = 8;
 constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
+// Weights are kept as 2^(kLift + S - m): the largest in fp16's upper half, at most 2^15, so that those that
+// fall below its smallest number are 2^-32 of the largest, not 2^-25.
+constexpr float kLift = 7.f;
 
 struct PromptParams {
   CUtensorMap tmap_q, tmap_k, tmap_v;   // (D, heads, tokens), boxes of 64 x 1 x 128 (q) or 64, 128-byte swizzle
@@ -188,7 +191,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
 
 // Warp roles:
 //   0-3      softmax: waits S(j), releases K slot, masks, takes the row maximum (moving the running
-//            one, and O, only past 2^8), writes P = 2^(S - m) as fp16 over the scores and arrives on
+//            one, and O, only past 2^8), writes P = 2^(7 + S - m) as fp16 over the scores and arrives on
 //            p_full; after an item's last tile, its output (with SPLIT the part of it for the cluster)
 //   W_S      one lane issues S(j) = Q K(j)^T once K(j) landed and PV(j - 2), the last reader of its
 //            buffer, is done
@@ -610,7 +613,7 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
           alpha = exp2f(m_ref - mx);
           m_ref = mx;
         }
-        const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
+        const float nref = m_ref == -INFINITY ? 0.f : kLift - m_ref;
         if (__any_sync(0xffffffffu, rescale && i > 0)) {
           if (!warp_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1)) {
             failed = true;

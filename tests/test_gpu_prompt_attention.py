@@ -311,3 +311,28 @@ def test_more_queries_than_announced_are_recorded(cuda_device):
         pkv.prompt_attention(q, k, v, qs, 0.1, announced, out=out)
         assert pkv.device_error() == 6
         assert torch.equal(out[:written], want[:written]) and (out[written:] == 3).all()
+
+
+@pytest.mark.parametrize("D,H,Hk,news,past", [(64, 2, 1, [1, 70], 9000), (128, 24, 24, [300], 2000)])
+def test_many_small_weights_beside_a_large_one(cuda_device, D, H, Hk, news, past):
+    # Each sequence's first key takes nearly all the weight and has a value of 0: the result is what thousands
+    # of weights of about 2^-27 of that key's add up to.  As want_and_tol, but a weight's fp16 rounding
+    # below the normals is 2^-32 of the largest weight, and of these weights' sum no more than that is lost.
+    q, k, v, qs, ks = make(45 + D, news, past, H, Hk, D)
+    k *= np.float16(0.05)
+    v[:] = np.abs(v)
+    q[..., 0], k[..., 0] = 4, 0
+    scale = D ** -0.5
+    k[ks[:-1], :, 0], k[ks[:-1], :, 1:], v[ks[:-1]] = 27 * np.log(2) / (4 * scale), 0, 0
+    got = run((q, k, v, qs, ks), scale, cuda_device).cpu().numpy().astype(np.float64)
+    assert pkv.device_error() == 0
+    want = o4.prompt_attention(q, k, v, qs, ks, scale)
+    for s in range(len(news)):
+        rows, keys = slice(qs[s], qs[s + 1]), slice(ks[s], ks[s + 1])
+        m = ks[s + 1] - ks[s]
+        dx = 2.0 ** -21 * (scale * np.abs(q[rows].astype(np.float64)).sum(-1).max() * np.abs(k[keys]).max()) + 2.0 ** -21
+        o = np.abs(want[rows])
+        tol = 2.0 ** -11 * 3 * o + 2.0 ** -25 + 2 * dx * o + m * 2.0 ** -32 * v[keys].max()
+        assert (tol < 0.25 * o).mean() > 0.9                 # the sums are not lost in the tolerance
+        err = np.abs(got[rows] - want[rows])
+        assert (err <= tol).all(), float((err / tol).max())
