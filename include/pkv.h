@@ -248,10 +248,9 @@ int pkv_paged_attention_decode_shared_prefix(const uint16_t* q, const uint16_t* 
  *   q, out        device [total_q, num_heads, head_dim] fp16, 16-byte aligned;
  *                 out must not overlap the inputs
  *   query_start   device [num_seqs + 1] int32, non-decreasing, last = total_q
- *   max_query_len host: the largest n_s (sizes the grid).  A larger n_s records
- *                 PKV_DEV_BAD_QUERY_RANGE, and its rows from max_query_len on,
- *                 rounded up to 128, are not written.  0: nothing
- *                 runs, and nothing is recorded.
+ *   max_query_len host: the largest n_s (sizes the grid).  An n_s above the next
+ *                 multiple of 256 records PKV_DEV_BAD_QUERY_RANGE, and its rows
+ *                 from there on are not written.
  *   pools, tables, context_lens as for pkv_paged_attention_decode.
  * scale must be positive.  A sequence with n_s = 0 is skipped; n_s > ctx_s or
  * rows outside q record PKV_DEV_BAD_QUERY_RANGE; a table entry outside
@@ -519,25 +518,25 @@ int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, c
  *                 8 and at least a token's length)
  *   query_start   device [num_seqs + 1] int32, non-decreasing
  *   key_start     device [num_seqs + 1] int32, non-decreasing, or NULL: query_start
- *   max_query_len host: the largest n_s (sizes the grid).  A larger n_s records
- *                 PKV_DEV_BAD_QUERY_RANGE, and its rows from max_query_len on,
- *                 rounded up to 128, are not written.  0: nothing
- *                 runs, and nothing is recorded.
+ *   max_query_len host: the largest n_s (sizes the grid; with 0 nothing runs).  A
+ *                 larger n_s records PKV_DEV_BAD_QUERY_RANGE, and its rows past
+ *                 the next multiple of 128 are not written.
  *   out           device [total_q, num_heads, head_dim] fp16, contiguous, 16-byte
  *                 aligned; must not overlap the inputs
- * scale must be positive; at most 2^26 queries and 2^26 keys.  A sequence without
- * queries is skipped; n_s > m_s or
+ * scale must be positive (row maxima are taken before it is applied); at most 2^26
+ * queries and 2^26 keys.  A sequence without queries is skipped; n_s > m_s or
  * rows outside q or key record PKV_DEV_BAD_QUERY_RANGE and the sequence's rows are
  * not written.  Rows of out in no sequence are left as they were.  Keys and values
  * that a query does not see (after it, or after its sequence's end) do not reach its
  * row, whatever they hold.
  * Tensor cores: fp16 products, fp32 sums; the softmax weights are rounded to fp16
  * before they multiply V, and to 0 below 2^-32 of the row's largest (an infinite
- * value with such a weight makes a NaN).  The tensor cores cut their sums off at the last bit: a
- * row over n keys loses up to n 2^-27 of itself to that, as much as the output's
- * own rounding from 2^16 keys on.  Few queries over many keys are shared out to
- * clusters of blocks, by num_seqs, total_q, total_k and max_query_len, so rows may
- * differ in their last bits between calls with other buffers around them.  No
+ * value with such a weight makes a NaN).  The tensor cores cut their sums off at
+ * the last bit: a row over n keys loses up to n 2^-27 of itself to that, as much as
+ * the output's own rounding from 2^16 keys on.  Few queries over many keys are
+ * shared out to clusters of blocks, by num_seqs, total_q, total_k and
+ * max_query_len, so rows may differ in their last bits between calls with other
+ * buffers around them.  No
  * workspace.
  * ------------------------------------------------------------------------- */
 int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t* value, const int32_t* query_start,
