@@ -76,10 +76,9 @@ constexpr float kLift = 7.f;
 
 struct PromptParams {
   CUtensorMap tmap_q, tmap_k, tmap_v;   // (D, heads, tokens), boxes of 64 x 1 x 128 (q) or 64, 128-byte swizzle
-  const __half* k;
   const __half* v;
   __half* out;
-  int64_t k_stride, v_stride;
+  int64_t v_stride;
   Layout layout;
   int group;
   int out_sectors;                      // out is 32-byte aligned
@@ -875,10 +874,8 @@ int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t*
   if (rc == PKV_OK) rc = encode_rows_map(&p.tmap_k, key, head_dim, num_kv_heads, total_k, key_stride, BN);
   if (rc == PKV_OK) rc = encode_rows_map(&p.tmap_v, value, head_dim, num_kv_heads, total_k, value_stride, BN);
   if (rc != PKV_OK) return rc;
-  p.k = reinterpret_cast<const __half*>(key);
   p.v = reinterpret_cast<const __half*>(value);
   p.out = reinterpret_cast<__half*>(out);
-  p.k_stride = key_stride;
   p.v_stride = value_stride;
   p.group = num_heads / num_kv_heads;
   p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;

@@ -184,7 +184,6 @@ __device__ __forceinline__ void fma2(float& y0, float& y1, float x0, float x1, f
       : "=f"(y0), "=f"(y1)
       : "f"(x0), "f"(x1), "f"(s), "f"(c));
 }
-// (a0, a1) += (x0, x1)
 // a0 += the low fp16 of `packed`, a1 += the high one (mixed-precision adds: the sum is taken over
 // exactly the rounded values that go to the tensor cores)
 __device__ __forceinline__ void add_half2(float& a0, float& a1, uint32_t packed) {
