@@ -48,20 +48,18 @@ struct Int4RowParams {
   int rows_per_warp;
 };
 
-// n of one value by the definition, from the estimate n0 (off by at most one): n s against x - lo, halves to
-// even.  n s is exact in fp32 (4 + 11 bits).  x - lo can take 40 bits: d is its rounding to fp32 and rest, by
-// a two-sum, exactly what that left.  Next to a border r = d - n s is exact too.  d is below 16 s (below
-// 22 s where s is below the normals, and exact there), so its last place is 2^-19 of s's leading bit at most:
-// 2 r and s are multiples of twice d's last place, 2 rest is at most one, and rest decides where 2 r meets s.
+// n of one value by the definition: n s against x - lo, halves to even.  n s is exact in fp32 (4 + 11 bits).  x - lo
+// can take 40 bits: d is its rounding to fp32 and rest, by a two-sum, exactly what that left.  The estimate
+// d inv is 2^-17 off at most, so a little less than it rounds to n or, at and just past a half, to n - 1: only
+// whether 2 (x - lo - n s) reaches s is left to see.  There r = d - n s is exact too, and d is below 16 s (below 22 s
+// where s is below the normals, and exact there), so its last place is 2^-19 of s's leading bit at most:
+// 2 r and s are multiples of twice d's last place, 2 rest is at most one, and decides where 2 r meets s.
 __device__ __forceinline__ unsigned nearest_exact(float x, float lo, float s, float inv) {
   const float d = x - lo, back = d - x, rest = (x - (d - back)) - (lo + back);
-  float n = fminf(fmaxf(rintf(d * inv), 0.f), 15.f);
-  const float r2 = 2.f * fmaf(-n, s, d);
-  const bool odd = (static_cast<int>(n) & 1) != 0;
-  const bool up = r2 > s || (r2 == s && (rest > 0.f || (rest == 0.f && odd)));
-  const bool down = r2 < -s || (r2 == -s && (rest < 0.f || (rest == 0.f && odd)));
-  n += up ? 1.f : down ? -1.f : 0.f;
-  return static_cast<unsigned>(fminf(fmaxf(n, 0.f), 15.f));
+  const float n = fminf(fmaxf(rintf(fmaf(d, inv, -0x1p-10f)), 0.f), 15.f);
+  const float over = fmaf(2.f, rest, 2.f * fmaf(-n, s, d) - s);
+  const unsigned whole = static_cast<unsigned>(n);
+  return min(whole + (over > 0.f || (over == 0.f && (whole & 1u)) ? 1u : 0u), 15u);
 }
 
 // two fp32 sums or fused products in one instruction
