@@ -25,7 +25,7 @@
 // V's rows as 16-bit elements: a lane gets tokens 2t, 2t + 1 of one element, that is of four
 // values, in the two halves of a register.  Of the low bytes both half bytes are masked out; of the
 // high bytes the low half is, and the whole byte enters as n + 16 n', whose n comes off in the
-// end (byte permutes of row words and four masks: 130 us for long grouped contexts, now 122).
+// end (byte permutes of row words and four masks took long grouped contexts 7 us more).
 // P^T comes from S^T's accumulator by an 8x8 transpose in registers (movmatrix).
 //
 // Where each cached head has one query head, the products' other seven columns are idle, and
@@ -52,11 +52,15 @@
 // stream is cut, its workers leave partial results that a second kernel joins by the
 // log-sum-exp identity.
 //
-// Measured (D = 128): 64 sequences of 128 to 2048 tokens, 40 heads, 72 us = 5.3 TB/s of cached
-// rows; 32 sequences of 8192 to 32768, 64 heads on 8, 120 us = 6.1 TB/s.  Copies alone take 94 and
-// 96 % of that; one sequence of 2048 tokens, 40 heads, 12.6 us, of which 9
-// are there at 128 tokens too.  Small blocks cost: 64 sequences of 1088 tokens take 69 us with
-// blocks of 32 tokens, 74 with 16 and 83 with 8 (tiles of 2176, 1088 and 544 bytes).
+// Measured (D = 128): 64 sequences of 128 to 2048 tokens, 40 heads, 71 us = 5.3 TB/s of cached
+// rows; 32 sequences of 8192 to 32768, 64 heads on 8, 118 us = 6.2 TB/s.  Copies alone take 94 and
+// 96 % of that; one sequence of 2048 tokens, 40 heads, 10.8 us in a row of such calls, of which 7
+// are there at 128 tokens too.  Small blocks cost: 64 sequences of 1088 tokens take 65 us with
+// blocks of 32 tokens, 69 with 16 and 78 with 8 (tiles of 2176, 1088 and 544 bytes).
+// Groups of 9 to 16 are held by issue, not by the copies: a chunk takes 1.8 times as long as with
+// 8 heads (twice the columns, and 108 to 132 bytes of spills at 168 registers), 32 sequences as above with
+// 64 heads on 4 105 us of 54 for their bytes.  Above 16 every 16 heads walk the rows again: 32 heads on
+// one 62 us, 48 on one 84, of 13.5.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -77,7 +81,7 @@ constexpr int NW = 12;                // warps on an SM, in one CTA; a small gri
 constexpr int CHUNK = 32;             // tokens a worker handles at a time
 constexpr int kMinChunks = 4;         // chunks a worker takes at least
 // Sixteen warps join a head's parts where there are at most kFewHeads heads in all and equal streams would be
-// cut into more than kManyParts: one sequence of 131072 tokens, 8 heads on 1, 87 -> 25 us, 32 on 8, 55 -> 36;
+// cut into more than kManyParts: one sequence of 131072 tokens, 8 heads on 1, 87 -> 21 us, 32 on 8, 55 -> 32;
 // elsewhere one warp does: 8 sequences of 512 tokens, 40 heads, 16.5 us against 22.6, one of 128 9.4 against 10.5.
 constexpr int kFewHeads = 256, kManyParts = 32;
 constexpr float kRescale = 8.f;       // the running maximum moves when a chunk passes it by this much
@@ -375,7 +379,7 @@ __device__ __forceinline__ void chunk_update(const unsigned char* stage, unsigne
   // The last chunk's sum u' n becomes sum u' (n - 8), late, when its products have long arrived.  Left in, the
   // 8 sum u' grew with the context while the result shrinks, and the tensor cores' sums, cut off at the
   // accumulator's last bit, cost 5.8e-4 of the result at 20 000 tokens where now 3.0e-4 are lost at any
-  // length (2.1e-4 by the output's own rounding): 127 -> 130 us for long grouped contexts.
+  // length (2.1e-4 by the output's own rounding), for 3 us of long grouped contexts' 118.
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const float2 even = make_float2(st.ones[n][0] * -0x1p-21f, st.ones[n][1] * -0x1p-21f);
@@ -866,7 +870,7 @@ int device_sms() {
 // Head tiles of 8 columns, or of 16 where a group has more than 8 heads (the rows are then unpacked
 // once for both).  One CTA of twelve warps to an SM, or, where even the longest contexts would not give
 // each of those kMinChunks chunks, as many CTAs of four warps as that takes (smaller CTAs start sooner:
-// 14.4 against 16.3 us for one sequence of 2048 tokens and 40 heads).
+// 1.9 us less for one sequence of 2048 tokens and 40 heads).
 struct Plan {
   int nt, head_tiles, head_rows, ctas, warps;
   long long slots, most_chunks;

@@ -10,8 +10,8 @@
 // runs at 98 % of the copy rate (160k tokens of 8 + 8 rows of 128: 124 us).
 //
 // The write has about 9 values to handle per clock and SM at HBM rate, so it counts
-// instructions: 32 values to a lane, which halves what a row costs beside its values (150 ->
-// 143 us for the write and read-back of 16 411 tokens of 2 x 40 rows of 128); minimum and
+// instructions: 32 values to a lane, which halves what a row costs beside its values (7 us of the
+// 139 that write and read-back of 16 411 tokens of 2 x 40 rows of 128 take); minimum and
 // maximum on packed fp16 pairs; the quotients two to an instruction.  u = x / s - lo / s is
 // rounded by adding and taking off 1.5 * 2^23, whose low bytes are then gathered; only where
 // u comes nearer to a half than its error bound (some 2^-16 of all values) is n decided by

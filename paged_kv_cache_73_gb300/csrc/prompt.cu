@@ -14,8 +14,8 @@
 // a tensor-memory lane.
 //  * One CTA takes 128 queries of one head, with a half of the tensor memory and of the
 //    shared memory, so two run on an SM: each hides the other's start, end and hand-offs.
-//    One CTA with two query tiles that share every K/V tile took 1187 us against 1074 for
-//    eight 4096-token prompts (40 heads on 8), and 126 against 101 for ragged short ones,
+//    One CTA with two query tiles that share every K/V tile took 1242 us against 1122 for
+//    eight 4096-token prompts (40 heads on 8), and 126 against 98 for ragged short ones,
 //    where starts and ends are most of the time.
 //  * Key tiles of 64 positions come by TMA through a ring.  Where some row of the CTA does
 //    not see a tile whole (the diagonal, and the tile that holds the sequence's end), a
@@ -42,9 +42,9 @@
 // (an SS product of 128 x 64 x 16 reads 6 KB), PV by math; both with the loads come to about 750
 // clocks of shared-memory traffic as counted, and 685 a tile are measured on long prompts.  Two S
 // buffers keep S(j + 1) running under the softmax of tile j (about 1000 clocks).
-// Measured: eight 4096-token prompts, 40 heads on 8, 1090 us (1.26 PFLOP/s); 32 prompts of 1 to 512
+// Measured: eight 4096-token prompts, 40 heads on 8, 1100 us (1.25 PFLOP/s); 32 prompts of 1 to 512
 // tokens, 40 heads, 71 us (4.7 TB/s of q, K, V and out); 16 chunks of 32 to 512 tokens over 1024
-// cached ones, 32 heads on 8, D = 64, 64 us.
+// cached ones, 32 heads on 8, D = 64, 63 us.
 #include <climits>
 #include <cmath>
 #include <cstdint>

@@ -21,8 +21,9 @@
 //    values, R/2 further on (or interleaved with them).  No shuffle is needed to turn
 //    them, and weights times sines are formed once per token, so a pair takes four fused
 //    operations (two to an instruction) and the product with the norm.
-// Measured: 32768 tokens of 40 + 8 heads of 128 with norms and three axes, 121 us, 98 % of the
-// copy rate; 64 tokens of 40 + 40 heads 6.2 us, a launch and two round trips.
+// Measured: 32768 tokens of 40 + 8 heads of 128 with norms and three axes, 122 us, 98 % of the
+// copy rate, and with interleaved pairs 139 us, 85 % (122 registers against 80, four CTAs to an SM against
+// six); 64 tokens of 40 + 40 heads 4.6 us in a row of such calls, a launch and two round trips.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -41,7 +42,7 @@ constexpr int kWarps = 4;            // per CTA
 constexpr int kMaxAxes = 8;
 // From kPairTokens tokens of at most kPairPasses warps' worth of rows each, half a warp takes a token: there a
 // warp's time is its chain of loads, angles and stores, and two chains share it (32768 tokens, 8 + 1 heads of
-// 64, 37 -> 26 us, of 128, 43 -> 36).  8192 tokens of 32 + 8 heads of 128 would go from 33 to 40 us.
+// 64, 37 -> 24 us, of 128, 43 -> 34).  8192 tokens of 32 + 8 heads of 128 would go from 33 to 40 us.
 constexpr int kPairTokens = 2 * pkv::kFullWarps, kPairPasses = 4;
 
 struct RopeParams {
