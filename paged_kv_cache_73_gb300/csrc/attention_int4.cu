@@ -57,10 +57,10 @@
 // 96 % of that; one sequence of 2048 tokens, 40 heads, 10.8 us in a row of such calls, of which 7
 // are there at 128 tokens too.  Small blocks cost: 64 sequences of 1088 tokens take 65 us with
 // blocks of 32 tokens, 69 with 16 and 78 with 8 (tiles of 2176, 1088 and 544 bytes).
-// Groups of 9 to 16 are held by issue, not by the copies: a chunk takes 1.8 times as long as with
-// 8 heads (twice the columns, and 108 to 132 bytes of spills at 168 registers), 32 sequences as above with
-// 64 heads on 4 105 us of 54 for their bytes.  Above 16 every 16 heads walk the rows again: 32 heads on
-// one 62 us, 48 on one 84, of 13.5.
+// Groups of 9 to 16 are held by the chain of a chunk, not by the copies: it takes 1.8 times as long as with
+// 8 heads (twice the columns, and 108 to 132 bytes of spills at 168 registers) and twelve warps fill half of
+// the issue slots; 32 sequences as above with 64 heads on 4 take 105 us of 54 for their bytes.  Above 16
+// every 16 heads walk the rows again: 32 heads on one 62 us, 48 on one 84, of 13.5.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
