@@ -531,7 +531,7 @@ int pkv_paged_attention_decode_int4(const uint16_t* q, const uint8_t* k_cache, c
  * row, whatever they hold.
  * Tensor cores: fp16 products, fp32 sums; the softmax weights are rounded to fp16
  * before they multiply V, and to 0 below 2^-32 of the row's largest (an infinite
- * value with such a weight makes a NaN).  The tensor cores cut their sums off at
+ * value with such a weight can make a NaN).  The tensor cores cut their sums off at
  * the last bit: a row over n keys loses up to n 2^-27 of itself to that, as much as
  * the output's own rounding from 2^16 keys on.  Few queries over many keys are
  * shared out to clusters of blocks, by num_seqs, total_q, total_k and

@@ -670,8 +670,8 @@ __global__ void __launch_bounds__(THREADS, 2) prompt_attention_kernel(const __gr
           }
         }
         if constexpr (SPLIT) {
-          if (fix) {
-            const int last = tid < item.rows ? min(pos, item.keys - 1) : -1;
+          if (fix) {                                          // of this part's tiles only: the others' have their own factor
+            const int last = tid < item.rows ? min(pos, min(item.keys, item.n_tiles * BN) - 1) : -1;
             const __half* v = p.v + (item.k_row + static_cast<int64_t>(item.edge) * BN) * p.v_stride +
                               static_cast<int64_t>(item.head / p.group) * D + c * 32;
 #pragma unroll 1

@@ -336,3 +336,20 @@ def test_many_small_weights_beside_a_large_one(cuda_device, D, H, Hk, news, past
         assert (tol < 0.25 * o).mean() > 0.9                 # the sums are not lost in the tolerance
         err = np.abs(got[rows] - want[rows])
         assert (err <= tol).all(), float((err / tol).max())
+
+
+def test_infinite_values_in_two_parts_of_a_split_item(cuda_device):
+    # 128 queries over 1018 keys, shared out to eight CTAs of two key tiles each: tile 13, which some queries do
+    # not see whole, is the seventh's, the keys from 896 on the eighth's.  These have logits of 160, the others of
+    # 0, so that the seventh's part counts for nothing in rows that see both; an infinity of the
+    # eighth's in another column than the seventh's own is still one there.
+    q, k, v, qs, ks = make(46, [128], 890, 1, 1, 64)
+    q[:], k[:] = 0, 0
+    q[..., 0], k[896:, :, 0] = 8, 20
+    v[850, 0, 3], v[897, 0, 9] = np.inf, np.inf
+    got = run((q, k, v, qs, ks), 1.0, cuda_device).float().cpu().numpy()[:, 0]
+    assert pkv.device_error() == 0
+    assert (got[:6, 3] == np.inf).all()                      # queries 0 to 5 see keys up to 890 .. 895
+    assert (got[7:, 9] == np.inf).all() and np.isfinite(got[:7, 9]).all()
+    rest = [c for c in range(64) if c not in (3, 9)]
+    assert np.isfinite(got[:, rest]).all()
