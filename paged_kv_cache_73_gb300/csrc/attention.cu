@@ -1006,16 +1006,8 @@ int decode_entry(const char* fn, const uint16_t* q, const uint16_t* k_cache, con
 }  // namespace
 
 namespace pkv {
-int read_device_error_attention(int reset, int* code) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_dev_error_attention, sizeof(int));
-  if (e == cudaSuccess && reset && v) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_dev_error_attention, &zero, sizeof(int));
-  }
-  if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "reading the attention check word: %s", cudaGetErrorString(e));
-  *code = v;
-  return PKV_OK;
+int device_error_word_attention(void** word) {
+  return static_cast<int>(cudaGetSymbolAddress(word, g_dev_error_attention));
 }
 }  // namespace pkv
 

@@ -316,16 +316,8 @@ int launch_rows(const char* fn, const Kernel (&kernels)[2][2], int values_per_la
 }  // namespace
 
 namespace pkv {
-int read_device_error_cache_int4(int reset, int* code) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_dev_error_cache_int4, sizeof(int));
-  if (e == cudaSuccess && reset && v) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_dev_error_cache_int4, &zero, sizeof(int));
-  }
-  if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "reading the four-bit cache's check word: %s", cudaGetErrorString(e));
-  *code = v;
-  return PKV_OK;
+int device_error_word_cache_int4(void** word) {
+  return static_cast<int>(cudaGetSymbolAddress(word, g_dev_error_cache_int4));
 }
 }  // namespace pkv
 

@@ -310,16 +310,8 @@ int swap_blocks(const char* fn, const void* const* src_k_caches, const void* con
 }  // namespace
 
 namespace pkv {
-int read_device_error_cache_ops(int reset, int* code) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_dev_error_cache_ops, sizeof(int));
-  if (e == cudaSuccess && reset && v) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_dev_error_cache_ops, &zero, sizeof(int));
-  }
-  if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "reading the cache-op check word: %s", cudaGetErrorString(e));
-  *code = v;
-  return PKV_OK;
+int device_error_word_cache_ops(void** word) {
+  return static_cast<int>(cudaGetSymbolAddress(word, g_dev_error_cache_ops));
 }
 }  // namespace pkv
 

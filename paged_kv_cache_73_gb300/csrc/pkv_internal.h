@@ -18,15 +18,15 @@ int fail(int code, const char* fmt, ...)
 // Clears the thread-local message (called at the start of successful paths).
 void clear_error();
 
-// Per-translation-unit readers of the device check word; each .cu that
-// launches kernels defines one.  They synchronise nothing themselves.
-int read_device_error_attention(int reset, int* code);
-int read_device_error_cache_ops(int reset, int* code);
-int read_device_error_prefill(int reset, int* code);
-int read_device_error_rope(int reset, int* code);
-int read_device_error_cache_int4(int reset, int* code);
-int read_device_error_attention_int4(int reset, int* code);
-int read_device_error_prompt(int reset, int* code);
+// Where the current device's check word of a translation unit lies (an int; 0, or the first code its
+// kernels recorded); each .cu that launches kernels defines one.  Returns a cudaError_t.
+int device_error_word_attention(void** word);
+int device_error_word_cache_ops(void** word);
+int device_error_word_prefill(void** word);
+int device_error_word_rope(void** word);
+int device_error_word_cache_int4(void** word);
+int device_error_word_attention_int4(void** word);
+int device_error_word_prompt(void** word);
 
 // Shared-prefix decode reads a group's prefix once only for groups of at least this many members;
 // smaller groups (where the prefix mostly comes from L2 anyway and a 128-row tensor-core tile would

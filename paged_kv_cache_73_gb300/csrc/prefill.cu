@@ -652,16 +652,8 @@ int encode_q_map(CUtensorMap* map, const void* q, int D, int H, int T) {
 }  // namespace
 
 namespace pkv {
-int read_device_error_prefill(int reset, int* code) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_dev_error_prefill, sizeof(int));
-  if (e == cudaSuccess && reset && v) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_dev_error_prefill, &zero, sizeof(int));
-  }
-  if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "reading the prefill check word: %s", cudaGetErrorString(e));
-  *code = v;
-  return PKV_OK;
+int device_error_word_prefill(void** word) {
+  return static_cast<int>(cudaGetSymbolAddress(word, g_dev_error_prefill));
 }
 }  // namespace pkv
 

@@ -814,16 +814,8 @@ int launch(const PromptParams& p, long long tiles, int parts, cudaStream_t st) {
 }  // namespace
 
 namespace pkv {
-int read_device_error_prompt(int reset, int* code) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_dev_error_prompt, sizeof(int));
-  if (e == cudaSuccess && reset && v) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_dev_error_prompt, &zero, sizeof(int));
-  }
-  if (e != cudaSuccess) return fail(PKV_ERR_CUDA, "reading the prompt attention's check word: %s", cudaGetErrorString(e));
-  *code = v;
-  return PKV_OK;
+int device_error_word_prompt(void** word) {
+  return static_cast<int>(cudaGetSymbolAddress(word, g_dev_error_prompt));
 }
 }  // namespace pkv
 
