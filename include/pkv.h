@@ -458,7 +458,8 @@ int pkv_reshape_and_cache_int4(const uint16_t* key, const uint16_t* value, uint8
 
 /* The inverse: rows key[t] and value[t] (device [num_tokens, num_kv_heads,
  * head_dim] fp16, contiguous, 16-byte aligned) receive what slot slot_mapping[t]
- * stands for, zero + scale * n rounded to fp16 once.  For the next chunk of a
+ * stands for, zero + scale * n rounded to fp16 once (which can be an infinity in rows
+ * whose greatest value is above 65440).  For the next chunk of a
  * prompt, whose tokens attend over the cached context (pkv_prompt_attention).
  * Rows with a negative slot are left as they were; a slot outside the pool records
  * PKV_DEV_BAD_SLOT and leaves its row. */
