@@ -43,8 +43,8 @@
  * (block, head) tile of a pool is block_size*head_dim*2 contiguous bytes.
  *
  * Supported shapes: head_dim in {64, 128}, block_size in {4, 8, 16, 32}, one K/V
- * head per query head (the four-bit cache and prompt attention also take grouped
- * heads).  Other values return PKV_ERR_UNSUPPORTED.
+ * head per query head (the four-bit cache, prompt attention and the operators on
+ * drafted tokens also take grouped heads).  Other values return PKV_ERR_UNSUPPORTED.
  */
 #ifndef PKV_H_
 #define PKV_H_
@@ -80,7 +80,10 @@ enum {
   PKV_DEV_PREFIX_MISMATCH = 7,  /* shared-prefix decode: a sequence's first prefix blocks differ
                                    from its group's first sequence's, a bad group layout, or a
                                    group larger than max_group_size */
-  PKV_DEV_BAD_AXIS = 8          /* rotation: a pair's position axis outside [0, num_axes) */
+  PKV_DEV_BAD_AXIS = 8,         /* rotation: a pair's position axis outside [0, num_axes) */
+  PKV_DEV_BAD_TREE = 9,         /* drafts: a node before its parent, or a path whose nodes do not go up */
+  PKV_DEV_BAD_TOKEN = 10,       /* drafts: a token outside [0, vocab_size) */
+  PKV_DEV_BAD_PROBABILITY = 11  /* drafts: a NaN, a value outside [0, 1], or a row whose sum is 0 or above 1.5 */
 };
 
 /* Message for the last non-OK status returned on this thread ("" if none). */
@@ -546,6 +549,157 @@ int pkv_prompt_attention(const uint16_t* q, const uint16_t* key, const uint16_t*
                          int64_t value_stride, float scale, uint16_t* out, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Decoding with drafted tokens (an addition of this library).  A cheap model
+ * drafts a few tokens that may follow each sequence, a chain or a tree; the
+ * target model runs over all of them in one step, and its distributions decide
+ * which stay.  A step is, per layer, pkv_rope_and_cache and
+ * pkv_paged_attention_tree, then pkv_verify_draft on the model's output and
+ * pkv_move_accepted over all layers.
+ *
+ * A sequence's drafts are its nodes query_start[s] .. query_start[s+1]-1 of the
+ * packed batch, numbered from 0 within it, parents before children.  Node 0, the
+ * root, is its last certain token, not in the cache yet either.  Their slots are
+ * those of the sequence's next positions (pkv_bm_extend), node i's that of
+ * position ctx - n + i, while its rotary position is ctx - n + its depth.  After
+ * the move the kept nodes lie in the first path_len[s] of those slots, and
+ * pkv_bm_truncate gives back the others.
+ * ------------------------------------------------------------------------- */
+
+/* pkv_qk_norm_rope followed by pkv_reshape_and_cache in one pass: the rotated
+ * queries go to q_out, the rotated keys to their slots of the K pool, the values,
+ * bit for bit, to theirs of the V pool.
+ *
+ *   q, key, value device fp16 [num_tokens, num_heads or num_kv_heads, head_dim]; a
+ *                 token's heads are contiguous, tokens are q_stride / k_stride /
+ *                 v_stride elements apart (multiples of 8, at least a token's length)
+ *   rotary_scale  factor of the turned values (long-context scalings use one
+ *                 besides their frequencies; else 1), applied in fp32
+ *   q_out         device fp16 like q with a stride of its own; may be q (same pointer
+ *                 and stride), otherwise must not overlap an input
+ *   k_cache,
+ *   v_cache       device [num_blocks, num_kv_heads, block_size, head_dim] fp16; must
+ *                 not overlap the inputs
+ *   slot_mapping  device [num_tokens] int64.  A negative slot marks a padding token:
+ *                 its query is rotated, nothing is stored.  A slot outside the pool
+ *                 records PKV_DEV_BAD_SLOT and is not written.  No two tokens may
+ *                 have the same slot: its row could mix theirs.
+ *   the weights, eps, positions, frequencies, pair_axis, rotary_dim and interleaved
+ *   as for pkv_qk_norm_rope.  q, key, value, weights, q_out and pools: 16-byte aligned. */
+int pkv_rope_and_cache(const uint16_t* q, const uint16_t* key, const uint16_t* value, const uint16_t* q_weight,
+                       const uint16_t* k_weight, float eps, const int32_t* positions, int num_axes,
+                       const int64_t* frequencies, const int32_t* pair_axis, int rotary_dim, int interleaved,
+                       float rotary_scale, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride, uint16_t* q_out, int64_t q_out_stride,
+                       uint16_t* k_cache, uint16_t* v_cache, const int64_t* slot_mapping, int block_size,
+                       int num_blocks, void* stream);
+
+/* Attention of each sequence's n_s new tokens over its cached context and over each
+ * other, with grouped heads.  Node i of sequence s sees every position
+ * t < context_lens[s] - n_s, and of the new ones position context_lens[s] - n_s + j
+ * where bit j % 32 of word j / 32 of its mask row is set:
+ *   out[query_start[s] + i, h, :] = sum_t softmax_t(scale * q . k_t) v_t
+ * with head h / (num_heads / num_kv_heads) of the pools.  A row that sees nothing is
+ * zeros.
+ *
+ *   q             device [total_q, num_heads, head_dim] fp16, 16-byte aligned, a token's
+ *                 heads contiguous, tokens q_stride elements apart (a multiple of 8)
+ *   k_cache,
+ *   v_cache       device [num_blocks, num_kv_heads, block_size, head_dim] fp16
+ *   block_tables, context_lens as for pkv_paged_attention_decode, device memory;
+ *                 context_lens[s] counts the new tokens, whose keys and values are
+ *                 in the pools already
+ *   query_start   device [num_seqs + 1] int32, non-decreasing
+ *   tree_mask     device [total_q, mask_words] words of 32 bits (pkv_tree_masks makes
+ *                 them from parents; any bits are allowed, also of later nodes), or
+ *                 NULL: node i sees nodes 0 .. i, a chain of drafts
+ *   max_query_len host: the largest n_s (sizes the work; with 0 nothing runs); a mask
+ *                 row must hold as many bits.  A larger n_s records
+ *                 PKV_DEV_BAD_QUERY_RANGE, and the sequence's rows are not written.
+ *   out           device [total_q, num_heads, head_dim] fp16, contiguous, 16-byte
+ *                 aligned; must not overlap the inputs
+ *   workspace     at least pkv_paged_attention_tree_workspace_size(...) bytes, asked for
+ *                 with the device current, 16-byte aligned; NULL where that is 0.
+ *                 Calls that may run at the same time need workspaces of their own.
+ * scale must be positive.  A sequence without new tokens is skipped; n_s > ctx_s or
+ * rows outside q record PKV_DEV_BAD_QUERY_RANGE, a length outside the table
+ * PKV_DEV_BAD_CONTEXT_LEN, and the sequence's rows are not written.  A table entry
+ * outside the pool records PKV_DEV_BAD_BLOCK_ID and its tokens get no weight.  Rows of
+ * out in no sequence are left as they were.  Keys and values of new tokens that a node
+ * does not see, and slots past the context, do not reach its row, whatever they hold. */
+size_t pkv_paged_attention_tree_workspace_size(int num_seqs, int total_q, int max_query_len, int num_heads,
+                                               int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                                               int block_size);
+
+int pkv_paged_attention_tree(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache, const uint16_t* v_cache,
+                             const int32_t* block_tables, const int32_t* context_lens, const int32_t* query_start,
+                             const int32_t* tree_mask, int mask_words, int num_seqs, int total_q, int max_query_len,
+                             int num_heads, int num_kv_heads, int head_dim, int num_blocks, int max_blocks_per_seq,
+                             float scale, int block_size, uint16_t* out, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Host only: each node's mask row (itself and its ancestors) and depth from its
+ * parent (host [query_start[num_seqs]], the parent's number within its sequence, before the
+ * node's own; negative: none).  masks_out host [.., mask_words], depths_out host [..] or NULL. */
+int pkv_tree_masks(const int32_t* parents, const int32_t* query_start, int num_seqs, int mask_words,
+                   int32_t* masks_out, int32_t* depths_out);
+
+/* Which drafts stay, by the target's distributions and given random numbers, and the
+ * token that follows them.  From node 0 on, the children of the current node c are tried in
+ * ascending order.  With R = p_c and M = 1 at first, child j with token x
+ *   stays, and becomes the current node, if u_j M q_c(x) < R(x);
+ *   otherwise R <- max(R - M q_c, 0) and M <- sum R.
+ * Without draft distributions (drafts that were looked up, not drawn) q_c(x) counts as 1,
+ * and a refusal is M <- M - R(x), R(x) <- 0.  Where no child stays, the next token is
+ * the least index whose running sum of R passes u_0 sum R (of p_c, should R be 0
+ * throughout).  For children drawn independently from q_c the kept and the drawn
+ * tokens are so distributed as the target alone would draw them.
+ * Everything is computed in whole numbers of 2^-60, products rounded down: the result is a
+ * function of the inputs alone.
+ *
+ *   target_probs device fp32 [total_q, vocab_size], row i the target's distribution
+ *                behind node i, rows target_stride elements apart
+ *   draft_probs  device fp32 alike: row i what node i's children were drawn from (rows of
+ *                nodes without children are not read); or NULL
+ *   tokens,
+ *   parents      device [total_q] int32; the root's are not read.  A negative parent
+ *                takes a node out of the tree (padding); one that is not before its node
+ *                records PKV_DEV_BAD_TREE, a token outside the vocabulary
+ *                PKV_DEV_BAD_TOKEN, and the node is out as well.
+ *   query_start  device [num_seqs + 1] int32, at most 1024 nodes to a sequence (more, or rows
+ *                outside total_q, record PKV_DEV_BAD_QUERY_RANGE and give path_len 0)
+ *   uniforms     device [total_q] fp32 in [0, 1): u_j decides on node j, the root's draws the
+ *                next token
+ *   max_path     places of a path, 1 to 1024: a path that fills them is not followed further
+ *   path         device [num_seqs, max_path] int32: the current nodes from 0 on, then -1
+ *   path_len     device [num_seqs] int32: how many; 0 for a sequence without nodes
+ *   next_token   device [num_seqs] int32; -1 for a sequence without nodes, and where the
+ *                row is no distribution (a value that is NaN, negative or above 1, a sum
+ *                of 0 or above 1.5: PKV_DEV_BAD_PROBABILITY)
+ * No output may overlap an input.  No workspace. */
+int pkv_verify_draft(const float* target_probs, const float* draft_probs, const int32_t* tokens,
+                     const int32_t* parents, const int32_t* query_start, const float* uniforms, int num_seqs,
+                     int total_q, int vocab_size, int64_t target_stride, int64_t draft_stride, int max_path,
+                     int32_t* path, int32_t* path_len, int32_t* next_token, void* stream);
+
+/* The kept drafts' rows to the places behind the context, in every layer:
+ *   row slot_mapping[query_start[s] + path[s, i]] -> row slot_mapping[query_start[s] + i]
+ * for 0 < i < path_len[s] and all heads, K and V, as if all rows were read first.
+ * Bit-exact.
+ *
+ *   k_caches, v_caches HOST arrays of num_layers device pool pointers, 16-byte aligned
+ *   slot_mapping       device [total_q] int64, the nodes' slots, no slot twice; a move
+ *                      from or to a negative one is left out, one outside the pool records
+ *                      PKV_DEV_BAD_SLOT and is left out
+ *   query_start, path, path_len as pkv_verify_draft takes and gives them.  A node
+ *                      path[i] < i or past the sequence's nodes records PKV_DEV_BAD_TREE, a
+ *                      path_len above max_path or nodes outside total_q
+ *                      PKV_DEV_BAD_QUERY_RANGE; neither moves anything. */
+int pkv_move_accepted(uint16_t* const* k_caches, uint16_t* const* v_caches, int num_layers, const int64_t* slot_mapping,
+                      const int32_t* query_start, const int32_t* path, const int32_t* path_len, int num_seqs,
+                      int total_q, int max_path, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                      void* stream);
+
+/* ---------------------------------------------------------------------------
  * Host block manager ([note] 关键设计 2 and 3; [lecture] PagedAttention 原理 and
  * Parallel Sampling 场景; [guide] 03 and 04).  No device memory, no CUDA.
  *
@@ -601,6 +755,11 @@ int pkv_bm_free(pkv_bm* bm, int64_t seq_id);
  * be NULL) with *num_cow = 1, else *num_cow = 0 (num_cow may be NULL).  The
  * prompt phase of a request uses it to place all of its new tokens at once. */
 int pkv_bm_extend(pkv_bm* bm, int64_t seq_id, int n, int64_t* slots_out, int64_t* cow_pair_out, int* num_cow);
+
+/* 0 <= n < its length drops a sequence's last n tokens (refused drafts): blocks that are
+ * left without tokens lose the sequence's reference, the last first.  What remains
+ * of a block shared with another sequence is copied before the next append, as ever. */
+int pkv_bm_truncate(pkv_bm* bm, int64_t seq_id, int n);
 
 /* A provider-stored prefix of len >= 1 tokens ([guide] 04); slots_out as in
  * pkv_bm_add_seq. */

@@ -21,6 +21,7 @@ Modules:
 * ``attention``     -- single-query attention over a paged K/V pool, fp64.
 * ``cache_ops``     -- the slot-mapping scatter of new K/V and the block copy.
 * ``block_manager`` -- block tables, free list, reference counts, copy-on-write.
+* ``drafts``        -- decoding with drafted tokens: tree attention, verification, the kept rows' move.
 * ``sizes``         -- K/V bytes per token.
 
 Every function is pinned by a ``-m "not gpu"`` test against facts fixed

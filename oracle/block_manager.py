@@ -185,6 +185,16 @@ class BlockManager:
                 copies.append((src, dst))
         return slots, copies
 
+    def truncate(self, seq_id: int, n: int) -> None:
+        """Drop the last n tokens (at least one stays); emptied blocks lose the sequence's reference, last first."""
+        blocks = self.seqs[seq_id]
+        if not 0 <= n < sum(b.filled for b in blocks):
+            raise ValueError("n must leave a token")
+        for _ in range(n):
+            blocks[-1].filled -= 1
+            if blocks[-1].filled == 0:
+                self._release(blocks.pop().physical)
+
     def free(self, seq_id: int) -> None:
         for b in self.seqs.pop(seq_id):
             self._release(b.physical)

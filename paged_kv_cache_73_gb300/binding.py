@@ -28,7 +28,8 @@ PKV_ERR_DEVICE_CHECK = -6
 PKV_ERR_NOT_FOUND = -7
 
 DEV_CODES = {0: "ok", 1: "bad block id", 2: "bad context length", 3: "bad slot", 4: "bad copy pair",
-             5: "wait timeout", 6: "bad query range", 7: "shared prefix mismatch", 8: "bad position axis"}
+             5: "wait timeout", 6: "bad query range", 7: "shared prefix mismatch", 8: "bad position axis", 9: "bad tree",
+             10: "bad token", 11: "bad probability"}
 
 
 class PkvError(RuntimeError):
@@ -80,6 +81,14 @@ _SIGNATURES = {
     "pkv_prompt_attention": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I64, _I64, _I64, _c.c_float, _P, _P]),
     "pkv_copy_blocks_int4": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _I, _P]),
     "pkv_swap_blocks_int4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "pkv_rope_and_cache": (_I, [_P, _P, _P, _P, _P, _c.c_float, _P, _I, _P, _P, _I, _I, _c.c_float, _I, _I, _I, _I, _I64,
+                                _I64, _I64, _P, _I64, _P, _P, _P, _I, _I, _P]),
+    "pkv_paged_attention_tree_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "pkv_paged_attention_tree": (_I, [_P, _I64, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _c.c_float, _I,
+                                      _P, _P, _SZ, _P]),
+    "pkv_tree_masks": (_I, [_P, _P, _I, _I, _P, _P]),
+    "pkv_verify_draft": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I64, _I64, _I, _P, _P, _P, _P]),
+    "pkv_move_accepted": (_I, [_P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "pkv_bm_create": (_P, [_I, _I, _P]),
     "pkv_bm_destroy": (None, [_P]),
     "pkv_bm_add_seq": (_I, [_P, _I64, _I, _P]),
@@ -90,6 +99,7 @@ _SIGNATURES = {
     "pkv_bm_register_prefix": (_I, [_P, _I64, _I, _P]),
     "pkv_bm_add_seq_with_prefix": (_I, [_P, _I64, _I64, _I, _P, _P, _c.POINTER(_I)]),
     "pkv_bm_extend": (_I, [_P, _I64, _I, _P, _P, _c.POINTER(_I)]),
+    "pkv_bm_truncate": (_I, [_P, _I64, _I]),
     "pkv_bm_drop_prefix": (_I, [_P, _I64]),
     "pkv_bm_block_table": (_I, [_P, _I64, _P, _I, _c.POINTER(_I), _c.POINTER(_I)]),
     "pkv_bm_block_tables": (_I, [_P, _P, _I, _P, _I, _P]),
@@ -772,6 +782,219 @@ def prompt_attention(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, qu
     return out
 
 
+
+# ---- decoding with drafted tokens --------------------------------------------------------------
+
+def _need_pools(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: int) -> Tuple[int, int, int, int]:
+    """(num_blocks, num_kv_heads, block_size, head_dim) of two fp16 pools on the current device, dev."""
+    if not (_is(k_cache, torch.float16, 4, dev) and _is(v_cache, torch.float16, 4, dev)):
+        _need(k_cache, "k_cache", torch.float16, 4)
+        _need(v_cache, "v_cache", torch.float16, 4)
+    if k_cache.shape != v_cache.shape:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"pools differ in shape: {tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+    return k_cache.shape
+
+
+def rope_and_cache(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor,
+                   frequencies: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   slot_mapping: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                   k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   pair_axis: Optional[torch.Tensor] = None, interleaved: bool = False, rotary_scale: float = 1.0,
+                   q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """qk_norm_rope, with the rotated keys and the values stored at slot_mapping[t] (negative = not stored) of the
+    fp16 pools [N, num_kv_heads, B, D]; returns the rotated queries.
+
+    q, key and value may be views into a packed projection (tokens strided); q_out may be q itself.
+    rotary_scale multiplies the turned values (long-context scalings)."""
+    dev = torch.cuda.current_device()
+    T, H, D, qs = _rows(q, "q", dev)
+    *kshape, ks = _rows(key, "key", dev)
+    *vshape, vs = _rows(value, "value", dev)
+    N, Hk, B, Dk = _need_pools(k_cache, v_cache, dev)
+    if kshape != [T, Hk, D] or vshape != kshape or Dk != D:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"rope_and_cache: q {tuple(q.shape)}, key {tuple(key.shape)}, value "
+                                            f"{tuple(value.shape)} and pools {tuple(k_cache.shape)} do not match")
+    dim = positions.dim()
+    if not _is(positions, torch.int32, 2 if dim == 2 else 1, dev):
+        _need(positions, "positions", torch.int32, 2 if dim == 2 else 1)
+    if not _is(frequencies, torch.int64, 1, dev):
+        _need(frequencies, "frequencies", torch.int64, 1)
+    if not _is(slot_mapping, torch.int64, 1, dev):
+        _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    pairs = frequencies.shape[0]
+    if positions.shape[dim - 1] != T or slot_mapping.shape[0] != T:
+        raise PkvError(PKV_ERR_INVALID_ARG, "rope_and_cache: positions must be [T] or [num_axes, T], slot_mapping [T]")
+    if pair_axis is not None:
+        if not _is(pair_axis, torch.int32, 1, dev):
+            _need(pair_axis, "pair_axis", torch.int32, 1)
+        if pair_axis.shape[0] != pairs:
+            raise PkvError(PKV_ERR_INVALID_ARG, "rope_and_cache: pair_axis must have one entry per frequency")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            if not _is(w, torch.float16, 1, dev):
+                _need(w, name, torch.float16, 1)
+            if w.shape[0] != D:
+                raise PkvError(PKV_ERR_INVALID_ARG, f"rope_and_cache: {name} must have head_dim entries")
+    qos = H * D
+    if q_out is None:
+        q_out = _empty((T, H, D), torch.float16, q, stream)
+    else:
+        *shape, qos = _rows(q_out, "q_out", dev)
+        if shape != [T, H, D]:
+            raise PkvError(PKV_ERR_INVALID_ARG, "rope_and_cache: q_out must be shaped like q")
+    _check(load().pkv_rope_and_cache(
+        q.data_ptr(), key.data_ptr(), value.data_ptr(), _ptr(q_weight), _ptr(k_weight), eps, positions.data_ptr(),
+        positions.shape[0] if dim == 2 else 1, frequencies.data_ptr(), _ptr(pair_axis), 2 * pairs, int(interleaved),
+        rotary_scale, T, H, Hk, D, qs, ks, vs, q_out.data_ptr(), qos, k_cache.data_ptr(), v_cache.data_ptr(),
+        slot_mapping.data_ptr(), B, N, _stream(stream, dev)))
+    return q_out
+
+
+def tree_masks(parents: Sequence[int], query_start: Sequence[int], device="cuda") -> Tuple[torch.Tensor, torch.Tensor]:
+    """The tree_mask [T, words] (each node and its ancestors) and the nodes' depths [T], int32, from each node's parent
+    (its number within its sequence; negative: none); sequence s's nodes are query_start[s] .. query_start[s + 1] - 1."""
+    par = np.ascontiguousarray(np.asarray(parents, dtype=np.int32))
+    start = np.ascontiguousarray(np.asarray(query_start, dtype=np.int32))
+    if par.ndim != 1 or start.ndim != 1 or start.shape[0] == 0 or start[0] != 0 or start[-1] != par.shape[0]:
+        raise PkvError(PKV_ERR_INVALID_ARG, "tree_masks: query_start must go from 0 to the number of parents")
+    words = max(1, (int(np.diff(start).max(initial=0)) + 31) // 32)
+    masks = np.empty((par.shape[0], words), dtype=np.int32)
+    depths = np.empty(par.shape[0], dtype=np.int32)
+    _check(load().pkv_tree_masks(par.ctypes.data, start.ctypes.data, start.shape[0] - 1, words, masks.ctypes.data,
+                                 depths.ctypes.data))
+    return torch.from_numpy(masks).to(device), torch.from_numpy(depths).to(device)
+
+
+def paged_attention_tree_workspace_size(num_seqs: int, total_q: int, max_query_len: int, num_heads: int,
+                                        num_kv_heads: int, head_dim: int, max_blocks_per_seq: int,
+                                        block_size: int) -> int:
+    return int(load().pkv_paged_attention_tree_workspace_size(num_seqs, total_q, max_query_len, num_heads, num_kv_heads,
+                                                              head_dim, max_blocks_per_seq, block_size))
+
+
+@functools.lru_cache(maxsize=1024)
+def _tree_workspace_size(device: int, *sizes: int) -> int:
+    """The size for a device's SM count and these sizes, as the library gives it."""
+    return paged_attention_tree_workspace_size(*sizes)
+
+
+def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                         context_lens: torch.Tensor, query_start: torch.Tensor, scale: float, block_size: int,
+                         max_query_len: int, tree_mask: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """Each sequence's new tokens over its cached context and over those of each other that tree_mask's rows name
+    (None: a chain, each sees itself and those before it).  Query heads are a multiple of the pools' heads."""
+    dev = torch.cuda.current_device()
+    T, H, D, qs = _rows(q, "q", dev)
+    N, Hk, B, Dk = _need_pools(k_cache, v_cache, dev)
+    for t, name, dim in ((block_tables, "block_tables", 2), (context_lens, "context_lens", 1), (query_start, "query_start", 1)):
+        if not _is(t, torch.int32, dim, dev):
+            _need(t, name, torch.int32, dim)
+    S, max_blocks = block_tables.shape
+    if B != block_size or Dk != D:
+        raise PkvError(PKV_ERR_INVALID_ARG, f"pools {tuple(k_cache.shape)} are not [N, Hk, {block_size}, {D}]")
+    if context_lens.shape[0] != S or query_start.shape[0] != S + 1:
+        raise PkvError(PKV_ERR_INVALID_ARG, "context_lens must have num_seqs entries and query_start one more")
+    words = 0
+    if tree_mask is not None:
+        if not _is(tree_mask, torch.int32, 2, dev):
+            _need(tree_mask, "tree_mask", torch.int32, 2)
+        words = tree_mask.shape[1]
+        if tree_mask.shape[0] != T or 32 * words < max_query_len:
+            raise PkvError(PKV_ERR_INVALID_ARG, "tree_mask must have a row per query, of max_query_len bits or more")
+    if out is None:
+        out = _empty((T, H, D), torch.float16, q, stream)
+    else:
+        if not _is(out, torch.float16, 3, dev):
+            _need(out, "out", torch.float16, 3)
+        if out.shape != q.shape:
+            raise PkvError(PKV_ERR_INVALID_ARG, "out must be shaped like q")
+    if workspace is None:
+        n = _tree_workspace_size(dev, S, T, max_query_len, H, Hk, D, max_blocks, block_size)
+        ws, ws_bytes = None, 0
+        if n:
+            workspace = _empty((n,), torch.uint8, q, stream)
+            ws, ws_bytes = workspace.data_ptr(), n
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise PkvError(PKV_ERR_INVALID_ARG, "workspace must be contiguous memory of the current device")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(load().pkv_paged_attention_tree(
+        q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+        query_start.data_ptr(), _ptr(tree_mask), words, S, T, max_query_len, H, Hk, D, N, max_blocks, scale, block_size,
+        out.data_ptr(), ws, ws_bytes, _stream(stream, dev)))
+    return out
+
+
+def _prob_rows(t: torch.Tensor, name: str, device: int) -> int:
+    """The row stride of a CUDA fp32 [T, V] tensor whose rows may be strided."""
+    if t.dtype is torch.float32 and t.dim() == 2 and t.get_device() == device and (t.stride(1) == 1 or t.shape[1] == 1):
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.is_cuda and t.get_device() != device:
+        _need(t, name, t.dtype, t.dim())                   # says which device is current
+    raise PkvError(PKV_ERR_INVALID_ARG, f"{name}: want a CUDA torch.float32 tensor of rank 2 with contiguous rows, "
+                                        f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} device={t.device}")
+
+
+def verify_draft(target_probs: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor, query_start: torch.Tensor,
+                 uniforms: torch.Tensor, max_path: int, draft_probs: Optional[torch.Tensor] = None,
+                 stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Which drafts stay by the target's distributions: (path [S, max_path] of kept nodes from the root, 0, on, filled up
+    with -1; path_len [S]; next_token [S]), int32.  Row i of target_probs is the distribution behind node i, row i of
+    draft_probs what node i's children were drawn from (None: they were not drawn); uniforms[i] in [0, 1) decides on
+    node i, the root's draws the next token."""
+    dev = torch.cuda.current_device()
+    ts = _prob_rows(target_probs, "target_probs", dev)
+    T, V = target_probs.shape
+    ds = 0
+    if draft_probs is not None:
+        ds = _prob_rows(draft_probs, "draft_probs", dev)
+        if draft_probs.shape != target_probs.shape:
+            raise PkvError(PKV_ERR_INVALID_ARG, "draft_probs must be shaped like target_probs")
+    for t, name, dtype in ((tokens, "tokens", torch.int32), (parents, "parents", torch.int32),
+                           (uniforms, "uniforms", torch.float32), (query_start, "query_start", torch.int32)):
+        if not _is(t, dtype, 1, dev):
+            _need(t, name, dtype, 1)
+        if t is not query_start and t.shape[0] != T:
+            raise PkvError(PKV_ERR_INVALID_ARG, f"verify_draft: {name} must have an entry per row of target_probs")
+    S = query_start.shape[0] - 1
+    if S < 0 or max_path <= 0:
+        raise PkvError(PKV_ERR_INVALID_ARG, "verify_draft: query_start needs num_seqs + 1 entries, max_path a place")
+    path = _empty((S, max_path), torch.int32, target_probs, stream)
+    path_len, next_token = _empty((2, S), torch.int32, target_probs, stream)
+    _check(load().pkv_verify_draft(
+        target_probs.data_ptr(), _ptr(draft_probs), tokens.data_ptr(), parents.data_ptr(), query_start.data_ptr(),
+        uniforms.data_ptr(), S, T, V, ts, ds, max_path, path.data_ptr(), path_len.data_ptr(), next_token.data_ptr(),
+        _stream(stream, dev)))
+    return path, path_len, next_token
+
+
+def move_accepted(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor], slot_mapping: torch.Tensor,
+                  query_start: torch.Tensor, path: torch.Tensor, path_len: torch.Tensor, stream=None) -> None:
+    """Move the kept drafts' rows, path[s, i] of sequence s's nodes, to node i's slot, in every layer's pools."""
+    dev = torch.cuda.current_device()
+    L = len(k_caches)
+    if len(v_caches) != L or L == 0:
+        raise PkvError(PKV_ERR_INVALID_ARG, "move_accepted: need as many K as V pools, at least one")
+    for k, v in zip(k_caches, v_caches):
+        if _need_pools(k, v, dev) != k_caches[0].shape:
+            raise PkvError(PKV_ERR_INVALID_ARG, "move_accepted: pools differ in shape")
+    for t, name, dtype, dim in ((slot_mapping, "slot_mapping", torch.int64, 1), (query_start, "query_start", torch.int32, 1),
+                                (path, "path", torch.int32, 2), (path_len, "path_len", torch.int32, 1)):
+        if not _is(t, dtype, dim, dev):
+            _need(t, name, dtype, dim)
+    S, max_path = path.shape
+    if query_start.shape[0] != S + 1 or path_len.shape[0] != S:
+        raise PkvError(PKV_ERR_INVALID_ARG, "move_accepted: path and path_len need a row per sequence of query_start")
+    N, H, B, D = k_caches[0].shape
+    kp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in k_caches])
+    vp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in v_caches])
+    _check(load().pkv_move_accepted(kp, vp, L, slot_mapping.data_ptr(), query_start.data_ptr(), path.data_ptr(),
+                                    path_len.data_ptr(), S, slot_mapping.shape[0], max_path, H, D, B, N,
+                                    _stream(stream, dev)))
+
+
 # ---- host block manager -----------------------------------------------------------------------
 
 def _np_ptr(a: np.ndarray) -> int:
@@ -856,6 +1079,10 @@ class BlockManager:
         nc = _c.c_int(0)
         _check(self._lib.pkv_bm_extend(self._h, seq_id, n, _np_ptr(slots), _np_ptr(pair), ctypes.byref(nc)))
         return slots[:n], pair.reshape(1, 2)[:nc.value]
+
+    def truncate(self, seq_id: int, n: int) -> None:
+        """Drop the sequence's last n tokens (0 <= n < its length) and give back blocks left without any."""
+        _check(self._lib.pkv_bm_truncate(self._h, seq_id, n))
 
     def drop_prefix(self, prefix_id: int) -> None:
         _check(self._lib.pkv_bm_drop_prefix(self._h, prefix_id))

@@ -30,7 +30,8 @@ namespace {
 int (*const kWords[])(void**) = {device_error_word_attention,  device_error_word_cache_ops,
                                  device_error_word_prefill,    device_error_word_rope,
                                  device_error_word_cache_int4, device_error_word_attention_int4,
-                                 device_error_word_prompt};
+                                 device_error_word_prompt,     device_error_word_tree_attention,
+                                 device_error_word_drafts};
 constexpr int kUnits = sizeof(kWords) / sizeof(kWords[0]);
 
 // Page-locked memory for one call's words, so that they come in copies one behind the other with one wait

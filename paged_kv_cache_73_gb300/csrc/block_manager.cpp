@@ -313,6 +313,29 @@ int pkv_bm_extend(pkv_bm* bm, int64_t seq_id, int n, int64_t* slots_out, int64_t
   return PKV_OK;
 }
 
+int pkv_bm_truncate(pkv_bm* bm, int64_t seq_id, int n) {
+  if (!bm || n < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "pkv_bm_truncate: bad argument (n=%d)", n);
+  Manager* m = M(bm);
+  auto it = m->seqs.find(seq_id);
+  if (it == m->seqs.end()) return pkv::fail(PKV_ERR_NOT_FOUND, "pkv_bm_truncate: no sequence %lld", (long long)seq_id);
+  std::vector<Logical>& blocks = it->second;
+  const int64_t len = ((int64_t)blocks.size() - 1) * m->B + blocks.back().filled;
+  if (n >= len)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "pkv_bm_truncate: sequence %lld has %lld tokens, %d to drop", (long long)seq_id,
+                     (long long)len, n);
+  while (n > 0) {
+    Logical& last = blocks.back();
+    if (n < last.filled) {
+      last.filled -= n;
+      break;
+    }
+    n -= last.filled;
+    m->release(last.phys);
+    blocks.pop_back();
+  }
+  return PKV_OK;
+}
+
 int pkv_bm_drop_prefix(pkv_bm* bm, int64_t prefix_id) {
   if (!bm) return pkv::fail(PKV_ERR_INVALID_ARG, "pkv_bm_drop_prefix: null manager");
   Manager* m = M(bm);

@@ -27,6 +27,8 @@ int device_error_word_rope(void** word);
 int device_error_word_cache_int4(void** word);
 int device_error_word_attention_int4(void** word);
 int device_error_word_prompt(void** word);
+int device_error_word_tree_attention(void** word);
+int device_error_word_drafts(void** word);
 
 // Shared-prefix decode reads a group's prefix once only for groups of at least this many members;
 // smaller groups (where the prefix mostly comes from L2 anyway and a 128-row tensor-core tile would
