@@ -3,21 +3,60 @@
 // query heads share a cached head.
 //
 //   o_i = sum_t softmax_t(scale q_i . k_t) v_t   over t < ctx - n and t = ctx - n + j, bit j of row i set
+//
+// The n new tokens' G query heads of one cached head are the rows of one product: n G rows over
+// the same keys, each cached row read once for all of them.  So it is bound by the cache's
+// bytes up to about 256 rows (4 D flops a row and key against 4 D bytes a key), and
+// the products run on the tensor cores from one row on: a tile of 128 rows costs 1024 clocks per 128 keys of
+// D = 128 however few are real, while their 64 KB take an SM 2800 at the copy rate.
+//
+//  * A stream is one sequence's cached head and tile of 128 rows.  All streams' key tiles (64 positions)
+//    lie on one line, cut evenly over the resident CTAs, two to an SM, each with half of the tensor memory: ragged
+//    contexts and few sequences fill the GPU alike.  A CTA walks its piece through a ring of K and V tiles
+//    that runs on over the ends of streams.
+//  * A stream that is cut leaves partial results (row maximum, sum, output) that a second kernel joins by the
+//    log-sum-exp identity; the first CTA of such a stream notes where they lie.  A CTA has at most
+//    two such parts, the first and the last of its piece.
+//  * K and V blocks come by TMA (one box per block and 64 columns) into the 128-byte swizzle.  V tiles
+//    that some row does not see whole (drafts, the context's end, a block outside the pool) come through
+//    registers instead: a masked weight of 0 times a value that is not finite would be a NaN, so such
+//    values of drafts become zeros, are noted, and put back in the end for the rows that see them.
+//  * Softmax as in prompt attention: a thread owns a row (a lane of tensor memory); the maximum, and with
+//    it O, moves only when a tile passes it by 2^8; weights are 2^(7 + S - m) as fp16, so that those
+//    lost below fp16's smallest are 2^-32 of the largest; sums are fp32 over the rounded weights.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "launch.cuh"
 #include "pkv_internal.h"
+#include "tcgen05.cuh"
 
 namespace {
 
 __device__ int g_dev_error_tree_attention = 0;
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error_tree_attention, 0, code); }
 
+using namespace pkv::tc;
+
+constexpr int BM = 128;            // rows of a product (MMA M)
+constexpr int BN = 64;             // key positions per tile
+constexpr int kMinTiles = 2;       // key tiles a CTA takes at least
+constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
+constexpr float kLift = 7.f;       // weights are kept as 2^(kLift + S - m)
+
+// A cut stream, as its first CTA notes it for the joining kernel (parts 0: none).
+struct Cut {
+  int parts, slot;                 // parts lie in slots slot, then 2 (w + 1), 2 (w + 2), .. of the CTAs that follow
+  int next;                        // the second part's slot
+  int rows, first_row, q0, kv_head, pad;
+};
+
 struct TreeParams {
+  CUtensorMap tmap_k, tmap_v;      // pools as (D, Hk B, num_blocks), boxes of 64 x B x 1, 128-byte swizzle
   const __half* q;
   const __half* k;
   const __half* v;
@@ -26,56 +65,837 @@ struct TreeParams {
   const int32_t* qstart;
   const uint32_t* mask;
   __half* out;
+  float2* ws_ml;                   // [2 workers][BM] (m, l), base-2 log domain
+  float* ws_o;                     // [2 workers][D][BM] unnormalised outputs
+  Cut* cuts;                       // [workers]
   int64_t q_stride;
   int mask_words, num_seqs, total_q, max_query_len;
   int num_heads, num_kv_heads, group, num_blocks, max_blocks, log2_block;
+  int use_tma, out_sectors;
   float scale_log2;
 };
 
-// grid (heads, max_query_len, sequences), a warp each
+// One sequence's share of the line: `tiles` key tiles for each of its num_kv_heads * row_tiles streams.
+struct Seq {
+  int ctx, n, q0, tiles, row_tiles;
+};
+__device__ __forceinline__ Seq seq_of(const TreeParams& p, int s, int* code) {
+  Seq x{0, 0, 0, 0, 0};
+  if (s >= p.num_seqs) return x;
+  x.ctx = p.lens[s];
+  x.q0 = p.qstart[s];
+  x.n = p.qstart[s + 1] - x.q0;
+  if (x.n == 0) return x;
+  if (x.ctx < 0 || x.ctx > (p.max_blocks << p.log2_block)) {
+    *code = PKV_DEV_BAD_CONTEXT_LEN;
+    return x;
+  }
+  if (x.n < 0 || x.n > x.ctx || x.n > p.max_query_len || x.q0 < 0 || x.q0 > p.total_q - x.n) {
+    *code = PKV_DEV_BAD_QUERY_RANGE;
+    return x;
+  }
+  x.tiles = (x.ctx + BN - 1) / BN;
+  x.row_tiles = (x.n * p.group + BM - 1) / BM;
+  return x;
+}
+
 template <int D>
-__global__ void __launch_bounds__(32) tree_attention_kernel(const TreeParams p) {
-  constexpr int V = D / 32;
+struct Cfg {
+  static constexpr int Q_BYTES = BM * D * 2;
+  static constexpr int KV_BYTES = BN * D * 2;
+  static constexpr int NS = D == 64 ? 4 : 2;                  // ring slots each for K and for V
+  static constexpr int BYTES = 1024 + Q_BYTES + 2 * NS * KV_BYTES + 512;
+  // so much that no third CTA, which would wait for tensor memory, fits an SM
+  static constexpr int SMEM = BYTES > 80 * 1024 ? BYTES : 80 * 1024;
+};
+// Tensor memory: the O accumulator and two S buffers of 64 columns, a half of the SM's 512 columns.
+constexpr uint32_t TMEM_COLS = 256, O_COL = 0, S_COL = 128;
+constexpr int W_K = 4, W_V = 5, W_S = 6, W_PV = 7;            // warps 0 to 3: softmax
+constexpr int THREADS = 256;
+
+// What a CTA does at a time: key tiles [tile0, tile0 + n_tiles) of one stream; n_tiles 0 ends the loop.
+struct Item {
+  int s, kv_head, first_row, rows, tile0, n_tiles, ctx, n, q0, slot;  // slot -1: the whole stream, to out
+};
+
+__device__ __forceinline__ bool finite16(unsigned h) { return (h & 0x7c00u) != 0x7c00u; }
+
+// Sixteen fp16 values to out: one 32-byte store where out's rows are whole sectors, else two of 16.
+__device__ __forceinline__ void store16(__half* dst, const uint32_t (&w)[8], bool sectors) {
+  if (sectors) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// A wait for the phase of `parity`, false once another role has raised the abort flag or after 2^19
+// tries (2 s: a failed try takes 3.9 us).
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_try_wait_parity(bar, parity); ++i)
+    if ((i & 1023u) == 0 && (*abort_flag != 0 || i >= (1u << 19))) return false;
+  return true;
+}
+
+// Which of the positions key0 .. key0 + 63 node i sees, those before the drafts (at first_new and on) all.
+__device__ __forceinline__ uint64_t seen_from(const TreeParams& p, int q_row, int i, int key0, int first_new) {
+  const int j0 = key0 - first_new;
+  if (j0 <= -BN) return ~0ull;
+  if (p.mask == nullptr) {
+    const int count = i + 1 - j0;
+    return count <= 0 ? 0 : count >= 64 ? ~0ull : (1ull << count) - 1;
+  }
+  const uint32_t* row = p.mask + static_cast<int64_t>(q_row) * p.mask_words;
+  auto word = [&](int w) { return w < p.mask_words ? row[w] : 0u; };
+  if (j0 < 0) return ((static_cast<uint64_t>(word(1)) << 32 | word(0)) << -j0) | ((1ull << -j0) - 1);
+  const int w = j0 >> 5, sh = j0 & 31;
+  const uint32_t x0 = word(w), x1 = word(w + 1), x2 = word(w + 2);
+  return static_cast<uint64_t>(__funnelshift_r(x1, x2, sh)) << 32 | __funnelshift_r(x0, x1, sh);
+}
+
+// Warp roles:
+//   0-3   softmax: waits S(j), releases K slot, masks, takes the row maximum (moving the running one, and
+//         O, only past 2^8), writes P over the scores and arrives on p_full; after an item's last tile its
+//         output or partial result.  A warp without rows only keeps step.
+//   W_K   finds the items and loads their K tiles
+//   W_V   loads the V tiles; those that some row does not see whole through registers
+//   W_S   gathers an item's Q; one lane issues S(j) = Q K(j)^T once K(j) landed and PV(j - 2), the last
+//         reader of its buffer, is done
+//   W_PV  one lane issues O += P(j) V(j) once V(j) and P(j) are there, then releases V
+// Key tiles are numbered through all of a CTA's items (j above), items too; every hand-off is an
+// mbarrier, and no waiter is more than one phase behind the barrier it waits on.  Every wait is
+// bounded; a role that gives up records PKV_DEV_WAIT_TIMEOUT and leaves its loop, the others give up
+// in turn, and the CTA still reaches its final barrier.
+template <int D>
+__global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid_constant__ TreeParams p) {
+  using C = Cfg<D>;
+  constexpr int NS = C::NS, CPR = D / 8;                      // 16-byte chunks per row
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* smem = smem_raw + (base - raw);
+  const uint32_t sq = base, sk = sq + C::Q_BYTES, sv = sk + NS * C::KV_BYTES, bars = sv + NS * C::KV_BYTES;
+  // per S buffer u (key tile j uses j % 2), per ring slot b, per item slot i (item number % 2)
+  auto s_full = [&](int u) { return bars + 8u * u; };
+  auto p_full = [&](int u) { return bars + 16u + 8u * u; };
+  auto pv_done = [&](int u) { return bars + 32u + 8u * u; };
+  auto item_full = [&](int i) { return bars + 48u + 8u * i; };
+  auto item_free = [&](int i) { return bars + 64u + 8u * i; };
+  const uint32_t q_free = bars + 80, o_free = bars + 88;
+  auto k_full = [&](int b) { return bars + 96u + 8u * b; };
+  auto v_full = [&](int b) { return bars + 96u + 8u * (NS + b); };
+  auto k_free = [&](int b) { return bars + 96u + 8u * (2 * NS + b); };
+  auto v_free = [&](int b) { return bars + 96u + 8u * (3 * NS + b); };
+  constexpr uint32_t AT = 96 + 32 * NS;
+  // per K slot: which of the tile's positions are in the context and in a block of the pool
+  volatile uint2* live = reinterpret_cast<volatile uint2*>(smem + (bars + AT - base));               // [NS]
+  volatile Item* items = reinterpret_cast<volatile Item*>(smem + (bars + AT + 8 * NS - base));       // [2]
+  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + AT + 8 * NS + 80 - base));  // [2]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + AT + 8 * NS + 88 - base));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + AT + 8 * NS + 92 - base));
+  static_assert(sizeof(Item) == 40 && AT + 8 * NS + 96 <= 512, "barrier area");
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pkv::pdl_trigger();
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  if (tid == 32) {
+    for (int u = 0; u < 2; ++u) {
+      mbar_init_count(s_full(u), 1);
+      mbar_init_count(p_full(u), 4);
+      mbar_init_count(pv_done(u), 1);
+      mbar_init_count(item_full(u), 1);
+      mbar_init_count(item_free(u), 7);                       // 4 softmax warps, both issuers, the V loader
+    }
+    mbar_init_count(q_free, 1);
+    mbar_init_count(o_free, 4);
+    for (int b = 0; b < NS; ++b) {
+      mbar_init_count(k_full(b), 1);
+      mbar_init_count(v_full(b), 1);
+      mbar_init_count(k_free(b), 4);
+      mbar_init_count(v_free(b), 1);
+    }
+    *abort_flag = 0;
+  }
+  if (tid == 64 && p.use_tma) {
+    prefetch_tensormap(&p.tmap_k);
+    prefetch_tensormap(&p.tmap_v);
+  }
+  pkv::pdl_wait();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto t_s = [&](int u) { return tmem + S_COL + 64u * u; };
+  const uint32_t t_o = tmem + O_COL;
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag); };
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+  auto give_up = [&]() {
+    if (!*abort_flag) record_error(PKV_DEV_WAIT_TIMEOUT);
+    *abort_flag = 1;
+  };
+  auto take_item = [&](int it, Item& item) {
+    if (!wait(item_full(it & 1), (it >> 1) & 1)) return false;
+    const volatile Item& x = items[it & 1];
+    item.s = x.s;
+    item.kv_head = x.kv_head;
+    item.first_row = x.first_row;
+    item.rows = x.rows;
+    item.tile0 = x.tile0;
+    item.n_tiles = x.n_tiles;
+    item.ctx = x.ctx;
+    item.n = x.n;
+    item.q0 = x.q0;
+    item.slot = x.slot;
+    return true;
+  };
+  const int lb = p.log2_block, B = 1 << lb;
+  bool failed = false;
+
+  if (warp == W_K || warp == W_V) {
+    // ---------------- loads ----------------
+    const bool is_k = warp == W_K;
+    const __half* pool = is_k ? p.k : p.v;
+    const CUtensorMap* map = is_k ? &p.tmap_k : &p.tmap_v;
+    const uint32_t ring = is_k ? sk : sv;
+    constexpr int ROWS = 32 / CPR;                            // rows per warp-wide copy
+    const int c = lane % CPR, rsub = lane / CPR;              // this lane's chunk and row offset
+    const int nb = BN >> lb;                                  // blocks per tile
+    const uint32_t all_blocks = (1u << nb) - 1u;
+    // the K loader's place on the line: sequence, stream of it, tile, and what is left of the piece
+    Seq seq{};
+    int s = 0, stream = 0, tile = 0;
+    long long left = 0;
+    bool notes = false;                                       // this CTA's Cut is written
+    const int worker = blockIdx.x;
+    long long per = 0, x = 0;
+    if (is_k) {
+      const int H = p.num_kv_heads;
+      long long total = 0;
+      int code = 0;
+      for (int i = lane; i < p.num_seqs; i += 32) {
+        const Seq y = seq_of(p, i, &code);
+        total += static_cast<long long>(y.tiles) * y.row_tiles * H;
+      }
+      if (code && worker == 0) record_error(code);
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xffffffffu, total, o);
+      per = (total + gridDim.x - 1) / gridDim.x;
+      if (per < kMinTiles) per = kMinTiles;
+      x = worker * per;
+      left = min(per, total - x);
+      if (left > 0) {
+        // the sequence: the first whose tiles, all streams together, reach past x
+        long long before = 0;
+        s = p.num_seqs;
+        for (int first = 0; first < p.num_seqs; first += 32) {
+          const Seq y = seq_of(p, first + lane, &code);
+          const long long mine = static_cast<long long>(y.tiles) * y.row_tiles * H;
+          long long upto = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o *= 2) {
+            const long long z = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += z;
+          }
+          const unsigned past = __ballot_sync(0xffffffffu, before + upto > x);
+          if (past) {
+            const int hit = __ffs(past) - 1;
+            s = first + hit;
+            before += __shfl_sync(0xffffffffu, upto - mine, hit);
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        seq = seq_of(p, s, &code);
+        if (seq.tiles == 0) {
+          left = 0;                                           // the lengths changed meanwhile
+        } else {
+          stream = static_cast<int>((x - before) / seq.tiles);
+          tile = static_cast<int>((x - before) % seq.tiles);
+        }
+      }
+    }
+    int j = 0;
+    for (int it = 0;; ++it) {
+      Item item;
+      if (is_k) {
+        // the next item, for all roles
+        item.n_tiles = left > 0 ? static_cast<int>(min(left, static_cast<long long>(seq.tiles - tile))) : 0;
+        if (item.n_tiles > 0) {
+          item.s = s;
+          item.kv_head = stream / seq.row_tiles;
+          item.first_row = stream % seq.row_tiles * BM;
+          item.rows = min(BM, seq.n * p.group - item.first_row);
+          item.tile0 = tile;
+          item.ctx = seq.ctx;
+          item.n = seq.n;
+          item.q0 = seq.q0;
+          item.slot = item.n_tiles == seq.tiles ? -1 : 2 * worker + (it > 0);
+        }
+        if (it >= 2 && !warp_wait(item_free(it & 1), ((it >> 1) - 1) & 1)) {
+          failed = true;
+          break;
+        }
+        if (lane == 0) {
+          volatile Item& out = items[it & 1];
+          out.n_tiles = item.n_tiles;
+          if (item.n_tiles > 0) {
+            out.s = item.s;
+            out.kv_head = item.kv_head;
+            out.first_row = item.first_row;
+            out.rows = item.rows;
+            out.tile0 = item.tile0;
+            out.ctx = item.ctx;
+            out.n = item.n;
+            out.q0 = item.q0;
+            out.slot = item.slot;
+          }
+          mbar_arrive(item_full(it & 1));
+        }
+        __syncwarp();
+        if (item.n_tiles > 0 && tile == 0 && item.n_tiles < seq.tiles) {
+          // a cut stream's first part: the others are the first items of the CTAs that follow
+          notes = true;
+          if (lane == 0) {
+            Cut cut{};
+            cut.parts = 1 + static_cast<int>((seq.tiles - item.n_tiles + per - 1) / per);
+            cut.parts = min(cut.parts, static_cast<int>(gridDim.x) - worker);
+            cut.slot = item.slot;
+            cut.next = 2 * (worker + 1);
+            cut.rows = item.rows;
+            cut.first_row = item.first_row;
+            cut.q0 = item.q0;
+            cut.kv_head = item.kv_head;
+            p.cuts[worker] = cut;
+          }
+        }
+      } else {
+        if (!__all_sync(0xffffffffu, take_item(it, item))) {
+          failed = true;
+          break;
+        }
+        if (lane == 0) not_finite[it & 1] = 0;
+        __syncwarp();
+      }
+      if (item.n_tiles == 0) break;
+      const int32_t* table = p.tables + static_cast<size_t>(item.s) * p.max_blocks;
+      const int first_new = item.ctx - item.n;
+      auto entry = [&](int tile_no) {                         // this lane's table entry for a tile
+        const int t0 = tile_no * BN + (lane << lb);
+        return lane < nb && t0 < item.ctx ? __ldg(table + (t0 >> lb)) : -1;
+      };
+      int next_entry = entry(item.tile0);
+      bool found = false;                                     // V: a value that is not finite
+      for (int i = 0; i < item.n_tiles; ++i, ++j) {
+        const int b = j % NS, key0 = (item.tile0 + i) * BN, t0 = key0 + (lane << lb);
+        const bool in_ctx = lane < nb && t0 < item.ctx;
+        int phys = next_entry;
+        if (i + 1 < item.n_tiles) next_entry = entry(item.tile0 + i + 1);
+        const bool good = in_ctx && phys >= 0 && phys < p.num_blocks;
+        if (is_k && in_ctx && !good) record_error(PKV_DEV_BAD_BLOCK_ID);
+        if (!good) phys = -1;
+        const uint32_t good_mask = __ballot_sync(0xffffffffu, good);
+        if (j >= NS && !warp_wait(is_k ? k_free(b) : v_free(b), (j / NS - 1) & 1)) {
+          failed = true;
+          break;
+        }
+        const uint32_t full = is_k ? k_full(b) : v_full(b), dst = ring + b * C::KV_BYTES;
+        if (is_k) {
+          // K rows past the context or of bad blocks may hold anything: their scores are masked
+          const int valid = good ? min(B, item.ctx - t0) : 0, at = lane << lb & 31;
+          const uint32_t bits = (valid >= 32 ? 0xffffffffu : (1u << valid) - 1u) << at;
+          const uint32_t lo = __reduce_or_sync(0xffffffffu, lane << lb < 32 ? bits : 0u);
+          const uint32_t hi = __reduce_or_sync(0xffffffffu, lane << lb < 32 ? 0u : bits);
+          if (lane == 0) {
+            live[b].x = lo;
+            live[b].y = hi;
+          }
+        }
+        const bool care = !is_k && (good_mask != all_blocks || key0 + BN > first_new);
+        if (p.use_tma && !care) {
+          if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(good_mask)) * B * D * 2);
+          __syncwarp();
+          if (good) {
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half)
+              tma_load_3d(dst + half * (BN * 128) + lane * B * 128, map, half * 64, item.kv_head * B, phys, full);
+          }
+          continue;
+        }
+        if (!care) {
+          for (int r0 = 0; r0 < BN; r0 += ROWS) {
+            const int pb = __shfl_sync(0xffffffffu, phys, r0 >> lb), r = r0 + rsub;   // ROWS <= 4 <= B: one block
+            const __half* src = pool + (((static_cast<size_t>(max(pb, 0)) * p.num_kv_heads + item.kv_head) << lb) + (r & (B - 1))) * D + c * 8;
+            cp_async16(dst + sw128(r, c, BN), src, pb >= 0 ? 16 : 0);
+          }
+          cp_async_wait_all();
+        } else {
+          // zeros where there is no row, and for a draft's values that are not finite
+          constexpr int FLY = 8;
+#pragma unroll 1
+          for (int r0 = 0; r0 < BN; r0 += ROWS * FLY) {
+            uint4 w[FLY];
+#pragma unroll
+            for (int u = 0; u < FLY; ++u) {
+              const int rb = r0 + u * ROWS, pb = __shfl_sync(0xffffffffu, phys, rb >> lb), r = rb + rsub;
+              w[u] = make_uint4(0, 0, 0, 0);
+              if (pb >= 0 && key0 + r < item.ctx)
+                w[u] = *reinterpret_cast<const uint4*>(
+                    pool + (((static_cast<size_t>(pb) * p.num_kv_heads + item.kv_head) << lb) + (r & (B - 1))) * D + c * 8);
+            }
+#pragma unroll
+            for (int u = 0; u < FLY; ++u) {
+              const int r = r0 + u * ROWS + rsub;
+              if (key0 + r >= first_new) {
+                uint32_t* e = reinterpret_cast<uint32_t*>(&w[u]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const bool ok0 = finite16(e[k]), ok1 = finite16(e[k] >> 16);
+                  found |= !ok0 || !ok1;
+                  e[k] = (ok0 ? e[k] & 0xffffu : 0u) | (ok1 ? e[k] & 0xffff0000u : 0u);
+                }
+              }
+              *reinterpret_cast<uint4*>(smem + (dst + sw128(r, c, BN) - base)) = w[u];
+            }
+          }
+        }
+        fence_proxy_async_smem();                             // these writes -> tensor-core reads
+        if (found) not_finite[it & 1] = 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+      }
+      if (failed) break;
+      if (is_k) {
+        left -= item.n_tiles;
+        tile += item.n_tiles;
+        if (tile == seq.tiles && left > 0) {
+          tile = 0;
+          if (++stream == p.num_kv_heads * seq.row_tiles) {
+            stream = 0;
+            int code = 0;
+            do seq = seq_of(p, ++s, &code);
+            while (seq.tiles == 0 && s < p.num_seqs);
+            if (seq.tiles == 0) left = 0;                     // the lengths changed meanwhile
+          }
+        }
+      } else {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_free(it & 1));
+      }
+    }
+    if (is_k && !notes && lane == 0) p.cuts[worker].parts = 0;
+    if (failed) give_up();
+    if (*abort_flag) {
+      // let the copies this warp issued land (bounded) before the CTA's shared memory is released
+      for (int t = max(0, j - NS); t < j; ++t) mbar_wait(is_k ? k_full(t % NS) : v_full(t % NS), (t / NS) & 1);
+    }
+  } else if (warp == W_S) {
+    // ---------------- Q, and S = Q K^T issue (one lane) ----------------
+    constexpr uint32_t IDESC_QK = umma_idesc_f16(BM, BN, false);
+    const uint64_t a0 = umma_smem_desc(sq, 16, 1024);
+    int j = 0;
+    for (int it = 0;; ++it) {
+      Item item;
+      if (!__all_sync(0xffffffffu, take_item(it, item) && (it == 0 || wait(q_free, (it - 1) & 1)))) {
+        failed = true;
+        break;
+      }
+      if (item.n_tiles == 0) break;
+      // Rows past the item's hold what was there: a row of the product depends on its own alone.
+      for (int k = lane; k < item.rows * CPR; k += 32) {
+        const int r = k / CPR, c = k % CPR, row = item.first_row + r, i = row / p.group, g = row - i * p.group;
+        cp_async16(sq + sw128(r, c, BM), p.q + (item.q0 + i) * p.q_stride + (item.kv_head * p.group + g) * D + c * 8, 16);
+      }
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(item_free(it & 1));
+        for (int i = 0; i < item.n_tiles; ++i, ++j) {
+          const int u = j & 1;
+          if (!wait(k_full(j % NS), (j / NS) & 1) || (j >= 2 && !wait(pv_done(u), ((j - 2) >> 1) & 1))) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t b0 = umma_smem_desc(sk + (j % NS) * C::KV_BYTES, 16, 1024);
+          const uint32_t d = t_s(u);
+          umma_ss(d, a0, b0, IDESC_QK, 0u);
+#pragma unroll
+          for (int kk = 1; kk < D / 16; ++kk)
+            umma_ss(d, a0 + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4),
+                    b0 + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), IDESC_QK, 1u);
+          umma_commit(s_full(u));
+        }
+        if (!failed) umma_commit(q_free);
+      }
+      j = __shfl_sync(0xffffffffu, j, 0);
+      failed = __shfl_sync(0xffffffffu, failed, 0);
+      if (failed) break;
+    }
+    if (failed) {
+      give_up();
+      if (j > 0) mbar_wait(s_full((j - 1) & 1), ((j - 1) >> 1) & 1);
+    }
+  } else if (warp == W_PV) {
+    // ---------------- O += P V issue (one lane) ----------------
+    if (lane == 0) {
+      constexpr uint32_t IDESC_PV = umma_idesc_f16(BM, D, true);
+      int j = 0;
+      for (int it = 0; !failed; ++it) {
+        Item item;
+        if (!take_item(it, item)) failed = true;
+        if (failed || item.n_tiles == 0) break;
+        mbar_arrive(item_free(it & 1));
+        for (int i = 0; i < item.n_tiles; ++i, ++j) {
+          const int u = j & 1, b = j % NS;
+          // the first product overwrites the accumulator: the last item's output has been read
+          if (!wait(v_full(b), (j / NS) & 1) || (i == 0 && it > 0 && !wait(o_free, (it - 1) & 1)) ||
+              !wait(p_full(u), (j >> 1) & 1)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t v0 = umma_smem_desc(sv + b * C::KV_BYTES, BN * 128, 1024);
+          const uint32_t pa = t_s(u);
+          umma_ts(t_o, pa, v0, IDESC_PV, i > 0 ? 1u : 0u);
+#pragma unroll
+          for (int kk = 1; kk < BN / 16; ++kk) umma_ts(t_o, pa + kk * 8, v0 + ((kk * 16 * 128) >> 4), IDESC_PV, 1u);
+          umma_commit(pv_done(u));
+          umma_commit(v_free(b));
+        }
+      }
+      if (failed) {
+        give_up();
+        if (j > 0) mbar_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax and output ----------------
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    int j = 0;
+    for (int it = 0; !failed; ++it) {
+      Item item;
+      // decisions stay warp-uniform: the tcgen05.ld/st below are warp-collective
+      if (!__all_sync(0xffffffffu, take_item(it, item))) failed = true;
+      if (failed || item.n_tiles == 0) break;
+      const bool works = warp * 32 < item.rows;
+      const int row = item.first_row + min(tid, item.rows - 1), node = row / p.group, first_new = item.ctx - item.n;
+      float l = 0.f, m_ref = -INFINITY;
+      for (int i = 0; i < item.n_tiles; ++i, ++j) {
+        const int u = j & 1, key0 = (item.tile0 + i) * BN;
+        const uint32_t ts = t_s(u);
+        if (!warp_wait(s_full(u), (j >> 1) & 1)) {
+          failed = true;
+          break;
+        }
+        if (!works) {
+          if (lane == 0) {
+            mbar_arrive(k_free(j % NS));
+            mbar_arrive(p_full(u));
+          }
+          continue;
+        }
+        tc_fence_after();
+        const uint32_t live_lo = live[j % NS].x, live_hi = live[j % NS].y;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_free(j % NS));
+        float sv_[BN];
+        tmem_ld32_nowait(ts + lane_off, *reinterpret_cast<float(*)[32]>(sv_));
+        tmem_ld32_nowait(ts + lane_off + 32, *reinterpret_cast<float(*)[32]>(sv_ + 32));
+        tmem_ld_wait();
+        if (key0 + BN > first_new || (live_lo & live_hi) != 0xffffffffu) {
+          const uint64_t seen = seen_from(p, item.q0 + node, node, key0, first_new);
+          const uint32_t lo = static_cast<uint32_t>(seen) & live_lo, hi = static_cast<uint32_t>(seen >> 32) & live_hi;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (!(lo >> c & 1)) sv_[c] = -INFINITY;
+            if (!(hi >> c & 1)) sv_[32 + c] = -INFINITY;
+          }
+        }
+        float m8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m8[e] = fmaxf(sv_[e], sv_[8 + e]);
+#pragma unroll
+        for (int c = 16; c < BN; c += 16)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m8[e] = max3(m8[e], sv_[c + e], sv_[c + 8 + e]);
+        float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        mx *= p.scale_log2;
+        const bool rescale = mx > m_ref + kRescale;           // also the first finite maximum
+        float alpha = 1.f;
+        if (rescale) {
+          alpha = exp2f(m_ref - mx);
+          m_ref = mx;
+        }
+        const float nref = m_ref == -INFINITY ? 0.f : kLift - m_ref;
+        if (__any_sync(0xffffffffu, rescale && i > 0)) {
+          if (!warp_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld32(t_o + lane_off + c * 32, o);
+            uint32_t ob[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e] * alpha);
+            tmem_st32(t_o + lane_off + c * 32, ob);
+          }
+        }
+        // P as fp16; the row sum adds the rounded weights, the ones that multiply V
+        float sum8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[BN / 2];
+#pragma unroll
+        for (int e = 0; e < BN / 2; ++e) {
+          float x0, x1;
+          fma2(x0, x1, sv_[2 * e], sv_[2 * e + 1], p.scale_log2, nref);
+          pk[e] = pack_half2(fast_exp2(x0), fast_exp2(x1));
+          add_half2(sum8[2 * (e & 3)], sum8[2 * (e & 3) + 1], pk[e]);
+        }
+        float sum4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum4[e] = sum8[2 * e] + sum8[2 * e + 1];
+        tmem_st32(ts + lane_off, pk);
+        l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(u));
+      }
+      if (!failed) failed = !warp_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1);
+      if (failed) break;
+      tc_fence_after();
+      if (works) {
+        // 32 columns at a time: the row to out, whole 32-byte sectors at once, or to the workspace, where
+        // a column's rows lie side by side
+        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // a row that sees nothing is zeros
+        const bool fix = not_finite[it & 1] != 0, real = tid < item.rows;
+        const int head = item.kv_head * p.group + (row - node * p.group);
+        __half* dst = p.out + (static_cast<size_t>(item.q0 + node) * p.num_heads + head) * D;
+        float* part = p.ws_o + static_cast<size_t>(max(item.slot, 0)) * D * BM + tid;
+        if (item.slot >= 0 && real) p.ws_ml[static_cast<size_t>(item.slot) * BM + tid] = make_float2(m_ref, l);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float x[32];
+          tmem_ld32(t_o + lane_off + c * 32, x);
+          if (fix) {
+            // values of drafts that are not finite, where the row sees them (rare, so small rather than fast)
+            const int from = max(first_new, item.tile0 * BN), to = min(item.ctx, (item.tile0 + item.n_tiles) * BN);
+#pragma unroll 1
+            for (int t = from; t < to; ++t) {
+              const int phys = p.tables[static_cast<size_t>(item.s) * p.max_blocks + (t >> lb)];
+              if (!(seen_from(p, item.q0 + node, node, t, first_new) & 1) || phys < 0 || phys >= p.num_blocks) continue;
+              const __half* v = p.v + (((static_cast<size_t>(phys) * p.num_kv_heads + item.kv_head) << lb) + (t & (B - 1))) * D + c * 32;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!finite16(__half_as_ushort(v[e]))) x[e] += __half2float(v[e]);
+            }
+            __syncwarp();
+          }
+          if (item.slot >= 0) {
+            if (real) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) part[(c * 32 + e) * BM] = x[e];
+            }
+          } else if (real) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w[k] = pack_half2(x[e + 2 * k] * inv, x[e + 2 * k + 1] * inv);
+              store16(dst + c * 32 + e, w, p.out_sectors);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(o_free);
+        mbar_arrive(item_free(it & 1));
+      }
+    }
+    if (failed) give_up();
+  }
+
+  // every tensor-memory access is done (tcgen05.ld and .st wait inline, the products are committed)
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+  }
+}
+
+// Joins the parts of the cut streams: CTA (w, y) columns 32 y .. of the one that CTA w of the grid before noted.
+// A thread takes a row and four columns at a time; where rows are few, groups of threads share the parts.
+// (CTA 0 of the grid before may note one, the last cannot: its last stream ends with it.)
+constexpr int JOIN_THREADS = 512;
+template <int D>
+__global__ void __launch_bounds__(JOIN_THREADS) tree_attention_join_kernel(const __grid_constant__ TreeParams p) {
+  __shared__ float group_m[JOIN_THREADS], group_l[JOIN_THREADS], group_o[4][JOIN_THREADS];
   pkv::pdl_trigger();
   pkv::pdl_wait();
-  const int h = blockIdx.x, i = blockIdx.y, s = blockIdx.z, lane = threadIdx.x, B = 1 << p.log2_block;
-  const int q0 = p.qstart[s], n = p.qstart[s + 1] - q0, ctx = p.lens[s];
-  if (n == 0 || i >= max(n, 1)) return;
-  if (ctx < 0 || ctx > p.max_blocks * B) {
-    if (lane == 0) record_error(PKV_DEV_BAD_CONTEXT_LEN);
-    return;
-  }
-  if (n < 0 || n > ctx || n > p.max_query_len || q0 < 0 || q0 > p.total_q - n) {
-    if (lane == 0) record_error(PKV_DEV_BAD_QUERY_RANGE);
-    return;
-  }
-  float q[V], o[V], m = -INFINITY, l = 0.f;
-  for (int c = 0; c < V; ++c) {
-    q[c] = __half2float(p.q[(q0 + i) * p.q_stride + h * D + lane * V + c]);
-    o[c] = 0.f;
-  }
-  for (int t = 0; t < ctx; ++t) {
-    const int j = t - (ctx - n);
-    if (j >= 0) {
-      if (p.mask == nullptr ? j > i : (p.mask[static_cast<int64_t>(q0 + i) * p.mask_words + j / 32] >> (j % 32) & 1) == 0) continue;
+  const Cut cut = p.cuts[blockIdx.x];
+  if (cut.parts <= 1) return;
+  int rp = 8;                                                 // the rows, to a power of two
+  while (rp < cut.rows) rp *= 2;
+  const int groups = max(1, JOIN_THREADS / (rp * 8));         // that share the parts
+  const int tid = threadIdx.x, r = tid & (rp - 1), cg = (tid / rp) & 7, pg = tid / (rp * 8);
+  const bool real = r < cut.rows;
+  auto slot_of = [&](int part) { return static_cast<size_t>(part == 0 ? cut.slot : cut.next + 2 * (part - 1)); };
+  const int row = cut.first_row + min(r, cut.rows - 1), node = row / p.group, head = cut.kv_head * p.group + row - node * p.group;
+  __half* dst = p.out + (static_cast<size_t>(cut.q0 + node) * p.num_heads + head) * D + blockIdx.y * 32;
+  // with 128 rows a thread takes two groups of columns, one after the other
+  for (int col = cg * 4; col < 32; col += max(1, JOIN_THREADS / rp) >= 8 ? 32 : JOIN_THREADS / rp * 4) {
+    float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int FLY = 4;
+    for (int k0 = pg; k0 < cut.parts; k0 += groups * FLY) {
+      float2 ml[FLY];
+      float x[FLY][4];
+#pragma unroll
+      for (int u = 0; u < FLY; ++u) {
+        const int k = k0 + u * groups;
+        ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[u][e] = 0.f;
+        if (k < cut.parts && real) {
+          ml[u] = p.ws_ml[slot_of(k) * BM + r];
+          const float* src = p.ws_o + (slot_of(k) * D + blockIdx.y * 32 + col) * BM + r;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][e] = src[e * BM];
+        }
+      }
+      float m = M;
+#pragma unroll
+      for (int u = 0; u < FLY; ++u) m = fmaxf(m, ml[u].x);
+      const float base = m == -INFINITY ? 0.f : m, carry = exp2f(M - base);   // nothing seen so far: 0
+      L *= carry;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] *= carry;
+#pragma unroll
+      for (int u = 0; u < FLY; ++u) {
+        // a part that saw nothing is left out; one with a NaN is not
+        if (ml[u].x == -INFINITY && ml[u].y == 0.f) continue;
+        const float f = exp2f(ml[u].x - base);
+        L = fmaf(ml[u].y, f, L);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[u][e], f, acc[e]);
+      }
+      M = m;
     }
-    const int phys = p.tables[static_cast<int64_t>(s) * p.max_blocks + (t >> p.log2_block)];
-    if (phys < 0 || phys >= p.num_blocks) {
-      if (lane == 0) record_error(PKV_DEV_BAD_BLOCK_ID);
-      continue;
+    if (groups > 1) {
+      group_m[tid] = M;
+      group_l[tid] = L;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) group_o[e][tid] = acc[e];
+      __syncthreads();
+      if (pg == 0) {
+        for (int g = 1; g < groups; ++g) {
+          const int other = tid + g * rp * 8;
+          const float om = group_m[other], m = fmaxf(M, om), a = M == -INFINITY ? 0.f : exp2f(M - m),
+                      b = om == -INFINITY ? 0.f : exp2f(om - m);
+          M = m;
+          L = L * a + group_l[other] * b;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] = acc[e] * a + group_o[e][other] * b;
+        }
+      }
     }
-    const int64_t at = (((static_cast<int64_t>(phys) * p.num_kv_heads + h / p.group) << p.log2_block) + (t & (B - 1))) * D + lane * V;
-    float dot = 0.f;
-    for (int c = 0; c < V; ++c) dot = fmaf(q[c], __half2float(p.k[at + c]), dot);
-    for (int d = 16; d > 0; d /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-    const float x = dot * p.scale_log2, top = fmaxf(m, x), f = exp2f(m - top), w = exp2f(x - top);
-    m = top;
-    l = fmaf(l, f, w);
-    for (int c = 0; c < V; ++c) o[c] = fmaf(o[c], f, w * __half2float(p.v[at + c]));
+    if (pg == 0 && real) {
+      const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
+      *reinterpret_cast<uint2*>(dst + col) = make_uint2(pack_half2(acc[0] * inv, acc[1] * inv), pack_half2(acc[2] * inv, acc[3] * inv));
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int c = 0; c < V; ++c)
-    p.out[(static_cast<int64_t>(q0 + i) * p.num_heads + h) * D + lane * V + c] = __float2half_rn(o[c] * inv);
+}
+
+int device_sms() {
+  static std::mutex mu;
+  static int cache[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  std::lock_guard<std::mutex> g(mu);
+  if (!cache[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+    cache[dev] = n;
+  }
+  return cache[dev];
+}
+
+// Two CTAs to an SM, or as many as the longest contexts would give kMinTiles key tiles each.
+struct Plan {
+  int workers;
+  long long most_tiles;
+};
+Plan plan_for(int num_seqs, int total_q, int max_query_len, int num_heads, int num_kv_heads, long long max_ctx) {
+  Plan pl{};
+  const int group = num_heads / num_kv_heads;
+  // streams: a sequence has one row tile at least, and all of them no more than their rows fill
+  const long long rows = static_cast<long long>(max_query_len) * group, per_seq = (rows + BM - 1) / BM;
+  const long long by_rows = num_seqs + static_cast<long long>(total_q) * group / BM;
+  const long long row_tiles = per_seq * num_seqs < by_rows ? per_seq * num_seqs : by_rows;
+  pl.most_tiles = row_tiles * num_kv_heads * ((max_ctx + BN - 1) / BN);
+  const long long want = (pl.most_tiles + kMinTiles - 1) / kMinTiles, most = 2 * device_sms();
+  pl.workers = static_cast<int>(want < most ? want : most);
+  return pl;
+}
+size_t ml_bytes(int workers) { return static_cast<size_t>(workers) * 2 * BM * sizeof(float2); }
+size_t cut_bytes(int workers) { return static_cast<size_t>(workers) * sizeof(Cut); }
+size_t workspace_bytes_for(const Plan& pl, int head_dim) {
+  return ml_bytes(pl.workers) + cut_bytes(pl.workers) + static_cast<size_t>(pl.workers) * 2 * BM * head_dim * sizeof(float);
+}
+
+// A pool [num_blocks][H][B][D] fp16 as the 3-D tensor (D, H B, num_blocks); a box is one head's B rows of one
+// 64-element half of the head dimension, written with the 128-byte swizzle.
+int encode_pool_map(const char* fn, CUtensorMap* map, const void* pool, int D, int H, int B, int num_blocks) {
+  const EncodeTiledFn encode = tensor_map_encoder();
+  if (!encode) return pkv::fail(PKV_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available", fn);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H) * B, static_cast<cuuint64_t>(num_blocks)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(H) * B * D * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(B), 1};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(pool), dims, strides, box, elem,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return pkv::fail(PKV_ERR_CUDA, "%s: tensor map encoding failed (%d)", fn, static_cast<int>(r));
+  return PKV_OK;
+}
+
+template <int D>
+int launch(const char* fn, const TreeParams& p, int workers, cudaStream_t st) {
+  using C = Cfg<D>;
+  static std::mutex mu;
+  static bool done[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) {
+    std::lock_guard<std::mutex> g(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+      e = cudaFuncSetAttribute(tree_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+      if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    }
+  }
+  if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s setup: %s", fn, cudaGetErrorString(e));
+  e = pkv::launch_pdl(tree_attention_kernel<D>, dim3(workers), dim3(THREADS), C::SMEM, st, p);
+  if (e == cudaSuccess && workers > 1)
+    e = pkv::launch_pdl(tree_attention_join_kernel<D>, dim3(workers - 1, D / 32), dim3(JOIN_THREADS), 0, st, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+  return PKV_OK;
 }
 
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
@@ -93,9 +913,13 @@ extern "C" {
 size_t pkv_paged_attention_tree_workspace_size(int num_seqs, int total_q, int max_query_len, int num_heads,
                                                int num_kv_heads, int head_dim, int max_blocks_per_seq,
                                                int block_size) {
-  (void)num_seqs, (void)total_q, (void)max_query_len, (void)num_heads, (void)num_kv_heads, (void)head_dim;
-  (void)max_blocks_per_seq, (void)block_size;
-  return 0;
+  if (num_seqs <= 0 || total_q <= 0 || max_query_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+      num_heads % num_kv_heads || head_dim <= 0 || max_blocks_per_seq <= 0 || block_size <= 0 ||
+      static_cast<long long>(max_blocks_per_seq) * block_size > (1LL << 30))
+    return 0;
+  return workspace_bytes_for(plan_for(num_seqs, total_q, max_query_len, num_heads, num_kv_heads,
+                                      static_cast<long long>(max_blocks_per_seq) * block_size),
+                             head_dim);
 }
 
 int pkv_paged_attention_tree(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache, const uint16_t* v_cache,
@@ -124,8 +948,10 @@ int pkv_paged_attention_tree(const uint16_t* q, int64_t q_stride, const uint16_t
     pkv::clear_error();
     return PKV_OK;
   }
-  if (num_seqs > 65535 || num_heads > 65535 || max_query_len > 65535)
-    return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: num_seqs/num_heads/max_query_len above 65535", fn);
+  if (num_seqs > 65535 || num_heads > 65535)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: num_seqs/num_heads above 65535", fn);
+  if (static_cast<long long>(max_query_len) * (num_heads / num_kv_heads) > (1LL << 26))
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: more than 2^26 rows to a cached head", fn);
   if (static_cast<long long>(max_blocks_per_seq) * block_size > (1LL << 30))
     return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: context capacity above 2^30 tokens", fn);
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start || !out)
@@ -136,7 +962,14 @@ int pkv_paged_attention_tree(const uint16_t* q, int64_t q_stride, const uint16_t
     return pkv::fail(PKV_ERR_INVALID_ARG, "%s: q_stride must be a multiple of 8 and at least a token's length", fn);
   if (!std::isfinite(scale) || !(scale > 0.f))
     return pkv::fail(PKV_ERR_INVALID_ARG, "%s: scale must be finite and positive", fn);
-  (void)workspace_bytes;
+  const Plan pl = plan_for(num_seqs, total_q, max_query_len, num_heads, num_kv_heads,
+                           static_cast<long long>(max_blocks_per_seq) * block_size);
+  const size_t need = workspace_bytes_for(pl, head_dim);
+  if (!workspace || workspace_bytes < need)
+    return pkv::fail(PKV_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                     workspace ? workspace_bytes : static_cast<size_t>(0));
+  if (pl.most_tiles / pl.workers >= (1LL << 30))
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "%s: more than 2^30 key tiles to a CTA", fn);
   TreeParams p{};
   p.q = reinterpret_cast<const __half*>(q);
   p.k = reinterpret_cast<const __half*>(k_cache);
@@ -158,14 +991,21 @@ int pkv_paged_attention_tree(const uint16_t* q, int64_t q_stride, const uint16_t
   p.max_blocks = max_blocks_per_seq;
   while ((1 << p.log2_block) < block_size) ++p.log2_block;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const dim3 grid(num_heads, max_query_len, num_seqs);
+  p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+  p.ws_ml = static_cast<float2*>(workspace);
+  p.cuts = reinterpret_cast<Cut*>(static_cast<char*>(workspace) + ml_bytes(pl.workers));
+  p.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(pl.workers) + cut_bytes(pl.workers));
+  // whole blocks of 8 or more rows are fetched by TMA; smaller blocks by 16-byte copies
+  p.use_tma = block_size >= 8 ? 1 : 0;
+  if (p.use_tma) {
+    int rc = encode_pool_map(fn, &p.tmap_k, k_cache, head_dim, num_kv_heads, block_size, num_blocks);
+    if (rc == PKV_OK) rc = encode_pool_map(fn, &p.tmap_v, v_cache, head_dim, num_kv_heads, block_size, num_blocks);
+    if (rc != PKV_OK) return rc;
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = head_dim == 128 ? pkv::launch_pdl(tree_attention_kernel<128>, grid, dim3(32), 0, st, p)
-                                  : pkv::launch_pdl(tree_attention_kernel<64>, grid, dim3(32), 0, st, p);
-  if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
-  pkv::clear_error();
-  return PKV_OK;
+  const int rc = head_dim == 128 ? launch<128>(fn, p, pl.workers, st) : launch<64>(fn, p, pl.workers, st);
+  if (rc == PKV_OK) pkv::clear_error();
+  return rc;
 }
 
 }  // extern "C"
