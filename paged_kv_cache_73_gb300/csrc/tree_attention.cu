@@ -18,9 +18,9 @@
 //    log-sum-exp identity; the first CTA of such a stream notes where they lie.  A CTA has at most
 //    two such parts, the first and the last of its piece.
 //  * K and V blocks come by TMA (one box per block and 64 columns) into the 128-byte swizzle.  V tiles
-//    that some row does not see whole (drafts, the context's end, a block outside the pool) come through
-//    registers instead: a masked weight of 0 times a value that is not finite would be a NaN, so such
-//    values of drafts become zeros, are noted, and put back in the end for the rows that see them.
+//    that some row does not see whole (drafts, the context's end) are looked over in shared memory before their
+//    product: a masked weight of 0 times a value that is not finite would be a NaN, so such values of
+//    drafts become zeros, are noted, and put back in the end for the rows that see them.
 //  * Softmax as in prompt attention: a thread owns a row (a lane of tensor memory); the maximum, and with
 //    it O, moves only when a tile passes it by 2^8; weights are 2^(7 + S - m) as fp16, so that those
 //    lost below fp16's smallest are 2^-32 of the largest; sums are fp32 over the rounded weights.
@@ -45,6 +45,7 @@ using namespace pkv::tc;
 constexpr int BM = 128;            // rows of a product (MMA M)
 constexpr int BN = 64;             // key positions per tile
 constexpr int kMinTiles = 2;       // key tiles a CTA takes at least
+constexpr int kStart = 1;          // what a stream costs besides its key tiles, in key tiles
 constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
 constexpr float kLift = 7.f;       // weights are kept as 2^(kLift + S - m)
 
@@ -75,7 +76,8 @@ struct TreeParams {
   float scale_log2;
 };
 
-// One sequence's share of the line: `tiles` key tiles for each of its num_kv_heads * row_tiles streams.
+// One sequence's share of the line: kStart places that hold no work and `tiles` key tiles for each of its
+// num_kv_heads * row_tiles streams.
 struct Seq {
   int ctx, n, q0, tiles, row_tiles;
 };
@@ -97,6 +99,9 @@ __device__ __forceinline__ Seq seq_of(const TreeParams& p, int s, int* code) {
   x.tiles = (x.ctx + BN - 1) / BN;
   x.row_tiles = (x.n * p.group + BM - 1) / BM;
   return x;
+}
+__device__ __forceinline__ long long places_of(const Seq& x, int kv_heads) {
+  return static_cast<long long>(x.tiles + kStart) * x.row_tiles * kv_heads;
 }
 
 template <int D>
@@ -162,10 +167,11 @@ __device__ __forceinline__ uint64_t seen_from(const TreeParams& p, int q_row, in
 //         O, only past 2^8), writes P over the scores and arrives on p_full; after an item's last tile its
 //         output or partial result.  A warp without rows only keeps step.
 //   W_K   finds the items and loads their K tiles
-//   W_V   loads the V tiles; those that some row does not see whole through registers
+//   W_V   loads the V tiles
 //   W_S   gathers an item's Q; one lane issues S(j) = Q K(j)^T once K(j) landed and PV(j - 2), the last
 //         reader of its buffer, is done
-//   W_PV  one lane issues O += P(j) V(j) once V(j) and P(j) are there, then releases V
+//   W_PV  looks over the V tiles that some row does not see whole; one lane issues O += P(j) V(j) once
+//         V(j) and P(j) are there, then releases V
 // Key tiles are numbered through all of a CTA's items (j above), items too; every hand-off is an
 // mbarrier, and no waiter is more than one phase behind the barrier it waits on.  Every wait is
 // bounded; a role that gives up records PKV_DEV_WAIT_TIMEOUT and leaves its loop, the others give up
@@ -269,10 +275,9 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
     constexpr int ROWS = 32 / CPR;                            // rows per warp-wide copy
     const int c = lane % CPR, rsub = lane / CPR;              // this lane's chunk and row offset
     const int nb = BN >> lb;                                  // blocks per tile
-    const uint32_t all_blocks = (1u << nb) - 1u;
-    // the K loader's place on the line: sequence, stream of it, tile, and what is left of the piece
+    // the K loader's place on the line: sequence, stream of it, place in that, and what is left of the piece
     Seq seq{};
-    int s = 0, stream = 0, tile = 0;
+    int s = 0, stream = 0, place = 0;
     long long left = 0;
     bool notes = false;                                       // this CTA's Cut is written
     const int worker = blockIdx.x;
@@ -283,13 +288,13 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       int code = 0;
       for (int i = lane; i < p.num_seqs; i += 32) {
         const Seq y = seq_of(p, i, &code);
-        total += static_cast<long long>(y.tiles) * y.row_tiles * H;
+        total += places_of(y, H);
       }
       if (code && worker == 0) record_error(code);
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xffffffffu, total, o);
       per = (total + gridDim.x - 1) / gridDim.x;
-      if (per < kMinTiles) per = kMinTiles;
+      if (per < kMinTiles + kStart) per = kMinTiles + kStart;
       x = worker * per;
       left = min(per, total - x);
       if (left > 0) {
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         s = p.num_seqs;
         for (int first = 0; first < p.num_seqs; first += 32) {
           const Seq y = seq_of(p, first + lane, &code);
-          const long long mine = static_cast<long long>(y.tiles) * y.row_tiles * H;
+          const long long mine = places_of(y, H);
           long long upto = mine;
 #pragma unroll
           for (int o = 1; o < 32; o *= 2) {
@@ -318,8 +323,8 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         if (seq.tiles == 0) {
           left = 0;                                           // the lengths changed meanwhile
         } else {
-          stream = static_cast<int>((x - before) / seq.tiles);
-          tile = static_cast<int>((x - before) % seq.tiles);
+          stream = static_cast<int>((x - before) / (seq.tiles + kStart));
+          place = static_cast<int>((x - before) % (seq.tiles + kStart));
         }
       }
     }
@@ -328,7 +333,14 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       Item item;
       if (is_k) {
         // the next item, for all roles
-        item.n_tiles = left > 0 ? static_cast<int>(min(left, static_cast<long long>(seq.tiles - tile))) : 0;
+        item.n_tiles = 0;
+        int tile = 0;
+        if (left > 0) {
+          tile = max(0, place - kStart);
+          const int to = static_cast<int>(min(static_cast<long long>(seq.tiles + kStart), place + left));
+          left -= to - place;
+          item.n_tiles = max(0, to - kStart) - tile;          // 0 where the piece ends before the stream's first
+        }
         if (item.n_tiles > 0) {
           item.s = s;
           item.kv_head = stream / seq.row_tiles;
@@ -382,18 +394,14 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           failed = true;
           break;
         }
-        if (lane == 0) not_finite[it & 1] = 0;
-        __syncwarp();
       }
       if (item.n_tiles == 0) break;
       const int32_t* table = p.tables + static_cast<size_t>(item.s) * p.max_blocks;
-      const int first_new = item.ctx - item.n;
       auto entry = [&](int tile_no) {                         // this lane's table entry for a tile
         const int t0 = tile_no * BN + (lane << lb);
         return lane < nb && t0 < item.ctx ? __ldg(table + (t0 >> lb)) : -1;
       };
       int next_entry = entry(item.tile0);
-      bool found = false;                                     // V: a value that is not finite
       for (int i = 0; i < item.n_tiles; ++i, ++j) {
         const int b = j % NS, key0 = (item.tile0 + i) * BN, t0 = key0 + (lane << lb);
         const bool in_ctx = lane < nb && t0 < item.ctx;
@@ -419,8 +427,8 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
             live[b].y = hi;
           }
         }
-        const bool care = !is_k && (good_mask != all_blocks || key0 + BN > first_new);
-        if (p.use_tma && !care) {
+        // V tiles with a block outside the pool, and small blocks, come in 16-byte copies, with zeros in its place
+        if (p.use_tma && (is_k || !__any_sync(0xffffffffu, in_ctx && !good))) {
           if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(good_mask)) * B * D * 2);
           __syncwarp();
           if (good) {
@@ -430,54 +438,20 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           }
           continue;
         }
-        if (!care) {
-          for (int r0 = 0; r0 < BN; r0 += ROWS) {
-            const int pb = __shfl_sync(0xffffffffu, phys, r0 >> lb), r = r0 + rsub;   // ROWS <= 4 <= B: one block
-            const __half* src = pool + (((static_cast<size_t>(max(pb, 0)) * p.num_kv_heads + item.kv_head) << lb) + (r & (B - 1))) * D + c * 8;
-            cp_async16(dst + sw128(r, c, BN), src, pb >= 0 ? 16 : 0);
-          }
-          cp_async_wait_all();
-        } else {
-          // zeros where there is no row, and for a draft's values that are not finite
-          constexpr int FLY = 8;
-#pragma unroll 1
-          for (int r0 = 0; r0 < BN; r0 += ROWS * FLY) {
-            uint4 w[FLY];
-#pragma unroll
-            for (int u = 0; u < FLY; ++u) {
-              const int rb = r0 + u * ROWS, pb = __shfl_sync(0xffffffffu, phys, rb >> lb), r = rb + rsub;
-              w[u] = make_uint4(0, 0, 0, 0);
-              if (pb >= 0 && key0 + r < item.ctx)
-                w[u] = *reinterpret_cast<const uint4*>(
-                    pool + (((static_cast<size_t>(pb) * p.num_kv_heads + item.kv_head) << lb) + (r & (B - 1))) * D + c * 8);
-            }
-#pragma unroll
-            for (int u = 0; u < FLY; ++u) {
-              const int r = r0 + u * ROWS + rsub;
-              if (key0 + r >= first_new) {
-                uint32_t* e = reinterpret_cast<uint32_t*>(&w[u]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const bool ok0 = finite16(e[k]), ok1 = finite16(e[k] >> 16);
-                  found |= !ok0 || !ok1;
-                  e[k] = (ok0 ? e[k] & 0xffffu : 0u) | (ok1 ? e[k] & 0xffff0000u : 0u);
-                }
-              }
-              *reinterpret_cast<uint4*>(smem + (dst + sw128(r, c, BN) - base)) = w[u];
-            }
-          }
+        for (int r0 = 0; r0 < BN; r0 += ROWS) {
+          const int pb = __shfl_sync(0xffffffffu, phys, r0 >> lb), r = r0 + rsub;   // ROWS <= 4 <= B: one block
+          const __half* src = pool + (((static_cast<size_t>(max(pb, 0)) * p.num_kv_heads + item.kv_head) << lb) + (r & (B - 1))) * D + c * 8;
+          cp_async16(dst + sw128(r, c, BN), src, pb >= 0 ? 16 : 0);
         }
+        cp_async_wait_all();
         fence_proxy_async_smem();                             // these writes -> tensor-core reads
-        if (found) not_finite[it & 1] = 1;
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
       }
       if (failed) break;
       if (is_k) {
-        left -= item.n_tiles;
-        tile += item.n_tiles;
-        if (tile == seq.tiles && left > 0) {
-          tile = 0;
+        if (left > 0) {                                       // on to the next stream
+          place = 0;
           if (++stream == p.num_kv_heads * seq.row_tiles) {
             stream = 0;
             int code = 0;
@@ -546,39 +520,73 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       if (j > 0) mbar_wait(s_full((j - 1) & 1), ((j - 1) >> 1) & 1);
     }
   } else if (warp == W_PV) {
-    // ---------------- O += P V issue (one lane) ----------------
-    if (lane == 0) {
-      constexpr uint32_t IDESC_PV = umma_idesc_f16(BM, D, true);
-      int j = 0;
-      for (int it = 0; !failed; ++it) {
-        Item item;
-        if (!take_item(it, item)) failed = true;
-        if (failed || item.n_tiles == 0) break;
-        mbar_arrive(item_free(it & 1));
-        for (int i = 0; i < item.n_tiles; ++i, ++j) {
-          const int u = j & 1, b = j % NS;
-          // the first product overwrites the accumulator: the last item's output has been read
-          if (!wait(v_full(b), (j / NS) & 1) || (i == 0 && it > 0 && !wait(o_free, (it - 1) & 1)) ||
-              !wait(p_full(u), (j >> 1) & 1)) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t v0 = umma_smem_desc(sv + b * C::KV_BYTES, BN * 128, 1024);
-          const uint32_t pa = t_s(u);
-          umma_ts(t_o, pa, v0, IDESC_PV, i > 0 ? 1u : 0u);
-#pragma unroll
-          for (int kk = 1; kk < BN / 16; ++kk) umma_ts(t_o, pa + kk * 8, v0 + ((kk * 16 * 128) >> 4), IDESC_PV, 1u);
-          umma_commit(pv_done(u));
-          umma_commit(v_free(b));
+    // ---------------- O += P V issue (one lane); V tiles that some row does not see whole ----------------
+    constexpr uint32_t IDESC_PV = umma_idesc_f16(BM, D, true);
+    int j = 0;
+    for (int it = 0;; ++it) {
+      Item item;
+      if (!__all_sync(0xffffffffu, take_item(it, item))) {
+        failed = true;
+        break;
+      }
+      if (item.n_tiles == 0) break;
+      if (lane == 0) not_finite[it & 1] = 0;
+      __syncwarp();
+      const int first_new = item.ctx - item.n;
+      for (int i = 0; i < item.n_tiles; ++i, ++j) {
+        const int u = j & 1, b = j % NS, key0 = (item.tile0 + i) * BN;
+        if (!warp_wait(v_full(b), (j / NS) & 1)) {
+          failed = true;
+          break;
         }
+        if (key0 + BN > first_new) {
+          // zeros past the context's end, and for drafts' values that are not finite
+          unsigned char* v = smem + (sv + b * C::KV_BYTES - base);
+          for (int k = max(0, first_new - key0) * CPR + lane; k < BN * CPR; k += 32) {
+            const int r = k / CPR;
+            uint4* at = reinterpret_cast<uint4*>(v + sw128(r, k % CPR, BN));
+            uint4 w = *at;
+            uint32_t* e = reinterpret_cast<uint32_t*>(&w);
+            bool zeros = key0 + r >= item.ctx, change = zeros;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const bool ok0 = finite16(e[h]), ok1 = finite16(e[h] >> 16);
+              change |= !ok0 || !ok1;
+              e[h] = zeros ? 0u : (ok0 ? e[h] & 0xffffu : 0u) | (ok1 ? e[h] & 0xffff0000u : 0u);
+            }
+            if (change) {
+              *at = w;
+              if (!zeros) not_finite[it & 1] = 1;
+            }
+          }
+          fence_proxy_async_smem();                           // these writes -> tensor-core reads
+          __syncwarp();
+        }
+        if (lane == 0) {
+          // the first product overwrites the accumulator: the last item's output has been read
+          if ((i == 0 && it > 0 && !wait(o_free, (it - 1) & 1)) || !wait(p_full(u), (j >> 1) & 1)) {
+            failed = true;
+          } else {
+            tc_fence_after();
+            const uint64_t v0 = umma_smem_desc(sv + b * C::KV_BYTES, BN * 128, 1024);
+            const uint32_t pa = t_s(u);
+            umma_ts(t_o, pa, v0, IDESC_PV, i > 0 ? 1u : 0u);
+#pragma unroll
+            for (int kk = 1; kk < BN / 16; ++kk) umma_ts(t_o, pa + kk * 8, v0 + ((kk * 16 * 128) >> 4), IDESC_PV, 1u);
+            umma_commit(pv_done(u));
+            umma_commit(v_free(b));
+          }
+        }
+        failed = __shfl_sync(0xffffffffu, failed, 0);
+        if (failed) break;
       }
-      if (failed) {
-        give_up();
-        if (j > 0) mbar_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1);
-      }
+      if (failed) break;
+      if (lane == 0) mbar_arrive(item_free(it & 1));
     }
-    __syncwarp();
+    if (failed) {
+      give_up();
+      if (j > 0) mbar_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1);
+    }
   } else {
     // ---------------- softmax and output ----------------
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
