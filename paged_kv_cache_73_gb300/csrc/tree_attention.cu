@@ -45,7 +45,7 @@ using namespace pkv::tc;
 constexpr int BM = 128;            // rows of a product (MMA M)
 constexpr int BN = 64;             // key positions per tile
 constexpr int kMinTiles = 2;       // key tiles a CTA takes at least
-constexpr int kStart = 1;          // what a stream costs besides its key tiles, in key tiles
+constexpr int kStart = 4;          // what a stream costs besides its key tiles, in key tiles
 constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
 constexpr float kLift = 7.f;       // weights are kept as 2^(kLift + S - m)
 
@@ -104,14 +104,19 @@ __device__ __forceinline__ long long places_of(const Seq& x, int kv_heads) {
   return static_cast<long long>(x.tiles + kStart) * x.row_tiles * kv_heads;
 }
 
-template <int D>
+// QR: rows of Q that are held (a multiple of 32, the most that an item has); the product's other rows read what
+// lies behind them, and depend on nothing else.
+template <int D, int QR>
 struct Cfg {
-  static constexpr int Q_BYTES = BM * D * 2;
+  static constexpr int Q_BYTES = QR * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
-  static constexpr int NS = D == 64 ? 4 : 2;                  // ring slots each for K and for V
-  static constexpr int BYTES = 1024 + Q_BYTES + 2 * NS * KV_BYTES + 512;
+  // ring slots for K and V: as many as two CTAs' shared memory holds
+  static constexpr int NK = D == 64 ? 5 : QR == 32 ? 3 : 2;
+  static constexpr int NV = D == 64 ? 6 : QR == 128 ? 2 : 3;
+  static constexpr int BYTES = 1024 + Q_BYTES + (NK + NV) * KV_BYTES + 512;
   // so much that no third CTA, which would wait for tensor memory, fits an SM
   static constexpr int SMEM = BYTES > 80 * 1024 ? BYTES : 80 * 1024;
+  static_assert(SMEM <= 113 * 1024 && BM * D * 2 <= Q_BYTES + (NK + NV) * KV_BYTES, "two to an SM; a product's rows lie inside");
 };
 // Tensor memory: the O accumulator and two S buffers of 64 columns, a half of the SM's 512 columns.
 constexpr uint32_t TMEM_COLS = 256, O_COL = 0, S_COL = 128;
@@ -163,28 +168,28 @@ __device__ __forceinline__ uint64_t seen_from(const TreeParams& p, int q_row, in
 }
 
 // Warp roles:
-//   0-3   softmax: waits S(j), releases K slot, masks, takes the row maximum (moving the running one, and
+//   0-3   softmax: waits S(j), masks, takes the row maximum (moving the running one, and
 //         O, only past 2^8), writes P over the scores and arrives on p_full; after an item's last tile its
 //         output or partial result.  A warp without rows only keeps step.
 //   W_K   finds the items and loads their K tiles
 //   W_V   loads the V tiles
 //   W_S   gathers an item's Q; one lane issues S(j) = Q K(j)^T once K(j) landed and PV(j - 2), the last
-//         reader of its buffer, is done
+//         reader of its buffer, is done, and then releases K
 //   W_PV  looks over the V tiles that some row does not see whole; one lane issues O += P(j) V(j) once
 //         V(j) and P(j) are there, then releases V
 // Key tiles are numbered through all of a CTA's items (j above), items too; every hand-off is an
 // mbarrier, and no waiter is more than one phase behind the barrier it waits on.  Every wait is
 // bounded; a role that gives up records PKV_DEV_WAIT_TIMEOUT and leaves its loop, the others give up
 // in turn, and the CTA still reaches its final barrier.
-template <int D>
+template <int D, int QR>
 __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid_constant__ TreeParams p) {
-  using C = Cfg<D>;
-  constexpr int NS = C::NS, CPR = D / 8;                      // 16-byte chunks per row
+  using C = Cfg<D, QR>;
+  constexpr int NK = C::NK, NV = C::NV, CPR = D / 8;          // CPR: 16-byte chunks per row
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - raw);
-  const uint32_t sq = base, sk = sq + C::Q_BYTES, sv = sk + NS * C::KV_BYTES, bars = sv + NS * C::KV_BYTES;
+  const uint32_t sq = base, sk = sq + C::Q_BYTES, sv = sk + NK * C::KV_BYTES, bars = sv + NV * C::KV_BYTES;
   // per S buffer u (key tile j uses j % 2), per ring slot b, per item slot i (item number % 2)
   auto s_full = [&](int u) { return bars + 8u * u; };
   auto p_full = [&](int u) { return bars + 16u + 8u * u; };
@@ -193,17 +198,19 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
   auto item_free = [&](int i) { return bars + 64u + 8u * i; };
   const uint32_t q_free = bars + 80, o_free = bars + 88;
   auto k_full = [&](int b) { return bars + 96u + 8u * b; };
-  auto v_full = [&](int b) { return bars + 96u + 8u * (NS + b); };
-  auto k_free = [&](int b) { return bars + 96u + 8u * (2 * NS + b); };
-  auto v_free = [&](int b) { return bars + 96u + 8u * (3 * NS + b); };
-  constexpr uint32_t AT = 96 + 32 * NS;
-  // per K slot: which of the tile's positions are in the context and in a block of the pool
-  volatile uint2* live = reinterpret_cast<volatile uint2*>(smem + (bars + AT - base));               // [NS]
-  volatile Item* items = reinterpret_cast<volatile Item*>(smem + (bars + AT + 8 * NS - base));       // [2]
-  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + AT + 8 * NS + 80 - base));  // [2]
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + AT + 8 * NS + 88 - base));
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + AT + 8 * NS + 92 - base));
-  static_assert(sizeof(Item) == 40 && AT + 8 * NS + 96 <= 512, "barrier area");
+  auto k_free = [&](int b) { return bars + 96u + 8u * (NK + b); };
+  auto v_full = [&](int b) { return bars + 96u + 8u * (2 * NK + b); };
+  auto v_free = [&](int b) { return bars + 96u + 8u * (2 * NK + NV + b); };
+  constexpr uint32_t AT = 96 + 16 * (NK + NV);
+  // Which of a tile's positions are in the context and in a block of the pool, for key tile j in place j % 8: K(j) is
+  // loaded once S(j - NK) is done, and so PV(j - NK - 2) and what the softmax read for that tile.
+  static_assert(NK + 2 <= 8, "a tile's word is read before it is written anew");
+  volatile uint2* live = reinterpret_cast<volatile uint2*>(smem + (bars + AT - base));               // [8]
+  volatile Item* items = reinterpret_cast<volatile Item*>(smem + (bars + AT + 64 - base));           // [2]
+  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + AT + 144 - base));       // [2]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + AT + 152 - base));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + AT + 156 - base));
+  static_assert(sizeof(Item) == 40 && AT + 160 <= 512, "barrier area");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pkv::pdl_trigger();
@@ -224,10 +231,12 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
     }
     mbar_init_count(q_free, 1);
     mbar_init_count(o_free, 4);
-    for (int b = 0; b < NS; ++b) {
+    for (int b = 0; b < NK; ++b) {
       mbar_init_count(k_full(b), 1);
+      mbar_init_count(k_free(b), 1);
+    }
+    for (int b = 0; b < NV; ++b) {
       mbar_init_count(v_full(b), 1);
-      mbar_init_count(k_free(b), 4);
       mbar_init_count(v_free(b), 1);
     }
     *abort_flag = 0;
@@ -272,6 +281,8 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
     const __half* pool = is_k ? p.k : p.v;
     const CUtensorMap* map = is_k ? &p.tmap_k : &p.tmap_v;
     const uint32_t ring = is_k ? sk : sv;
+    const int slots = is_k ? NK : NV;
+    int b = 0, round = 0;                                     // tile j goes to slot b = j % slots, round = j / slots
     constexpr int ROWS = 32 / CPR;                            // rows per warp-wide copy
     const int c = lane % CPR, rsub = lane / CPR;              // this lane's chunk and row offset
     const int nb = BN >> lb;                                  // blocks per tile
@@ -403,7 +414,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       };
       int next_entry = entry(item.tile0);
       for (int i = 0; i < item.n_tiles; ++i, ++j) {
-        const int b = j % NS, key0 = (item.tile0 + i) * BN, t0 = key0 + (lane << lb);
+        const int key0 = (item.tile0 + i) * BN, t0 = key0 + (lane << lb);
         const bool in_ctx = lane < nb && t0 < item.ctx;
         int phys = next_entry;
         if (i + 1 < item.n_tiles) next_entry = entry(item.tile0 + i + 1);
@@ -411,11 +422,15 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         if (is_k && in_ctx && !good) record_error(PKV_DEV_BAD_BLOCK_ID);
         if (!good) phys = -1;
         const uint32_t good_mask = __ballot_sync(0xffffffffu, good);
-        if (j >= NS && !warp_wait(is_k ? k_free(b) : v_free(b), (j / NS - 1) & 1)) {
+        if (round > 0 && !warp_wait(is_k ? k_free(b) : v_free(b), (round - 1) & 1)) {
           failed = true;
           break;
         }
         const uint32_t full = is_k ? k_full(b) : v_full(b), dst = ring + b * C::KV_BYTES;
+        if (++b == slots) {
+          b = 0;
+          ++round;
+        }
         if (is_k) {
           // K rows past the context or of bad blocks may hold anything: their scores are masked
           const int valid = good ? min(B, item.ctx - t0) : 0, at = lane << lb & 31;
@@ -423,8 +438,8 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           const uint32_t lo = __reduce_or_sync(0xffffffffu, lane << lb < 32 ? bits : 0u);
           const uint32_t hi = __reduce_or_sync(0xffffffffu, lane << lb < 32 ? 0u : bits);
           if (lane == 0) {
-            live[b].x = lo;
-            live[b].y = hi;
+            live[j & 7].x = lo;
+            live[j & 7].y = hi;
           }
         }
         // V tiles with a block outside the pool, and small blocks, come in 16-byte copies, with zeros in its place
@@ -469,7 +484,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
     if (failed) give_up();
     if (*abort_flag) {
       // let the copies this warp issued land (bounded) before the CTA's shared memory is released
-      for (int t = max(0, j - NS); t < j; ++t) mbar_wait(is_k ? k_full(t % NS) : v_full(t % NS), (t / NS) & 1);
+      for (int t = max(0, j - slots); t < j; ++t) mbar_wait(is_k ? k_full(t % NK) : v_full(t % NV), (t / slots) & 1);
     }
   } else if (warp == W_S) {
     // ---------------- Q, and S = Q K^T issue (one lane) ----------------
@@ -486,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       // Rows past the item's hold what was there: a row of the product depends on its own alone.
       for (int k = lane; k < item.rows * CPR; k += 32) {
         const int r = k / CPR, c = k % CPR, row = item.first_row + r, i = row / p.group, g = row - i * p.group;
-        cp_async16(sq + sw128(r, c, BM), p.q + (item.q0 + i) * p.q_stride + (item.kv_head * p.group + g) * D + c * 8, 16);
+        cp_async16(sq + sw128(r, c, QR), p.q + (item.q0 + i) * p.q_stride + (item.kv_head * p.group + g) * D + c * 8, 16);
       }
       cp_async_wait_all();
       fence_proxy_async_smem();
@@ -495,19 +510,20 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         mbar_arrive(item_free(it & 1));
         for (int i = 0; i < item.n_tiles; ++i, ++j) {
           const int u = j & 1;
-          if (!wait(k_full(j % NS), (j / NS) & 1) || (j >= 2 && !wait(pv_done(u), ((j - 2) >> 1) & 1))) {
+          if (!wait(k_full(j % NK), (j / NK) & 1) || (j >= 2 && !wait(pv_done(u), ((j - 2) >> 1) & 1))) {
             failed = true;
             break;
           }
           tc_fence_after();
-          const uint64_t b0 = umma_smem_desc(sk + (j % NS) * C::KV_BYTES, 16, 1024);
+          const uint64_t b0 = umma_smem_desc(sk + (j % NK) * C::KV_BYTES, 16, 1024);
           const uint32_t d = t_s(u);
           umma_ss(d, a0, b0, IDESC_QK, 0u);
 #pragma unroll
           for (int kk = 1; kk < D / 16; ++kk)
-            umma_ss(d, a0 + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4),
+            umma_ss(d, a0 + (((kk >> 2) * (QR * 128) + (kk & 3) * 32) >> 4),
                     b0 + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), IDESC_QK, 1u);
           umma_commit(s_full(u));
+          umma_commit(k_free(j % NK));
         }
         if (!failed) umma_commit(q_free);
       }
@@ -534,8 +550,8 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       __syncwarp();
       const int first_new = item.ctx - item.n;
       for (int i = 0; i < item.n_tiles; ++i, ++j) {
-        const int u = j & 1, b = j % NS, key0 = (item.tile0 + i) * BN;
-        if (!warp_wait(v_full(b), (j / NS) & 1)) {
+        const int u = j & 1, b = j % NV, key0 = (item.tile0 + i) * BN;
+        if (!warp_wait(v_full(b), (j / NV) & 1)) {
           failed = true;
           break;
         }
@@ -607,16 +623,11 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           break;
         }
         if (!works) {
-          if (lane == 0) {
-            mbar_arrive(k_free(j % NS));
-            mbar_arrive(p_full(u));
-          }
+          if (lane == 0) mbar_arrive(p_full(u));
           continue;
         }
         tc_fence_after();
-        const uint32_t live_lo = live[j % NS].x, live_hi = live[j % NS].y;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_free(j % NS));
+        const uint32_t live_lo = live[j & 7].x, live_hi = live[j & 7].y;
         float sv_[BN];
         tmem_ld32_nowait(ts + lane_off, *reinterpret_cast<float(*)[32]>(sv_));
         tmem_ld32_nowait(ts + lane_off + 32, *reinterpret_cast<float(*)[32]>(sv_ + 32));
@@ -883,9 +894,9 @@ int encode_pool_map(const char* fn, CUtensorMap* map, const void* pool, int D, i
   return PKV_OK;
 }
 
-template <int D>
+template <int D, int QR>
 int launch(const char* fn, const TreeParams& p, int workers, cudaStream_t st) {
-  using C = Cfg<D>;
+  using C = Cfg<D, QR>;
   static std::mutex mu;
   static bool done[64] = {false};
   int dev = 0;
@@ -893,12 +904,12 @@ int launch(const char* fn, const TreeParams& p, int workers, cudaStream_t st) {
   if (e == cudaSuccess) {
     std::lock_guard<std::mutex> g(mu);
     if (dev < 0 || dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(tree_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+      e = cudaFuncSetAttribute(tree_attention_kernel<D, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
       if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
     }
   }
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s setup: %s", fn, cudaGetErrorString(e));
-  e = pkv::launch_pdl(tree_attention_kernel<D>, dim3(workers), dim3(THREADS), C::SMEM, st, p);
+  e = pkv::launch_pdl(tree_attention_kernel<D, QR>, dim3(workers), dim3(THREADS), C::SMEM, st, p);
   if (e == cudaSuccess && workers > 1)
     e = pkv::launch_pdl(tree_attention_join_kernel<D>, dim3(workers - 1, D / 32), dim3(JOIN_THREADS), 0, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
@@ -1011,7 +1022,12 @@ int pkv_paged_attention_tree(const uint16_t* q, int64_t q_stride, const uint16_t
     if (rc != PKV_OK) return rc;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int rc = head_dim == 128 ? launch<128>(fn, p, pl.workers, st) : launch<64>(fn, p, pl.workers, st);
+  // few rows leave shared memory for more key tiles in flight
+  const int rows = max_query_len * p.group;
+  const int rc = head_dim == 64 ? launch<64, 128>(fn, p, pl.workers, st)
+                 : rows <= 32   ? launch<128, 32>(fn, p, pl.workers, st)
+                 : rows <= 64   ? launch<128, 64>(fn, p, pl.workers, st)
+                                : launch<128, 128>(fn, p, pl.workers, st);
   if (rc == PKV_OK) pkv::clear_error();
   return rc;
 }
