@@ -14,6 +14,9 @@
 //    lie on one line, cut evenly over the resident CTAs, two to an SM, each with half of the tensor memory: ragged
 //    contexts and few sequences fill the GPU alike.  A CTA walks its piece through a ring of K and V tiles
 //    that runs on over the ends of streams.
+//  * Where a sequence has more than 128 rows, two CTAs walk two row tiles over the same keys at the same time, so
+//    that the second reads from L2 what the first brought there; one after the other they read 2 x from memory (32
+//    sequences of 20480 tokens, 64 heads on 8, 32 drafts: KV2 us against PAIR2).
 //  * A stream that is cut leaves partial results (row maximum, sum, output) that a second kernel joins by the
 //    log-sum-exp identity; the first CTA of such a stream notes where they lie.  A CTA has at most
 //    two such parts, the first and the last of its piece.
@@ -100,8 +103,13 @@ __device__ __forceinline__ Seq seq_of(const TreeParams& p, int s, int* code) {
   x.row_tiles = (x.n * p.group + BM - 1) / BM;
   return x;
 }
-__device__ __forceinline__ long long places_of(const Seq& x, int kv_heads) {
-  return static_cast<long long>(x.tiles + kStart) * x.row_tiles * kv_heads;
+// Streams of a kind to a cached head: pairs of row tiles, row tiles left alone by those, or (kind ALL) every row tile.
+enum Kind { ALL, PAIRS, ALONE };
+__device__ __forceinline__ int streams_of(const Seq& x, Kind kind) {
+  return kind == ALL ? x.row_tiles : kind == PAIRS ? x.row_tiles / 2 : x.row_tiles % 2;
+}
+__device__ __forceinline__ long long places_of(const Seq& x, int kv_heads, Kind kind) {
+  return static_cast<long long>(x.tiles + kStart) * streams_of(x, kind) * kv_heads;
 }
 
 // QR: rows of Q that are held (a multiple of 32, the most that an item has); the product's other rows read what
@@ -291,30 +299,50 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
     int s = 0, stream = 0, place = 0;
     long long left = 0;
     bool notes = false;                                       // this CTA's Cut is written
-    const int worker = blockIdx.x;
-    long long per = 0, x = 0;
+    // The CTA's kind of streams, its number among the CTAs that share them out, their count, which row tile of a
+    // pair it takes, and its number in the workspace, where a kind's CTAs lie side by side.
+    Kind kind = ALL;
+    int number = blockIdx.x, count = gridDim.x, half = 0, worker = blockIdx.x;
+    long long per = 0;
     if (is_k) {
       const int H = p.num_kv_heads;
-      long long total = 0;
+      long long pairs = 0, alone = 0;
       int code = 0;
       for (int i = lane; i < p.num_seqs; i += 32) {
         const Seq y = seq_of(p, i, &code);
-        total += places_of(y, H);
+        pairs += places_of(y, H, PAIRS);
+        alone += places_of(y, H, ALONE);
       }
-      if (code && worker == 0) record_error(code);
+      if (code && blockIdx.x == 0) record_error(code);
 #pragma unroll
-      for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xffffffffu, total, o);
-      per = (total + gridDim.x - 1) / gridDim.x;
+      for (int o = 16; o > 0; o /= 2) {
+        pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
+        alone += __shfl_xor_sync(0xffffffffu, alone, o);
+      }
+      const int teams = gridDim.x / 2;
+      long long total = 2 * pairs + alone;
+      if (pairs > 0 && teams >= 2) {
+        // CTA w and CTA w + teams, which mostly share an SM, take a pair together; the others single row tiles
+        const int team = blockIdx.x % teams;
+        half = blockIdx.x / teams;
+        int mine = static_cast<int>((2 * pairs * teams + total / 2) / total);
+        if (alone > 0) mine = max(1, min(teams - 1, mine));
+        kind = team < mine ? PAIRS : ALONE;
+        count = kind == PAIRS ? mine : 2 * (teams - mine);
+        number = kind == PAIRS ? team : half * (teams - mine) + team - mine;
+        worker = kind == PAIRS ? half * mine + team : 2 * mine + number;
+        total = kind == PAIRS ? pairs : alone;
+      }
+      per = (total + count - 1) / count;
       if (per < kMinTiles + kStart) per = kMinTiles + kStart;
-      x = worker * per;
+      const long long x = number * per;
       left = min(per, total - x);
       if (left > 0) {
         // the sequence: the first whose tiles, all streams together, reach past x
         long long before = 0;
         s = p.num_seqs;
         for (int first = 0; first < p.num_seqs; first += 32) {
-          const Seq y = seq_of(p, first + lane, &code);
-          const long long mine = places_of(y, H);
+          const long long mine = places_of(seq_of(p, first + lane, &code), H, kind);
           long long upto = mine;
 #pragma unroll
           for (int o = 1; o < 32; o *= 2) {
@@ -331,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           before += __shfl_sync(0xffffffffu, upto, 31);
         }
         seq = seq_of(p, s, &code);
-        if (seq.tiles == 0) {
+        if (streams_of(seq, kind) == 0) {
           left = 0;                                           // the lengths changed meanwhile
         } else {
           stream = static_cast<int>((x - before) / (seq.tiles + kStart));
@@ -354,8 +382,9 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         }
         if (item.n_tiles > 0) {
           item.s = s;
-          item.kv_head = stream / seq.row_tiles;
-          item.first_row = stream % seq.row_tiles * BM;
+          const int streams = streams_of(seq, kind), tile_no = stream % streams;
+          item.kv_head = stream / streams;
+          item.first_row = (kind == ALL ? tile_no : kind == PAIRS ? 2 * tile_no + half : seq.row_tiles - 1) * BM;
           item.rows = min(BM, seq.n * p.group - item.first_row);
           item.tile0 = tile;
           item.ctx = seq.ctx;
@@ -384,13 +413,21 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           mbar_arrive(item_full(it & 1));
         }
         __syncwarp();
+        if (item.n_tiles > 0) {
+          // its queries, for when the products come to it: lines of 128 bytes
+          for (int k = lane; k < item.rows * (D / 64); k += 32) {
+            const int row = item.first_row + k / (D / 64), i = row / p.group, g = row - i * p.group;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (item.q0 + i) * p.q_stride +
+                                                          (item.kv_head * p.group + g) * D + k % (D / 64) * 64));
+          }
+        }
         if (item.n_tiles > 0 && tile == 0 && item.n_tiles < seq.tiles) {
           // a cut stream's first part: the others are the first items of the CTAs that follow
           notes = true;
           if (lane == 0) {
             Cut cut{};
             cut.parts = 1 + static_cast<int>((seq.tiles - item.n_tiles + per - 1) / per);
-            cut.parts = min(cut.parts, static_cast<int>(gridDim.x) - worker);
+            cut.parts = min(cut.parts, count - number);
             cut.slot = item.slot;
             cut.next = 2 * (worker + 1);
             cut.rows = item.rows;
@@ -467,12 +504,12 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       if (is_k) {
         if (left > 0) {                                       // on to the next stream
           place = 0;
-          if (++stream == p.num_kv_heads * seq.row_tiles) {
+          if (++stream == p.num_kv_heads * streams_of(seq, kind)) {
             stream = 0;
             int code = 0;
             do seq = seq_of(p, ++s, &code);
-            while (seq.tiles == 0 && s < p.num_seqs);
-            if (seq.tiles == 0) left = 0;                     // the lengths changed meanwhile
+            while (streams_of(seq, kind) == 0 && s < p.num_seqs);
+            if (streams_of(seq, kind) == 0) left = 0;         // the lengths changed meanwhile
           }
         }
       } else {
@@ -632,6 +669,8 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       const bool works = warp * 32 < item.rows;
       const int row = item.first_row + min(tid, item.rows - 1), node = row / p.group, first_new = item.ctx - item.n;
       float l = 0.f, m_ref = -INFINITY;
+      if (p.mask != nullptr && (item.tile0 + item.n_tiles) * BN > first_new)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.mask + static_cast<int64_t>(item.q0 + node) * p.mask_words));
       for (int i = 0; i < item.n_tiles; ++i, ++j) {
         const int u = j & 1, key0 = (item.tile0 + i) * BN;
         const uint32_t ts = t_s(u);
@@ -778,7 +817,6 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
 
 // Joins the parts of the cut streams: CTA (w, y) columns 32 y .. of the one that CTA w of the grid before noted.
 // A thread takes a row and four columns at a time; where rows are few, groups of threads share the parts.
-// (CTA 0 of the grid before may note one, the last cannot: its last stream ends with it.)
 constexpr int JOIN_THREADS = 512;
 template <int D>
 __global__ void __launch_bounds__(JOIN_THREADS) tree_attention_join_kernel(const __grid_constant__ TreeParams p) {
@@ -887,6 +925,7 @@ Plan plan_for(int num_seqs, int total_q, int max_query_len, int num_heads, int n
   pl.most_tiles = row_tiles * num_kv_heads * ((max_ctx + BN - 1) / BN);
   const long long want = (pl.most_tiles + kMinTiles - 1) / kMinTiles, most = 2 * device_sms();
   pl.workers = static_cast<int>(want < most ? want : most);
+  if (rows > BM) pl.workers += pl.workers & 1;                // pairs of row tiles want pairs of CTAs
   return pl;
 }
 size_t ml_bytes(int workers) { return static_cast<size_t>(workers) * 2 * BM * sizeof(float2); }
@@ -928,7 +967,7 @@ int launch(const char* fn, const TreeParams& p, int workers, cudaStream_t st) {
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s setup: %s", fn, cudaGetErrorString(e));
   e = pkv::launch_pdl(tree_attention_kernel<D, QR>, dim3(workers), dim3(THREADS), C::SMEM, st, p);
   if (e == cudaSuccess && workers > 1)
-    e = pkv::launch_pdl(tree_attention_join_kernel<D>, dim3(workers - 1, D / 32), dim3(JOIN_THREADS), 0, st, p);
+    e = pkv::launch_pdl(tree_attention_join_kernel<D>, dim3(workers, D / 32), dim3(JOIN_THREADS), 0, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
   return PKV_OK;
