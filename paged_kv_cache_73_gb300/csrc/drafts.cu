@@ -24,6 +24,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "launch.cuh"
 #include "pkv_internal.h"
@@ -37,10 +38,18 @@ typedef unsigned long long u64;
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kMaxNodes = 1024;      // of a sequence
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;         // of a cluster
 constexpr u64 kOne = 1ull << 60, kMost = 1ull << 61;
 
+// The same of a row's values where all of them are in [0, 1] (largest: the bits of the largest met, so that the
+// others, whose bits are above those of 1, are noticed): a shift of the 24-bit mantissa from the top.
+constexpr unsigned kOneBits = 0x3f800000u;
+__device__ __forceinline__ u64 whole_fast(float p, unsigned& largest) {
+  const unsigned b = __float_as_uint(p);
+  largest = max(largest, b);
+  return (static_cast<u64>((b << 5) & 0x0fffffe0u | 0x10000000u) << 32) >> min(127u - (b >> 23), 63u);
+}
 // floor(p 2^60) of p in [0, 1]; what is no probability (a NaN, negative, above 1 by more than
 // rounding) sets `bad` and counts as 0 or 1
 __device__ __forceinline__ u64 whole(float p, bool& bad) {
@@ -115,7 +124,7 @@ struct Order {
   u64 u0;
 };
 
-__global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 3) verify_draft_kernel(const VerifyParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   // the refusals at the current node: M before each (with a draft distribution), or the tokens
   u64* refused_m = reinterpret_cast<u64*>(smem);
@@ -219,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyPara
           if (lane < ctas) st_cluster(map_to_rank(refused_m + k, lane), share);
           ++k;
           wants = true;                                       // M is the sum of what is left
-        } else {
+        } else if (has > 0) {                                 // a token that is left nothing is noted already, or was 0
           __syncwarp();
           if (lane < ctas) st_cluster(map_to_rank(refused_x + k, lane), nodes.token[j]);
           ++k;
@@ -249,12 +258,15 @@ __global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyPara
     if (o.row < 0) break;                                     // no nodes
     const float* prow = p.target + static_cast<int64_t>(o.row) * p.target_stride;
     const float* qrow = p.draft == nullptr ? nullptr : p.draft + static_cast<int64_t>(o.row) * p.draft_stride;
-    // this warp's piece of the row: whole lines of 32 values
-    const int lines = (p.vocab + 31) / 32, pieces = ctas * kWarps, mine = rank * kWarps + warp;
-    const int first = static_cast<int>(static_cast<int64_t>(lines) * mine / pieces) * 32;
-    const int end = min(p.vocab, static_cast<int>(static_cast<int64_t>(lines) * (mine + 1) / pieces) * 32);
+    // This warp's piece of the row, in lines of 128 values that start at multiples of 16 bytes: value i of the row is
+    // value i + shift of the lines.  Where the two rows lie differently, or the strides are odd, a value at a time.
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(prow) >> 2 & 3);
+    const bool wide = qrow == nullptr || static_cast<int>(reinterpret_cast<uintptr_t>(qrow) >> 2 & 3) == shift;
+    const int lines = (p.vocab + shift + 127) / 128, pieces = ctas * kWarps, mine = rank * kWarps + warp;
+    const int first = static_cast<int>(static_cast<int64_t>(lines) * mine / pieces);
+    const int end = static_cast<int>(static_cast<int64_t>(lines) * (mine + 1) / pieces);
     int refused = o.refused;
-    bool bad = false;
+    bool bad = false, slow = false;
     auto left = [&](int i) {                                  // R(i) after the refusals
       u64 r = whole(prow[i], bad);
       if (qrow != nullptr) {
@@ -271,13 +283,89 @@ __global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyPara
       }
       return r;
     };
+    // the sum over lines [from, to) of this lane's values, one by one
+    auto slow_sum = [&](int from, int to) {
+      u64 sum = 0;
+#pragma unroll 1
+      for (int k = from * 128 + lane; k < to * 128; k += 32)
+        if (k >= shift && k - shift < p.vocab) sum = add_most(sum, left(k - shift));
+      return sum;
+    };
+    // the same of whole lines, 16 bytes at a time; STEPS: refusals that leave their mark (2: two or more)
+    auto fast_sum = [&](auto steps, int from, int to) {
+      constexpr int STEPS = decltype(steps)::value, FLY = STEPS == 0 ? 8 : 4;
+      u64 sum = 0;
+      unsigned largest = 0;
+      const float4* pv = reinterpret_cast<const float4*>(prow - shift) + lane;
+      const float4* qv = STEPS == 0 ? nullptr : reinterpret_cast<const float4*>(qrow - shift) + lane;
+#pragma unroll 1
+      for (int line = from; line < to; line += FLY) {
+        float4 x[FLY], y[FLY];
+#pragma unroll
+        for (int u = 0; u < FLY; ++u) {
+          x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (line + u < to) {
+            x[u] = pv[(line + u) * 32];
+            if (STEPS > 0) y[u] = qv[(line + u) * 32];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < FLY; ++u) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float xe = e == 0 ? x[u].x : e == 1 ? x[u].y : e == 2 ? x[u].z : x[u].w;
+            u64 r = whole_fast(xe, largest);
+            if (STEPS > 0) {
+              const float ye = e == 0 ? y[u].x : e == 1 ? y[u].y : e == 2 ? y[u].z : y[u].w;
+              const u64 q = whole_fast(ye, largest);
+              r = r > q ? r - q : 0;                          // the first refusal's M is 1
+              if (STEPS > 1) {
+#pragma unroll 1
+                for (int j = 1; j < refused; ++j) {
+                  const u64 off = part_of(refused_m[j], q);
+                  r = r > off ? r - off : 0;
+                }
+              }
+            }
+            sum += r;                                         // eight at most before the next line holds it down
+          }
+          if (u & 1) sum = add_most(sum, 0);
+        }
+      }
+      if (__any_sync(FULL, largest > kOneBits)) {             // something is no probability
+        sum = slow_sum(from, to);
+        slow = true;
+      }
+      return sum;
+    };
     u64 total = 0;
     int parity = pass & 1;
     for (int attempt = 0; attempt < 2; ++attempt) {
       u64 sum = 0;
-      for (int i = first + lane; i < end; i += 32) sum = add_most(sum, left(i));
+      int fast_from = 0, fast_to = 0;
+      if (wide) {
+        // the lines that hold something else than the row's values apart
+        const int from = first + (first == 0 && shift > 0 && end > 0), to = end - (end == lines && (p.vocab + shift) % 128 != 0 && end > from);
+        if (first < from) sum = slow_sum(first, from);
+        if (to < end) sum = add_most(sum, slow_sum(to, end));
+        const u64 inner = qrow == nullptr || refused == 0 ? fast_sum(std::integral_constant<int, 0>(), from, to)
+                          : refused == 1                  ? fast_sum(std::integral_constant<int, 1>(), from, to)
+                                                          : fast_sum(std::integral_constant<int, 2>(), from, to);
+        sum = add_most(sum, inner);
+        fast_from = from;
+        fast_to = to;
+      } else {
+        sum = slow_sum(first, end);
+      }
 #pragma unroll
       for (int d = 16; d > 0; d /= 2) sum = add_most(sum, __shfl_xor_sync(FULL, sum, d));
+      if (qrow == nullptr) {
+        // refused tokens have nothing left (slow_sum counts that)
+        for (int j = 0; j < refused; ++j) {
+          const int line = (refused_x[j] + shift) / 128;
+          if (!slow && line >= fast_from && line < fast_to) sum -= min(sum, whole(prow[refused_x[j]], bad));
+        }
+      }
       if (lane == 0) warp_sum[warp] = sum;
       const int any_bad = __syncthreads_or(bad);
       if (tid == 0) {
@@ -326,9 +414,9 @@ __global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyPara
           aim -= warp_sum[w];
         }
         if (here && aim < warp_sum[warp]) {
-          for (int base = first; base < end; base += 32) {
-            const u64 r = base + lane < end ? left(base + lane) : 0;
-            u64 upto = r;
+          for (int base = first * 128 - shift; base < end * 128 - shift; base += 32) {
+            const int i = base + lane;
+            u64 upto = i >= 0 && i < p.vocab ? left(i) : 0;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
               const u64 y = __shfl_up_sync(FULL, upto, d);

@@ -49,6 +49,7 @@ constexpr int BM = 128;            // rows of a product (MMA M)
 constexpr int BN = 64;             // key positions per tile
 constexpr int kMinTiles = 2;       // key tiles a CTA takes at least
 constexpr int kStart = 4;          // what a stream costs besides its key tiles, in key tiles
+constexpr int kManyParts = 16;     // a stream cut into more is joined by CTAs of four columns each, not 32
 constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
 constexpr float kLift = 7.f;       // weights are kept as 2^(kLift + S - m)
 
@@ -135,6 +136,11 @@ constexpr int THREADS = 256;
 struct Item {
   int s, kv_head, first_row, rows, tile0, n_tiles, ctx, n, q0, slot;  // slot -1: the whole stream, to out
 };
+
+// Divisions on the line: 64-bit ones take some 500 clocks, and few lines are that long.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
 
 __device__ __forceinline__ bool finite16(unsigned h) { return (h & 0x7c00u) != 0x7c00u; }
 
@@ -308,6 +314,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       const int H = p.num_kv_heads;
       long long pairs = 0, alone = 0;
       int code = 0;
+#pragma unroll 1
       for (int i = lane; i < p.num_seqs; i += 32) {
         const Seq y = seq_of(p, i, &code);
         pairs += places_of(y, H, PAIRS);
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         // CTA w and CTA w + teams, which mostly share an SM, take a pair together; the others single row tiles
         const int team = blockIdx.x % teams;
         half = blockIdx.x / teams;
-        int mine = static_cast<int>((2 * pairs * teams + total / 2) / total);
+        int mine = static_cast<int>(divide(2 * pairs * teams + total / 2, total));
         if (alone > 0) mine = max(1, min(teams - 1, mine));
         kind = team < mine ? PAIRS : ALONE;
         count = kind == PAIRS ? mine : 2 * (teams - mine);
@@ -333,7 +340,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         worker = kind == PAIRS ? half * mine + team : 2 * mine + number;
         total = kind == PAIRS ? pairs : alone;
       }
-      per = (total + count - 1) / count;
+      per = divide(total + count - 1, count);
       if (per < kMinTiles + kStart) per = kMinTiles + kStart;
       const long long x = number * per;
       left = min(per, total - x);
@@ -362,8 +369,8 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         if (streams_of(seq, kind) == 0) {
           left = 0;                                           // the lengths changed meanwhile
         } else {
-          stream = static_cast<int>((x - before) / (seq.tiles + kStart));
-          place = static_cast<int>((x - before) % (seq.tiles + kStart));
+          stream = static_cast<int>(divide(x - before, seq.tiles + kStart));
+          place = static_cast<int>(x - before - static_cast<long long>(stream) * (seq.tiles + kStart));
         }
       }
     }
@@ -413,30 +420,6 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           mbar_arrive(item_full(it & 1));
         }
         __syncwarp();
-        if (item.n_tiles > 0) {
-          // its queries, for when the products come to it: lines of 128 bytes
-          for (int k = lane; k < item.rows * (D / 64); k += 32) {
-            const int row = item.first_row + k / (D / 64), i = row / p.group, g = row - i * p.group;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (item.q0 + i) * p.q_stride +
-                                                          (item.kv_head * p.group + g) * D + k % (D / 64) * 64));
-          }
-        }
-        if (item.n_tiles > 0 && tile == 0 && item.n_tiles < seq.tiles) {
-          // a cut stream's first part: the others are the first items of the CTAs that follow
-          notes = true;
-          if (lane == 0) {
-            Cut cut{};
-            cut.parts = 1 + static_cast<int>((seq.tiles - item.n_tiles + per - 1) / per);
-            cut.parts = min(cut.parts, count - number);
-            cut.slot = item.slot;
-            cut.next = 2 * (worker + 1);
-            cut.rows = item.rows;
-            cut.first_row = item.first_row;
-            cut.q0 = item.q0;
-            cut.kv_head = item.kv_head;
-            p.cuts[worker] = cut;
-          }
-        }
       } else {
         if (!__all_sync(0xffffffffu, take_item(it, item))) {
           failed = true;
@@ -445,16 +428,21 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       }
       if (item.n_tiles == 0) break;
       const int32_t* table = p.tables + static_cast<size_t>(item.s) * p.max_blocks;
-      auto entry = [&](int tile_no) {                         // this lane's table entry for a tile
-        const int t0 = tile_no * BN + (lane << lb);
-        return lane < nb && t0 < item.ctx ? __ldg(table + (t0 >> lb)) : -1;
+      // the table entries of 32 of the item's blocks, one a lane, and of the next 32
+      auto entries = [&](int block) {
+        const int t0 = item.tile0 * BN + ((block + lane) << lb);
+        return t0 < item.ctx ? __ldg(table + (t0 >> lb)) : -1;
       };
-      int next_entry = entry(item.tile0);
+      int entry = entries(0), next_entries = entries(32);
       for (int i = 0; i < item.n_tiles; ++i, ++j) {
         const int key0 = (item.tile0 + i) * BN, t0 = key0 + (lane << lb);
         const bool in_ctx = lane < nb && t0 < item.ctx;
-        int phys = next_entry;
-        if (i + 1 < item.n_tiles) next_entry = entry(item.tile0 + i + 1);
+        const int at_block = i * nb & 31;
+        if (at_block == 0 && i > 0) {
+          entry = next_entries;
+          next_entries = entries(i * nb + 32);
+        }
+        int phys = __shfl_sync(0xffffffffu, entry, at_block + lane);
         const bool good = in_ctx && phys >= 0 && phys < p.num_blocks;
         if (is_k && in_ctx && !good) record_error(PKV_DEV_BAD_BLOCK_ID);
         if (!good) phys = -1;
@@ -490,6 +478,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           }
           continue;
         }
+#pragma unroll 4
         for (int r0 = 0; r0 < BN; r0 += ROWS) {
           const int pb = __shfl_sync(0xffffffffu, phys, r0 >> lb), r = r0 + rsub;   // ROWS <= 4 <= B: one block
           const __half* src = pool + (((static_cast<size_t>(max(pb, 0)) * p.num_kv_heads + item.kv_head) << lb) + (r & (B - 1))) * D + c * 8;
@@ -502,6 +491,22 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       }
       if (failed) break;
       if (is_k) {
+        if (item.tile0 == 0 && item.n_tiles < seq.tiles) {
+          // a cut stream's first part: the others are the first items of the CTAs that follow
+          notes = true;
+          if (lane == 0) {
+            Cut cut{};
+            cut.parts = 1 + static_cast<int>(divide(seq.tiles - item.n_tiles + per - 1, per));
+            cut.parts = min(cut.parts, count - number);
+            cut.slot = item.slot;
+            cut.next = 2 * (worker + 1);
+            cut.rows = item.rows;
+            cut.first_row = item.first_row;
+            cut.q0 = item.q0;
+            cut.kv_head = item.kv_head;
+            p.cuts[worker] = cut;
+          }
+        }
         if (left > 0) {                                       // on to the next stream
           place = 0;
           if (++stream == p.num_kv_heads * streams_of(seq, kind)) {
@@ -536,9 +541,22 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       }
       if (item.n_tiles == 0) break;
       // Rows past the item's hold what was there: a row of the product depends on its own alone.
-      for (int k = lane; k < item.rows * CPR; k += 32) {
-        const int r = k / CPR, c = k % CPR, row = item.first_row + r, i = row / p.group, g = row - i * p.group;
-        cp_async16(sq + sw128(r, c, QR), p.q + (item.q0 + i) * p.q_stride + (item.kv_head * p.group + g) * D + c * 8, 16);
+      {
+        constexpr int ROWS = 32 / CPR;                        // rows per warp-wide copy
+        const int c = lane % CPR;
+        int r = lane / CPR, i = (item.first_row + r) / p.group, g = item.first_row + r - i * p.group;
+        const __half* src = p.q + (item.q0 + i) * p.q_stride + (item.kv_head * p.group + g) * D + c * 8;
+#pragma unroll 1
+        for (; r < item.rows; r += ROWS) {
+          cp_async16(sq + sw128(r, c, QR), src, 16);
+          // ROWS rows on: so many heads further, or in a later node
+          g += ROWS;
+          src += ROWS * D;
+          while (g >= p.group) {
+            g -= p.group;
+            src += p.q_stride - p.group * D;
+          }
+        }
       }
       cp_async_wait_all();
       fence_proxy_async_smem();
@@ -593,23 +611,24 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           break;
         }
         if (key0 + BN > first_new) {
-          // Zeros past the context's end, and for drafts' values that are not finite; eight chunks in flight to a
+          // Zeros past the context's end, and for drafts' values that are not finite; four chunks in flight to a
           // lane (one after the other they took 6500 clocks of a short stream's 15000).
           unsigned char* v = smem + (sv + b * C::KV_BYTES - base);
           const int end = min(BN, item.ctx - key0) * CPR;
-          for (int k0 = max(0, first_new - key0) * CPR + lane; k0 < end; k0 += 8 * 32) {
-            uint4 w[8];
+          const __half2 zero = __float2half2_rn(0.f);
+#pragma unroll 1
+          for (int k0 = max(0, first_new - key0) * CPR + lane; k0 < end; k0 += 4 * 32) {
+            uint4 w[4];
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {
+            for (int h = 0; h < 4; ++h) {
               const int k = k0 + h * 32;
               w[h] = make_uint4(0, 0, 0, 0);
               if (k < end) w[h] = *reinterpret_cast<const uint4*>(v + sw128(k / CPR, k % CPR, BN));
             }
             // 0 times a value is a NaN if the value is not finite; sums of those are NaN
-            const __half2 zero = __float2half2_rn(0.f);
             __half2 acc = zero;
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {
+            for (int h = 0; h < 4; ++h) {
               acc = __hfma2(*reinterpret_cast<const __half2*>(&w[h].x), zero, acc);
               acc = __hfma2(*reinterpret_cast<const __half2*>(&w[h].y), zero, acc);
               acc = __hfma2(*reinterpret_cast<const __half2*>(&w[h].z), zero, acc);
@@ -618,7 +637,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
             if (__hisnan(__low2half(acc)) || __hisnan(__high2half(acc))) {
               not_finite[it & 1] = 1;
 #pragma unroll 1
-              for (int k = k0; k < min(end, k0 + 8 * 32); k += 32) {
+              for (int k = k0; k < min(end, k0 + 4 * 32); k += 32) {
                 uint32_t* e = reinterpret_cast<uint32_t*>(v + sw128(k / CPR, k % CPR, BN));
 #pragma unroll 1
                 for (int h = 0; h < 4; ++h)
@@ -626,9 +645,11 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
               }
             }
           }
-#pragma unroll 8
-          for (int k = end + lane; k < BN * CPR; k += 32)
-            *reinterpret_cast<uint4*>(v + sw128(k / CPR, k % CPR, BN)) = make_uint4(0, 0, 0, 0);
+          // a lane's rows ROWS apart: the same chunk of each
+          constexpr int ROWS = 32 / CPR;
+#pragma unroll 2
+          for (int r = end / CPR + lane / CPR; r < BN; r += ROWS)
+            *reinterpret_cast<uint4*>(v + sw128(r, lane % CPR, BN)) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();                           // these writes -> tensor-core reads
           __syncwarp();
         }
@@ -669,8 +690,6 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       const bool works = warp * 32 < item.rows;
       const int row = item.first_row + min(tid, item.rows - 1), node = row / p.group, first_new = item.ctx - item.n;
       float l = 0.f, m_ref = -INFINITY;
-      if (p.mask != nullptr && (item.tile0 + item.n_tiles) * BN > first_new)
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.mask + static_cast<int64_t>(item.q0 + node) * p.mask_words));
       for (int i = 0; i < item.n_tiles; ++i, ++j) {
         const int u = j & 1, key0 = (item.tile0 + i) * BN;
         const uint32_t ts = t_s(u);
@@ -765,20 +784,6 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         for (int c = 0; c < D / 32; ++c) {
           float x[32];
           tmem_ld32(t_o + lane_off + c * 32, x);
-          if (fix) {
-            // values of drafts that are not finite, where the row sees them (rare, so small rather than fast)
-            const int from = max(first_new, item.tile0 * BN), to = min(item.ctx, (item.tile0 + item.n_tiles) * BN);
-#pragma unroll 1
-            for (int t = from; t < to; ++t) {
-              const int phys = p.tables[static_cast<size_t>(item.s) * p.max_blocks + (t >> lb)];
-              if (!(seen_from(p, item.q0 + node, node, t, first_new) & 1) || phys < 0 || phys >= p.num_blocks) continue;
-              const __half* v = p.v + (((static_cast<size_t>(phys) * p.num_kv_heads + item.kv_head) << lb) + (t & (B - 1))) * D + c * 32;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!finite16(__half_as_ushort(v[e]))) x[e] += __half2float(v[e]);
-            }
-            __syncwarp();
-          }
           if (item.slot >= 0) {
             if (real) {
 #pragma unroll
@@ -795,6 +800,24 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           }
           __syncwarp();
         }
+        if (fix && real) {
+          // values of drafts that are not finite were left out: added to what is stored, where the row sees them
+          // (rare, so its code is small rather than fast)
+          const int from = max(first_new, item.tile0 * BN), to = min(item.ctx, (item.tile0 + item.n_tiles) * BN);
+#pragma unroll 1
+          for (int t = from; t < to; ++t) {
+            const int phys = p.tables[static_cast<size_t>(item.s) * p.max_blocks + (t >> lb)];
+            if (!(seen_from(p, item.q0 + node, node, t, first_new) & 1) || phys < 0 || phys >= p.num_blocks) continue;
+            const __half* v = p.v + (((static_cast<size_t>(phys) * p.num_kv_heads + item.kv_head) << lb) + (t & (B - 1))) * D;
+#pragma unroll 1
+            for (int e = 0; e < D; ++e) {
+              if (finite16(__half_as_ushort(v[e]))) continue;
+              if (item.slot >= 0) part[e * BM] += __half2float(v[e]);
+              else dst[e] = __float2half_rn(__half2float(dst[e]) + __half2float(v[e]));
+            }
+          }
+        }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -815,10 +838,10 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
   }
 }
 
-// Joins the parts of the cut streams: CTA (w, y) columns 32 y .. of the one that CTA w of the grid before noted.
+// Joins the parts of the cut streams: CTA (w, y) columns COLS y .. of the one that CTA w of the grid before noted.
 // A thread takes a row and four columns at a time; where rows are few, groups of threads share the parts.
 constexpr int JOIN_THREADS = 512;
-template <int D>
+template <int D, int COLS>
 __global__ void __launch_bounds__(JOIN_THREADS) tree_attention_join_kernel(const __grid_constant__ TreeParams p) {
   __shared__ float group_m[JOIN_THREADS], group_l[JOIN_THREADS], group_o[4][JOIN_THREADS];
   pkv::pdl_trigger();
@@ -827,14 +850,15 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_attention_join_kernel(const
   if (cut.parts <= 1) return;
   int rp = 8;                                                 // the rows, to a power of two
   while (rp < cut.rows) rp *= 2;
-  const int groups = max(1, JOIN_THREADS / (rp * 8));         // that share the parts
-  const int tid = threadIdx.x, r = tid & (rp - 1), cg = (tid / rp) & 7, pg = tid / (rp * 8);
+  constexpr int CG = COLS / 4;
+  const int groups = max(1, JOIN_THREADS / (rp * CG));        // that share the parts
+  const int tid = threadIdx.x, r = tid & (rp - 1), cg = (tid / rp) & (CG - 1), pg = tid / (rp * CG);
   const bool real = r < cut.rows;
   auto slot_of = [&](int part) { return static_cast<size_t>(part == 0 ? cut.slot : cut.next + 2 * (part - 1)); };
   const int row = cut.first_row + min(r, cut.rows - 1), node = row / p.group, head = cut.kv_head * p.group + row - node * p.group;
-  __half* dst = p.out + (static_cast<size_t>(cut.q0 + node) * p.num_heads + head) * D + blockIdx.y * 32;
+  __half* dst = p.out + (static_cast<size_t>(cut.q0 + node) * p.num_heads + head) * D + blockIdx.y * COLS;
   // with 128 rows a thread takes two groups of columns, one after the other
-  for (int col = cg * 4; col < 32; col += max(1, JOIN_THREADS / rp) >= 8 ? 32 : JOIN_THREADS / rp * 4) {
+  for (int col = cg * 4; col < COLS; col += min(CG, JOIN_THREADS / rp) * 4) {
     float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     constexpr int FLY = 4;
     for (int k0 = pg; k0 < cut.parts; k0 += groups * FLY) {
@@ -848,7 +872,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_attention_join_kernel(const
         for (int e = 0; e < 4; ++e) x[u][e] = 0.f;
         if (k < cut.parts && real) {
           ml[u] = p.ws_ml[slot_of(k) * BM + r];
-          const float* src = p.ws_o + (slot_of(k) * D + blockIdx.y * 32 + col) * BM + r;
+          const float* src = p.ws_o + (slot_of(k) * D + blockIdx.y * COLS + col) * BM + r;
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[u][e] = src[e * BM];
         }
@@ -879,7 +903,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_attention_join_kernel(const
       __syncthreads();
       if (pg == 0) {
         for (int g = 1; g < groups; ++g) {
-          const int other = tid + g * rp * 8;
+          const int other = tid + g * rp * CG;
           const float om = group_m[other], m = fmaxf(M, om), a = M == -INFINITY ? 0.f : exp2f(M - m),
                       b = om == -INFINITY ? 0.f : exp2f(om - m);
           M = m;
@@ -913,6 +937,7 @@ int device_sms() {
 // Two CTAs to an SM, or as many as the longest contexts would give kMinTiles key tiles each.
 struct Plan {
   int workers;
+  long long streams;               // at most
   long long most_tiles;
 };
 Plan plan_for(int num_seqs, int total_q, int max_query_len, int num_heads, int num_kv_heads, long long max_ctx) {
@@ -922,7 +947,8 @@ Plan plan_for(int num_seqs, int total_q, int max_query_len, int num_heads, int n
   const long long rows = static_cast<long long>(max_query_len) * group, per_seq = (rows + BM - 1) / BM;
   const long long by_rows = num_seqs + static_cast<long long>(total_q) * group / BM;
   const long long row_tiles = per_seq * num_seqs < by_rows ? per_seq * num_seqs : by_rows;
-  pl.most_tiles = row_tiles * num_kv_heads * ((max_ctx + BN - 1) / BN);
+  pl.streams = row_tiles * num_kv_heads;
+  pl.most_tiles = pl.streams * ((max_ctx + BN - 1) / BN);
   const long long want = (pl.most_tiles + kMinTiles - 1) / kMinTiles, most = 2 * device_sms();
   pl.workers = static_cast<int>(want < most ? want : most);
   if (rows > BM) pl.workers += pl.workers & 1;                // pairs of row tiles want pairs of CTAs
@@ -951,7 +977,7 @@ int encode_pool_map(const char* fn, CUtensorMap* map, const void* pool, int D, i
 }
 
 template <int D, int QR>
-int launch(const char* fn, const TreeParams& p, int workers, cudaStream_t st) {
+int launch(const char* fn, const TreeParams& p, int workers, bool many_parts, cudaStream_t st) {
   using C = Cfg<D, QR>;
   static std::mutex mu;
   static bool done[64] = {false};
@@ -967,7 +993,8 @@ int launch(const char* fn, const TreeParams& p, int workers, cudaStream_t st) {
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s setup: %s", fn, cudaGetErrorString(e));
   e = pkv::launch_pdl(tree_attention_kernel<D, QR>, dim3(workers), dim3(THREADS), C::SMEM, st, p);
   if (e == cudaSuccess && workers > 1)
-    e = pkv::launch_pdl(tree_attention_join_kernel<D>, dim3(workers, D / 32), dim3(JOIN_THREADS), 0, st, p);
+    e = many_parts ? pkv::launch_pdl(tree_attention_join_kernel<D, 4>, dim3(workers, D / 4), dim3(JOIN_THREADS), 0, st, p)
+                   : pkv::launch_pdl(tree_attention_join_kernel<D, 32>, dim3(workers, D / 32), dim3(JOIN_THREADS), 0, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
   return PKV_OK;
@@ -1080,10 +1107,11 @@ int pkv_paged_attention_tree(const uint16_t* q, int64_t q_stride, const uint16_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // few rows leave shared memory for more key tiles in flight
   const int rows = max_query_len * p.group;
-  const int rc = head_dim == 64 ? launch<64, 128>(fn, p, pl.workers, st)
-                 : rows <= 32   ? launch<128, 32>(fn, p, pl.workers, st)
-                 : rows <= 64   ? launch<128, 64>(fn, p, pl.workers, st)
-                                : launch<128, 128>(fn, p, pl.workers, st);
+  const bool many = pl.workers > kManyParts * pl.streams;
+  const int rc = head_dim == 64 ? launch<64, 128>(fn, p, pl.workers, many, st)
+                 : rows <= 32   ? launch<128, 32>(fn, p, pl.workers, many, st)
+                 : rows <= 64   ? launch<128, 64>(fn, p, pl.workers, many, st)
+                                : launch<128, 128>(fn, p, pl.workers, many, st);
   if (rc == PKV_OK) pkv::clear_error();
   return rc;
 }
