@@ -9,6 +9,9 @@
 // Where none stays the next token is drawn from R: the least index whose running sum passes u_0 sum R.
 // So each kept and drawn token is distributed as the target alone would draw it.
 //
+// After k refusals at a node R = max(p - C q, 0) with C = 1 + M_1 + .. + M_(k-1), so a pass over a row costs one
+// product a value however often something was refused there.
+//
 // R and M are whole numbers in units of 2^-60 (fp32 values up to 1 lose only what is below 2^-60):
 // sums of whole numbers do not depend on their order, and the drawn token is the same however a row is
 // cut up.  In fp32 a running sum over 131072 values is off by more than most of its steps.
@@ -40,6 +43,8 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kMaxNodes = 1024;      // of a sequence
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;         // of a cluster
+constexpr int kResident = 4;         // CTAs to an SM
+constexpr int kEnough = 1024;
 constexpr u64 kOne = 1ull << 60, kMost = 1ull << 61;
 
 // The same of a row's values where all of them are in [0, 1] (largest: the bits of the largest met, so that the
@@ -61,6 +66,16 @@ __device__ __forceinline__ u64 whole(float p, bool& bad) {
 }
 // floor(a b / 2^60), a and b up to 2^61
 __device__ __forceinline__ u64 part_of(u64 a, u64 b) { return __umul64hi(a << 2, b << 2); }
+// What refusals take from a value: C q with C = whole + part / 2^60; off - p is what counts, so no more than 2.
+struct Taken {
+  unsigned whole;
+  u64 part;
+};
+__device__ __forceinline__ u64 less(u64 p, u64 q, const Taken& c) {
+  const u64 high = static_cast<u64>(static_cast<unsigned>(q >> 32)) * c.whole;
+  const u64 off = high >> 29 ? kMost : q * c.whole + part_of(c.part, q);
+  return p > off ? p - off : 0;
+}
 // sums that stay below 2^62 whatever the rows hold
 __device__ __forceinline__ u64 add_most(u64 a, u64 b) {
   const u64 c = a + b;
@@ -120,19 +135,18 @@ struct Nodes {
 // What the first CTA tells the others: a pass over row `row` with the first `refused` of its refusals, and
 // whether the next token is drawn from what it leaves.
 struct Order {
-  int row, refused, last, pad;
-  u64 u0;
+  int row, refused, last;
+  unsigned taken_whole;
+  u64 taken_part, u0;
 };
 
-__global__ void __launch_bounds__(kThreads, 3) verify_draft_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const VerifyParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  // the refusals at the current node: M before each (with a draft distribution), or the tokens
-  u64* refused_m = reinterpret_cast<u64*>(smem);
-  int* refused_x = reinterpret_cast<int*>(smem);
-  Nodes& nodes = *reinterpret_cast<Nodes*>(smem + kMaxNodes * 8);     // the first CTA's only
+  int* refused_x = reinterpret_cast<int*>(smem);                      // without draft distributions: the refused tokens
+  Nodes& nodes = *reinterpret_cast<Nodes*>(smem + kMaxNodes * 4);     // the first CTA's only
   __shared__ Order order;
   __shared__ u64 cta_sum[2][kMostCtas];
-  __shared__ u64 warp_sum[kWarps];
+  __shared__ u64 warp_sum[kWarps], part_sum[kWarps];
   __shared__ int cta_bad[2][kMostCtas];
 
   pkv::pdl_trigger();
@@ -177,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 3) verify_draft_kernel(const VerifyP
   // the walk's state, in the first CTA's first warp
   int at = 0, size = 1, next = 1, k = 0;
   u64 share = kOne;
+  Taken taken{0, 0};
   bool ended = false;                                         // the row's sum is all that is left to find
   const int most = p.max_path;
   if (rank == 0 && tid < p.max_path) p.path[static_cast<int64_t>(s) * most + tid] = tid == 0 && ok ? 0 : -1;
@@ -209,10 +224,7 @@ __global__ void __launch_bounds__(kThreads, 3) verify_draft_kernel(const VerifyP
         u64 has = nodes.has[j];
         const u64 drawn = nodes.drawn[j];
         if (p.draft != nullptr) {
-          for (int i = 0; i < k; ++i) {
-            const u64 off = part_of(refused_m[i], drawn);
-            has = has > off ? has - off : 0;
-          }
+          has = less(has, drawn, taken);
         } else {
           for (int i = 0; i < k; ++i)
             if (refused_x[i] == nodes.token[j]) has = 0;
@@ -223,9 +235,11 @@ __global__ void __launch_bounds__(kThreads, 3) verify_draft_kernel(const VerifyP
           at = j;
           share = kOne;
           k = 0;
+          taken = Taken{0, 0};
         } else if (p.draft != nullptr) {
-          __syncwarp();
-          if (lane < ctas) st_cluster(map_to_rank(refused_m + k, lane), share);
+          const u64 c = taken.part + share;
+          taken.whole += static_cast<unsigned>(c >> 60);
+          taken.part = c & (kOne - 1);
           ++k;
           wants = true;                                       // M is the sum of what is left
         } else if (has > 0) {                                 // a token that is left nothing is noted already, or was 0
@@ -250,7 +264,9 @@ __global__ void __launch_bounds__(kThreads, 3) verify_draft_kernel(const VerifyP
         st_cluster(to, ok ? q0 + at : -1);
         st_cluster(to + 4, k);
         st_cluster(to + 8, static_cast<int>(ended));
-        st_cluster(to + 16, ok ? nodes.u[0] : 0ull);
+        st_cluster(to + 12, static_cast<int>(taken.whole));
+        st_cluster(to + 16, taken.part);
+        st_cluster(to + 24, ok ? nodes.u[0] : 0ull);
       }
     }
     cluster_sync();
@@ -263,20 +279,15 @@ __global__ void __launch_bounds__(kThreads, 3) verify_draft_kernel(const VerifyP
     const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(prow) >> 2 & 3);
     const bool wide = qrow == nullptr || static_cast<int>(reinterpret_cast<uintptr_t>(qrow) >> 2 & 3) == shift;
     const int lines = (p.vocab + shift + 127) / 128, pieces = ctas * kWarps, mine = rank * kWarps + warp;
-    const int first = static_cast<int>(static_cast<int64_t>(lines) * mine / pieces);
-    const int end = static_cast<int>(static_cast<int64_t>(lines) * (mine + 1) / pieces);
+    auto first_line = [&](int piece) { return static_cast<int>(static_cast<int64_t>(lines) * piece / pieces); };
+    const int first = first_line(mine), end = first_line(mine + 1);
     int refused = o.refused;
+    const Taken all_taken{o.taken_whole, o.taken_part};
     bool bad = false, slow = false;
     auto left = [&](int i) {                                  // R(i) after the refusals
       u64 r = whole(prow[i], bad);
       if (qrow != nullptr) {
-        if (refused > 0) {
-          const u64 q = whole(qrow[i], bad);
-          for (int j = 0; j < refused; ++j) {
-            const u64 off = part_of(refused_m[j], q);
-            r = r > off ? r - off : 0;
-          }
-        }
+        if (refused > 0) r = less(r, whole(qrow[i], bad), all_taken);
       } else {
         for (int j = 0; j < refused; ++j)
           if (refused_x[j] == i) r = 0;
@@ -291,9 +302,9 @@ __global__ void __launch_bounds__(kThreads, 3) verify_draft_kernel(const VerifyP
         if (k >= shift && k - shift < p.vocab) sum = add_most(sum, left(k - shift));
       return sum;
     };
-    // the same of whole lines, 16 bytes at a time; STEPS: refusals that leave their mark (2: two or more)
+    // the same of whole lines, 16 bytes at a time; STEPS: refusals (2: two or more)
     auto fast_sum = [&](auto steps, int from, int to) {
-      constexpr int STEPS = decltype(steps)::value, FLY = STEPS == 0 ? 8 : 4;
+      constexpr int STEPS = decltype(steps)::value, FLY = STEPS == 0 ? 4 : 2;
       u64 sum = 0;
       unsigned largest = 0;
       const float4* pv = reinterpret_cast<const float4*>(prow - shift) + lane;
@@ -311,23 +322,18 @@ __global__ void __launch_bounds__(kThreads, 3) verify_draft_kernel(const VerifyP
         }
 #pragma unroll
         for (int u = 0; u < FLY; ++u) {
+          const float4 a = x[u], c = y[u];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float xe = e == 0 ? x[u].x : e == 1 ? x[u].y : e == 2 ? x[u].z : x[u].w;
+            const float xe = e == 0 ? a.x : e == 1 ? a.y : e == 2 ? a.z : a.w;
             u64 r = whole_fast(xe, largest);
             if (STEPS > 0) {
-              const float ye = e == 0 ? y[u].x : e == 1 ? y[u].y : e == 2 ? y[u].z : y[u].w;
+              const float ye = e == 0 ? c.x : e == 1 ? c.y : e == 2 ? c.z : c.w;
               const u64 q = whole_fast(ye, largest);
-              r = r > q ? r - q : 0;                          // the first refusal's M is 1
-              if (STEPS > 1) {
-#pragma unroll 1
-                for (int j = 1; j < refused; ++j) {
-                  const u64 off = part_of(refused_m[j], q);
-                  r = r > off ? r - off : 0;
-                }
-              }
+              if (STEPS > 1) r = less(r, q, all_taken);
+              else r = r > q ? r - q : 0;                     // the first refusal takes q
             }
-            sum += r;                                         // eight at most before the next line holds it down
+            sum += r;                                         // eight at most before they are held down
           }
           if (u & 1) sum = add_most(sum, 0);
         }
@@ -409,14 +415,36 @@ __global__ void __launch_bounds__(kThreads, 3) verify_draft_kernel(const VerifyP
         aim -= cta_sum[parity][c];
       }
       if (here && aim < cta_sum[parity][rank]) {
+        // in this CTA: its warps share the piece that holds the token, and the one whose lines do goes through
+        // them again, four values to a lane
+        int piece = 0;
+        while (piece < kWarps - 1 && aim >= warp_sum[piece]) aim -= warp_sum[piece++];
+        const int from = first_line(rank * kWarps + piece), count = first_line(rank * kWarps + piece + 1) - from;
+        const int l0 = from + count * warp / kWarps, l1 = from + count * (warp + 1) / kWarps;
+        auto four = [&](int line, u64 (&r)[4]) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = line * 128 + lane * 4 + e - shift;
+            r[e] = i >= 0 && i < p.vocab ? left(i) : 0;
+          }
+          return r[0] + r[1] + r[2] + r[3];
+        };
+        u64 r[4], sum = 0;
+#pragma unroll 2
+        for (int line = l0; line < l1; ++line) sum += four(line, r);
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(FULL, sum, d);
+        if (lane == 0) part_sum[warp] = sum;
+        __syncthreads();
         for (int w = 0; w < warp; ++w) {
-          here &= aim >= warp_sum[w];
-          aim -= warp_sum[w];
+          here &= aim >= part_sum[w];
+          aim -= part_sum[w];
         }
-        if (here && aim < warp_sum[warp]) {
-          for (int base = first * 128 - shift; base < end * 128 - shift; base += 32) {
-            const int i = base + lane;
-            u64 upto = i >= 0 && i < p.vocab ? left(i) : 0;
+        if (here && aim < part_sum[warp]) {
+#pragma unroll 1
+          for (int line = l0; line < l1; ++line) {
+            const u64 mine = four(line, r);
+            u64 upto = mine;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
               const u64 y = __shfl_up_sync(FULL, upto, d);
@@ -424,7 +452,12 @@ __global__ void __launch_bounds__(kThreads, 3) verify_draft_kernel(const VerifyP
             }
             const unsigned past = __ballot_sync(FULL, upto > aim);
             if (past) {
-              if (lane == 0) p.next_token[s] = base + __ffs(past) - 1;
+              if (lane == __ffs(past) - 1) {
+                u64 rest = aim - (upto - mine);
+                int e = 0;
+                while (e < 3 && rest >= r[e]) rest -= r[e++];
+                p.next_token[s] = line * 128 + lane * 4 + e - shift;
+              }
               break;
             }
             aim -= __shfl_sync(FULL, upto, 31);
@@ -562,10 +595,12 @@ int pkv_verify_draft(const float* target_probs, const float* draft_probs, const 
   p.total_q = total_q;
   p.vocab = vocab_size;
   p.max_path = max_path;
-  constexpr int smem = kMaxNodes * 8 + static_cast<int>(sizeof(Nodes));
+  constexpr int smem = kMaxNodes * 4 + static_cast<int>(sizeof(Nodes));
   static_assert(smem <= 47 * 1024, "fits without asking for more");
-  cudaError_t e = pkv::launch_pdl_cluster(verify_draft_kernel, dim3(num_seqs * kMostCtas), dim3(kThreads), smem,
-                                          static_cast<cudaStream_t>(stream), kMostCtas, p);
+  int ctas = kMostCtas;
+  while (ctas > 1 && num_seqs * ctas > kEnough) ctas /= 2;
+  cudaError_t e = pkv::launch_pdl_cluster(verify_draft_kernel, dim3(num_seqs * ctas), dim3(kThreads), smem,
+                                          static_cast<cudaStream_t>(stream), ctas, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
   pkv::clear_error();
