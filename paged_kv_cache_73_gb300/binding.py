@@ -8,8 +8,10 @@ or a call fails, a ``PkvError`` is raised.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
+import operator
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -795,6 +797,20 @@ def _need_pools(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: int) -> Tuple
     return k_cache.shape
 
 
+_dtype_and_shape = operator.attrgetter("dtype", "shape")
+
+
+def _layer_pointers(pools: Sequence[torch.Tensor], shape: torch.Size, dev: int, name: str) -> array.array:
+    """The addresses of every layer's fp16 pool, all of them contiguous, of `shape` and on the current device, dev.
+    (The checks run through map: a loop's over 80 pools takes longer than everything else of a call.)"""
+    if list(map(_dtype_and_shape, pools)) != [(torch.float16, shape)] * len(pools) \
+            or not all(map(torch.Tensor.is_contiguous, pools)) or set(map(torch.Tensor.get_device, pools)) != {dev}:
+        for t in pools:
+            _need(t, name, torch.float16, 4)
+        raise PkvError(PKV_ERR_INVALID_ARG, f"{name}: pools differ in shape")
+    return array.array("Q", map(torch.Tensor.data_ptr, pools))
+
+
 def rope_and_cache(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor,
                    frequencies: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                    slot_mapping: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
@@ -962,7 +978,8 @@ def verify_draft(target_probs: torch.Tensor, tokens: torch.Tensor, parents: torc
     if S < 0 or max_path <= 0:
         raise PkvError(PKV_ERR_INVALID_ARG, "verify_draft: query_start needs num_seqs + 1 entries, max_path a place")
     path = _empty((S, max_path), torch.int32, target_probs, stream)
-    path_len, next_token = _empty((2, S), torch.int32, target_probs, stream)
+    path_len = _empty((S,), torch.int32, target_probs, stream)
+    next_token = _empty((S,), torch.int32, target_probs, stream)
     _check(load().pkv_verify_draft(
         target_probs.data_ptr(), _ptr(draft_probs), tokens.data_ptr(), parents.data_ptr(), query_start.data_ptr(),
         uniforms.data_ptr(), S, T, V, ts, ds, max_path, path.data_ptr(), path_len.data_ptr(), next_token.data_ptr(),
@@ -977,9 +994,10 @@ def move_accepted(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Ten
     L = len(k_caches)
     if len(v_caches) != L or L == 0:
         raise PkvError(PKV_ERR_INVALID_ARG, "move_accepted: need as many K as V pools, at least one")
-    for k, v in zip(k_caches, v_caches):
-        if _need_pools(k, v, dev) != k_caches[0].shape:
-            raise PkvError(PKV_ERR_INVALID_ARG, "move_accepted: pools differ in shape")
+    shape = k_caches[0].shape
+    ks, vs = _layer_pointers(k_caches, shape, dev, "k_caches"), _layer_pointers(v_caches, shape, dev, "v_caches")
+    if len(shape) != 4:
+        raise PkvError(PKV_ERR_INVALID_ARG, "move_accepted: pools must be [N, H, B, D]")
     for t, name, dtype, dim in ((slot_mapping, "slot_mapping", torch.int64, 1), (query_start, "query_start", torch.int32, 1),
                                 (path, "path", torch.int32, 2), (path_len, "path_len", torch.int32, 1)):
         if not _is(t, dtype, dim, dev):
@@ -987,10 +1005,8 @@ def move_accepted(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Ten
     S, max_path = path.shape
     if query_start.shape[0] != S + 1 or path_len.shape[0] != S:
         raise PkvError(PKV_ERR_INVALID_ARG, "move_accepted: path and path_len need a row per sequence of query_start")
-    N, H, B, D = k_caches[0].shape
-    kp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in k_caches])
-    vp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in v_caches])
-    _check(load().pkv_move_accepted(kp, vp, L, slot_mapping.data_ptr(), query_start.data_ptr(), path.data_ptr(),
+    N, H, B, D = shape
+    _check(load().pkv_move_accepted(ks.buffer_info()[0], vs.buffer_info()[0], L, slot_mapping.data_ptr(), query_start.data_ptr(), path.data_ptr(),
                                     path_len.data_ptr(), S, slot_mapping.shape[0], max_path, H, D, B, N,
                                     _stream(stream, dev)))
 
