@@ -24,7 +24,10 @@
 //
 // With CACHED the turned keys go to their slots of a paged pool instead, and the values, which
 // are not touched, to theirs: the key's second trip through memory (written, then read by the scatter) and
-// one launch are saved.  A token's slot is read once by the warp that takes the token.
+// one launch are saved.  A token's slot is read once by the warp that takes the token.  The addresses
+// want more registers than 80: with five CTAs to an SM 16411 tokens of 40 + 8 + 8 heads of 128 with norms take
+// 75 us, 94 % of the copy rate (six, with spills, 87, four 80), 1024 of 64 + 8 + 8 with interleaved pairs 9.8, and
+// 64 of 40 + 40 + 40 heads 3.4 in a row of such calls.
 // Measured: 32768 tokens of 40 + 8 heads of 128 with norms and three axes, 122 us, 98 % of the
 // copy rate, and with interleaved pairs 139 us, 85 % (122 registers against 80, four CTAs to an SM against
 // six); 64 tokens of 40 + 40 heads 4.6 us in a row of such calls, a launch and two round trips.
@@ -92,7 +95,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 
 // grid (tokens / (kWarps TPW), parts of a token's query and key (and value) heads); TPW tokens to a warp
 template <int D, bool INTERLEAVED, int TPW, bool CACHED>
-__global__ void __launch_bounds__(kWarps * 32, INTERLEAVED ? 4 : 6) qk_norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, INTERLEAVED ? 4 : CACHED ? 5 : 6) qk_norm_rope_kernel(const RopeParams p) {
   constexpr int LPR = D / 16;                       // lanes per row
   constexpr int LANES = 32 / TPW;                   // lanes per token
   constexpr int RPP = LANES / LPR;                  // rows they take at a time
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kWarps * 32, INTERLEAVED ? 4 : 6) qk_norm_rope
     __half* dst_base = part == 0 ? q_out : k_out;
     // the prefetched rows run on from the query rows into the key rows only where a pass ends there:
     // otherwise the key rows start anew
-    if (part == 1 && begin < p.num_heads) {
+    if (part == 1 && begin < p.num_heads && (p.num_heads - begin) % (PF * RPP) != 0) {
 #pragma unroll
       for (int u = 0; u < PF; ++u) load(r0 + u * RPP + sub, raw[u]);
     }
@@ -269,8 +272,8 @@ __global__ void __launch_bounds__(kWarps * 32, INTERLEAVED ? 4 : 6) qk_norm_rope
   }
   if constexpr (CACHED) {
     // the values, as they are
-    const int r0 = max(begin, turned_rows);
-    if (begin < turned_rows) {
+    const int r0 = max(begin, turned_rows), before = max(begin, p.num_heads);
+    if (begin < turned_rows && (turned_rows - before) % (PF * RPP) != 0) {
 #pragma unroll
       for (int u = 0; u < PF; ++u) load(r0 + u * RPP + sub, raw[u]);
     }
