@@ -122,13 +122,16 @@ struct Cfg {
   // ring slots for K and V: as many as two CTAs' shared memory holds
   static constexpr int NK = D == 64 ? 5 : QR == 32 ? 3 : 2;
   static constexpr int NV = D == 64 ? 6 : QR == 128 ? 2 : 3;
+  // S buffers: with three S(j + 1) need not wait for PV(j - 1) (D = 64 wide trees W2 -> W3 us)
+  static constexpr int NB = D == 64 ? 3 : 2;
   static constexpr int BYTES = 1024 + Q_BYTES + (NK + NV) * KV_BYTES + 512;
   // so much that no third CTA, which would wait for tensor memory, fits an SM
   static constexpr int SMEM = BYTES > 80 * 1024 ? BYTES : 80 * 1024;
   static_assert(SMEM <= 113 * 1024 && BM * D * 2 <= Q_BYTES + (NK + NV) * KV_BYTES, "two to an SM; a product's rows lie inside");
 };
-// Tensor memory: the O accumulator and two S buffers of 64 columns, a half of the SM's 512 columns.
-constexpr uint32_t TMEM_COLS = 256, O_COL = 0, S_COL = 128;
+// Tensor memory: the O accumulator (D columns) and as many S buffers of 64 columns as a half of the SM's 512
+// columns has room for.
+constexpr uint32_t TMEM_COLS = 256;
 constexpr int W_K = 4, W_V = 5, W_S = 6, W_PV = 7;            // warps 0 to 3: softmax
 constexpr int THREADS = 256;
 
@@ -198,27 +201,27 @@ __device__ __forceinline__ uint64_t seen_from(const TreeParams& p, int q_row, in
 template <int D, int QR>
 __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<D, QR>;
-  constexpr int NK = C::NK, NV = C::NV, CPR = D / 8;          // CPR: 16-byte chunks per row
+  constexpr int NK = C::NK, NV = C::NV, NB = C::NB, CPR = D / 8;   // CPR: 16-byte chunks per row
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - raw);
   const uint32_t sq = base, sk = sq + C::Q_BYTES, sv = sk + NK * C::KV_BYTES, bars = sv + NV * C::KV_BYTES;
-  // per S buffer u (key tile j uses j % 2), per ring slot b, per item slot i (item number % 2)
+  // per S buffer u (key tile j uses j % NB), per ring slot b, per item slot i (item number % 2)
   auto s_full = [&](int u) { return bars + 8u * u; };
-  auto p_full = [&](int u) { return bars + 16u + 8u * u; };
-  auto pv_done = [&](int u) { return bars + 32u + 8u * u; };
-  auto item_full = [&](int i) { return bars + 48u + 8u * i; };
-  auto item_free = [&](int i) { return bars + 64u + 8u * i; };
-  const uint32_t q_free = bars + 80, o_free = bars + 88;
-  auto k_full = [&](int b) { return bars + 96u + 8u * b; };
-  auto k_free = [&](int b) { return bars + 96u + 8u * (NK + b); };
-  auto v_full = [&](int b) { return bars + 96u + 8u * (2 * NK + b); };
-  auto v_free = [&](int b) { return bars + 96u + 8u * (2 * NK + NV + b); };
-  constexpr uint32_t AT = 96 + 16 * (NK + NV);
+  auto p_full = [&](int u) { return bars + 24u + 8u * u; };
+  auto pv_done = [&](int u) { return bars + 48u + 8u * u; };
+  auto item_full = [&](int i) { return bars + 72u + 8u * i; };
+  auto item_free = [&](int i) { return bars + 88u + 8u * i; };
+  const uint32_t q_free = bars + 104, o_free = bars + 112;
+  auto k_full = [&](int b) { return bars + 120u + 8u * b; };
+  auto k_free = [&](int b) { return bars + 120u + 8u * (NK + b); };
+  auto v_full = [&](int b) { return bars + 120u + 8u * (2 * NK + b); };
+  auto v_free = [&](int b) { return bars + 120u + 8u * (2 * NK + NV + b); };
+  constexpr uint32_t AT = 120 + 16 * (NK + NV);
   // Which of a tile's positions are in the context and in a block of the pool, for key tile j in place j % 8: K(j) is
-  // loaded once S(j - NK) is done, and so PV(j - NK - 2) and what the softmax read for that tile.
-  static_assert(NK + 2 <= 8, "a tile's word is read before it is written anew");
+  // loaded once S(j - NK) is done, and so PV(j - NK - NB) and what the softmax read for that tile.
+  static_assert(NK + NB <= 8 && NB <= 3, "a tile's word is read before it is written anew");
   volatile uint2* live = reinterpret_cast<volatile uint2*>(smem + (bars + AT - base));               // [8]
   volatile Item* items = reinterpret_cast<volatile Item*>(smem + (bars + AT + 64 - base));           // [2]
   volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + AT + 144 - base));       // [2]
@@ -236,10 +239,12 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
     tc_fence_before();
   }
   if (tid == 32) {
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < NB; ++u) {
       mbar_init_count(s_full(u), 1);
       mbar_init_count(p_full(u), 4);
       mbar_init_count(pv_done(u), 1);
+    }
+    for (int u = 0; u < 2; ++u) {
       mbar_init_count(item_full(u), 1);
       mbar_init_count(item_free(u), 7);                       // 4 softmax warps, both issuers, the V loader
     }
@@ -263,8 +268,9 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto t_s = [&](int u) { return tmem + S_COL + 64u * u; };
-  const uint32_t t_o = tmem + O_COL;
+  auto t_s = [&](int u) { return tmem + D + 64u * u; };
+  const uint32_t t_o = tmem;
+  static_assert(D + 64 * NB <= TMEM_COLS, "tensor memory");
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag); };
   auto warp_wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   auto give_up = [&]() {
@@ -314,11 +320,14 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       const int H = p.num_kv_heads;
       long long pairs = 0, alone = 0;
       int code = 0;
+      const Seq first32 = seq_of(p, lane, &code);
+      Seq y = first32;
 #pragma unroll 1
-      for (int i = lane; i < p.num_seqs; i += 32) {
-        const Seq y = seq_of(p, i, &code);
+      for (int i = lane;;) {
         pairs += places_of(y, H, PAIRS);
         alone += places_of(y, H, ALONE);
+        if ((i += 32) >= p.num_seqs) break;
+        y = seq_of(p, i, &code);
       }
       if (code && blockIdx.x == 0) record_error(code);
 #pragma unroll
@@ -348,8 +357,10 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         // the sequence: the first whose tiles, all streams together, reach past x
         long long before = 0;
         s = p.num_seqs;
-        for (int first = 0; first < p.num_seqs; first += 32) {
-          const long long mine = places_of(seq_of(p, first + lane, &code), H, kind);
+        y = first32;
+#pragma unroll 1
+        for (int first = 0;;) {
+          const long long mine = places_of(y, H, kind);
           long long upto = mine;
 #pragma unroll
           for (int o = 1; o < 32; o *= 2) {
@@ -361,11 +372,17 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
             const int hit = __ffs(past) - 1;
             s = first + hit;
             before += __shfl_sync(0xffffffffu, upto - mine, hit);
+            seq.ctx = __shfl_sync(0xffffffffu, y.ctx, hit);
+            seq.n = __shfl_sync(0xffffffffu, y.n, hit);
+            seq.q0 = __shfl_sync(0xffffffffu, y.q0, hit);
+            seq.tiles = __shfl_sync(0xffffffffu, y.tiles, hit);
+            seq.row_tiles = __shfl_sync(0xffffffffu, y.row_tiles, hit);
             break;
           }
           before += __shfl_sync(0xffffffffu, upto, 31);
+          if ((first += 32) >= p.num_seqs) break;
+          y = seq_of(p, first + lane, &code);
         }
-        seq = seq_of(p, s, &code);
         if (streams_of(seq, kind) == 0) {
           left = 0;                                           // the lengths changed meanwhile
         } else {
@@ -532,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
     // ---------------- Q, and S = Q K^T issue (one lane) ----------------
     constexpr uint32_t IDESC_QK = umma_idesc_f16(BM, BN, false);
     const uint64_t a0 = umma_smem_desc(sq, 16, 1024);
-    int j = 0;
+    int j = 0, u = 0, phase = 0;                              // tile j: S buffer u = j % NB, phase = j / NB
     for (int it = 0;; ++it) {
       Item item;
       if (!__all_sync(0xffffffffu, take_item(it, item) && (it == 0 || wait(q_free, (it - 1) & 1)))) {
@@ -564,8 +581,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       if (lane == 0) {
         mbar_arrive(item_free(it & 1));
         for (int i = 0; i < item.n_tiles; ++i, ++j) {
-          const int u = j & 1;
-          if (!wait(k_full(j % NK), (j / NK) & 1) || (j >= 2 && !wait(pv_done(u), ((j - 2) >> 1) & 1))) {
+          if (!wait(k_full(j % NK), (j / NK) & 1) || (phase > 0 && !wait(pv_done(u), (phase - 1) & 1))) {
             failed = true;
             break;
           }
@@ -579,6 +595,10 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
                     b0 + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), IDESC_QK, 1u);
           umma_commit(s_full(u));
           umma_commit(k_free(j % NK));
+          if (++u == NB) {
+            u = 0;
+            ++phase;
+          }
         }
         if (!failed) umma_commit(q_free);
       }
@@ -588,12 +608,12 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
     }
     if (failed) {
       give_up();
-      if (j > 0) mbar_wait(s_full((j - 1) & 1), ((j - 1) >> 1) & 1);
+      if (j > 0) mbar_wait(s_full((j - 1) % NB), ((j - 1) / NB) & 1);
     }
   } else if (warp == W_PV) {
     // ---------------- O += P V issue (one lane); V tiles that some row does not see whole ----------------
     constexpr uint32_t IDESC_PV = umma_idesc_f16(BM, D, true);
-    int j = 0;
+    int j = 0, u = 0, phase = 0;
     for (int it = 0;; ++it) {
       Item item;
       if (!__all_sync(0xffffffffu, take_item(it, item))) {
@@ -605,7 +625,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       __syncwarp();
       const int first_new = item.ctx - item.n;
       for (int i = 0; i < item.n_tiles; ++i, ++j) {
-        const int u = j & 1, b = j % NV, key0 = (item.tile0 + i) * BN;
+        const int b = j % NV, key0 = (item.tile0 + i) * BN;
         if (!warp_wait(v_full(b), (j / NV) & 1)) {
           failed = true;
           break;
@@ -655,7 +675,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         }
         if (lane == 0) {
           // the first product overwrites the accumulator: the last item's output has been read
-          if ((i == 0 && it > 0 && !wait(o_free, (it - 1) & 1)) || !wait(p_full(u), (j >> 1) & 1)) {
+          if ((i == 0 && it > 0 && !wait(o_free, (it - 1) & 1)) || !wait(p_full(u), phase & 1)) {
             failed = true;
           } else {
             tc_fence_after();
@@ -670,18 +690,23 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         }
         failed = __shfl_sync(0xffffffffu, failed, 0);
         if (failed) break;
+        if (++u == NB) {
+          u = 0;
+          ++phase;
+        }
       }
       if (failed) break;
       if (lane == 0) mbar_arrive(item_free(it & 1));
     }
     if (failed) {
       give_up();
-      if (j > 0) mbar_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1);
+      if (j > 0) mbar_wait(pv_done((j - 1) % NB), ((j - 1) / NB) & 1);
     }
   } else {
     // ---------------- softmax and output ----------------
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    int j = 0;
+    int j = 0, u = 0, phase = 0;
+    uint32_t last = 0, last_phase = 0;                        // of the tile before: its pv_done barrier and phase
     for (int it = 0; !failed; ++it) {
       Item item;
       // decisions stay warp-uniform: the tcgen05.ld/st below are warp-collective
@@ -691,14 +716,20 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       const int row = item.first_row + min(tid, item.rows - 1), node = row / p.group, first_new = item.ctx - item.n;
       float l = 0.f, m_ref = -INFINITY;
       for (int i = 0; i < item.n_tiles; ++i, ++j) {
-        const int u = j & 1, key0 = (item.tile0 + i) * BN;
-        const uint32_t ts = t_s(u);
-        if (!warp_wait(s_full(u), (j >> 1) & 1)) {
+        const int key0 = (item.tile0 + i) * BN;
+        const uint32_t ts = t_s(u), before = last, before_phase = last_phase, here = p_full(u);
+        if (!warp_wait(s_full(u), phase & 1)) {
           failed = true;
           break;
         }
+        last = pv_done(u);
+        last_phase = phase & 1;
+        if (++u == NB) {
+          u = 0;
+          ++phase;
+        }
         if (!works) {
-          if (lane == 0) mbar_arrive(p_full(u));
+          if (lane == 0) mbar_arrive(here);
           continue;
         }
         tc_fence_after();
@@ -733,7 +764,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         }
         const float nref = m_ref == -INFINITY ? 0.f : kLift - m_ref;
         if (__any_sync(0xffffffffu, rescale && i > 0)) {
-          if (!warp_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1)) {
+          if (!warp_wait(before, before_phase)) {
             failed = true;
             break;
           }
@@ -766,9 +797,9 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(u));
+        if (lane == 0) mbar_arrive(here);
       }
-      if (!failed) failed = !warp_wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1);
+      if (!failed) failed = !warp_wait(last, last_phase);
       if (failed) break;
       tc_fence_after();
       if (works) {
