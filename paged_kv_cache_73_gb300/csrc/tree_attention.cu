@@ -16,7 +16,7 @@
 //    that runs on over the ends of streams.
 //  * Where a sequence has more than 128 rows, two CTAs walk two row tiles over the same keys at the same time, so
 //    that the second reads from L2 what the first brought there; one after the other they read 2 x from memory (32
-//    sequences of 20480 tokens, 64 heads on 8, 32 drafts: KV2 us against PAIR2).
+//    sequences of 20480 tokens, 64 heads on 8, 32 drafts: 791 us against 572).
 //  * A stream that is cut leaves partial results (row maximum, sum, output) that a second kernel joins by the
 //    log-sum-exp identity; the first CTA of such a stream notes where they lie.  A CTA has at most
 //    two such parts, the first and the last of its piece.
@@ -47,9 +47,16 @@ using namespace pkv::tc;
 
 constexpr int BM = 128;            // rows of a product (MMA M)
 constexpr int BN = 64;             // key positions per tile
-constexpr int kMinTiles = 2;       // key tiles a CTA takes at least
-constexpr int kStart = 4;          // what a stream costs besides its key tiles, in key tiles
-constexpr int kManyParts = 16;     // a stream cut into more is joined by CTAs of four columns each, not 32
+// Key tiles a CTA takes at least: one sequence of 128 tokens and 40 heads takes 8.5 us with two, 9.9 with one (a
+// second CTA to start for each), 11.2 with three.
+constexpr int kMinTiles = 2;
+// What a stream costs besides its key tiles, in key tiles: 16 wide trees over 276 to 4608 tokens (D = 64) take 49.5 us
+// with 2, 45.0 with 4 and with 6; one sequence of 2048 tokens 16.1, 16.6 and 17.4.
+constexpr int kStart = 4;
+// Where streams are cut into more parts than this (by the longest contexts), CTAs of four columns join them, not of 32:
+// one sequence of 16384 tokens, 32 heads on 8 (38 parts) 20.6 -> 17.8 us, of 131072 on one head (304) 66 -> 27; one of
+// 2048 with 40 heads (8 parts) would go from 16.7 to 36.5, for there are so many streams' CTAs to launch.
+constexpr int kManyParts = 16;
 constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
 constexpr float kLift = 7.f;       // weights are kept as 2^(kLift + S - m)
 
@@ -76,7 +83,7 @@ struct TreeParams {
   int64_t q_stride;
   int mask_words, num_seqs, total_q, max_query_len;
   int num_heads, num_kv_heads, group, num_blocks, max_blocks, log2_block;
-  int use_tma, out_sectors;
+  int use_tma, out_sectors, workers;
   float scale_log2;
 };
 
@@ -85,12 +92,8 @@ struct TreeParams {
 struct Seq {
   int ctx, n, q0, tiles, row_tiles;
 };
-__device__ __forceinline__ Seq seq_of(const TreeParams& p, int s, int* code) {
-  Seq x{0, 0, 0, 0, 0};
-  if (s >= p.num_seqs) return x;
-  x.ctx = p.lens[s];
-  x.q0 = p.qstart[s];
-  x.n = p.qstart[s + 1] - x.q0;
+__device__ __forceinline__ Seq make_seq(const TreeParams& p, int ctx, int q0, int q1, int* code) {
+  Seq x{ctx, q1 - q0, q0, 0, 0};
   if (x.n == 0) return x;
   if (x.ctx < 0 || x.ctx > (p.max_blocks << p.log2_block)) {
     *code = PKV_DEV_BAD_CONTEXT_LEN;
@@ -103,6 +106,9 @@ __device__ __forceinline__ Seq seq_of(const TreeParams& p, int s, int* code) {
   x.tiles = (x.ctx + BN - 1) / BN;
   x.row_tiles = (x.n * p.group + BM - 1) / BM;
   return x;
+}
+__device__ __forceinline__ Seq seq_of(const TreeParams& p, int s, int* code) {
+  return s < p.num_seqs ? make_seq(p, p.lens[s], p.qstart[s], p.qstart[s + 1], code) : Seq{0, 0, 0, 0, 0};
 }
 // Streams of a kind to a cached head: pairs of row tiles, row tiles left alone by those, or (kind ALL) every row tile.
 enum Kind { ALL, PAIRS, ALONE };
@@ -122,9 +128,10 @@ struct Cfg {
   // ring slots for K and V: as many as two CTAs' shared memory holds
   static constexpr int NK = D == 64 ? 5 : QR == 32 ? 3 : 2;
   static constexpr int NV = D == 64 ? 6 : QR == 128 ? 2 : 3;
-  // S buffers: with three S(j + 1) need not wait for PV(j - 1) (D = 64 wide trees W2 -> W3 us)
+  // S buffers: with three S(j + 1) need not wait for PV(j - 1) (16 wide trees of D = 64, 45.0 -> 44.0 us)
   static constexpr int NB = D == 64 ? 3 : 2;
-  static constexpr int BYTES = 1024 + Q_BYTES + (NK + NV) * KV_BYTES + 512;
+  static constexpr int BARS = 1024;
+  static constexpr int BYTES = 1024 + Q_BYTES + (NK + NV) * KV_BYTES + BARS;
   // so much that no third CTA, which would wait for tensor memory, fits an SM
   static constexpr int SMEM = BYTES > 80 * 1024 ? BYTES : 80 * 1024;
   static_assert(SMEM <= 113 * 1024 && BM * D * 2 <= Q_BYTES + (NK + NV) * KV_BYTES, "two to an SM; a product's rows lie inside");
@@ -134,12 +141,17 @@ struct Cfg {
 constexpr uint32_t TMEM_COLS = 256;
 constexpr int W_K = 4, W_V = 5, W_S = 6, W_PV = 7;            // warps 0 to 3: softmax
 constexpr int THREADS = 256;
+constexpr int NI = 2;                                         // items that may be on their way (four or eight change nothing)
 
 // What a CTA does at a time: key tiles [tile0, tile0 + n_tiles) of one stream; n_tiles 0 ends the loop.
 struct Item {
   int s, kv_head, first_row, rows, tile0, n_tiles, ctx, n, q0, slot;  // slot -1: the whole stream, to out
 };
 
+// 4-byte async copy global -> shared
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 // Divisions on the line: 64-bit ones take some 500 clocks, and few lines are that long.
 __device__ __forceinline__ long long divide(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
@@ -207,27 +219,29 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - raw);
   const uint32_t sq = base, sk = sq + C::Q_BYTES, sv = sk + NK * C::KV_BYTES, bars = sv + NV * C::KV_BYTES;
-  // per S buffer u (key tile j uses j % NB), per ring slot b, per item slot i (item number % 2)
+  // per S buffer u (key tile j uses j % NB), per ring slot b, per item slot i (item number % NI)
   auto s_full = [&](int u) { return bars + 8u * u; };
   auto p_full = [&](int u) { return bars + 24u + 8u * u; };
   auto pv_done = [&](int u) { return bars + 48u + 8u * u; };
   auto item_full = [&](int i) { return bars + 72u + 8u * i; };
-  auto item_free = [&](int i) { return bars + 88u + 8u * i; };
-  const uint32_t q_free = bars + 104, o_free = bars + 112;
-  auto k_full = [&](int b) { return bars + 120u + 8u * b; };
-  auto k_free = [&](int b) { return bars + 120u + 8u * (NK + b); };
-  auto v_full = [&](int b) { return bars + 120u + 8u * (2 * NK + b); };
-  auto v_free = [&](int b) { return bars + 120u + 8u * (2 * NK + NV + b); };
-  constexpr uint32_t AT = 120 + 16 * (NK + NV);
+  auto item_free = [&](int i) { return bars + 72u + 8u * (NI + i); };
+  constexpr uint32_t RINGS = 72 + 16 * NI + 16;
+  const uint32_t q_free = bars + RINGS - 16, o_free = bars + RINGS - 8;
+  auto k_full = [&](int b) { return bars + RINGS + 8u * b; };
+  auto k_free = [&](int b) { return bars + RINGS + 8u * (NK + b); };
+  auto v_full = [&](int b) { return bars + RINGS + 8u * (2 * NK + b); };
+  auto v_free = [&](int b) { return bars + RINGS + 8u * (2 * NK + NV + b); };
+  constexpr uint32_t AT = RINGS + 16 * (NK + NV);
   // Which of a tile's positions are in the context and in a block of the pool, for key tile j in place j % 8: K(j) is
   // loaded once S(j - NK) is done, and so PV(j - NK - NB) and what the softmax read for that tile.
   static_assert(NK + NB <= 8 && NB <= 3, "a tile's word is read before it is written anew");
   volatile uint2* live = reinterpret_cast<volatile uint2*>(smem + (bars + AT - base));               // [8]
-  volatile Item* items = reinterpret_cast<volatile Item*>(smem + (bars + AT + 64 - base));           // [2]
-  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + AT + 144 - base));       // [2]
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + AT + 152 - base));
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + AT + 156 - base));
-  static_assert(sizeof(Item) == 40 && AT + 160 <= 512, "barrier area");
+  constexpr uint32_t ITEMS = AT + 64, LAST = ITEMS + NI * sizeof(Item);
+  volatile Item* items = reinterpret_cast<volatile Item*>(smem + (bars + ITEMS - base));             // [NI]
+  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + (bars + LAST - base));           // [NI]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + (bars + LAST + 4 * NI - base));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars + LAST + 4 * NI + 4 - base));
+  static_assert(AT % 8 == 0 && LAST + 4 * NI + 8 <= C::BARS, "barrier area");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pkv::pdl_trigger();
@@ -244,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       mbar_init_count(p_full(u), 4);
       mbar_init_count(pv_done(u), 1);
     }
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < NI; ++u) {
       mbar_init_count(item_full(u), 1);
       mbar_init_count(item_free(u), 7);                       // 4 softmax warps, both issuers, the V loader
     }
@@ -278,8 +292,8 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
     *abort_flag = 1;
   };
   auto take_item = [&](int it, Item& item) {
-    if (!wait(item_full(it & 1), (it >> 1) & 1)) return false;
-    const volatile Item& x = items[it & 1];
+    if (!wait(item_full(it % NI), (it / NI) & 1)) return false;
+    const volatile Item& x = items[it % NI];
     item.s = x.s;
     item.kv_head = x.kv_head;
     item.first_row = x.first_row;
@@ -320,14 +334,36 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       const int H = p.num_kv_heads;
       long long pairs = 0, alone = 0;
       int code = 0;
-      const Seq first32 = seq_of(p, lane, &code);
-      Seq y = first32;
+      // lengths and starts by way of the K ring, where nothing has landed yet: all on their way at once, and read twice
+      // (waiting for each 32 sequences' loads, 4000 sequences of 60 tokens took 179 us for 111)
+      constexpr int CHUNK = 4064;
+      static_assert((2 * CHUNK + 1) * 4 <= NK * C::KV_BYTES && CHUNK % 32 == 0, "fits");
+      const int* lens = reinterpret_cast<const int*>(smem + (sk - base));
+      auto fetch = [&](int first) {
+        const int n = min(CHUNK, p.num_seqs - first);
 #pragma unroll 1
-      for (int i = lane;;) {
-        pairs += places_of(y, H, PAIRS);
-        alone += places_of(y, H, ALONE);
-        if ((i += 32) >= p.num_seqs) break;
-        y = seq_of(p, i, &code);
+        for (int i = lane; i < n; i += 32) {
+          cp_async4(sk + 4 * i, p.lens + first + i);
+          cp_async4(sk + 4 * (CHUNK + i), p.qstart + first + i);
+        }
+        if (lane == 0) cp_async4(sk + 4 * (CHUNK + n), p.qstart + first + n);
+        cp_async_wait_all();
+        __syncwarp();
+      };
+      // sequence first + i, of those that are there
+      auto seq_at = [&](int first, int i) {
+        return first + i < p.num_seqs ? make_seq(p, lens[i], lens[CHUNK + i], lens[CHUNK + i + 1], &code) : Seq{0, 0, 0, 0, 0};
+      };
+#pragma unroll 1
+      for (int first = 0; first < p.num_seqs; first += CHUNK) {
+        __syncwarp();
+        fetch(first);
+#pragma unroll 1
+        for (int i = lane; i < min(CHUNK, p.num_seqs - first); i += 32) {
+          const Seq y = seq_at(first, i);
+          pairs += places_of(y, H, PAIRS);
+          alone += places_of(y, H, ALONE);
+        }
       }
       if (code && blockIdx.x == 0) record_error(code);
 #pragma unroll
@@ -357,9 +393,14 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         // the sequence: the first whose tiles, all streams together, reach past x
         long long before = 0;
         s = p.num_seqs;
-        y = first32;
 #pragma unroll 1
-        for (int first = 0;;) {
+        for (int at = 0; at < p.num_seqs; at += 32) {
+          const int first = at / CHUNK * CHUNK;
+          if (p.num_seqs > CHUNK && at == first) {
+            __syncwarp();
+            fetch(first);
+          }
+          const Seq y = seq_at(first, at - first + lane);
           const long long mine = places_of(y, H, kind);
           long long upto = mine;
 #pragma unroll
@@ -370,7 +411,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           const unsigned past = __ballot_sync(0xffffffffu, before + upto > x);
           if (past) {
             const int hit = __ffs(past) - 1;
-            s = first + hit;
+            s = at + hit;
             before += __shfl_sync(0xffffffffu, upto - mine, hit);
             seq.ctx = __shfl_sync(0xffffffffu, y.ctx, hit);
             seq.n = __shfl_sync(0xffffffffu, y.n, hit);
@@ -380,8 +421,6 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
             break;
           }
           before += __shfl_sync(0xffffffffu, upto, 31);
-          if ((first += 32) >= p.num_seqs) break;
-          y = seq_of(p, first + lane, &code);
         }
         if (streams_of(seq, kind) == 0) {
           left = 0;                                           // the lengths changed meanwhile
@@ -390,6 +429,8 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           place = static_cast<int>(x - before - static_cast<long long>(stream) * (seq.tiles + kStart));
         }
       }
+      __syncwarp();
+      fence_proxy_async_smem();                               // these reads -> the ring's copies
     }
     int j = 0;
     for (int it = 0;; ++it) {
@@ -416,12 +457,12 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
           item.q0 = seq.q0;
           item.slot = item.n_tiles == seq.tiles ? -1 : 2 * worker + (it > 0);
         }
-        if (it >= 2 && !warp_wait(item_free(it & 1), ((it >> 1) - 1) & 1)) {
+        if (it >= NI && !warp_wait(item_free(it % NI), (it / NI - 1) & 1)) {
           failed = true;
           break;
         }
         if (lane == 0) {
-          volatile Item& out = items[it & 1];
+          volatile Item& out = items[it % NI];
           out.n_tiles = item.n_tiles;
           if (item.n_tiles > 0) {
             out.s = item.s;
@@ -434,7 +475,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
             out.q0 = item.q0;
             out.slot = item.slot;
           }
-          mbar_arrive(item_full(it & 1));
+          mbar_arrive(item_full(it % NI));
         }
         __syncwarp();
       } else {
@@ -536,7 +577,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         }
       } else {
         __syncwarp();
-        if (lane == 0) mbar_arrive(item_free(it & 1));
+        if (lane == 0) mbar_arrive(item_free(it % NI));
       }
     }
     if (is_k && !notes && lane == 0) p.cuts[worker].parts = 0;
@@ -579,7 +620,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(item_free(it & 1));
+        mbar_arrive(item_free(it % NI));
         for (int i = 0; i < item.n_tiles; ++i, ++j) {
           if (!wait(k_full(j % NK), (j / NK) & 1) || (phase > 0 && !wait(pv_done(u), (phase - 1) & 1))) {
             failed = true;
@@ -621,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         break;
       }
       if (item.n_tiles == 0) break;
-      if (lane == 0) not_finite[it & 1] = 0;
+      if (lane == 0) not_finite[it % NI] = 0;
       __syncwarp();
       const int first_new = item.ctx - item.n;
       for (int i = 0; i < item.n_tiles; ++i, ++j) {
@@ -655,7 +696,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
               acc = __hfma2(*reinterpret_cast<const __half2*>(&w[h].w), zero, acc);
             }
             if (__hisnan(__low2half(acc)) || __hisnan(__high2half(acc))) {
-              not_finite[it & 1] = 1;
+              not_finite[it % NI] = 1;
 #pragma unroll 1
               for (int k = k0; k < min(end, k0 + 4 * 32); k += 32) {
                 uint32_t* e = reinterpret_cast<uint32_t*>(v + sw128(k / CPR, k % CPR, BN));
@@ -696,7 +737,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         }
       }
       if (failed) break;
-      if (lane == 0) mbar_arrive(item_free(it & 1));
+      if (lane == 0) mbar_arrive(item_free(it % NI));
     }
     if (failed) {
       give_up();
@@ -806,7 +847,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
         // 32 columns at a time: the row to out, whole 32-byte sectors at once, or to the workspace, where
         // a column's rows lie side by side
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // a row that sees nothing is zeros
-        const bool fix = not_finite[it & 1] != 0, real = tid < item.rows;
+        const bool fix = not_finite[it % NI] != 0, real = tid < item.rows;
         const int head = item.kv_head * p.group + (row - node * p.group);
         __half* dst = p.out + (static_cast<size_t>(item.q0 + node) * p.num_heads + head) * D;
         float* part = p.ws_o + static_cast<size_t>(max(item.slot, 0)) * D * BM + tid;
@@ -854,7 +895,7 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(o_free);
-        mbar_arrive(item_free(it & 1));
+        mbar_arrive(item_free(it % NI));
       }
     }
     if (failed) give_up();
@@ -869,7 +910,8 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
   }
 }
 
-// Joins the parts of the cut streams: CTA (w, y) columns COLS y .. of the one that CTA w of the grid before noted.
+// Joins the parts of the cut streams: CTA (w, y) columns COLS y .. of the one that CTA w of the grid before noted, or,
+// where there are few streams and so many parts (COLS 4), of the w-th that was noted.
 // A thread takes a row and four columns at a time; where rows are few, groups of threads share the parts.
 constexpr int JOIN_THREADS = 512;
 template <int D, int COLS>
@@ -877,7 +919,31 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_attention_join_kernel(const
   __shared__ float group_m[JOIN_THREADS], group_l[JOIN_THREADS], group_o[4][JOIN_THREADS];
   pkv::pdl_trigger();
   pkv::pdl_wait();
-  const Cut cut = p.cuts[blockIdx.x];
+  int from = blockIdx.x;
+  if constexpr (COLS == 4) {
+    // the blockIdx.x-th of the cut streams
+    __shared__ int before[JOIN_THREADS / 32], found;
+    if (threadIdx.x == 0) found = -1;
+    int seen = 0;
+    for (int w0 = 0; w0 < p.workers; w0 += JOIN_THREADS) {
+      const int w = w0 + threadIdx.x, warp = threadIdx.x >> 5;
+      const bool is_cut = w < p.workers && p.cuts[w].parts > 1;
+      const unsigned mine = __ballot_sync(0xffffffffu, is_cut);
+      __syncthreads();
+      before[warp] = __popc(mine);
+      __syncthreads();
+      int rank = seen + __popc(mine & ((1u << (threadIdx.x & 31)) - 1));
+      for (int i = 0; i < JOIN_THREADS / 32; ++i) {
+        if (i < warp) rank += before[i];
+        seen += before[i];
+      }
+      if (is_cut && rank == from) found = w;
+    }
+    __syncthreads();
+    from = found;
+    if (from < 0) return;
+  }
+  const Cut cut = p.cuts[from];
   if (cut.parts <= 1) return;
   int rp = 8;                                                 // the rows, to a power of two
   while (rp < cut.rows) rp *= 2;
@@ -1008,7 +1074,7 @@ int encode_pool_map(const char* fn, CUtensorMap* map, const void* pool, int D, i
 }
 
 template <int D, int QR>
-int launch(const char* fn, const TreeParams& p, int workers, bool many_parts, cudaStream_t st) {
+int launch(const char* fn, const TreeParams& p, int workers, int few_streams, cudaStream_t st) {
   using C = Cfg<D, QR>;
   static std::mutex mu;
   static bool done[64] = {false};
@@ -1024,8 +1090,8 @@ int launch(const char* fn, const TreeParams& p, int workers, bool many_parts, cu
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s setup: %s", fn, cudaGetErrorString(e));
   e = pkv::launch_pdl(tree_attention_kernel<D, QR>, dim3(workers), dim3(THREADS), C::SMEM, st, p);
   if (e == cudaSuccess && workers > 1)
-    e = many_parts ? pkv::launch_pdl(tree_attention_join_kernel<D, 4>, dim3(workers, D / 4), dim3(JOIN_THREADS), 0, st, p)
-                   : pkv::launch_pdl(tree_attention_join_kernel<D, 32>, dim3(workers, D / 32), dim3(JOIN_THREADS), 0, st, p);
+    e = few_streams ? pkv::launch_pdl(tree_attention_join_kernel<D, 4>, dim3(few_streams, D / 4), dim3(JOIN_THREADS), 0, st, p)
+                    : pkv::launch_pdl(tree_attention_join_kernel<D, 32>, dim3(workers, D / 32), dim3(JOIN_THREADS), 0, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
   return PKV_OK;
@@ -1138,11 +1204,12 @@ int pkv_paged_attention_tree(const uint16_t* q, int64_t q_stride, const uint16_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // few rows leave shared memory for more key tiles in flight
   const int rows = max_query_len * p.group;
-  const bool many = pl.workers > kManyParts * pl.streams;
-  const int rc = head_dim == 64 ? launch<64, 128>(fn, p, pl.workers, many, st)
-                 : rows <= 32   ? launch<128, 32>(fn, p, pl.workers, many, st)
-                 : rows <= 64   ? launch<128, 64>(fn, p, pl.workers, many, st)
-                                : launch<128, 128>(fn, p, pl.workers, many, st);
+  const int few = pl.workers > kManyParts * pl.streams ? static_cast<int>(pl.streams) : 0;
+  p.workers = pl.workers;
+  const int rc = head_dim == 64 ? launch<64, 128>(fn, p, pl.workers, few, st)
+                 : rows <= 32   ? launch<128, 32>(fn, p, pl.workers, few, st)
+                 : rows <= 64   ? launch<128, 64>(fn, p, pl.workers, few, st)
+                                : launch<128, 128>(fn, p, pl.workers, few, st);
   if (rc == PKV_OK) pkv::clear_error();
   return rc;
 }

@@ -340,3 +340,22 @@ def test_refusals(cuda_device):
                dict(tree_mask=torch.zeros(8, 0, dtype=torch.int32, device=cuda_device)), dict(out=q[:5].contiguous())):
         with pytest.raises(pkv.PkvError):
             pkv.paged_attention_tree(*ok, **kw)
+
+
+def test_more_sequences_than_are_looked_up_at_a_time(cuda_device):
+    """9000 sequences of few tokens, some without any or with a length that is refused."""
+    rng = np.random.default_rng(60)
+    lens = rng.integers(1, 40, 9000)
+    counts = np.minimum(lens, rng.integers(0, 4, 9000))
+    c = make(61, lens.tolist(), counts.tolist(), 2, 1, 64, 16)
+    got = check(c, cuda_device)
+    bad = c["lens"].copy()
+    bad[4100] = -5
+    out = torch.full((c["q"].shape[0], 2, 64), 7.0, dtype=torch.float16, device=cuda_device)
+    call(dict(c, lens=bad), cuda_device, out=out)
+    assert pkv.device_error() == (2 if counts[4100] else 0)
+    out = out.cpu().numpy().astype(np.float64)
+    mine = slice(c["start"][4100], c["start"][4101])
+    assert (out[mine] == 7).all()
+    out[mine] = got[mine]
+    assert np.abs(out - got).max() < 2e-3               # cut elsewhere: other parts are joined
