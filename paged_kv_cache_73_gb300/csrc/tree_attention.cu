@@ -910,111 +910,143 @@ __global__ void __launch_bounds__(THREADS, 2) tree_attention_kernel(const __grid
   }
 }
 
-// Joins the parts of the cut streams: CTA (w, y) columns COLS y .. of the one that CTA w of the grid before noted, or,
-// where there are few streams and so many parts (COLS 4), of the w-th that was noted.
-// A thread takes a row and four columns at a time; where rows are few, groups of threads share the parts.
-constexpr int JOIN_THREADS = 512;
-template <int D, int COLS>
+// ---- joining the parts of cut streams, by the log-sum-exp identity ---------------------------------
+// A row's running result over parts, of which one that saw nothing (m -inf, l 0) is left out; one with a NaN is not.
+struct Joined {
+  float M, L, acc[4];
+  __device__ __forceinline__ void add(const float2 (&ml)[4], const float (&x)[4][4]) {
+    float m = M;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m = fmaxf(m, ml[u].x);
+    const float base = m == -INFINITY ? 0.f : m, carry = exp2f(M - base);   // nothing seen so far: 0
+    L *= carry;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] *= carry;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (ml[u].x == -INFINITY && ml[u].y == 0.f) continue;
+      const float f = exp2f(ml[u].x - base);
+      L = fmaf(ml[u].y, f, L);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[u][e], f, acc[e]);
+    }
+    M = m;
+  }
+  __device__ __forceinline__ void store(__half* dst) const {
+    const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half2(acc[0] * inv, acc[1] * inv), pack_half2(acc[2] * inv, acc[3] * inv));
+  }
+};
+// Row r's (m, l) and four columns' values in parts k, k + step, ..: all of them on their way at once.
+template <int D>
+__device__ __forceinline__ void load_parts(const TreeParams& p, const Cut& cut, int k, int step, int r, int col,
+                                           float2 (&ml)[4], float (&x)[4][4]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u, k += step) {
+    ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[u][e] = 0.f;
+    if (k < cut.parts) {
+      const size_t slot = k == 0 ? cut.slot : cut.next + 2 * (k - 1);
+      ml[u] = p.ws_ml[slot * BM + r];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[u][e] = p.ws_o[(slot * D + col + e) * BM + r];
+    }
+  }
+}
+__device__ __forceinline__ __half* row_of(const TreeParams& p, const Cut& cut, int r, int D) {
+  const int row = cut.first_row + r, node = row / p.group, head = cut.kv_head * p.group + row - node * p.group;
+  return p.out + (static_cast<size_t>(cut.q0 + node) * p.num_heads + head) * D;
+}
+
+// CTA (w, y): the y-th share of the columns of the stream that CTA w of the grid before noted; a thread has a row
+// and four columns at a time.
+constexpr int JOIN_THREADS = 256;
+// One sequence of 2048 tokens and 40 heads takes 16.7 us with one share of the columns, 15.2 with four, 16.1 with eight;
+// 8 of 4096 with 64 rows 44.9, 37.1 and 36.2.
+constexpr int kJoinShares = 4;
+template <int D>
 __global__ void __launch_bounds__(JOIN_THREADS) tree_attention_join_kernel(const __grid_constant__ TreeParams p) {
-  __shared__ float group_m[JOIN_THREADS], group_l[JOIN_THREADS], group_o[4][JOIN_THREADS];
   pkv::pdl_trigger();
   pkv::pdl_wait();
-  int from = blockIdx.x;
-  if constexpr (COLS == 4) {
-    // the blockIdx.x-th of the cut streams
-    __shared__ int before[JOIN_THREADS / 32], found;
-    if (threadIdx.x == 0) found = -1;
-    int seen = 0;
-    for (int w0 = 0; w0 < p.workers; w0 += JOIN_THREADS) {
-      const int w = w0 + threadIdx.x, warp = threadIdx.x >> 5;
-      const bool is_cut = w < p.workers && p.cuts[w].parts > 1;
-      const unsigned mine = __ballot_sync(0xffffffffu, is_cut);
-      __syncthreads();
-      before[warp] = __popc(mine);
-      __syncthreads();
-      int rank = seen + __popc(mine & ((1u << (threadIdx.x & 31)) - 1));
-      for (int i = 0; i < JOIN_THREADS / 32; ++i) {
-        if (i < warp) rank += before[i];
-        seen += before[i];
-      }
-      if (is_cut && rank == from) found = w;
-    }
-    __syncthreads();
-    from = found;
-    if (from < 0) return;
-  }
-  const Cut cut = p.cuts[from];
+  const Cut cut = p.cuts[blockIdx.x];
   if (cut.parts <= 1) return;
-  int rp = 8;                                                 // the rows, to a power of two
-  while (rp < cut.rows) rp *= 2;
-  constexpr int CG = COLS / 4;
-  const int groups = max(1, JOIN_THREADS / (rp * CG));        // that share the parts
-  const int tid = threadIdx.x, r = tid & (rp - 1), cg = (tid / rp) & (CG - 1), pg = tid / (rp * CG);
-  const bool real = r < cut.rows;
-  auto slot_of = [&](int part) { return static_cast<size_t>(part == 0 ? cut.slot : cut.next + 2 * (part - 1)); };
-  const int row = cut.first_row + min(r, cut.rows - 1), node = row / p.group, head = cut.kv_head * p.group + row - node * p.group;
-  __half* dst = p.out + (static_cast<size_t>(cut.q0 + node) * p.num_heads + head) * D + blockIdx.y * COLS;
-  // with 128 rows a thread takes two groups of columns, one after the other
-  for (int col = cg * 4; col < COLS; col += min(CG, JOIN_THREADS / rp) * 4) {
-    float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    constexpr int FLY = 4;
-    for (int k0 = pg; k0 < cut.parts; k0 += groups * FLY) {
-      float2 ml[FLY];
-      float x[FLY][4];
-#pragma unroll
-      for (int u = 0; u < FLY; ++u) {
-        const int k = k0 + u * groups;
-        ml[u] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[u][e] = 0.f;
-        if (k < cut.parts && real) {
-          ml[u] = p.ws_ml[slot_of(k) * BM + r];
-          const float* src = p.ws_o + (slot_of(k) * D + blockIdx.y * COLS + col) * BM + r;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[u][e] = src[e * BM];
-        }
-      }
-      float m = M;
-#pragma unroll
-      for (int u = 0; u < FLY; ++u) m = fmaxf(m, ml[u].x);
-      const float base = m == -INFINITY ? 0.f : m, carry = exp2f(M - base);   // nothing seen so far: 0
-      L *= carry;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] *= carry;
-#pragma unroll
-      for (int u = 0; u < FLY; ++u) {
-        // a part that saw nothing is left out; one with a NaN is not
-        if (ml[u].x == -INFINITY && ml[u].y == 0.f) continue;
-        const float f = exp2f(ml[u].x - base);
-        L = fmaf(ml[u].y, f, L);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[u][e], f, acc[e]);
-      }
-      M = m;
+  int log2_rows = 3;                                          // the rows, to a power of two
+  while ((1 << log2_rows) < cut.rows) ++log2_rows;
+  const int r = threadIdx.x & ((1 << log2_rows) - 1), share = D / gridDim.y;
+  if (r >= cut.rows) return;
+  __half* dst = row_of(p, cut, r, D);
+  for (int c = (threadIdx.x >> log2_rows) * 4; c < share; c += JOIN_THREADS >> log2_rows << 2) {
+    const int col = blockIdx.y * share + c;
+    Joined all{-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+    for (int k = 0; k < cut.parts; k += 4) {
+      float2 ml[4];
+      float x[4][4];
+      load_parts<D>(p, cut, k, 1, r, col, ml, x);
+      all.add(ml, x);
     }
-    if (groups > 1) {
-      group_m[tid] = M;
-      group_l[tid] = L;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) group_o[e][tid] = acc[e];
-      __syncthreads();
-      if (pg == 0) {
-        for (int g = 1; g < groups; ++g) {
-          const int other = tid + g * rp * CG;
-          const float om = group_m[other], m = fmaxf(M, om), a = M == -INFINITY ? 0.f : exp2f(M - m),
-                      b = om == -INFINITY ? 0.f : exp2f(om - m);
-          M = m;
-          L = L * a + group_l[other] * b;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] = acc[e] * a + group_o[e][other] * b;
-        }
-      }
+    all.store(dst + col);
+  }
+}
+
+// The same where there are few streams, and so many parts: CTA (k, y) columns 4 y .. of the k-th stream that was
+// noted; groups of threads share its parts.
+constexpr int MANY_THREADS = 512;
+template <int D>
+__global__ void __launch_bounds__(MANY_THREADS) tree_attention_join_many_kernel(const __grid_constant__ TreeParams p) {
+  __shared__ Joined groups[MANY_THREADS];
+  __shared__ int before[MANY_THREADS / 32], found;
+  pkv::pdl_trigger();
+  pkv::pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) found = -1;
+  int seen = 0;
+  for (int w0 = 0; w0 < p.workers; w0 += MANY_THREADS) {
+    const int w = w0 + tid;
+    const bool is_cut = w < p.workers && p.cuts[w].parts > 1;
+    const unsigned mine = __ballot_sync(0xffffffffu, is_cut);
+    __syncthreads();
+    before[warp] = __popc(mine);
+    __syncthreads();
+    int rank = seen + __popc(mine & ((1u << lane) - 1));
+    for (int i = 0; i < MANY_THREADS / 32; ++i) {
+      if (i < warp) rank += before[i];
+      seen += before[i];
     }
-    if (pg == 0 && real) {
-      const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
-      *reinterpret_cast<uint2*>(dst + col) = make_uint2(pack_half2(acc[0] * inv, acc[1] * inv), pack_half2(acc[2] * inv, acc[3] * inv));
+    if (is_cut && rank == static_cast<int>(blockIdx.x)) found = w;
+  }
+  __syncthreads();
+  if (found < 0) return;
+  const Cut cut = p.cuts[found];
+  int log2_rows = 3;
+  while ((1 << log2_rows) < cut.rows) ++log2_rows;
+  const int r = tid & ((1 << log2_rows) - 1), count = MANY_THREADS >> log2_rows, col = blockIdx.y * 4;
+  Joined all{-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+  if (r < cut.rows) {
+    for (int k = tid >> log2_rows; k < cut.parts; k += 4 * count) {
+      float2 ml[4];
+      float x[4][4];
+      load_parts<D>(p, cut, k, count, r, col, ml, x);
+      all.add(ml, x);
     }
   }
+  groups[tid] = all;
+  __syncthreads();
+  if (tid >= cut.rows) return;
+  all = Joined{-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+  for (int g = 0; g < count; g += 4) {                        // count is at least 4
+    float2 ml[4];
+    float x[4][4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const Joined& other = groups[((g + u) << log2_rows) + r];
+      ml[u] = make_float2(other.M, other.L);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[u][e] = other.acc[e];
+    }
+    all.add(ml, x);
+  }
+  all.store(row_of(p, cut, r, D) + col);
 }
 
 int device_sms() {
@@ -1090,8 +1122,8 @@ int launch(const char* fn, const TreeParams& p, int workers, int few_streams, cu
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s setup: %s", fn, cudaGetErrorString(e));
   e = pkv::launch_pdl(tree_attention_kernel<D, QR>, dim3(workers), dim3(THREADS), C::SMEM, st, p);
   if (e == cudaSuccess && workers > 1)
-    e = few_streams ? pkv::launch_pdl(tree_attention_join_kernel<D, 4>, dim3(few_streams, D / 4), dim3(JOIN_THREADS), 0, st, p)
-                    : pkv::launch_pdl(tree_attention_join_kernel<D, 32>, dim3(workers, D / 32), dim3(JOIN_THREADS), 0, st, p);
+    e = few_streams ? pkv::launch_pdl(tree_attention_join_many_kernel<D>, dim3(few_streams, D / 4), dim3(MANY_THREADS), 0, st, p)
+                    : pkv::launch_pdl(tree_attention_join_kernel<D>, dim3(workers, kJoinShares), dim3(JOIN_THREADS), 0, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return pkv::fail(PKV_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
   return PKV_OK;
