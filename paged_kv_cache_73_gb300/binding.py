@@ -824,10 +824,10 @@ def rope_and_cache(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, posi
     rotary_scale multiplies the turned values (long-context scalings)."""
     dev = torch.cuda.current_device()
     T, H, D, qs = _rows(q, "q", dev)
-    *kshape, ks = _rows(key, "key", dev)
-    *vshape, vs = _rows(value, "value", dev)
+    Tk, Hq, Dq, ks = _rows(key, "key", dev)
+    Tv, Hv, Dv, vs = _rows(value, "value", dev)
     N, Hk, B, Dk = _need_pools(k_cache, v_cache, dev)
-    if kshape != [T, Hk, D] or vshape != kshape or Dk != D:
+    if not (Tk == Tv == T and Hq == Hv == Hk and Dq == Dv == Dk == D):
         raise PkvError(PKV_ERR_INVALID_ARG, f"rope_and_cache: q {tuple(q.shape)}, key {tuple(key.shape)}, value "
                                             f"{tuple(value.shape)} and pools {tuple(k_cache.shape)} do not match")
     dim = positions.dim()
@@ -845,15 +845,15 @@ def rope_and_cache(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, posi
             _need(pair_axis, "pair_axis", torch.int32, 1)
         if pair_axis.shape[0] != pairs:
             raise PkvError(PKV_ERR_INVALID_ARG, "rope_and_cache: pair_axis must have one entry per frequency")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            if not _is(w, torch.float16, 1, dev):
-                _need(w, name, torch.float16, 1)
-            if w.shape[0] != D:
-                raise PkvError(PKV_ERR_INVALID_ARG, f"rope_and_cache: {name} must have head_dim entries")
-    qos = H * D
+    if q_weight is not None or k_weight is not None:
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                if not _is(w, torch.float16, 1, dev):
+                    _need(w, name, torch.float16, 1)
+                if w.shape[0] != D:
+                    raise PkvError(PKV_ERR_INVALID_ARG, f"rope_and_cache: {name} must have head_dim entries")
     if q_out is None:
-        q_out = _empty((T, H, D), torch.float16, q, stream)
+        q_out, qos = _empty((T, H, D), torch.float16, q, stream), H * D
     else:
         *shape, qos = _rows(q_out, "q_out", dev)
         if shape != [T, H, D]:
@@ -904,9 +904,11 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     dev = torch.cuda.current_device()
     T, H, D, qs = _rows(q, "q", dev)
     N, Hk, B, Dk = _need_pools(k_cache, v_cache, dev)
-    for t, name, dim in ((block_tables, "block_tables", 2), (context_lens, "context_lens", 1), (query_start, "query_start", 1)):
-        if not _is(t, torch.int32, dim, dev):
-            _need(t, name, torch.int32, dim)
+    i32 = torch.int32
+    if not (_is(block_tables, i32, 2, dev) and _is(context_lens, i32, 1, dev) and _is(query_start, i32, 1, dev)):
+        _need(block_tables, "block_tables", i32, 2)
+        _need(context_lens, "context_lens", i32, 1)
+        _need(query_start, "query_start", i32, 1)
     S, max_blocks = block_tables.shape
     if B != block_size or Dk != D:
         raise PkvError(PKV_ERR_INVALID_ARG, f"pools {tuple(k_cache.shape)} are not [N, Hk, {block_size}, {D}]")
@@ -968,13 +970,16 @@ def verify_draft(target_probs: torch.Tensor, tokens: torch.Tensor, parents: torc
         ds = _prob_rows(draft_probs, "draft_probs", dev)
         if draft_probs.shape != target_probs.shape:
             raise PkvError(PKV_ERR_INVALID_ARG, "draft_probs must be shaped like target_probs")
-    for t, name, dtype in ((tokens, "tokens", torch.int32), (parents, "parents", torch.int32),
-                           (uniforms, "uniforms", torch.float32), (query_start, "query_start", torch.int32)):
-        if not _is(t, dtype, 1, dev):
-            _need(t, name, dtype, 1)
-        if t is not query_start and t.shape[0] != T:
-            raise PkvError(PKV_ERR_INVALID_ARG, f"verify_draft: {name} must have an entry per row of target_probs")
-    S = query_start.shape[0] - 1
+    i32 = torch.int32
+    if not (_is(tokens, i32, 1, dev) and _is(parents, i32, 1, dev) and _is(query_start, i32, 1, dev)
+            and _is(uniforms, torch.float32, 1, dev)):
+        _need(tokens, "tokens", i32, 1)
+        _need(parents, "parents", i32, 1)
+        _need(query_start, "query_start", i32, 1)
+        _need(uniforms, "uniforms", torch.float32, 1)
+    if not tokens.numel() == parents.numel() == uniforms.numel() == T:
+        raise PkvError(PKV_ERR_INVALID_ARG, "verify_draft: tokens, parents and uniforms must have an entry per row of target_probs")
+    S = query_start.numel() - 1
     if S < 0 or max_path <= 0:
         raise PkvError(PKV_ERR_INVALID_ARG, "verify_draft: query_start needs num_seqs + 1 entries, max_path a place")
     path = _empty((S, max_path), torch.int32, target_probs, stream)
