@@ -625,7 +625,11 @@ int pkv_rope_and_cache(const uint16_t* q, const uint16_t* key, const uint16_t* v
  * PKV_DEV_BAD_CONTEXT_LEN, and the sequence's rows are not written.  A table entry
  * outside the pool records PKV_DEV_BAD_BLOCK_ID and its tokens get no weight.  Rows of
  * out in no sequence are left as they were.  Keys and values of new tokens that a node
- * does not see, and slots past the context, do not reach its row, whatever they hold. */
+ * does not see, and slots past the context, do not reach its row, whatever they hold.
+ * Tensor cores: as pkv_prompt_attention (fp16 products, fp32 sums, weights rounded to
+ * fp16 before they multiply V and to 0 below 2^-32 of the row's largest, up to n 2^-27 of
+ * a row over n keys cut off).  All sequences' keys are cut evenly over the GPU, so a row may
+ * differ in its last bits between batches. */
 size_t pkv_paged_attention_tree_workspace_size(int num_seqs, int total_q, int max_query_len, int num_heads,
                                                int num_kv_heads, int head_dim, int max_blocks_per_seq,
                                                int block_size);

@@ -53,9 +53,9 @@ constexpr int kMinTiles = 2;
 // What a stream costs besides its key tiles, in key tiles: 16 wide trees over 276 to 4608 tokens (D = 64) take 49.5 us
 // with 2, 45.0 with 4 and with 6; one sequence of 2048 tokens 16.1, 16.6 and 17.4.
 constexpr int kStart = 4;
-// Where streams are cut into more parts than this (by the longest contexts), CTAs of four columns join them, not of 32:
-// one sequence of 16384 tokens, 32 heads on 8 (38 parts) 20.6 -> 17.8 us, of 131072 on one head (304) 66 -> 27; one of
-// 2048 with 40 heads (8 parts) would go from 16.7 to 36.5, for there are so many streams' CTAs to launch.
+// Where streams are cut into more parts than this (by the longest contexts), a CTA joins four columns of one, with groups of
+// threads to share the parts: one sequence of 16384 tokens, 32 heads on 8 (38 parts) 20.6 -> 17.8 us, of 131072 on one
+// head (304) 66 -> 27; one of 2048 with 40 heads (8 parts) would go from 16.7 to 36.5, for so many CTAs are launched.
 constexpr int kManyParts = 16;
 constexpr float kRescale = 8.f;    // the running maximum moves when a tile passes it by this much
 constexpr float kLift = 7.f;       // weights are kept as 2^(kLift + S - m)

@@ -152,6 +152,17 @@ def test_rows_that_are_no_distributions(cuda_device):
     assert token[:5] == [-1] * 5 and token[5] >= 0
 
 
+def test_random_numbers_at_their_ends(cuda_device):
+    c = make(14, [3] * 40, 333)
+    for u in (np.float32(0), np.float32(1 - 2.0 ** -24)):
+        check(dict(c, u=np.full_like(c["u"], u)), cuda_device, 3)
+    # 1 is none of them: it counts as the largest below, and no draft stays by chance alone
+    _, size, token = call(dict(c, u=np.ones_like(c["u"])), cuda_device, 3)
+    assert ((token >= 0) & (token < 333)).all() and pkv.device_error() == 0
+    _, size, token = call(dict(c, u=np.full_like(c["u"], np.nan)), cuda_device, 3)
+    assert pkv.device_error() == 11 and ((token >= 0) & (token < 333)).all()
+
+
 def test_captured_and_on_two_streams(cuda_device):
     cs = [make(20 + i, [9, 9, 9], 3001) for i in range(2)]
     want = [[x.clone() for x in call(c, cuda_device, 9)] for c in cs]
