@@ -132,6 +132,7 @@ struct Nodes {
   u64 has[kMaxNodes];     // p and q of the node's token behind its parent, and the node's own u
   u64 drawn[kMaxNodes];
   u64 u[kMaxNodes];
+  unsigned char stays[kMaxNodes];  // where no sibling before it was refused
 };
 
 // What the first CTA tells the others: a pass over row `row` with the first `refused` of its refusals, and
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
         nodes.has[j] = has;
         nodes.drawn[j] = drawn;
         nodes.u[j] = u;
+        nodes.stays[j] = part_of(drawn, u) < has;
       }
     }
     __syncthreads();
@@ -223,15 +225,19 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
           break;
         }
         next = j + 1;
+        bool stays = nodes.stays[j] != 0;
         u64 has = nodes.has[j];
-        const u64 drawn = nodes.drawn[j];
-        if (p.draft != nullptr) {
-          has = less(has, drawn, taken);
-        } else {
-          for (int i = 0; i < k; ++i)
-            if (refused_x[i] == nodes.token[j]) has = 0;
+        if (k > 0) {
+          const u64 drawn = nodes.drawn[j];
+          if (p.draft != nullptr) {
+            has = less(has, drawn, taken);
+          } else {
+            for (int i = 0; i < k; ++i)
+              if (refused_x[i] == nodes.token[j]) has = 0;
+          }
+          stays = part_of(part_of(share, drawn), nodes.u[j]) < has;
         }
-        if (part_of(part_of(share, drawn), nodes.u[j]) < has) {
+        if (stays) {
           if (lane == 0) p.path[static_cast<int64_t>(s) * most + size] = j;
           ++size;
           at = j;
