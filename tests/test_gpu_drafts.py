@@ -329,3 +329,55 @@ def test_steps_with_drafts_through_the_block_manager(cuda_device):
                 for pool, x in ((pools[0][l], k), (pools[1][l], rows[:, H + Hk:])):
                     have = oa.gather_sequence(pool.cpu().numpy(), tab, n)
                     assert np.array_equal(have, x.cpu().numpy().astype(np.float64))
+
+
+def test_a_captured_step_of_all_four(cuda_device):
+    """A step over three layers as one graph, its products' output and the appended rows read by the next call without
+    a wait between them; replayed with other inputs in the same buffers, it gives what the calls one by one give."""
+    dev, B, H, Hk, D, L, V = cuda_device, 16, 8, 2, 128, 3, 501
+    counts, ctx = [9, 1, 17, 4], [700, 33, 17, 2100]
+    start = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    T, blocks = int(start[-1]), -(-max(ctx) // B)
+    t = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(dev)
+    freq = pkv.rope_frequencies(10000.0 ** (-np.arange(D // 2) / (D // 2)), dev)
+    N = len(counts) * blocks + 2
+
+    def inputs(seed):
+        rng = np.random.default_rng(seed)
+        tables = rng.permutation(N)[:len(counts) * blocks].reshape(len(counts), blocks).astype(np.int32)
+        parents = [[-1] + [int(rng.integers(max(0, j - 3), j)) for j in range(1, n)] for n in counts]
+        mask, depths = pkv.tree_masks(sum(parents, []), start, dev)
+        base = np.repeat(np.array(ctx) - counts, counts).astype(np.int32)
+        slots = [int(tables[s, (ctx[s] - n + i) // B]) * B + (ctx[s] - n + i) % B for s, n in enumerate(counts) for i in range(n)]
+        c = make(seed, counts, V)
+        return dict(qkv=t(rng.standard_normal((L, T, H + 2 * Hk, D)).astype(np.float16)), tables=t(tables), mask=mask,
+                    positions=t(base) + depths, slots=t(np.array(slots, np.int64)), parents=t(np.array(sum(parents, []), np.int32)),
+                    pools=t(rng.standard_normal((2, L, N, Hk, B, D)).astype(np.float16)),
+                    **{n: t(c[n]) for n in ("target", "draft", "tokens", "u")})
+
+    lens, begin = t(np.array(ctx, np.int32)), t(start)
+
+    def step(x):
+        ks, vs = [list(p) for p in x["pools"]]
+        outs = []
+        for l in range(L):
+            y = x["qkv"][l]
+            q = pkv.rope_and_cache(y[:, :H], y[:, H:H + Hk], y[:, H + Hk:], x["positions"], freq, ks[l], vs[l], x["slots"])
+            outs.append(pkv.paged_attention_tree(q, ks[l], vs[l], x["tables"], lens, begin, D ** -0.5, B, max(counts), tree_mask=x["mask"]))
+        kept = pkv.verify_draft(x["target"], x["tokens"], x["parents"], begin, x["u"], 17, draft_probs=x["draft"])
+        pkv.move_accepted(ks, vs, x["slots"], begin, kept[0], kept[1])
+        return [*outs, *kept, x["pools"]]
+
+    want = [[y.clone() for y in step(inputs(seed))] for seed in (70, 71, 72)]
+    x = inputs(70)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(x)
+    for seed in (71, 72, 70):
+        for name, y in inputs(seed).items():
+            x[name].copy_(y)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[seed - 70])), seed
+    assert pkv.device_error() == 0

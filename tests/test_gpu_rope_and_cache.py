@@ -129,3 +129,22 @@ def test_offsets_past_32_bits(cuda_device):
     want = pkv.qk_norm_rope(qkv[:, :8], qkv[:, 8:16], p, f)[1]
     pkv.rope_and_cache(qkv[:, :8], qkv[:, 8:16], qkv[:, 16:], p, f, kc, vc, sl)
     assert torch.equal(kc[sl // B, :, sl % B], want) and torch.equal(vc[sl // B, :, sl % B], qkv[:, 16:])
+
+
+def test_on_two_streams_at_once(cuda_device):
+    cases = [make(8 + i, 300, 8, 2, 128, 128, 1, 16, cuda_device) for i in range(2)]
+    f = pkv.rope_frequencies(cases[0][1], cuda_device)
+    def run(i, kc, vc, stream=None):
+        qkv, _, pos, _, w, slots, _ = cases[i]
+        p, sl = torch.from_numpy(pos[0]).to(cuda_device), torch.from_numpy(slots).to(cuda_device)
+        torch.cuda.synchronize()
+        return pkv.rope_and_cache(qkv[:, :8], qkv[:, 8:10], qkv[:, 10:], p, f, kc, vc, sl, *w, stream=stream), p, sl
+    want = []
+    for i, c in enumerate(cases):
+        kc, vc = [x.clone() for x in c[6]]
+        want.append((run(i, kc, vc)[0], kc, vc))
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [run(i, *cases[i][6], stream=st) for i, st in enumerate(streams)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip((got[i][0], *cases[i][6]), want[i]))
