@@ -111,6 +111,12 @@ __device__ __forceinline__ int cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The two halves of a barrier that only tells that every CTA of the cluster runs: shared memory of one that does
+// not yet may not be written to.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t map_to_rank(const void* p, int rank) {
   uint32_t out;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
@@ -152,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
   __shared__ u64 warp_sum[kWarps], part_sum[kWarps];
   __shared__ int cta_bad[2][kMostCtas];
 
+  cluster_arrive_relaxed();
   pkv::pdl_trigger();
   pkv::pdl_wait();
   const int rank = cluster_rank(), ctas = cluster_size(), s = blockIdx.x / ctas;
@@ -202,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
   if (rank == 0)
     for (int i = tid + kThreads; i < most; i += kThreads) p.path[static_cast<int64_t>(s) * most + i] = -1;
   __syncthreads();
+  cluster_wait();                                             // from here on the first CTA writes to the others
 
   for (int pass = 0;; ++pass) {
     if (rank == 0 && warp == 0) {

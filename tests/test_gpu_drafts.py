@@ -184,6 +184,35 @@ def test_captured_and_on_two_streams(cuda_device):
     assert all(torch.equal(a, b) for a, b in zip(out, want[1]))
 
 
+@pytest.mark.parametrize("seqs", [1, 20, 200, 300, 600])   # clusters of eight, eight, four, two CTAs and of one
+def test_clusters_without_nodes(cuda_device, seqs):
+    """A sequence without nodes, or with rows that are none, is over as soon as its cluster runs: call upon call of
+    those, between sequences that have some."""
+    V = 333
+    c = make(15, [0, 3, 0, 0], V)
+    t = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(cuda_device)
+    args = [t(c[n]) for n in ("target", "tokens", "parents")]
+    empty = torch.zeros(seqs + 1, dtype=torch.int32, device=cuda_device)
+    mixed = empty.clone()
+    mixed[seqs // 2 + 1:] = 3                               # one sequence in the middle has all three
+    bad = empty.clone()
+    bad[seqs // 2 + 1:] = 4                                 # or one more than there are
+    u, draft = t(c["u"]), t(c["draft"])
+    want, x = od.verify(c["target"], c["draft"], c["tokens"], c["parents"], c["u"], 3)
+    torch.cuda.synchronize()
+    for start in (empty, mixed, bad):
+        got = [pkv.verify_draft(*args, start, u, 3, draft_probs=draft if i % 2 else None) for i in range(20)]
+        assert pkv.device_error() == (6 if start is bad else 0)
+        for i, (path, size, token) in enumerate(got):
+            some = [seqs // 2] if start is mixed else []
+            rest = torch.ones(seqs, dtype=torch.bool)
+            rest[some] = False
+            assert (size.cpu()[rest] == 0).all() and (token.cpu()[rest] == -1).all() and (path.cpu()[rest] == -1).all()
+            if some and i % 2:
+                n = int(size[some[0]])
+                assert path[some[0], :n].tolist() == want and int(token[some[0]]) == x
+
+
 def test_verify_refusals(cuda_device):
     c = make(13, [4], 20)
     t = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(cuda_device)
