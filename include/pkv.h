@@ -83,7 +83,8 @@ enum {
   PKV_DEV_BAD_AXIS = 8,         /* rotation: a pair's position axis outside [0, num_axes) */
   PKV_DEV_BAD_TREE = 9,         /* drafts: a node before its parent, or a path whose nodes do not go up */
   PKV_DEV_BAD_TOKEN = 10,       /* drafts: a token outside [0, vocab_size) */
-  PKV_DEV_BAD_PROBABILITY = 11  /* drafts: a NaN, a value outside [0, 1], or a row whose sum is 0 or above 1.5 */
+  PKV_DEV_BAD_PROBABILITY = 11  /* drafts: a NaN, a value outside [0, 1], or a row whose sum is 0 or, after the
+                                   refusals, above 1.5 */
 };
 
 /* Message for the last non-OK status returned on this thread ("" if none). */
@@ -677,8 +678,9 @@ int pkv_tree_masks(const int32_t* parents, const int32_t* query_start, int num_s
  *   path         device [num_seqs, max_path] int32: the current nodes from 0 on, then -1
  *   path_len     device [num_seqs] int32: how many; 0 for a sequence without nodes
  *   next_token   device [num_seqs] int32; -1 for a sequence without nodes, and where the
- *                row is no distribution (a value that is NaN, negative or above 1, a sum
- *                of 0 or above 1.5: PKV_DEV_BAD_PROBABILITY)
+ *                row is no distribution: it has a value that is NaN, negative or above 1
+ *                by more than 2^-10 (less counts as 1), or its sum, after the refusals, is
+ *                above 1.5, or it is 0 throughout (PKV_DEV_BAD_PROBABILITY)
  * No output may overlap an input.  No workspace. */
 int pkv_verify_draft(const float* target_probs, const float* draft_probs, const int32_t* tokens,
                      const int32_t* parents, const int32_t* query_start, const float* uniforms, int num_seqs,

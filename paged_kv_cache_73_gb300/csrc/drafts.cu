@@ -384,6 +384,12 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
       }
 #pragma unroll
       for (int d = 16; d > 0; d /= 2) sum = add_most(sum, __shfl_xor_sync(FULL, sum, d));
+      if (qrow == nullptr && refused > 0 && !slow && sum >= kMost) {
+        // held down before the refused tokens are taken off: no distribution, but what is left of it may be one
+        sum = slow_sum(first, end);
+        slow = true;
+        for (int d = 16; d > 0; d /= 2) sum = add_most(sum, __shfl_xor_sync(FULL, sum, d));
+      }
       if (qrow == nullptr) {
         // refused tokens have nothing left (slow_sum counts that)
         for (int j = 0; j < refused; ++j) {

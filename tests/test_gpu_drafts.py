@@ -152,6 +152,20 @@ def test_rows_that_are_no_distributions(cuda_device):
     assert token[:5] == [-1] * 5 and token[5] >= 0
 
 
+@pytest.mark.parametrize("V", [3, 256, 4096])
+def test_refused_tokens_of_a_row_that_sums_to_more_than_one(cuda_device, V):
+    """Without draft distributions what the refused tokens leave decides, also where the row's sum is past what the
+    kernel adds up to: 2.25 less 0.75 is just not too much, 2.375 less 0.75 is."""
+    c = make(16, [2], V)
+    c["tokens"][:] = 0
+    c["u"][:] = 0.9375                                      # refuses what has 0.75
+    for third, token in ((0.75, 2), (0.875, -1)):
+        c["target"][:] = 0
+        c["target"][:, :2], c["target"][:, 2] = 0.75, third
+        path, size, got = call(c, cuda_device, 2, with_draft=False)
+        assert size.tolist() == [1] and got.tolist() == [token] and pkv.device_error() == (11 if token < 0 else 0)
+
+
 def test_random_numbers_at_their_ends(cuda_device):
     c = make(14, [3] * 40, 333)
     for u in (np.float32(0), np.float32(1 - 2.0 ** -24)):
