@@ -694,6 +694,10 @@ int pkv_tree_masks(const int32_t* parents, const int32_t* query_start, int num_s
     if (q0 < 0 || n < 0 || n > static_cast<int64_t>(mask_words) * 32)
       return pkv::fail(PKV_ERR_INVALID_ARG, "%s: sequence %d has %lld nodes from %lld on, %d words a row", fn, s,
                        static_cast<long long>(n), static_cast<long long>(q0), mask_words);
+  }
+  // the starts go up, so no parent behind the last of them is read
+  for (int s = 0; s < num_seqs; ++s) {
+    const int64_t q0 = query_start[s], n = query_start[s + 1] - q0;
     for (int64_t j = 0; j < n; ++j)
       if (parents[q0 + j] >= j)
         return pkv::fail(PKV_ERR_INVALID_ARG, "%s: node %lld of sequence %d comes before its parent %d", fn,

@@ -103,6 +103,19 @@ def test_tree_masks_refuse_bad_trees():
             pkv.tree_masks(parents, start, device="cpu")
 
 
+def test_tree_masks_look_at_all_starts_before_any_parent(lib):
+    """The parents end at query_start's last entry: a start before it that is larger, or a decreasing one behind, is refused
+    without reading past them (what lies there would be refused in another way)."""
+    past = np.full(64, 99, np.int32)
+    past[0] = -1
+    for start in ([0, 40, 1], [0, 1, 60, 1], [0, 1, -5, 1], [-1, 1]):
+        st, masks = np.array(start, np.int32), np.full((64, 4), 7, np.int32)
+        assert lib.pkv_tree_masks(past.ctypes.data, st.ctypes.data, len(st) - 1, 4, masks.ctypes.data, None) == pkv.PKV_ERR_INVALID_ARG
+        assert b"nodes from" in lib.pkv_last_error() and (masks == 7).all(), lib.pkv_last_error()
+    with pytest.raises(pkv.PkvError):
+        pkv.tree_masks([-1], [0, 40, 1], device="cpu")
+
+
 @pytest.mark.parametrize("B", [4, 16])
 def test_truncate_matches_the_oracle(B):
     rng = np.random.default_rng(B)
