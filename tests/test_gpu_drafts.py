@@ -227,6 +227,15 @@ def test_clusters_without_nodes(cuda_device, seqs):
                 assert path[some[0], :n].tolist() == want and int(token[some[0]]) == x
 
 
+@pytest.mark.parametrize("with_draft", [True, False])
+@pytest.mark.parametrize("seqs,V", [(120, 333), (200, 333), (300, 333), (600, 333), (600, 3), (300, 1301)])
+def test_many_sequences(cuda_device, seqs, V, with_draft):
+    """Clusters of eight, four, two CTAs and of one; sequences without nodes among them."""
+    rng = np.random.default_rng(seqs)
+    sizes = check(make(seqs + V, rng.integers(0, 5, seqs).tolist(), V, branch=3, sharp=2.0), cuda_device, 4, with_draft)
+    assert len(set(sizes)) > 1
+
+
 @pytest.mark.parametrize("V", [3, 130, 1000, 50257])
 @pytest.mark.parametrize("refusals", [1, 2, 3, 4, 5, 7])
 def test_each_refusal_is_rounded_by_itself(cuda_device, refusals, V):
