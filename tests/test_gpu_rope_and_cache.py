@@ -148,3 +148,30 @@ def test_on_two_streams_at_once(cuda_device):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(a, b) for a, b in zip((got[i][0], *cases[i][6]), want[i]))
+
+
+def test_many_calls_on_two_streams(cuda_device):
+    """Calls of different shapes on two streams, all of them issued before any is waited for."""
+    shapes = [(300, 8, 2, 128, 128, 1, 16), (2000, 12, 3, 64, 32, 1, 8)]
+    cases = [make(10 + i, *shape, cuda_device) for i, shape in enumerate(shapes)]
+    args, want = [], []
+    for (qkv, inv, pos, _, w, slots, pools), (_, H, Hk, *_) in zip(cases, shapes):
+        p, sl = torch.from_numpy(pos[0]).to(cuda_device), torch.from_numpy(slots).to(cuda_device)
+        f = pkv.rope_frequencies(inv, cuda_device)
+        args.append(lambda kc, vc, st=None, a=(qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:], p, f), b=(sl, *w):
+                    pkv.rope_and_cache(*a, kc, vc, *b, stream=st))
+        alone = [x.clone() for x in pools]
+        want.append((args[-1](*alone), *alone))
+    calls = 12
+    pools = [[[x.clone() for x in c[6]] for _ in range(calls)] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for n in range(calls):
+        for i, st in enumerate(streams):
+            got[i].append(args[i](*pools[i][n], st))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for q, kv in zip(got[i], pools[i]):
+            assert all(torch.equal(a, b) for a, b in zip((q, *kv), want[i]))
+    assert pkv.device_error() == 0
