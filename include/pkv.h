@@ -599,8 +599,8 @@ int pkv_rope_and_cache(const uint16_t* q, const uint16_t* key, const uint16_t* v
  * t < context_lens[s] - n_s, and of the new ones position context_lens[s] - n_s + j
  * where bit j % 32 of word j / 32 of its mask row is set:
  *   out[query_start[s] + i, h, :] = sum_t softmax_t(scale * q . k_t) v_t
- * with head h / (num_heads / num_kv_heads) of the pools.  A row that sees nothing is
- * zeros.
+ * with head h / (num_heads / num_kv_heads) of the pools.  A row that sees nothing, or
+ * only logits of -inf, is zeros.
  *
  *   q             device [total_q, num_heads, head_dim] fp16, 16-byte aligned, a token's
  *                 heads contiguous, tokens q_stride elements apart (a multiple of 8)

@@ -212,6 +212,65 @@ def test_a_row_that_sees_only_infinite_logits(cuda_device):
     assert np.abs(got - want).max() <= 2.0 ** -9 * 4        # one key takes all, or all alike; |v| below 4 or so
 
 
+@pytest.mark.parametrize("ctx", [40, 3000])                 # one part, and many
+def test_infinite_logits(cuda_device, ctx):
+    """A key of -inf in the context has no weight, one of +inf (exp(inf - inf)) makes its row a NaN; a draft's reach the
+    rows that see it alone."""
+    nodes = 6
+    c = make(44, [ctx], [nodes], 2, 1, 64, 16, trees=[[-1, 0, 0, 1, 1, 2]])
+    c["q"][:] = np.abs(c["q"]) + np.float16(0.125)          # logits of such a key have one sign
+    at = lambda t: (c["tables"][0][t // 16], 0, t % 16)
+    c["k"][at(7)] = -np.inf
+    got = call(c, cuda_device).cpu().numpy().astype(np.float64)
+    assert pkv.device_error() == 0
+    keep = np.arange(ctx) != 7
+    k, v = (oa.gather_sequence(c[n], c["tables"][0], ctx)[keep] for n in ("k", "v"))
+    for i in range(nodes):
+        live = np.concatenate([np.ones(ctx - nodes - 1, bool), c["seen"][0][i]])
+        # as above with |o| and a at most the largest |v|, and dx below 2^-15 (logits here stay under 2^5)
+        most = (3 * 2.0 ** -11 + 2.0 ** -13) * np.abs(v).max()
+        assert np.abs(got[i] - oa.contiguous_attention(c["q"][i], np.repeat(k[live], 2, axis=1), np.repeat(v[live], 2, axis=1), 0.125)).max() < most
+    c["k"][at(ctx - nodes + 2)] = np.inf                    # node 2, which itself and its child 5 see
+    row = call(c, cuda_device).cpu().numpy().astype(np.float64)
+    assert np.isnan(row[[2, 5]]).all() and np.array_equal(row[[0, 1, 3, 4]], got[[0, 1, 3, 4]])
+    c["k"][at(9)] = np.inf
+    assert np.isnan(call(c, cuda_device).cpu().numpy()).all()
+    # nothing but keys without weight: as a row that sees nothing
+    c = make(45, [6], [6], 2, 1, 64, 16)
+    c["q"][:], c["k"][:] = 1, -np.inf
+    assert (call(c, cuda_device).cpu().numpy() == 0).all() and pkv.device_error() == 0
+
+
+@pytest.mark.parametrize("nodes,ctx,H,Hk,D", [(700, 700, 2, 2, 64), (1100, 1500, 2, 1, 128)])
+def test_prompt_chunks(cuda_device, nodes, ctx, H, Hk, D):
+    """Hundreds of new tokens, as a chain without a mask and as a tree."""
+    c = make(nodes, [ctx, 50], [nodes, 3], H, Hk, D, 16, trees=[list(range(-1, nodes - 1)), [-1, 0, 1]])
+    a, b = check(c, cuda_device, mask=False), check(c, cuda_device)
+    assert np.array_equal(a, b)
+    check(make(nodes + 1, [ctx], [nodes], H, Hk, D, 16), cuda_device)
+
+
+def test_the_same_twice(cuda_device):
+    """Parts are cut and joined in one order: a call repeats itself bit for bit, whatever ran in between."""
+    cs = [make(46, [2048], [8], 8, 8, 128, 16), make(47, [900, 77, 3, 1500], [12, 5, 3, 40], 8, 2, 128, 16),
+          make(48, [1000] * 9, [33] * 9, 8, 2, 64, 16)]
+    n = max(pkv.paged_attention_tree_workspace_size(len(c["lens"]), c["q"].shape[0], 64, *c["q"].shape[1:2], c["k"].shape[1], 128,
+                                                    c["tables"].shape[1], 16) for c in cs)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=cuda_device)
+    want = [call(c, cuda_device, workspace=ws).clone() for c in cs]
+    for order in ((2, 0, 1), (0, 0, 2), (1, 2, 0)):
+        for i in order:
+            assert torch.equal(call(cs[i], cuda_device, workspace=ws), want[i])
+
+
+def test_an_output_at_half_a_sector(cuda_device):
+    c = make(49, [300, 20], [9, 3], 4, 2, 64, 16)
+    want = call(c, cuda_device)
+    buf = torch.full((12 * 4 * 64 + 16,), 7.0, dtype=torch.float16, device=cuda_device)
+    out = buf[8:-8].view(12, 4, 64)                          # 16 bytes past a 32-byte boundary
+    assert torch.equal(call(c, cuda_device, out=out), want) and (buf[:8] == 7).all() and (buf[-8:] == 7).all()
+
+
 @pytest.mark.parametrize("q_scale", [0.0, 2.0 ** -20, 30.0])
 def test_queries_of_any_size(cuda_device, q_scale):
     check(make(37, [300, 5], [9, 5], 4, 2, 128, 16, q_scale=q_scale), cuda_device)
