@@ -9,9 +9,8 @@
 // Where none stays the next token is drawn from R: the least index whose running sum passes u_0 sum R.
 // So each kept and drawn token is distributed as the target alone would draw it.
 //
-// After k refusals at a node R is p less q and less M_1 q, .., M_(k-1) q, each rounded down to a whole number and none
-// below 0: the first refusal costs a difference a value, each further one a product.  (One product with
-// 1 + M_1 + .. + M_(k-1) instead takes up to a unit less or more for each refusal past the second.)
+// After k refusals at a node R = max(p - C q, 0) with C = 1 + M_1 + .. + M_(k-1), so a pass over a row costs one
+// product a value however often something was refused there.
 //
 // R and M are whole numbers in units of 2^-60 (fp32 values up to 1 lose only what is below 2^-60):
 // sums of whole numbers do not depend on their order, and the drawn token is the same however a row is
@@ -69,15 +68,15 @@ __device__ __forceinline__ u64 whole(float p, bool& bad) {
 }
 // floor(a b / 2^60), a and b up to 2^61
 __device__ __forceinline__ u64 part_of(u64 a, u64 b) { return __umul64hi(a << 2, b << 2); }
-// What `refused` refusals leave of p; shares: the sum before each of them (the first's, 1, is not looked at)
-__device__ __forceinline__ u64 less(u64 p, u64 q, const u64* shares, int refused) {
-  u64 r = p > q ? p - q : 0;
-#pragma unroll 1
-  for (int i = 1; i < refused; ++i) {
-    const u64 off = part_of(shares[i], q);
-    r = r > off ? r - off : 0;
-  }
-  return r;
+// What refusals take from a value: C q with C = whole + part / 2^60; off - p is what counts, so no more than 2.
+struct Taken {
+  unsigned whole;
+  u64 part;
+};
+__device__ __forceinline__ u64 less(u64 p, u64 q, const Taken& c) {
+  const u64 high = static_cast<u64>(static_cast<unsigned>(q >> 32)) * c.whole;
+  const u64 off = high >> 29 ? kMost : q * c.whole + part_of(c.part, q);
+  return p > off ? p - off : 0;
 }
 // sums that stay below 2^62 whatever the rows hold
 __device__ __forceinline__ u64 add_most(u64 a, u64 b) {
@@ -146,15 +145,14 @@ struct Nodes {
 // whether the next token is drawn from what it leaves.
 struct Order {
   int row, refused, last;
-  u64 u0;
+  unsigned taken_whole;
+  u64 taken_part, u0;
 };
 
 __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const VerifyParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  // of the current node's refusals: without draft distributions the tokens, with them the sum that was left before each
-  int* refused_x = reinterpret_cast<int*>(smem);
-  u64* shares = reinterpret_cast<u64*>(smem);
-  Nodes& nodes = *reinterpret_cast<Nodes*>(smem + kMaxNodes * 8);     // the first CTA's only
+  int* refused_x = reinterpret_cast<int*>(smem);                      // without draft distributions: the refused tokens
+  Nodes& nodes = *reinterpret_cast<Nodes*>(smem + kMaxNodes * 4);     // the first CTA's only
   __shared__ Order order;
   __shared__ u64 cta_sum[2][kMostCtas];
   __shared__ u64 warp_sum[kWarps], part_sum[kWarps];
@@ -204,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
   // the walk's state, in the first CTA's first warp
   int at = 0, size = 1, next = 1, k = 0;
   u64 share = kOne;
+  Taken taken{0, 0};
   bool ended = false;                                         // the row's sum is all that is left to find
   const int most = p.max_path;
   if (rank == 0 && tid < p.max_path) p.path[static_cast<int64_t>(s) * most + tid] = tid == 0 && ok ? 0 : -1;
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
         if (k > 0) {
           const u64 drawn = nodes.drawn[j];
           if (p.draft != nullptr) {
-            has = less(has, drawn, shares, k);
+            has = less(has, drawn, taken);
           } else {
             for (int i = 0; i < k; ++i)
               if (refused_x[i] == nodes.token[j]) has = 0;
@@ -252,7 +251,11 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
           at = j;
           share = kOne;
           k = 0;
+          taken = Taken{0, 0};
         } else if (p.draft != nullptr) {
+          const u64 c = taken.part + share;
+          taken.whole += static_cast<unsigned>(c >> 60);
+          taken.part = c & (kOne - 1);
           ++k;
           wants = true;                                       // M is the sum of what is left
         } else if (has > 0) {                                 // a token that is left nothing is noted already, or was 0
@@ -277,7 +280,9 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
         st_cluster(to, ok ? q0 + at : -1);
         st_cluster(to + 4, k);
         st_cluster(to + 8, static_cast<int>(ended));
-        st_cluster(to + 16, ok ? nodes.u[0] : 0ull);
+        st_cluster(to + 12, static_cast<int>(taken.whole));
+        st_cluster(to + 16, taken.part);
+        st_cluster(to + 24, ok ? nodes.u[0] : 0ull);
       }
     }
     cluster_sync();
@@ -293,11 +298,12 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
     auto first_line = [&](int piece) { return static_cast<int>(static_cast<int64_t>(lines) * piece / pieces); };
     const int first = first_line(mine), end = first_line(mine + 1);
     int refused = o.refused;
+    const Taken all_taken{o.taken_whole, o.taken_part};
     bool bad = false, slow = false;
     auto left = [&](int i) {                                  // R(i) after the refusals
       u64 r = whole(prow[i], bad);
       if (qrow != nullptr) {
-        if (refused > 0) r = less(r, whole(qrow[i], bad), shares, refused);
+        if (refused > 0) r = less(r, whole(qrow[i], bad), all_taken);
       } else {
         for (int j = 0; j < refused; ++j)
           if (refused_x[j] == i) r = 0;
@@ -312,10 +318,9 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
         if (k >= shift && k - shift < p.vocab) sum = add_most(sum, left(k - shift));
       return sum;
     };
-    // the same of whole lines, 16 bytes at a time; STEPS: refusals (3: three or more)
+    // the same of whole lines, 16 bytes at a time; STEPS: refusals (2: two or more)
     auto fast_sum = [&](auto steps, int from, int to) {
       constexpr int STEPS = decltype(steps)::value, FLY = STEPS == 0 ? 4 : 2;
-      const u64 second = STEPS == 2 ? shares[1] : 0;
       u64 sum = 0;
       unsigned largest = 0;
       const float4* pv = reinterpret_cast<const float4*>(prow - shift) + lane;
@@ -341,15 +346,8 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
             if (STEPS > 0) {
               const float ye = e == 0 ? c.x : e == 1 ? c.y : e == 2 ? c.z : c.w;
               const u64 q = whole_fast(ye, largest);
-              if (STEPS > 2) {
-                r = less(r, q, shares, refused);
-              } else {
-                r = r > q ? r - q : 0;                        // the first refusal takes q
-                if (STEPS > 1) {
-                  const u64 off = part_of(second, q);
-                  r = r > off ? r - off : 0;
-                }
-              }
+              if (STEPS > 1) r = less(r, q, all_taken);
+              else r = r > q ? r - q : 0;                     // the first refusal takes q
             }
             sum += r;                                         // eight at most before they are held down
           }
@@ -374,8 +372,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
         if (to < end) sum = add_most(sum, slow_sum(to, end));
         const u64 inner = qrow == nullptr || refused == 0 ? fast_sum(std::integral_constant<int, 0>(), from, to)
                           : refused == 1                  ? fast_sum(std::integral_constant<int, 1>(), from, to)
-                          : refused == 2                  ? fast_sum(std::integral_constant<int, 2>(), from, to)
-                                                          : fast_sum(std::integral_constant<int, 3>(), from, to);
+                                                          : fast_sum(std::integral_constant<int, 2>(), from, to);
         sum = add_most(sum, inner);
         fast_from = from;
         fast_to = to;
@@ -422,8 +419,6 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_draft_kernel(const
     }
     if (!o.last) {
       share = total;
-      // each CTA keeps the sums for itself; the next order's barrier lies between this and their use elsewhere in it
-      if (tid == 0) shares[o.refused] = total;
       if (bad && rank == 0 && tid == 0) record_error(PKV_DEV_BAD_PROBABILITY);
       continue;
     }
@@ -622,7 +617,7 @@ int pkv_verify_draft(const float* target_probs, const float* draft_probs, const 
   p.total_q = total_q;
   p.vocab = vocab_size;
   p.max_path = max_path;
-  constexpr int smem = kMaxNodes * 8 + static_cast<int>(sizeof(Nodes));
+  constexpr int smem = kMaxNodes * 4 + static_cast<int>(sizeof(Nodes));
   static_assert(smem <= 47 * 1024, "fits without asking for more");
   int ctas = kMostCtas;
   while (ctas > 1 && num_seqs * ctas > kEnough) ctas /= 2;
