@@ -650,16 +650,17 @@ int pkv_tree_masks(const int32_t* parents, const int32_t* query_start, int num_s
 
 /* Which drafts stay, by the target's distributions and given random numbers, and the
  * token that follows them.  From node 0 on, the children of the current node c are tried in
- * ascending order.  With R = p_c and M = 1 at first, child j with token x
+ * ascending order.  With R = p_c, M = 1 and C = 0 at first, child j with token x
  *   stays, and becomes the current node, if u_j M q_c(x) < R(x);
- *   otherwise R <- max(R - M q_c, 0) and M <- sum R.
+ *   otherwise C <- C + M, R <- max(p_c - C q_c, 0) and M <- sum R
+ * (in exact numbers the same as R <- max(R - M q_c, 0)).
  * Without draft distributions (drafts that were looked up, not drawn) q_c(x) counts as 1,
  * and a refusal is M <- M - R(x), R(x) <- 0.  Where no child stays, the next token is
  * the least index whose running sum of R passes u_0 sum R (of p_c, should R be 0
  * throughout).  For children drawn independently from q_c the kept and the drawn
  * tokens are so distributed as the target alone would draw them.
- * Everything is computed in whole numbers of 2^-60, products rounded down: the result is a
- * function of the inputs alone.
+ * Everything is computed in whole numbers of 2^-60, each product (M q_c(x), that times
+ * u_j, C q_c, u_0 sum R) rounded down, so that the result is a function of the inputs alone.
  *
  *   target_probs device fp32 [total_q, vocab_size], row i the target's distribution
  *                behind node i, rows target_stride elements apart

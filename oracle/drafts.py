@@ -50,7 +50,7 @@ def _whole(x) -> list:
 def verify(target, draft, tokens, parents, uniforms, max_path):
     """One sequence's (path, next token) from its rows, by the rule's own words."""
     at, path = 0, [0]
-    left, mass = _whole(target[0]), ONE
+    left, mass, taken = _whole(target[0]), ONE, 0
     j = 1
     while j < len(tokens) and len(path) < max_path:
         if parents[j] == at:
@@ -59,15 +59,16 @@ def verify(target, draft, tokens, parents, uniforms, max_path):
             threshold = (mass * (ONE if q is None else q[x]) >> 60) * u >> 60
             if threshold < left[x]:
                 path.append(j)
-                at, left, mass = j, _whole(target[j]), ONE
+                at, left, mass, taken = j, _whole(target[j]), ONE, 0
             elif q is None:
                 mass = max(mass - left[x], 0)
                 left[x] = 0
             else:
-                left = [max(r - (mass * d >> 60), 0) for r, d in zip(left, q)]
+                taken += mass
+                left = [max(p - (taken * d >> 60), 0) for p, d in zip(_whole(target[at]), q)]
                 mass = sum(left)
         j += 1
-    # children of the last node are tried even where the path is full: they are not, so its row is untouched
+    # where the path is full the last node's children are not tried, and its row is untouched
     if sum(left) == 0:
         left = _whole(target[at])
     aim, upto = sum(left) * _whole([uniforms[0]])[0] >> 60, 0

@@ -236,6 +236,27 @@ def test_many_sequences(cuda_device, seqs, V, with_draft):
     assert len(set(sizes)) > 1
 
 
+@pytest.mark.parametrize("V", [3, 130, 1000, 50257])
+@pytest.mark.parametrize("refusals", [1, 2, 3, 4, 5, 7])
+def test_refusals_are_rounded_in_their_sum(cuda_device, refusals, V):
+    """The draft's distribution misses the target's by one step of fp32 in one token, so that every refusal leaves the
+    2^24-th part of that step: 2^36, 2^12 and 1 units, and with the fourth nothing, so that the token comes from
+    the whole row.  (Rounding every refusal's product by itself would leave the one unit for good.)"""
+    e = 2.0 ** -24
+    first, few, never = np.random.default_rng(V).choice(V, 3, replace=False)
+    if few < first:
+        first, few = few, first                             # the token that the whole row gives lies behind
+    target, draft = np.zeros((2, V), np.float32)
+    target[first], target[few] = 1 - 4 * e, 4 * e
+    draft[first], draft[few], draft[never] = 1 - 5 * e, 4 * e, e
+    n = refusals + 1
+    c = dict(target=np.tile(target, (n, 1)), draft=np.tile(draft, (n, 1)), tokens=np.full(n, never, np.int32),
+             parents=np.array([-1] + [0] * refusals, np.int32), start=np.array([0, n], np.int32), u=np.full(n, 1 - e, np.float32))
+    assert od.verify(c["target"], c["draft"], c["tokens"], c["parents"], c["u"], 4) == ([0], first if refusals < 4 else few)
+    check(c, cuda_device, 4)
+    check(dict(c, draft=c["target"]), cuda_device, 4)       # nothing is left from the first refusal on
+
+
 def test_verify_refusals(cuda_device):
     c = make(13, [4], 20)
     t = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(cuda_device)

@@ -68,6 +68,17 @@ def test_a_draft_like_the_target_always_stays():
     assert od.verify(np.stack([p, p, p]), np.stack([p, p, p]), [0, 2, 1], [-1, 0, 1], [0.5, 0.9, 0.9], 2)[0] == [0, 1]
 
 
+@pytest.mark.parametrize("refusals", [1, 2, 3, 4, 6])
+def test_what_refusals_take_is_rounded_once(refusals):
+    """p = 1 - 2^-22 and q = p - 2^-24 on token 0: with C_1 = 1 and C_k+1 = C_k + M_k, floor(C_k q) leaves 2^36, 2^12, 1 and
+    0 units of 2^-60, worked out by hand; the rest of the row is covered by q."""
+    e = 2.0 ** -24
+    p, q = np.array([1 - 4 * e, 4 * e, 0], np.float32), np.array([1 - 5 * e, 4 * e, e], np.float32)
+    n = refusals + 1
+    path, token = od.verify(np.stack([p] * n), np.stack([q] * n), [2] * n, [-1] + [0] * refusals, [1 - e] * n, 4)
+    assert path == [0] and token == (0 if refusals < 4 else 1)
+
+
 def test_a_row_that_leaves_nothing_falls_back_on_the_target():
     p, q = np.array([0.25, 0.75], np.float32), np.array([0.5, 1.0], np.float32)   # q covers p: nothing is left
     path, tok = od.verify(p[None].repeat(2, 0), q[None].repeat(2, 0), [0, 0], [-1, 0], [0.3, 0.9], 4)
