@@ -81,7 +81,7 @@ enum {
                                    from its group's first sequence's, a bad group layout, or a
                                    group larger than max_group_size */
   PKV_DEV_BAD_AXIS = 8,         /* rotation: a pair's position axis outside [0, num_axes) */
-  PKV_DEV_BAD_TREE = 9,         /* drafts: a node before its parent, or a path whose nodes do not go up */
+  PKV_DEV_BAD_TREE = 9,         /* drafts: a node before its parent, or a path's node before its place or past the last */
   PKV_DEV_BAD_TOKEN = 10,       /* drafts: a token outside [0, vocab_size) */
   PKV_DEV_BAD_PROBABILITY = 11  /* drafts: a NaN, a value outside [0, 1], or a row whose sum is 0 or, after the
                                    refusals, above 1.5 */
@@ -629,7 +629,12 @@ int pkv_rope_and_cache(const uint16_t* q, const uint16_t* key, const uint16_t* v
  * does not see, and slots past the context, do not reach its row, whatever they hold.
  * Tensor cores: as pkv_prompt_attention (fp16 products, fp32 sums, weights rounded to
  * fp16 before they multiply V and to 0 below 2^-32 of the row's largest, up to n 2^-27 of
- * a row over n keys cut off).  All sequences' keys are cut evenly over the GPU, so a row may
+ * a row over n keys cut off).  So with one new token it is a little less exact than
+ * pkv_paged_attention_decode, whose weights are fp32 (2.9e-4 of the result in the 2-norm,
+ * the output's rounding alone is 2.1e-4).  Without a mask all of a sequence's keys are still
+ * gone through for every 128 rows, those behind a row's own included: for hundreds of
+ * new tokens over a short context pkv_prompt_attention or pkv_paged_attention_prefill
+ * does half the work.  All sequences' keys are cut evenly over the GPU, so a row may
  * differ in its last bits between batches. */
 size_t pkv_paged_attention_tree_workspace_size(int num_seqs, int total_q, int max_query_len, int num_heads,
                                                int num_kv_heads, int head_dim, int max_blocks_per_seq,
@@ -693,7 +698,8 @@ int pkv_verify_draft(const float* target_probs, const float* draft_probs, const 
  * for 0 < i < path_len[s] and all heads, K and V, as if all rows were read first.
  * Bit-exact.
  *
- *   k_caches, v_caches HOST arrays of num_layers device pool pointers, 16-byte aligned
+ *   k_caches, v_caches HOST arrays of num_layers device pool pointers, 16-byte aligned, no
+ *                      pool twice (also not as a layer's K and V): it would be moved twice
  *   slot_mapping       device [total_q] int64, the nodes' slots, no slot twice; a move
  *                      from or to a negative one is left out, one outside the pool records
  *                      PKV_DEV_BAD_SLOT and is left out
