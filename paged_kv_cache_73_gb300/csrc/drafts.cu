@@ -21,8 +21,10 @@
 // What it has to read: a few values a node, and of the vocabulary only the rows of nodes where a
 // draft was refused, or where the path ends.  Those are read once per refusal, by the CTAs of a cluster (a
 // row's later passes come from L2), each warp a piece of its own; the last pass's piece sums
-// find the piece that holds the drawn token, and one warp reads that piece again.  The cluster's
-// first CTA decides and tells the others, so that all of them come to the same barriers.
+// find the piece that holds the drawn token, and the warps of its CTA read that piece again.  The cluster's
+// first CTA decides and tells the others, so that all of them come to the same barriers.  It writes into their
+// shared memory, so the first barrier, which tells that they run, is arrived at ahead of all else and waited for
+// behind the loads of the nodes.
 //
 // The move.  A path's nodes go up with their place, path[i] >= i, so a thread that takes its 16 bytes of every
 // kept row in the path's order reads each row before it overwrites it: no staging, no barrier.
@@ -45,28 +47,28 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kMaxNodes = 1024;      // of a sequence
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;         // of a cluster
-constexpr int kResident = 4;         // CTAs to an SM: three leave 64 chains over 50257 tokens at 20 us for 16.5
+constexpr int kResident = 4;         // CTAs to an SM: three leave 64 chains over 50257 tokens at 20 us for 16
 // A cluster has eight CTAs, less where all of them would be more than kEnough: 256 chains over 32000 tokens take 42 us
 // with eight each, 31 with four; 128 trees over 131072, where refusals follow one another, 77 with eight, 94 with four.
 constexpr int kEnough = 1024;
 constexpr u64 kOne = 1ull << 60, kMost = 1ull << 61;
 
-// The same of a row's values where all of them are in [0, 1] (largest: the bits of the largest met, so that the
-// others, whose bits are above those of 1, are noticed): a shift of the 24-bit mantissa from the top.
-constexpr unsigned kOneBits = 0x3f800000u;
-__device__ __forceinline__ u64 whole_fast(float p, unsigned& largest) {
-  const unsigned b = __float_as_uint(p);
-  largest = max(largest, b);
-  return (static_cast<u64>((b << 5) & 0x0fffffe0u | 0x10000000u) << 32) >> min(127u - (b >> 23), 63u);
-}
-// floor(p 2^60) of p in [0, 1]; what is no probability (a NaN, negative, above 1 by more than
-// rounding) sets `bad` and counts as 0 or 1
+// floor(p 2^60) of p in [0, 1]; what is no probability (a NaN, negative, above 1 by more than 2^-10, as rounded
+// softmaxes are not) sets `bad`, and counts as 0 or 1
 __device__ __forceinline__ u64 whole(float p, bool& bad) {
   bad |= !(p >= 0.f && p <= 1.0009765625f);
   const unsigned b = p >= 0.f ? __float_as_uint(fminf(p, 1.f)) & 0x7fffffffu : 0u;
   const int e = static_cast<int>(b >> 23) - 90;
   const u64 m = (b & 0x7fffffu) | 0x800000u;
   return e >= 0 ? m << e : e > -24 ? m >> -e : 0;
+}
+// The same of values that are all in [0, 1] (largest: the bits of the largest met, so that the
+// others, whose bits are above those of 1, are noticed): a shift of the 24-bit mantissa from the top.
+constexpr unsigned kOneBits = 0x3f800000u;
+__device__ __forceinline__ u64 whole_fast(float p, unsigned& largest) {
+  const unsigned b = __float_as_uint(p);
+  largest = max(largest, b);
+  return (static_cast<u64>((b << 5) & 0x0fffffe0u | 0x10000000u) << 32) >> min(127u - (b >> 23), 63u);
 }
 // floor(a b / 2^60), a and b up to 2^61
 __device__ __forceinline__ u64 part_of(u64 a, u64 b) { return __umul64hi(a << 2, b << 2); }

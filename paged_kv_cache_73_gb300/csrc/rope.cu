@@ -26,8 +26,8 @@
 // are not touched, to theirs: the key's second trip through memory (written, then read by the scatter) and
 // one launch are saved.  A token's slot is read once by the warp that takes the token.  The addresses
 // want more registers than 80: with five CTAs to an SM 16411 tokens of 40 + 8 + 8 heads of 128 with norms take
-// 75 us, 94 % of the copy rate (six, with spills, 87, four 80), 1024 of 64 + 8 + 8 with interleaved pairs 9.8, and
-// 64 of 40 + 40 + 40 heads 3.4 in a row of such calls.
+// 75 us, 94 % of the copy rate (six, with spills, 87, four 80), 1024 of 64 + 8 + 8 with interleaved pairs 9.4, and
+// 64 of 40 + 40 + 40 heads 3.3 in a row of such calls.
 // Measured: 32768 tokens of 40 + 8 heads of 128 with norms and three axes, 122 us, 98 % of the
 // copy rate, and with interleaved pairs 139 us, 85 % (122 registers against 80, four CTAs to an SM against
 // six); 64 tokens of 40 + 40 heads 4.6 us in a row of such calls, a launch and two round trips.
