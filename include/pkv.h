@@ -699,7 +699,7 @@ int pkv_verify_draft(const float* target_probs, const float* draft_probs, const 
  * Bit-exact.
  *
  *   k_caches, v_caches HOST arrays of num_layers device pool pointers, 16-byte aligned, no
- *                      pool twice (also not as a layer's K and V): it would be moved twice
+ *                      pool twice (also not as a layer's K and V): such a call is refused
  *   slot_mapping       device [total_q] int64, the nodes' slots, no slot twice; a move
  *                      from or to a negative one is left out, one outside the pool records
  *                      PKV_DEV_BAD_SLOT and is left out

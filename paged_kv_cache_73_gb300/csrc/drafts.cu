@@ -30,8 +30,12 @@
 // kept row in the path's order reads each row before it overwrites it: no staging, no barrier.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <functional>
+#include <new>
 #include <type_traits>
+#include <vector>
 
 #include "launch.cuh"
 #include "pkv_internal.h"
@@ -650,6 +654,16 @@ int pkv_move_accepted(uint16_t* const* k_caches, uint16_t* const* v_caches, int 
   for (int l = 0; l < num_layers; ++l)
     if (!k_caches[l] || !v_caches[l] || !aligned16(k_caches[l]) || !aligned16(v_caches[l]))
       return pkv::fail(PKV_ERR_INVALID_ARG, "%s: layer %d: a pool is null or not 16-byte aligned", fn, l);
+  // a pool that is there twice would have its rows moved by two CTAs, each over what the other may have moved already
+  try {
+    std::vector<const void*> pools(k_caches, k_caches + num_layers);
+    pools.insert(pools.end(), v_caches, v_caches + num_layers);
+    std::sort(pools.begin(), pools.end(), std::less<const void*>());
+    if (std::adjacent_find(pools.begin(), pools.end()) != pools.end())
+      return pkv::fail(PKV_ERR_INVALID_ARG, "%s: a pool is given twice", fn);
+  } catch (const std::bad_alloc&) {
+    return pkv::fail(PKV_ERR_OOM, "%s: out of host memory", fn);
+  }
   if (num_seqs == 0) {
     pkv::clear_error();
     return PKV_OK;

@@ -230,6 +230,12 @@ def move(lib, **kw):
     return lib.pkv_move_accepted(arr(a["k"]), arr(a["v"]), *[a[n] for n in "L slots start path size S T most Hk D B N".split()], None)
 
 
+@pytest.mark.parametrize("kw", [dict(k=(16, 16)), dict(v=(48, 48)), dict(v=(48, 16)), dict(k=(64, 32))])
+def test_move_accepted_refuses_a_pool_twice(lib, kw):
+    """Layers that share their cache, or keys that are the values: its rows would be moved twice."""
+    assert move(lib, **kw) == pkv.PKV_ERR_INVALID_ARG and b"twice" in lib.pkv_last_error()
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(S=0), pkv.PKV_OK), (dict(L=0), pkv.PKV_ERR_INVALID_ARG), (dict(k=None), pkv.PKV_ERR_INVALID_ARG),
     (dict(v=(48, 8)), pkv.PKV_ERR_INVALID_ARG), (dict(D=32), pkv.PKV_ERR_UNSUPPORTED), (dict(B=2), pkv.PKV_ERR_UNSUPPORTED),
